@@ -29,7 +29,9 @@ ABI_SYMBOLS = ("tok_abi_version", "tok_status_str", "tok_last_cuda_error", "tok_
                "tok_haar_inv_windows", "tok_haar_fwd_single", "tok_haar_inv_single", "tok_haar_fwd_channels_last", "tok_haar_padded_extents", "tok_haar_fwd_padded", "tok_haar_inv_cropped",
                "tok_haar_fwd_chunk", "tok_haar_inv_chunk", "tok_conv_spatial", "tok_conv_temporal_causal",
                "tok_conv_factorized", "tok_patch_embed_pack_weights", "tok_patch_embed_spatial", "tok_fsq_encode", "tok_fsq_decode", "tok_fsq_backward_workspace_size",
-               "tok_fsq_encode_backward", "tok_fsq_encode_backward_noalloc", "tok_fsq_decode_backward")
+               "tok_fsq_encode_backward", "tok_fsq_encode_backward_noalloc", "tok_fsq_decode_backward",
+               "tok_rope_table", "tok_rope_grid", "tok_rope_grid_adjoint", "tok_rope_positions",
+               "tok_rope_positions_adjoint")
 
 _lib = None
 
@@ -96,6 +98,15 @@ def lib():
         L.tok_conv_factorized.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i64, vp]
         L.tok_fsq_encode.restype = i32
         L.tok_fsq_encode.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp]
+        f64 = ctypes.c_double
+        L.tok_rope_table.restype = i32
+        L.tok_rope_table.argtypes = [vp] + [i64] * 6 + [f64] * 6 + [vp]
+        for f in (L.tok_rope_grid, L.tok_rope_grid_adjoint):
+            f.restype = i32
+            f.argtypes = [vp, vp, vp, i32] + [i64] * 19 + [i32, vp]
+        for f in (L.tok_rope_positions, L.tok_rope_positions_adjoint):
+            f.restype = i32
+            f.argtypes = [vp] * 5 + [i32] + [i64] * 13 + [i32, vp]
         L.tok_fsq_decode.restype = i32
         L.tok_fsq_decode.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp]
         _lib = L
@@ -552,6 +563,112 @@ def tok_fsq_decode_backward(idx, w, grad_out, grad_codes, grad_w, workspace, str
 
 
 # ---------------------------------------------------------------------------
+# Rotary positions of the axes (time, height, width).
+# ---------------------------------------------------------------------------
+def _triple(v):
+    return tuple(v) if isinstance(v, (tuple, list)) else (v, v, v)
+
+
+def rope_table(sizes, dims, base=10000.0, scale=1.0, device="cuda", stream=None) -> torch.Tensor:
+    """cos and sin of positions [0, sizes[a]) and the dims[a] / 2 pairs of each axis (t, h, w), for the
+    rope_* calls: float32 [sum sizes[a] * dims[a]].  base, scale: one number or one per axis."""
+    (nt, nh, nw), (dt, dh, dw) = sizes, dims
+    if min(nt, nh, nw, dt, dh, dw) < 0:
+        raise ValueError("sizes and dims must not be negative")
+    if torch.device(device).type != "cuda":
+        raise ValueError("the table must be on a CUDA device (there is no CPU path)")
+    table = _new(nt * dt + nh * dh + nw * dw, torch.float32, device, stream)
+    with torch.cuda.device(table.device):
+        _check(lib().tok_rope_table(_ptr(table), nt, nh, nw, dt, dh, dw, *_triple(base), *_triple(scale),
+                                    _stream(table, stream)), "tok_rope_table")
+    return table
+
+
+def _rope_check(x, y, table, sizes, dims):
+    if not (x.is_cuda and y.is_cuda and table.is_cuda):
+        raise ValueError("x, y and table must be CUDA tensors (there is no CPU path)")
+    if x.device != y.device or x.device != table.device:
+        raise ValueError("x, y and table must be on one device")
+    if x.shape != y.shape or x.dtype != y.dtype:
+        raise ValueError("x and y must have the same shape and dtype")
+    (nt, nh, nw), (dt, dh, dw) = sizes, dims
+    if table.dtype != torch.float32 or not table.is_contiguous() or table.numel() != nt * dt + nh * dh + nw * dw:
+        raise ValueError("table must be the float32 rope_table of these sizes and dims")
+    if x.shape[-1] > 1 and (x.stride(-1) != 1 or y.stride(-1) != 1):
+        raise ValueError("the channels of x and y must be dense")
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """The one stride of the leading dimensions of [..., heads, D] taken as one index."""
+    stride = None
+    for n, s in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if n != 1:
+            if stride is None:
+                first, stride = s, s
+            elif s != stride:
+                raise ValueError(f"the leading dimensions of {name} must have one common stride")
+            stride *= n
+    return 0 if stride is None else first
+
+
+def _rope_grid(name, x, y, table, sizes, dims, origin, interleaved, stream):
+    _rope_check(x, y, table, sizes, dims)
+    if x.dim() != 6:
+        raise ValueError("the tensors must be [B, T, h, w, heads, D]")
+    B, T, h, w, H, D = x.shape
+    with torch.cuda.device(x.device):
+        _check(getattr(lib(), name)(x.data_ptr(), y.data_ptr(), table.data_ptr(), _dtype_code(x), B, T, h, w, H, D,
+                                    _token_stride(x, "x"), x.stride(4), _token_stride(y, "y"), y.stride(4), *origin,
+                                    *sizes, *dims, bool(interleaved), _stream(x, stream)), name)
+    return y
+
+
+def tok_rope_grid(x, y, table, sizes, dims, origin=(0, 0, 0), interleaved=False, stream=None):
+    """Rotary positions of every token of a grid: x [B,T,h,w,heads,D] -> y, token (t, i, j) at position
+    origin + (t, i, j).  x and y may be strided (dense channels, one token stride); y may be x."""
+    return _rope_grid("tok_rope_grid", x, y, table, sizes, dims, origin, interleaved, stream)
+
+
+def tok_rope_grid_adjoint(gy, gx, table, sizes, dims, origin=(0, 0, 0), interleaved=False, stream=None):
+    """Gradient of tok_rope_grid: gy -> gx."""
+    return _rope_grid("tok_rope_grid_adjoint", gy, gx, table, sizes, dims, origin, interleaved, stream)
+
+
+def _rope_positions(name, x, y, pos, table, sizes, dims, interleaved, bad_count, stream):
+    _rope_check(x, y, table, sizes, dims)
+    if x.dim() < 3:
+        raise ValueError("the tensors must be [..., heads, D]")
+    if not pos.is_cuda or pos.device != x.device or pos.dtype != torch.int32 or not pos.is_contiguous() \
+            or pos.shape != x.shape[:-2] + (3,):
+        raise ValueError("pos must be a contiguous int32 CUDA tensor [..., 3] of (t, h, w)")
+    if bad_count is not None and (not bad_count.is_cuda or bad_count.device != x.device
+                                  or bad_count.dtype != torch.int32 or bad_count.numel() < 1):
+        raise ValueError("bad_count must be an int32 CUDA tensor")
+    H, D = x.shape[-2:]
+    N = 1
+    for n in x.shape[:-2]:
+        N *= n
+    with torch.cuda.device(x.device):
+        _check(getattr(lib(), name)(x.data_ptr(), y.data_ptr(), pos.data_ptr(), table.data_ptr(),
+                                    None if bad_count is None else bad_count.data_ptr(), _dtype_code(x), N, H, D,
+                                    _token_stride(x, "x"), x.stride(-2), _token_stride(y, "y"), y.stride(-2), *sizes,
+                                    *dims, bool(interleaved), _stream(x, stream)), name)
+    return y
+
+
+def tok_rope_positions(x, y, pos, table, sizes, dims, interleaved=False, bad_count=None, stream=None):
+    """Rotary positions of tokens at given places: x [..., heads, D], pos [..., 3] int32 -> y.  A position
+    outside the table gives NaN in the rotated channels and adds 1 to bad_count (int32 CUDA tensor)."""
+    return _rope_positions("tok_rope_positions", x, y, pos, table, sizes, dims, interleaved, bad_count, stream)
+
+
+def tok_rope_positions_adjoint(gy, gx, pos, table, sizes, dims, interleaved=False, bad_count=None, stream=None):
+    """Gradient of tok_rope_positions: gy -> gx."""
+    return _rope_positions("tok_rope_positions_adjoint", gy, gx, pos, table, sizes, dims, interleaved, bad_count,
+                           stream)
+
+
+# ---------------------------------------------------------------------------
 # Allocating wrappers.
 # ---------------------------------------------------------------------------
 def haar_fwd(x: torch.Tensor, stream=None) -> torch.Tensor:
@@ -641,3 +758,32 @@ def fsq_decode_backward(idx: torch.Tensor, w: torch.Tensor, grad_out: torch.Tens
     grad_codes = torch.empty((B, FSQ_DIM) + tuple(grad_out.shape[2:]), dtype=torch.float32, device=idx.device)
     grad_w = torch.empty_like(w)
     return tok_fsq_decode_backward(idx, w, grad_out, grad_codes, grad_w, _workspace(B, C, S, idx.device), stream)
+
+
+def _new(shape, dtype, device, stream):
+    """A tensor for work on `stream` (memory that no other stream may still be using)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _dense(x, stream):
+    return _new(x.shape, x.dtype, x.device, stream)
+
+
+def rope_grid(x, table, sizes, dims, origin=(0, 0, 0), interleaved=False, stream=None) -> torch.Tensor:
+    return tok_rope_grid(x, _dense(x, stream), table, sizes, dims, origin, interleaved, stream)
+
+
+def rope_grid_adjoint(gy, table, sizes, dims, origin=(0, 0, 0), interleaved=False, stream=None) -> torch.Tensor:
+    return tok_rope_grid_adjoint(gy, _dense(gy, stream), table, sizes, dims, origin, interleaved, stream)
+
+
+def rope_positions(x, pos, table, sizes, dims, interleaved=False, bad_count=None, stream=None) -> torch.Tensor:
+    return tok_rope_positions(x, _dense(x, stream), pos, table, sizes, dims, interleaved, bad_count, stream)
+
+
+def rope_positions_adjoint(gy, pos, table, sizes, dims, interleaved=False, bad_count=None,
+                           stream=None) -> torch.Tensor:
+    return tok_rope_positions_adjoint(gy, _dense(gy, stream), pos, table, sizes, dims, interleaved, bad_count, stream)

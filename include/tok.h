@@ -453,6 +453,65 @@ TOK_API tok_status tok_fsq_decode_backward(const int32_t *idx, const float *w, c
                                            int64_t workspace_bytes, int64_t B, int64_t C, int64_t S,
                                            cudaStream_t stream);
 
+/*
+ * Operators of a model over the latent grid's tokens.  [notes] (world models): an
+ * autoregressive transformer predicts the FSQ codes of the grid, with rotary
+ * positions of three axes and cross attention to the prompt's encoder states.
+ * Not on the pages' API: the layers the pages name, on the caller's tensors.
+ * Unlike the calls above, these take strided tensors (strides in elements, the
+ * last index dense) where stated.
+ */
+
+/*
+ * Rotary positions of the axes time, height, width.  Axis a has d_a channels (even,
+ * possibly 0); its pair i turns by pos_a * scale_a * base_a^(-2i / d_a):
+ *   (p, q) -> (p cos - q sin, p sin + q cos).
+ * The R = dt + dh + dw <= D first channels of each head are the pairs of time,
+ * height, width in turn; pair j is channels (2j, 2j + 1) if `interleaved`, else
+ * (j, j + R/2).  Channels from R on are copied.  Computed in fp32, rounded once.
+ *
+ * tok_rope_table -- cos and sin of every position and pair, made once for a model:
+ *   table : nt*dt + nh*dh + nw*dw floats, 8-byte aligned (output): [nt][dt/2][2],
+ *           then [nh][dh/2][2], then [nw][dw/2][2], (cos, sin); computed in 64 bits.
+ *   The apply calls take any table of this layout.
+ *
+ * tok_rope_grid -- every token of a grid: x [B, T, h, w, heads, D] -> y, token
+ *   ((b*T + t)*h + i)*w + j at position (t0 + t, h0 + i, w0 + j).  Token and head
+ *   strides are given (so the queries and keys of one fused projection are one
+ *   call); y == x with equal strides turns in place.
+ * tok_rope_positions -- x [N, heads, D] with pos [N, 3] int32 (t, h, w) of each
+ *   token.  A token with a position outside the table gets NaN in its rotated
+ *   channels and adds 1 to bad_count (device int32 or NULL; the caller zeroes it).
+ * tok_rope_grid_adjoint, tok_rope_positions_adjoint -- the gradients: the opposite
+ *   angles, gy -> gx.
+ * Errors: TOK_ERR_SHAPE (odd or negative widths, R > D, odd D, grid outside the
+ * table, negative strides, a y that holds an element twice, 2^31 tokens or more),
+ * TOK_ERR_DTYPE, TOK_ERR_NULL, TOK_ERR_ALIGN, TOK_ERR_ALIAS, TOK_ERR_CUDA.
+ */
+TOK_API tok_status tok_rope_table(float *table, int64_t nt, int64_t nh, int64_t nw, int64_t dt, int64_t dh,
+                                  int64_t dw, double base_t, double base_h, double base_w, double scale_t,
+                                  double scale_h, double scale_w, cudaStream_t stream);
+TOK_API tok_status tok_rope_grid(const void *x, void *y, const float *table, tok_dtype dtype, int64_t B, int64_t T,
+                                 int64_t h, int64_t w, int64_t heads, int64_t D, int64_t x_token, int64_t x_head,
+                                 int64_t y_token, int64_t y_head, int64_t t0, int64_t h0, int64_t w0, int64_t nt,
+                                 int64_t nh, int64_t nw, int64_t dt, int64_t dh, int64_t dw, int interleaved,
+                                 cudaStream_t stream);
+TOK_API tok_status tok_rope_grid_adjoint(const void *gy, void *gx, const float *table, tok_dtype dtype, int64_t B,
+                                         int64_t T, int64_t h, int64_t w, int64_t heads, int64_t D,
+                                         int64_t gy_token, int64_t gy_head, int64_t gx_token, int64_t gx_head,
+                                         int64_t t0, int64_t h0, int64_t w0, int64_t nt, int64_t nh, int64_t nw,
+                                         int64_t dt, int64_t dh, int64_t dw, int interleaved, cudaStream_t stream);
+TOK_API tok_status tok_rope_positions(const void *x, void *y, const int32_t *pos, const float *table,
+                                      int32_t *bad_count, tok_dtype dtype, int64_t N, int64_t heads, int64_t D,
+                                      int64_t x_token, int64_t x_head, int64_t y_token, int64_t y_head, int64_t nt,
+                                      int64_t nh, int64_t nw, int64_t dt, int64_t dh, int64_t dw, int interleaved,
+                                      cudaStream_t stream);
+TOK_API tok_status tok_rope_positions_adjoint(const void *gy, void *gx, const int32_t *pos, const float *table,
+                                              int32_t *bad_count, tok_dtype dtype, int64_t N, int64_t heads,
+                                              int64_t D, int64_t gy_token, int64_t gy_head, int64_t gx_token,
+                                              int64_t gx_head, int64_t nt, int64_t nh, int64_t nw, int64_t dt,
+                                              int64_t dh, int64_t dw, int interleaved, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

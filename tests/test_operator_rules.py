@@ -1,0 +1,87 @@
+"""The token-model operators refuse bad arguments on the host before anything is launched.
+
+No call here reaches a kernel launch: each case fails validation (or is empty) first, so
+the tests run on CPU-only machines; the addresses are stand-ins, never dereferenced.
+"""
+import ctypes
+
+import pytest
+import torch
+
+import haar_wavelet_patching_b200 as hwp
+
+F = ctypes.c_void_p
+NULL = F(0)
+X, Y, TB, POS, BAD = F(0x1000000), F(0x2000000), F(0x3000000), F(0x4000000), F(0x5000000)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from haar_wavelet_patching_b200.build import build
+    build()
+    return hwp.lib()
+
+
+def grid(lib, x=X, y=Y, table=TB, dtype=1, B=1, T=2, h=3, w=4, H=2, D=16, xs=(32, 16), ys=(32, 16), o=(0, 0, 0),
+         sizes=(2, 3, 4), dims=(4, 4, 8), il=0, f="tok_rope_grid"):
+    return getattr(lib, f)(x, y, table, dtype, B, T, h, w, H, D, *xs, *ys, *o, *sizes, *dims, il, NULL)
+
+
+@pytest.mark.parametrize("f", ["tok_rope_grid", "tok_rope_grid_adjoint"])
+def test_rope_grid_rules(lib, f):
+    E = hwp
+    bad = [dict(dims=(3, 4, 8)), dict(dims=(4, 8, 8)), dict(dims=(-2, 4, 8)), dict(D=15, dims=(4, 4, 6)), dict(B=-1),
+           dict(o=(1, 0, 0)), dict(o=(0, -1, 0)), dict(sizes=(2, 3, 3)), dict(ys=(16, 16)), dict(ys=(32, 8)),
+           dict(xs=(-32, 16)), dict(B=1 << 30, T=1 << 30), dict(B=1 << 40), dict(w=1 << 62, h=1 << 62)]
+    for kw in bad:
+        assert grid(lib, f=f, **kw) == E.TOK_ERR_SHAPE, kw
+    assert grid(lib, f=f, dtype=2) == E.TOK_ERR_DTYPE
+    for kw in (dict(x=NULL), dict(y=NULL), dict(table=NULL)):
+        assert grid(lib, f=f, **kw) == E.TOK_ERR_NULL
+    assert grid(lib, f=f, x=F(0x1000001)) == E.TOK_ERR_ALIGN
+    assert grid(lib, f=f, y=F(0x2000002), dtype=0) == E.TOK_ERR_ALIGN
+    assert grid(lib, f=f, table=F(0x3000004)) == E.TOK_ERR_ALIGN
+    assert grid(lib, f=f, y=F(0x1000010)) == E.TOK_ERR_ALIAS               # shifted overlap
+    assert grid(lib, f=f, y=X, ys=(64, 16)) == E.TOK_ERR_ALIAS             # in place, other strides
+    assert grid(lib, f=f, y=F(0x3000000 - 64)) == E.TOK_ERR_ALIAS          # output over the table
+    for kw in (dict(B=0), dict(H=0), dict(T=0), dict(D=0, dims=(0, 0, 0))):
+        assert grid(lib, f=f, x=NULL, y=NULL, table=NULL, **kw) == E.TOK_OK
+
+
+def positions(lib, x=X, y=Y, pos=POS, table=TB, bad=BAD, dtype=1, N=5, H=2, D=16, xs=(32, 16), ys=(32, 16),
+              sizes=(2, 3, 4), dims=(4, 4, 8), f="tok_rope_positions"):
+    return getattr(lib, f)(x, y, pos, table, bad, dtype, N, H, D, *xs, *ys, *sizes, *dims, 0, NULL)
+
+
+@pytest.mark.parametrize("f", ["tok_rope_positions", "tok_rope_positions_adjoint"])
+def test_rope_positions_rules(lib, f):
+    assert positions(lib, f=f, N=-1) == hwp.TOK_ERR_SHAPE
+    assert positions(lib, f=f, N=1 << 31) == hwp.TOK_ERR_SHAPE
+    assert positions(lib, f=f, pos=NULL) == hwp.TOK_ERR_NULL
+    assert positions(lib, f=f, pos=F(0x4000002)) == hwp.TOK_ERR_ALIGN
+    assert positions(lib, f=f, bad=F(0x5000001)) == hwp.TOK_ERR_ALIGN
+    assert positions(lib, f=f, pos=Y) == hwp.TOK_ERR_ALIAS
+    assert positions(lib, f=f, bad=Y) == hwp.TOK_ERR_ALIAS
+    assert positions(lib, f=f, bad=POS) == hwp.TOK_ERR_ALIAS
+    assert positions(lib, f=f, N=0, x=NULL, y=NULL, pos=NULL, table=NULL, bad=NULL) == hwp.TOK_OK
+
+
+def test_rope_table_rules(lib):
+    def table(t=TB, n=(4, 5, 6), d=(4, 2, 2), base=(1e4,) * 3):
+        return lib.tok_rope_table(t, *n, *d, *base, 1.0, 1.0, 1.0, NULL)
+    for kw in (dict(n=(-1, 5, 6)), dict(d=(3, 2, 2)), dict(base=(1e4, 0.0, 1e4)), dict(base=(float("nan"), 1e4, 1e4)),
+               dict(n=(1 << 31, 1, 1)), dict(d=(1 << 17, 2, 2)), dict(n=((1 << 31) - 1, 1, 1), d=(65536, 0, 0))):
+        assert table(**kw) == hwp.TOK_ERR_SHAPE, kw
+    assert table(t=NULL) == hwp.TOK_ERR_NULL
+    assert table(t=F(0x3000004)) == hwp.TOK_ERR_ALIGN
+    assert table(t=NULL, n=(0, 0, 0)) == hwp.TOK_OK
+
+
+def test_rope_binding_refuses():
+    x = torch.zeros(1, 2, 3, 4, 2, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        hwp.rope_grid(x, torch.zeros(10), (2, 3, 4), (4, 2, 2))
+    with pytest.raises(ValueError, match="CUDA"):
+        hwp.rope_table((2, 3, 4), (4, 2, 2), device="cpu")
+    with pytest.raises(ValueError, match="negative"):
+        hwp.rope_table((2, -3, 4), (4, 2, 2))
