@@ -31,7 +31,7 @@ ABI_SYMBOLS = ("tok_abi_version", "tok_status_str", "tok_last_cuda_error", "tok_
                "tok_conv_factorized", "tok_patch_embed_pack_weights", "tok_patch_embed_spatial", "tok_fsq_encode", "tok_fsq_decode", "tok_fsq_backward_workspace_size",
                "tok_fsq_encode_backward", "tok_fsq_encode_backward_noalloc", "tok_fsq_decode_backward",
                "tok_rope_table", "tok_rope_grid", "tok_rope_grid_adjoint", "tok_rope_positions",
-               "tok_rope_positions_adjoint")
+               "tok_rope_positions_adjoint", "tok_sample_codes")
 
 _lib = None
 
@@ -107,6 +107,9 @@ def lib():
         for f in (L.tok_rope_positions, L.tok_rope_positions_adjoint):
             f.restype = i32
             f.argtypes = [vp] * 5 + [i32] + [i64] * 13 + [i32, vp]
+        f32 = ctypes.c_float
+        L.tok_sample_codes.restype = i32
+        L.tok_sample_codes.argtypes = [vp, i32, i64, i64, i64, vp, vp, f32, vp, i32, vp, f32, vp, f32, vp, vp, vp]
         L.tok_fsq_decode.restype = i32
         L.tok_fsq_decode.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp]
         _lib = L
@@ -669,6 +672,48 @@ def tok_rope_positions_adjoint(gy, gx, pos, table, sizes, dims, interleaved=Fals
 
 
 # ---------------------------------------------------------------------------
+# Drawing codes from logits.
+# ---------------------------------------------------------------------------
+def _setting(v, name, dtype, logits):
+    """A sampling setting: (device pointer or None, value for every row)."""
+    if not isinstance(v, torch.Tensor):
+        return None, v
+    if not v.is_cuda or v.device != logits.device or v.dtype != dtype or v.numel() != logits.numel() // logits.shape[-1] \
+            or not v.is_contiguous():
+        raise ValueError(f"{name} must be a number or a contiguous {dtype} CUDA tensor with one value per row")
+    return v.data_ptr(), 0
+
+
+def tok_sample_codes(logits, u, idx, logprob=None, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, stream=None):
+    """Draw one code per row: logits [..., V] (float32 or bfloat16), u [...] fp32 in [0, 1) -> idx [...] int32
+    (-1 for a row of -inf) and, if given, logprob [...] fp32 under the filtered distribution.  The settings
+    are numbers or tensors with one value per row (float32; top_k int32).  Filters: top_k largest, then the
+    top_p nucleus, then weight >= min_p of the largest; ties to the lower index; temperature 0 is greedy."""
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor (there is no CPU path)")
+    if logits.dim() < 1 or logits.shape[-1] < 1:
+        raise ValueError("logits must be [..., V] with V >= 1")
+    V = logits.shape[-1]
+    if V > 1 and logits.stride(-1) != 1:
+        raise ValueError("the last dimension of logits must be dense")
+    for t, name, dtype in ((u, "u", torch.float32), (idx, "idx", torch.int32), (logprob, "logprob", torch.float32)):
+        if t is not None and (not t.is_cuda or t.device != logits.device or t.dtype != dtype
+                              or t.shape != logits.shape[:-1] or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor with one value per row")
+    tp, ta = _setting(temperature, "temperature", torch.float32, logits)
+    kp, ka = _setting(top_k, "top_k", torch.int32, logits)
+    pp, pa = _setting(top_p, "top_p", torch.float32, logits)
+    mp, ma = _setting(min_p, "min_p", torch.float32, logits)
+    stride = _token_stride(logits.unsqueeze(-2), "logits")
+    with torch.cuda.device(logits.device):
+        _check(lib().tok_sample_codes(logits.data_ptr(), _dtype_code(logits), u.numel(), V, stride, u.data_ptr(), tp,
+                                      ta, kp, max(-1, min(ka, 2 ** 31 - 1)), pp, pa, mp, ma, idx.data_ptr(),
+                                      None if logprob is None else logprob.data_ptr(), _stream(logits, stream)),
+               "tok_sample_codes")
+    return idx, logprob
+
+
+# ---------------------------------------------------------------------------
 # Allocating wrappers.
 # ---------------------------------------------------------------------------
 def haar_fwd(x: torch.Tensor, stream=None) -> torch.Tensor:
@@ -787,3 +832,11 @@ def rope_positions(x, pos, table, sizes, dims, interleaved=False, bad_count=None
 def rope_positions_adjoint(gy, pos, table, sizes, dims, interleaved=False, bad_count=None,
                            stream=None) -> torch.Tensor:
     return tok_rope_positions_adjoint(gy, _dense(gy, stream), pos, table, sizes, dims, interleaved, bad_count, stream)
+
+
+def sample_codes(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, with_logprob=False, stream=None):
+    """idx, or (idx, logprob): see tok_sample_codes.  idx feeds fsq_decode where V is the FSQ codebook."""
+    idx = _new(logits.shape[:-1], torch.int32, logits.device, stream)
+    logprob = _new(logits.shape[:-1], torch.float32, logits.device, stream) if with_logprob else None
+    tok_sample_codes(logits, u, idx, logprob, temperature, top_k, top_p, min_p, stream)
+    return (idx, logprob) if with_logprob else idx

@@ -512,6 +512,33 @@ TOK_API tok_status tok_rope_positions_adjoint(const void *gy, void *gx, const in
                                               int64_t gx_head, int64_t nt, int64_t nh, int64_t nw, int64_t dt,
                                               int64_t dh, int64_t dw, int interleaved, cudaStream_t stream);
 
+/*
+ * tok_sample_codes -- draw one code per row of logits.
+ *   logits   : [R, V] of `dtype`, rows `row_stride` elements apart (input); NaN counts as -inf
+ *   u        : [R] fp32 in [0, 1), one given random number per row (input)
+ *   temperature, top_k, top_p, min_p : [R] settings of each row, or NULL: the value
+ *              `..._all` for every row
+ *   idx      : [R] int32 (output); -1 for a row whose logits are all -inf
+ *   logprob  : [R] fp32, ln of the drawn code's probability under the filtered
+ *              distribution, or NULL (output); -inf beside idx -1
+ * Token i has the weight exp((x_i - max x) / temperature).  Kept are, in turn: the
+ * top_k largest (top_k <= 0: all); of those, by falling weight, each before which
+ * less than top_p of their weight lies (top_p >= 1: all; the largest always); of
+ * those, the ones with a weight of at least min_p (min_p <= 0: all; above 1 counts
+ * as 1).  Equal logits rank by index, the lower one first.  Drawn is the first kept
+ * token, in index order, at which the running sum of weights exceeds u times their
+ * total.  temperature <= 0: the largest token (the first of equals).  u is clamped
+ * to [0, 1]; from 1 on, the last token with a weight.  Weights are taken in 64 bits
+ * and summed as integers of 2^-44, so results do not depend on the device or order.
+ * Shape rule: 0 <= R <= 2^27, 1 <= V <= 2^18, row_stride >= 0.  The indices are
+ * tok_fsq_decode's input where V = TOK_FSQ_CODEBOOK (which marks -1 as bad).
+ */
+TOK_API tok_status tok_sample_codes(const void *logits, tok_dtype dtype, int64_t R, int64_t V, int64_t row_stride,
+                                    const float *u, const float *temperature, float temperature_all,
+                                    const int32_t *top_k, int32_t top_k_all, const float *top_p, float top_p_all,
+                                    const float *min_p, float min_p_all, int32_t *idx, float *logprob,
+                                    cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

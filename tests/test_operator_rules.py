@@ -85,3 +85,28 @@ def test_rope_binding_refuses():
         hwp.rope_table((2, 3, 4), (4, 2, 2), device="cpu")
     with pytest.raises(ValueError, match="negative"):
         hwp.rope_table((2, -3, 4), (4, 2, 2))
+
+
+def sample(lib, x=X, dtype=1, R=4, V=100, stride=100, u=Y, t=NULL, k=NULL, p=NULL, m=NULL, idx=TB, lp=POS):
+    return lib.tok_sample_codes(x, dtype, R, V, stride, u, t, 1.0, k, 0, p, 1.0, m, 0.0, idx, lp, NULL)
+
+
+def test_sample_rules(lib):
+    for kw in (dict(R=-1), dict(V=0), dict(V=(1 << 18) + 1), dict(R=(1 << 27) + 1), dict(stride=-1),
+               dict(stride=1 << 61)):
+        assert sample(lib, **kw) == hwp.TOK_ERR_SHAPE, kw
+    assert sample(lib, dtype=2) == hwp.TOK_ERR_DTYPE
+    for kw in (dict(x=NULL), dict(u=NULL), dict(idx=NULL)):
+        assert sample(lib, **kw) == hwp.TOK_ERR_NULL
+    for kw in (dict(x=F(0x1000001)), dict(u=F(0x2000002)), dict(t=F(0x5000001)), dict(k=F(0x5000002)),
+               dict(p=F(0x5000003)), dict(m=F(0x5000001)), dict(idx=F(0x3000002)), dict(lp=F(0x4000002))):
+        assert sample(lib, **kw) == hwp.TOK_ERR_ALIGN
+    for kw in (dict(idx=F(0x1000000 + 796)), dict(lp=X), dict(idx=Y), dict(lp=TB), dict(t=TB), dict(k=POS), dict(p=TB),
+               dict(m=F(0x3000000 + 12))):
+        assert sample(lib, **kw) == hwp.TOK_ERR_ALIAS, kw
+    assert sample(lib, R=0, x=NULL, u=NULL, idx=NULL, lp=NULL) == hwp.TOK_OK
+
+
+def test_sample_binding_refuses():
+    with pytest.raises(ValueError, match="CUDA"):
+        hwp.sample_codes(torch.zeros(2, 5), torch.zeros(2))
