@@ -31,9 +31,16 @@ ABI_SYMBOLS = ("tok_abi_version", "tok_status_str", "tok_last_cuda_error", "tok_
                "tok_conv_factorized", "tok_patch_embed_pack_weights", "tok_patch_embed_spatial", "tok_fsq_encode", "tok_fsq_decode", "tok_fsq_backward_workspace_size",
                "tok_fsq_encode_backward", "tok_fsq_encode_backward_noalloc", "tok_fsq_decode_backward",
                "tok_rope_table", "tok_rope_grid", "tok_rope_grid_adjoint", "tok_rope_positions",
-               "tok_rope_positions_adjoint", "tok_sample_codes")
+               "tok_rope_positions_adjoint", "tok_sample_codes", "tok_cross_attention_workspace_size",
+               "tok_cross_attention", "tok_cross_attention_backward_workspace_size", "tok_cross_attention_backward")
 
 _lib = None
+
+
+class _Heads(ctypes.Structure):
+    """tok_heads: a [B, N, H, D] tensor with dense channels."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch", ctypes.c_int64), ("token", ctypes.c_int64),
+                ("head", ctypes.c_int64)]
 
 
 class TokError(RuntimeError):
@@ -108,6 +115,14 @@ def lib():
             f.restype = i32
             f.argtypes = [vp] * 5 + [i32] + [i64] * 13 + [i32, vp]
         f32 = ctypes.c_float
+        for f in (L.tok_cross_attention_workspace_size, L.tok_cross_attention_backward_workspace_size):
+            f.restype = i64
+            f.argtypes = [i64] * 6
+        hp = ctypes.POINTER(_Heads)
+        L.tok_cross_attention.restype = i32
+        L.tok_cross_attention.argtypes = [hp] * 4 + [vp, vp] + [i64] * 6 + [f32, vp, i64, vp]
+        L.tok_cross_attention_backward.restype = i32
+        L.tok_cross_attention_backward.argtypes = [hp] * 4 + [vp, hp, vp] + [hp] * 3 + [i64] * 6 + [f32, vp, i64, vp]
         L.tok_sample_codes.restype = i32
         L.tok_sample_codes.argtypes = [vp, i32, i64, i64, i64, vp, vp, f32, vp, i32, vp, f32, vp, f32, vp, vp, vp]
         L.tok_fsq_decode.restype = i32
@@ -714,6 +729,102 @@ def tok_sample_codes(logits, u, idx, logprob=None, temperature=1.0, top_k=0, top
 
 
 # ---------------------------------------------------------------------------
+# Cross attention.
+# ---------------------------------------------------------------------------
+def _heads(t: torch.Tensor) -> _Heads:
+    s = t.stride()
+    return _Heads(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _attn_dims(q, k, v, k_lens, others):
+    """(B, Nq, Nk, Hq, Hkv, D) of checked tensors; others: (tensor, name, like q or like k)."""
+    dev = q.device
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, Nq, Hq, D], k and v [B, Nk, Hkv, D]")
+    B, Nq, Hq, D = q.shape
+    Nk, Hkv = k.shape[1], k.shape[2]
+    sq, sk = q.shape, torch.Size((B, Nk, Hkv, D))
+    for t, name, like_q in ((q, "q", True), (k, "k", False), (v, "v", False), *others):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+        if t.dtype != torch.bfloat16 or t.device != dev:
+            raise ValueError(f"{name} must be bfloat16, on the device of q")
+        if t.shape != (sq if like_q else sk):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(sq if like_q else sk)}")
+        if t.stride(3) != 1:
+            raise ValueError(f"the channels of {name} must be dense")
+    if k_lens is not None and (not k_lens.is_cuda or k_lens.device != dev or k_lens.dtype != torch.int32
+                               or k_lens.shape != (B,) or not k_lens.is_contiguous()):
+        raise ValueError("k_lens must be a contiguous int32 CUDA tensor [B]")
+    return B, Nq, Nk, Hq, Hkv, D
+
+
+def _stats(t, name, dims, device):
+    B, Nq, _, Hq, _, _ = dims
+    if t is not None and (not t.is_cuda or t.device != device or t.dtype != torch.float32
+                          or t.shape != (B, Hq, Nq) or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous float32 CUDA tensor [B, Hq, Nq]")
+
+
+def _attn_workspace(f, dims, workspace, device, stream):
+    need = f(*dims)
+    if need < 0:
+        raise ValueError(f"no cross attention for (B, Nq, Nk, Hq, Hkv, D) = {dims}: D a multiple of 8, at most 128; "
+                         "Hq a multiple of Hkv")
+    if workspace is None:
+        return _new(need, torch.uint8, device, stream) if need else None
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the device of q")
+    return workspace
+
+
+def _bytes(t):
+    return (None, 0) if t is None else (t.data_ptr(), t.numel() * t.element_size())
+
+
+def cross_attention_workspace_size(B, Nq, Nk, Hq, Hkv, D) -> int:
+    return int(lib().tok_cross_attention_workspace_size(B, Nq, Nk, Hq, Hkv, D))
+
+
+def cross_attention_backward_workspace_size(B, Nq, Nk, Hq, Hkv, D) -> int:
+    return int(lib().tok_cross_attention_backward_workspace_size(B, Nq, Nk, Hq, Hkv, D))
+
+
+def tok_cross_attention(q, k, v, o, lse=None, k_lens=None, scale=None, workspace=None, stream=None):
+    """o = softmax(scale q k^T) v over the first k_lens[b] keys: q, o [B,Nq,Hq,D], k, v [B,Nk,Hkv,D] bf16 (dense
+    channels, other strides free), lse [B,Hq,Nq] fp32 or None, k_lens [B] int32 or None; scale: 1/sqrt(D) by
+    default; workspace: cross_attention_workspace_size bytes, allocated if None."""
+    dims = _attn_dims(q, k, v, k_lens, ((o, "o", True),))
+    _stats(lse, "lse", dims, q.device)
+    L = lib()
+    ws = _attn_workspace(L.tok_cross_attention_workspace_size, dims, workspace, q.device, stream)
+    with torch.cuda.device(q.device):
+        _check(L.tok_cross_attention(_heads(q), _heads(k), _heads(v), _heads(o),
+                                     None if lse is None else lse.data_ptr(),
+                                     None if k_lens is None else k_lens.data_ptr(), *dims,
+                                     dims[5] ** -0.5 if scale is None else scale, *_bytes(ws), _stream(q, stream)),
+               "tok_cross_attention")
+    return o
+
+
+def tok_cross_attention_backward(q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v, k_lens=None, scale=None,
+                                 workspace=None, stream=None):
+    """Gradients of tok_cross_attention into grad_q, grad_k, grad_v, from its inputs, o and lse."""
+    dims = _attn_dims(q, k, v, k_lens, ((o, "o", True), (grad_o, "grad_o", True), (grad_q, "grad_q", True),
+                                        (grad_k, "grad_k", False), (grad_v, "grad_v", False)))
+    _stats(lse, "lse", dims, q.device)
+    L = lib()
+    ws = _attn_workspace(L.tok_cross_attention_backward_workspace_size, dims, workspace, q.device, stream)
+    with torch.cuda.device(q.device):
+        _check(L.tok_cross_attention_backward(_heads(q), _heads(k), _heads(v), _heads(o), lse.data_ptr(),
+                                              _heads(grad_o), None if k_lens is None else k_lens.data_ptr(),
+                                              _heads(grad_q), _heads(grad_k), _heads(grad_v), *dims,
+                                              dims[5] ** -0.5 if scale is None else scale, *_bytes(ws),
+                                              _stream(q, stream)), "tok_cross_attention_backward")
+    return grad_q, grad_k, grad_v
+
+
+# ---------------------------------------------------------------------------
 # Allocating wrappers.
 # ---------------------------------------------------------------------------
 def haar_fwd(x: torch.Tensor, stream=None) -> torch.Tensor:
@@ -840,3 +951,17 @@ def sample_codes(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, with
     logprob = _new(logits.shape[:-1], torch.float32, logits.device, stream) if with_logprob else None
     tok_sample_codes(logits, u, idx, logprob, temperature, top_k, top_p, min_p, stream)
     return (idx, logprob) if with_logprob else idx
+
+
+def cross_attention(q, k, v, k_lens=None, scale=None, with_lse=False, stream=None):
+    """o, or (o, lse): see tok_cross_attention."""
+    o = _dense(q, stream)
+    lse = _new((q.shape[0], q.shape[2], q.shape[1]), torch.float32, q.device, stream) if with_lse else None
+    tok_cross_attention(q, k, v, o, lse, k_lens, scale, None, stream)
+    return (o, lse) if with_lse else o
+
+
+def cross_attention_backward(q, k, v, o, lse, grad_o, k_lens=None, scale=None, stream=None):
+    """(grad_q, grad_k, grad_v): see tok_cross_attention_backward."""
+    return tok_cross_attention_backward(q, k, v, o, lse, grad_o, _dense(q, stream), _dense(k, stream),
+                                        _dense(v, stream), k_lens, scale, None, stream)

@@ -1,0 +1,119 @@
+// What the cross-attention kernels share: the call's tensors, and warp-level matrix
+// products on fragments that are loaded straight from global memory.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "tok_common.cuh"
+#include "tok_internal.h"
+
+namespace tok {
+
+// One [B, N, H, D] tensor: strides in elements, channels dense.
+struct HeadsView {
+    __nv_bfloat16 *p;
+    int64_t b, n, h;
+    __device__ __forceinline__ __nv_bfloat16 *row(int64_t ib, int64_t in, int64_t ih) const
+    {
+        return p + ib * b + in * n + ih * h;
+    }
+};
+
+struct AttnArgs {
+    HeadsView q, k, v, o, go, dq, dk, dv;
+    const float *lse_in; // backward
+    float *lse;          // [B, Hq, Nq] or null
+    float *delta;        // [B, Hq, Nq]: rowsum(go * o)
+    float *part;         // split partials
+    const int32_t *lens; // [B] or null
+    int B, Nq, Nk, Hq, Hkv, G, D;
+    int splits;
+    float scale, scale2; // scale2 = scale * log2(e)
+};
+
+__device__ __forceinline__ int key_count(const AttnArgs &a, int b)
+{
+    return a.lens ? min(max(a.lens[b], 0), a.Nk) : a.Nk;
+}
+
+// 2^x, 2 ulp; 0 for -inf.
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// D += A B on one 16 x 8 x 16 tile.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 load16(const __nv_bfloat16 *p, bool ok)
+{
+    return ok ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
+}
+
+// Fragments for products over channels (both operands [row][channel]).  The order of a
+// contraction is free, so lane c = lane % 4 takes the 16 bytes of channels 32 i + 8 c ..
+// + 7 of row lane / 4: its first half is its part of MMA step 2i, the second of 2i + 1.
+// chan<NC>: NC = ceil(D / 32) chunks; rows and channels outside are zero.
+template <int NC>
+__device__ __forceinline__ void load_chan(uint4 (&f)[NC], const __nv_bfloat16 *row, bool ok, int c8, int D)
+{
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+        f[i] = load16(row + 32 * i + c8, ok && 32 * i + c8 < D);
+}
+
+// One 16 x 8 tile: rows of lo / hi (lane / 4 and + 8) against the 8 rows of b.
+template <int NC>
+__device__ __forceinline__ void mma_chan(float (&d)[4], const uint4 (&lo)[NC], const uint4 (&hi)[NC],
+                                         const uint4 (&b)[NC])
+{
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        mma16816(d, lo[i].x, hi[i].x, lo[i].y, hi[i].y, b[i].x, b[i].y);
+        mma16816(d, lo[i].z, hi[i].z, lo[i].w, hi[i].w, b[i].z, b[i].w);
+    }
+}
+
+// Fragments for products over 16 rows (the B operand is [row][channel], the result's
+// columns are channels).  Lane (g = lane / 4, c = lane % 4) takes the 16 bytes of
+// channels 64 p + 8 g .. + 7 of rows 2c, 2c + 1, 2c + 8, 2c + 9; column n of tile j is
+// channel 64 p + 8 n + j, so a lane's results are the channels 64 p + 16 c + j (and + 8).
+struct RowFrag {
+    uint4 r[4];
+};
+
+__device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+__device__ __forceinline__ void mma_rows(float (&acc)[8][4], const uint32_t (&a)[4], const RowFrag &f)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+        const uint32_t b0 = __byte_perm(word(f.r[0], j / 2), word(f.r[1], j / 2), sel);
+        const uint32_t b1 = __byte_perm(word(f.r[2], j / 2), word(f.r[3], j / 2), sel);
+        mma16816(acc[j], a[0], a[1], a[2], a[3], b0, b1);
+    }
+}
+
+__device__ __forceinline__ float quad_max(float v)
+{
+    v = fmaxf(v, __shfl_xor_sync(~0u, v, 1));
+    return fmaxf(v, __shfl_xor_sync(~0u, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v)
+{
+    v += __shfl_xor_sync(~0u, v, 1);
+    return v + __shfl_xor_sync(~0u, v, 2);
+}
+
+} // namespace tok

@@ -539,6 +539,55 @@ TOK_API tok_status tok_sample_codes(const void *logits, tok_dtype dtype, int64_t
                                     const float *min_p, float min_p_all, int32_t *idx, float *logprob,
                                     cudaStream_t stream);
 
+/*
+ * Cross attention of queries [B, Nq, Hq, D] to an encoder's keys and values
+ * [B, Nk, Hkv, D], all bf16: o = softmax(scale * q k^T) v per head, query head h
+ * reading key head h / (Hq / Hkv).  Batch entry b has the keys [0, k_lens[b])
+ * (clamped to [0, Nk]; NULL: all Nk); what lies behind them is not read into any
+ * result, NaN included.  A query without a key has o = 0 and lse = -inf, and gives
+ * no gradient.  Products accumulate in fp32, the softmax is fp32; its weights (and
+ * in the backward the score gradients) are rounded to bf16 once, as operands of the
+ * second product, and outputs once.  Results do not depend on the device's timing
+ * (every sum has a fixed order).
+ *
+ * A tensor is a tok_heads: pointer and strides in elements of batch, token and head,
+ * the D channels dense -- slices of a fused projection are read and written in place,
+ * and an input's stride may be 0 (one encoder state for the whole batch; its gradient
+ * is per batch entry).  Shape rule: D a multiple of 8, 8 <= D <= 128; Hq a multiple
+ * of Hkv; B, Hq <= 65535; B * Hq * Nq, B * Hkv * Nk < 2^30.  Pointers and strides are
+ * multiples of 16 bytes (TOK_ERR_ALIGN).  Outputs may interleave with inputs and each
+ * other (slices of one buffer) but share no element (TOK_ERR_ALIAS).
+ *
+ * tok_cross_attention -- o and, if not NULL, lse [B, Hq, Nq] fp32: ln of the sum of
+ *   exponentials, which the backward takes.  workspace: 16-byte-aligned device memory
+ *   of tok_cross_attention_workspace_size() bytes (may be 0), overwritten; calls that
+ *   may overlap need one each.
+ * tok_cross_attention_backward -- grad_q, grad_k, grad_v (overwritten; rows of
+ *   grad_k, grad_v behind k_lens are zero) from the forward's inputs, o, lse and the
+ *   gradient of o.  workspace: ..._backward_workspace_size() bytes.
+ * The sizes are -1 for an invalid shape.
+ */
+typedef struct {
+    void *ptr;
+    int64_t batch, token, head; /* strides in elements */
+} tok_heads;
+
+TOK_API int64_t tok_cross_attention_workspace_size(int64_t B, int64_t Nq, int64_t Nk, int64_t Hq, int64_t Hkv,
+                                                   int64_t D);
+TOK_API tok_status tok_cross_attention(const tok_heads *q, const tok_heads *k, const tok_heads *v,
+                                       const tok_heads *o, float *lse, const int32_t *k_lens, int64_t B, int64_t Nq,
+                                       int64_t Nk, int64_t Hq, int64_t Hkv, int64_t D, float scale, void *workspace,
+                                       int64_t workspace_bytes, cudaStream_t stream);
+TOK_API int64_t tok_cross_attention_backward_workspace_size(int64_t B, int64_t Nq, int64_t Nk, int64_t Hq,
+                                                            int64_t Hkv, int64_t D);
+TOK_API tok_status tok_cross_attention_backward(const tok_heads *q, const tok_heads *k, const tok_heads *v,
+                                                const tok_heads *o, const float *lse, const tok_heads *grad_o,
+                                                const int32_t *k_lens, const tok_heads *grad_q,
+                                                const tok_heads *grad_k, const tok_heads *grad_v, int64_t B,
+                                                int64_t Nq, int64_t Nk, int64_t Hq, int64_t Hkv, int64_t D,
+                                                float scale, void *workspace, int64_t workspace_bytes,
+                                                cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

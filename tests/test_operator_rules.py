@@ -110,3 +110,66 @@ def test_sample_rules(lib):
 def test_sample_binding_refuses():
     with pytest.raises(ValueError, match="CUDA"):
         hwp.sample_codes(torch.zeros(2, 5), torch.zeros(2))
+
+
+HP = ctypes.POINTER(hwp._Heads)
+
+
+def heads(addr, strides):
+    return ctypes.byref(hwp._Heads(addr, *strides))
+
+
+Q, K, V, O, LSE, WS = 0x10000000, 0x20000000, 0x30000000, 0x40000000, 0x50000000, 0x60000000
+SQ, SK = (4 * 64 * 10, 4 * 64, 64), (2 * 64 * 20, 2 * 64, 64)   # B = 3, Nq = 10, Nk = 20, Hq = 4, Hkv = 2, D = 64
+
+
+def attend(lib, q=Q, k=K, v=V, o=O, lse=LSE, lens=0, B=3, Nq=10, Nk=20, Hq=4, Hkv=2, D=64, sq=SQ, sk=SK, sv=SK, so=SQ,
+           ws=WS, wb=1 << 26):
+    return lib.tok_cross_attention(heads(q, sq), heads(k, sk), heads(v, sv), heads(o, so), F(lse), F(lens), B, Nq, Nk, Hq,
+                                   Hkv, D, 0.125, F(ws), wb, NULL)
+
+
+def test_cross_attention_rules(lib):
+    for kw in (dict(D=4), dict(D=12), dict(D=136), dict(D=0), dict(Hq=3), dict(Hkv=0), dict(B=-1), dict(Nq=-1), dict(Nk=-1),
+               dict(Nq=1 << 30), dict(B=65536), dict(Hq=1 << 17), dict(so=(0, 256, 64)), dict(so=(2560, 256, 32)),
+               dict(sk=(2560, -128, 64)), dict(sq=(1 << 40, 256, 64)), dict(B=1, Nq=1, Nk=100000, wb=16)):
+        assert attend(lib, **kw) == hwp.TOK_ERR_SHAPE, kw
+    for kw in (dict(q=0), dict(k=0), dict(v=0), dict(o=0), dict(B=1, Nq=1, Nk=100000, ws=0)):
+        assert attend(lib, **kw) == hwp.TOK_ERR_NULL, kw
+    for kw in (dict(q=Q + 8), dict(k=K + 2), dict(o=O + 8), dict(sk=(2560, 132, 64)), dict(lse=LSE + 2), dict(lens=LSE + 1),
+               dict(B=1, Nq=1, Nk=100000, ws=WS + 8)):
+        assert attend(lib, **kw) == hwp.TOK_ERR_ALIGN, kw
+    for kw in (dict(o=Q), dict(o=K), dict(o=Q + 128), dict(o=V - 64), dict(lse=O), dict(lse=Q), dict(lens=LSE),
+               dict(B=1, Nq=1, Nk=100000, ws=O), dict(B=1, Nq=1, Nk=100000, ws=K), dict(B=1, Nq=1, Nk=100000, ws=LSE)):
+        assert attend(lib, **kw) == hwp.TOK_ERR_ALIAS, kw
+    assert attend(lib, B=0, q=0, k=0, v=0, o=0, lse=0) == hwp.TOK_OK
+    assert attend(lib, Nq=0, q=0, k=0, v=0, o=0, lse=0) == hwp.TOK_OK
+    size = lib.tok_cross_attention_workspace_size
+    assert size(1, 1, 8, 3, 2, 64) == -1 and size(1, 1, 8, 2, 2, 65) == -1 and size(0, 1, 8, 2, 2, 64) == 0
+
+
+def backward(lib, q=Q, k=K, v=V, o=O, lse=LSE, go=0x48000000, lens=0, gq=0x70000000, gk=0x80000000, gv=0x90000000, B=3,
+             Nq=10, Nk=20, Hq=4, Hkv=2, D=64, sq=SQ, sgk=SK, sgv=SK, ws=WS, wb=1 << 26):
+    return lib.tok_cross_attention_backward(
+        heads(q, SQ), heads(k, SK), heads(v, SK), heads(o, SQ), F(lse), heads(go, SQ), F(lens), heads(gq, sq),
+        heads(gk, sgk), heads(gv, sgv), B, Nq, Nk, Hq, Hkv, D, 0.125, F(ws), wb, NULL)
+
+
+def test_cross_attention_backward_rules(lib):
+    for kw in (dict(D=20), dict(Hq=5), dict(sgk=(0, 128, 64)), dict(sq=(2560, 200, 64)), dict(wb=64)):
+        assert backward(lib, **kw) == hwp.TOK_ERR_SHAPE, kw
+    for kw in (dict(q=0), dict(lse=0), dict(go=0), dict(gq=0), dict(gk=0), dict(gv=0), dict(ws=0)):
+        assert backward(lib, **kw) == hwp.TOK_ERR_NULL, kw
+    for kw in (dict(gq=0x70000004), dict(ws=WS + 8), dict(lse=LSE + 2)):
+        assert backward(lib, **kw) == hwp.TOK_ERR_ALIGN, kw
+    fused = (2 * 2560, 256, 64)  # keys' and values' gradients of one [B, Nk, 2, H, D] buffer, overlapping by a head
+    for kw in (dict(gq=Q), dict(gk=0x90000000), dict(gv=V), dict(gk=0x70000000), dict(ws=LSE), dict(ws=0x80000000),
+               dict(gq=LSE), dict(lens=0x90000000), dict(gk=0x80000000, gv=0x80000000 + 128, sgk=fused, sgv=fused)):
+        assert backward(lib, **kw) == hwp.TOK_ERR_ALIAS, kw
+    assert backward(lib, B=0, q=0, k=0, v=0, o=0, lse=0, go=0, gq=0, gk=0, gv=0, ws=0) == hwp.TOK_OK
+
+
+def test_cross_attention_binding_refuses():
+    x = torch.zeros(1, 2, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        hwp.cross_attention(x, x, x)
