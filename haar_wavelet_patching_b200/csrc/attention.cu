@@ -479,11 +479,23 @@ HeadsView view(const tok_heads *t)
     return HeadsView{static_cast<__nv_bfloat16 *>(t->ptr), t->batch, t->token, t->head};
 }
 
-// CTAs that the keys of one row tile are split over: enough for four CTAs per SM, each
-// with at least four rounds of its warps.
+// Query rows per key head from which the tensor-core kernel takes a call.
+constexpr int64_t kTcRows = 64;
+
+bool wants_tc(const Dims &d) { return d.Nq * (d.Hq / d.Hkv) > kTcRows && d.Nk > 0; }
+
+// CTAs that the keys of one row tile are split over.
 int64_t fwd_splits(const Dims &d)
 {
-    const int64_t G = d.Hq / d.Hkv, tiles = (d.Nq * G + kRows - 1) / kRows, units = d.B * d.Hkv * tiles;
+    const int64_t G = d.Hq / d.Hkv;
+    if (wants_tc(d)) { // one CTA per SM, each with at least four key tiles
+        const int64_t gp = attn_tc_group((int)G), items = d.B * (d.Hq / gp) * ((d.Nq * gp + 255) / 256);
+        if (items == 0)
+            return 1;
+        return std::max<int64_t>(1, std::min(148 / items, d.Nk / 512));
+    }
+    // Four CTAs per SM, each with at least four rounds of its warps.
+    const int64_t tiles = (d.Nq * G + kRows - 1) / kRows, units = d.B * d.Hkv * tiles;
     if (units == 0)
         return 1;
     const int64_t want = (148 * 4 + units - 1) / units, most = d.Nk / (4 * kFwdWarps * kKeyStep);
@@ -565,11 +577,16 @@ extern "C" tok_status tok_cross_attention(const tok_heads *q, const tok_heads *k
     a.scale = scale;
     a.scale2 = (float)((double)scale * 1.4426950408889634);
     const int64_t blocks = B * Hkv * ((Nq * a.G + kRows - 1) / kRows) * splits;
-    if (D <= 64)
+    tok_status st;
+    if (wants_tc(dim) && !attn_tc_broadcast_tokens(a)) {
+        st = attn_tc_forward(a, stream);
+    } else if (D <= 64) {
         attn_rows_kernel<1><<<(unsigned)blocks, kFwdWarps * 32, 0, stream>>>(a);
-    else
+        st = launch_status();
+    } else {
         attn_rows_kernel<2><<<(unsigned)blocks, kFwdWarps * 32, 0, stream>>>(a);
-    tok_status st = launch_status();
+        st = launch_status();
+    }
     if (st == TOK_OK && splits > 1) {
         attn_join_kernel<<<(unsigned)((B * Hq * Nq + 3) / 4), 128, 0, stream>>>(a);
         st = launch_status();

@@ -32,6 +32,13 @@ struct AttnArgs {
     float scale, scale2; // scale2 = scale * log2(e)
 };
 
+// The forward on the 5th-generation tensor cores (attention_tc.cu): query heads per row tile
+// for groups of G, and the call.  Takes everything but tensors broadcast over tokens or
+// query heads.
+int attn_tc_group(int G);
+bool attn_tc_broadcast_tokens(const AttnArgs &a);
+tok_status attn_tc_forward(const AttnArgs &a, cudaStream_t stream);
+
 __device__ __forceinline__ int key_count(const AttnArgs &a, int b)
 {
     return a.lens ? min(max(a.lens[b], 0), a.Nk) : a.Nk;
