@@ -1,11 +1,11 @@
 // Cross attention to an encoder's states of another length: o = softmax(scale q k^T) v
 // over the first len[b] keys of each batch entry, query heads in groups that share a key
-// head; its gradients; and the split form for few queries.
+// head.  Argument rules, the choice of kernel, and the kernel for few query rows (calls
+// with more run on the 5th-generation tensor cores, attention_tc.cu and attention_bwd_tc.cu).
 //
-// Warp-level kernels: every product runs on m16n8k16 tiles whose fragments come straight
-// from global memory as 16-byte loads (see attention.cuh), so there is no staging.
-//
-// attn_rows_kernel (forward): 16 query rows of one key head (queries x the heads of its
+// attn_rows_kernel: with few query rows the call is bound by reading the keys and values, so
+// it runs on warp-level m16n8k16 tiles whose fragments come straight from global memory as
+// 16-byte loads (attention.cuh), without staging.  16 query rows of one key head (queries x the heads of its
 // group) per CTA; its 4 warps take 16 keys each in turn with a running maximum and sum of
 // their own, joined through shared memory.  The keys are split over `splits` CTAs; with
 // more than one, attn_join_kernel adds up their partial results in split order.
@@ -219,180 +219,6 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a)
         a.lse[stat] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
-// delta = rowsum(go * o) of every query row: 8 lanes per row.
-__global__ void __launch_bounds__(256) attn_delta_kernel(const AttnArgs a)
-{
-    const int64_t stat = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
-    const int c = threadIdx.x & 7;
-    const bool live = stat < (int64_t)a.B * a.Hq * a.Nq;
-    float s = 0.0f;
-    if (live) { // heads of a token lie next to each other
-        const int h = (int)(stat % a.Hq), iq = (int)(stat / a.Hq % a.Nq), b = (int)(stat / a.Hq / a.Nq);
-        for (int d = 8 * c; d < a.D; d += 64) {
-            float x[8], y[8];
-            Row<__nv_bfloat16, 8, true>::load(a.go.row(b, iq, h) + d, x);
-            Row<__nv_bfloat16, 8, true>::load(a.o.row(b, iq, h) + d, y);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                s = fmaf(x[j], y[j], s);
-        }
-        s += __shfl_xor_sync(__activemask(), s, 1);
-        s += __shfl_xor_sync(__activemask(), s, 2);
-        s += __shfl_xor_sync(__activemask(), s, 4);
-        if (c == 0)
-            a.delta[((int64_t)b * a.Hq + h) * a.Nq + iq] = s;
-    }
-}
-
-// dq = scale * ds k with ds = p (go v^T - delta): one warp per 16 query rows, over all keys.
-template <int NP> __global__ void __launch_bounds__(128) attn_dq_kernel(const AttnArgs a)
-{
-    constexpr int NC = 2 * NP;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    const int rows = a.Nq * a.G, tiles = (rows + 4 * kRows - 1) / (4 * kRows);
-    const int tile = (int)blockIdx.x % tiles, bh = (int)blockIdx.x / tiles, b = bh / a.Hkv, hk = bh - b * a.Hkv;
-    const int lo = (tile * 4 + warp) * kRows + g, hi = lo + 8, len = key_count(a, b);
-    const int iqlo = lo / a.G, hlo = hk * a.G + lo % a.G, iqhi = hi / a.G, hhi = hk * a.G + hi % a.G;
-    uint4 qlo[NC], qhi[NC], glo[NC], ghi[NC];
-    load_chan<NC>(qlo, a.q.row(b, iqlo, hlo), lo < rows, 8 * c, a.D);
-    load_chan<NC>(qhi, a.q.row(b, iqhi, hhi), hi < rows, 8 * c, a.D);
-    load_chan<NC>(glo, a.go.row(b, iqlo, hlo), lo < rows, 8 * c, a.D);
-    load_chan<NC>(ghi, a.go.row(b, iqhi, hhi), hi < rows, 8 * c, a.D);
-    const int64_t slo = ((int64_t)b * a.Hq + hlo) * a.Nq + iqlo, shi = ((int64_t)b * a.Hq + hhi) * a.Nq + iqhi;
-    const float l2lo = lo < rows ? a.lse_in[slo] * 1.4426950408889634f : 0.0f;
-    const float l2hi = hi < rows ? a.lse_in[shi] * 1.4426950408889634f : 0.0f;
-    const float dlo = lo < rows ? a.delta[slo] : 0.0f, dhi = hi < rows ? a.delta[shi] : 0.0f;
-    float acc[NP][8][4] = {};
-    for (int kk = 0; kk < len; kk += kKeyStep) {
-        uint4 kf[2][NC], vf[2][NC];
-        RowFrag kr[NP];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int key = kk + 8 * t + g;
-            load_chan<NC>(kf[t], a.k.row(b, key, hk), key < len, 8 * c, a.D);
-            load_chan<NC>(vf[t], a.v.row(b, key, hk), key < len, 8 * c, a.D);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int key = kk + 2 * c + (i & 1) + 8 * (i >> 1);
-#pragma unroll
-            for (int p = 0; p < NP; ++p)
-                kr[p].r[i] = load16(a.k.row(b, key, hk) + 64 * p + 8 * g, key < len && 64 * p + 8 * g < a.D);
-        }
-        float s[2][4] = {}, dp[2][4] = {};
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            mma_chan<NC>(s[t], qlo, qhi, kf[t]);
-            mma_chan<NC>(dp[t], glo, ghi, vf[t]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool in = kk + 8 * t + 2 * c + (e & 1) < len;
-                const float p = exp2_fast(fmaf(s[t][e], a.scale2, e < 2 ? -l2lo : -l2hi));
-                s[t][e] = in ? p * (dp[t][e] - (e < 2 ? dlo : dhi)) : 0.0f;
-            }
-        }
-        const uint32_t ds[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
-                                pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])};
-#pragma unroll
-        for (int p = 0; p < NP; ++p)
-            mma_rows(acc[p], ds, kr[p]);
-    }
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r = e < 2 ? lo : hi, d = 64 * p + 16 * c + 8 * (e & 1);
-            if (r < rows && d < a.D) {
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] = acc[p][j][e] * a.scale;
-                Row<__nv_bfloat16, 8, true>::store(
-                    (e < 2 ? a.dq.row(b, iqlo, hlo) : a.dq.row(b, iqhi, hhi)) + d, v);
-            }
-        }
-}
-
-// dv = p^T go and dk = scale * ds^T q: one warp per 16 keys of a key head, over the queries
-// of all heads of its group in order.
-template <int NP> __global__ void __launch_bounds__(128) attn_dkv_kernel(const AttnArgs a)
-{
-    constexpr int NC = 2 * NP;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    const int tiles = (a.Nk + 4 * kKeyStep - 1) / (4 * kKeyStep);
-    const int tile = (int)blockIdx.x % tiles, bh = (int)blockIdx.x / tiles, b = bh / a.Hkv, hk = bh - b * a.Hkv;
-    const int len = key_count(a, b), lo = (tile * 4 + warp) * kKeyStep + g, hi = lo + 8;
-    uint4 klo[NC], khi[NC], vlo[NC], vhi[NC];
-    load_chan<NC>(klo, a.k.row(b, lo, hk), lo < len, 8 * c, a.D);
-    load_chan<NC>(khi, a.k.row(b, hi, hk), hi < len, 8 * c, a.D);
-    load_chan<NC>(vlo, a.v.row(b, lo, hk), lo < len, 8 * c, a.D);
-    load_chan<NC>(vhi, a.v.row(b, hi, hk), hi < len, 8 * c, a.D);
-    float dk[NP][8][4] = {}, dv[NP][8][4] = {};
-    const bool any = (tile * 4 + warp) * kKeyStep < len;
-    for (int h = hk * a.G; any && h < (hk + 1) * a.G; ++h) {
-        const int64_t stat = ((int64_t)b * a.Hq + h) * a.Nq;
-        for (int qq = 0; qq < a.Nq; qq += 16) {
-            uint4 qf[2][NC], gf[2][NC];
-            float st[2][4] = {}, dp[2][4] = {};
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int iq = qq + 8 * t + g;
-                load_chan<NC>(qf[t], a.q.row(b, iq, h), iq < a.Nq, 8 * c, a.D);
-                load_chan<NC>(gf[t], a.go.row(b, iq, h), iq < a.Nq, 8 * c, a.D);
-                mma_chan<NC>(st[t], klo, khi, qf[t]);
-                mma_chan<NC>(dp[t], vlo, vhi, gf[t]);
-            }
-            uint32_t pa[4], ds[4];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                float p[4], d[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int iq = qq + 8 * t + 2 * c + (e & 1);
-                    const bool in = iq < a.Nq && (e < 2 ? lo : hi) < len;
-                    const float l2 = iq < a.Nq ? a.lse_in[stat + iq] * 1.4426950408889634f : 0.0f;
-                    const float de = iq < a.Nq ? a.delta[stat + iq] : 0.0f;
-                    p[e] = in ? exp2_fast(fmaf(st[t][e], a.scale2, -l2)) : 0.0f;
-                    d[e] = in ? p[e] * (dp[t][e] - de) : 0.0f;
-                }
-                pa[2 * t] = pack_bf16x2(p[0], p[1]);
-                pa[2 * t + 1] = pack_bf16x2(p[2], p[3]);
-                ds[2 * t] = pack_bf16x2(d[0], d[1]);
-                ds[2 * t + 1] = pack_bf16x2(d[2], d[3]);
-            }
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                RowFrag gr, qr;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int iq = qq + 2 * c + (i & 1) + 8 * (i >> 1);
-                    const bool ok = iq < a.Nq && 64 * p + 8 * g < a.D;
-                    gr.r[i] = load16(a.go.row(b, iq, h) + 64 * p + 8 * g, ok);
-                    qr.r[i] = load16(a.q.row(b, iq, h) + 64 * p + 8 * g, ok);
-                }
-                mma_rows(dv[p], pa, gr);
-                mma_rows(dk[p], ds, qr);
-            }
-        }
-    }
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int key = e < 2 ? lo : hi, d = 64 * p + 16 * c + 8 * (e & 1);
-            if (key < a.Nk && d < a.D) { // keys past the length: zeros
-                float x[8], y[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[j] = dk[p][j][e] * a.scale;
-                    y[j] = dv[p][j][e];
-                }
-                Row<__nv_bfloat16, 8, true>::store(a.dk.row(b, key, hk) + d, x);
-                Row<__nv_bfloat16, 8, true>::store(a.dv.row(b, key, hk) + d, y);
-            }
-        }
-}
-
 // ---------------------------------------------------------------------------
 // Host: argument rules.
 // ---------------------------------------------------------------------------
@@ -437,13 +263,14 @@ struct View {
     const tok_heads *t;
     int64_t B, N, H, D;
     int64_t span() const { return (B - 1) * t->batch + (N - 1) * t->token + (H - 1) * t->head + D; }
+    bool kv; // keys or values: heads may be broadcast, as batch entries may in all tensors
     bool strides_ok() const
     {
         constexpr int64_t kMax = (int64_t)1 << 38; // elements: byte strides and spans stay far inside 64 bits
         for (const Axis &x : {Axis{B, t->batch}, Axis{N, t->token}, Axis{H, t->head}})
             if (x.n > 1 && (x.s < 0 || x.s >= kMax))
                 return false;
-        return true;
+        return (N <= 1 || t->token > 0) && (H <= 1 || t->head > 0 || kv);
     }
     bool distinct() const { return nested({{B, t->batch}, {N, t->token}, {H, t->head}}, D); }
     bool aligned16() const
@@ -519,7 +346,7 @@ extern "C" int64_t tok_cross_attention_backward_workspace_size(int64_t B, int64_
                                                                int64_t Hkv, int64_t D)
 {
     const tok::Dims d{B, Nq, Nk, Hq, Hkv, D};
-    return d.ok() ? B * Hq * Nq * 4 : -1;
+    return d.ok() ? tok::attn_tc_backward_workspace(B, Nq, Nk, Hq, Hkv, D) : -1;
 }
 
 extern "C" tok_status tok_cross_attention(const tok_heads *q, const tok_heads *k, const tok_heads *v,
@@ -536,7 +363,8 @@ extern "C" tok_status tok_cross_attention(const tok_heads *q, const tok_heads *k
     if (!q || !k || !v || !o || !q->ptr || !o->ptr || (Nk > 0 && (!k->ptr || !v->ptr)))
         return TOK_ERR_NULL;
     const int64_t splits = fwd_splits(dim), need = tok_cross_attention_workspace_size(B, Nq, Nk, Hq, Hkv, D);
-    const View vq{q, B, Nq, Hq, D}, vk{k, B, Nk, Hkv, D}, vv{v, B, Nk, Hkv, D}, vo{o, B, Nq, Hq, D};
+    const View vq{q, B, Nq, Hq, D, false}, vk{k, B, Nk, Hkv, D, true}, vv{v, B, Nk, Hkv, D, true},
+        vo{o, B, Nq, Hq, D, false};
     for (const View &x : {vq, vk, vv, vo})
         if (!x.strides_ok())
             return TOK_ERR_SHAPE;
@@ -578,7 +406,7 @@ extern "C" tok_status tok_cross_attention(const tok_heads *q, const tok_heads *k
     a.scale2 = (float)((double)scale * 1.4426950408889634);
     const int64_t blocks = B * Hkv * ((Nq * a.G + kRows - 1) / kRows) * splits;
     tok_status st;
-    if (wants_tc(dim) && !attn_tc_broadcast_tokens(a)) {
+    if (wants_tc(dim)) {
         st = attn_tc_forward(a, stream);
     } else if (D <= 64) {
         attn_rows_kernel<1><<<(unsigned)blocks, kFwdWarps * 32, 0, stream>>>(a);
@@ -615,8 +443,9 @@ extern "C" tok_status tok_cross_attention_backward(const tok_heads *q, const tok
         (Nk > 0 && (!k->ptr || !v->ptr || !grad_k->ptr || !grad_v->ptr)))
         return TOK_ERR_NULL;
     const int64_t need = tok_cross_attention_backward_workspace_size(B, Nq, Nk, Hq, Hkv, D);
-    const View ins[] = {{q, B, Nq, Hq, D}, {o, B, Nq, Hq, D}, {grad_o, B, Nq, Hq, D}, {k, B, Nk, Hkv, D}, {v, B, Nk, Hkv, D}};
-    const View outs[] = {{grad_q, B, Nq, Hq, D}, {grad_k, B, Nk, Hkv, D}, {grad_v, B, Nk, Hkv, D}};
+    const View ins[] = {{q, B, Nq, Hq, D, false}, {o, B, Nq, Hq, D, false}, {grad_o, B, Nq, Hq, D, false},
+                        {k, B, Nk, Hkv, D, true}, {v, B, Nk, Hkv, D, true}};
+    const View outs[] = {{grad_q, B, Nq, Hq, D, false}, {grad_k, B, Nk, Hkv, D, true}, {grad_v, B, Nk, Hkv, D, true}};
     for (const View &x : ins)
         if (!x.strides_ok())
             return TOK_ERR_SHAPE;
@@ -667,7 +496,6 @@ extern "C" tok_status tok_cross_attention_backward(const tok_heads *q, const tok
     a.dk = view(grad_k);
     a.dv = view(grad_v);
     a.lse_in = lse;
-    a.delta = static_cast<float *>(workspace);
     a.lens = k_lens;
     a.B = (int)B;
     a.Nq = (int)Nq;
@@ -679,26 +507,5 @@ extern "C" tok_status tok_cross_attention_backward(const tok_heads *q, const tok
     a.splits = 1;
     a.scale = scale;
     a.scale2 = (float)((double)scale * 1.4426950408889634);
-    tok_status st = TOK_OK;
-    if (Nq > 0) {
-        attn_delta_kernel<<<(unsigned)((B * Hq * Nq + 31) / 32), 256, 0, stream>>>(a);
-        st = launch_status();
-        const unsigned blocks = (unsigned)(B * Hkv * ((Nq * a.G + 4 * kRows - 1) / (4 * kRows)));
-        if (st == TOK_OK) {
-            if (D <= 64)
-                attn_dq_kernel<1><<<blocks, 128, 0, stream>>>(a);
-            else
-                attn_dq_kernel<2><<<blocks, 128, 0, stream>>>(a);
-            st = launch_status();
-        }
-    }
-    if (st == TOK_OK && Nk > 0) {
-        const unsigned blocks = (unsigned)(B * Hkv * ((Nk + 4 * kKeyStep - 1) / (4 * kKeyStep)));
-        if (D <= 64)
-            attn_dkv_kernel<1><<<blocks, 128, 0, stream>>>(a);
-        else
-            attn_dkv_kernel<2><<<blocks, 128, 0, stream>>>(a);
-        st = launch_status();
-    }
-    return st;
+    return attn_tc_backward(a, static_cast<float *>(workspace), stream);
 }

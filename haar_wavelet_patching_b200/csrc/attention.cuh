@@ -7,6 +7,7 @@
 
 #include "tok_common.cuh"
 #include "tok_internal.h"
+#include "umma.cuh"
 
 namespace tok {
 
@@ -24,7 +25,6 @@ struct AttnArgs {
     HeadsView q, k, v, o, go, dq, dk, dv;
     const float *lse_in; // backward
     float *lse;          // [B, Hq, Nq] or null
-    float *delta;        // [B, Hq, Nq]: rowsum(go * o)
     float *part;         // split partials
     const int32_t *lens; // [B] or null
     int B, Nq, Nk, Hq, Hkv, G, D;
@@ -33,11 +33,11 @@ struct AttnArgs {
 };
 
 // The forward on the 5th-generation tensor cores (attention_tc.cu): query heads per row tile
-// for groups of G, and the call.  Takes everything but tensors broadcast over tokens or
-// query heads.
+// for groups of G, and the call.  Backward (attention_bwd_tc.cu): workspace bytes and the call.
 int attn_tc_group(int G);
-bool attn_tc_broadcast_tokens(const AttnArgs &a);
 tok_status attn_tc_forward(const AttnArgs &a, cudaStream_t stream);
+int64_t attn_tc_backward_workspace(int64_t B, int64_t Nq, int64_t Nk, int64_t Hq, int64_t Hkv, int64_t D);
+tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t stream);
 
 __device__ __forceinline__ int key_count(const AttnArgs &a, int b)
 {
@@ -121,6 +121,18 @@ __device__ __forceinline__ float quad_sum(float v)
 {
     v += __shfl_xor_sync(~0u, v, 1);
     return v + __shfl_xor_sync(~0u, v, 2);
+}
+
+// Tensor map of a [B, N, H, D] view with boxes of 64 channels x `heads` x `rows` tokens.
+// A dimension of stride 0 becomes one of extent 1 (its coordinate factor is 0).
+inline bool heads_map(CUtensorMap *map, const HeadsView &x, int64_t B, int64_t N, int64_t H, int64_t D, int heads, int rows)
+{
+    auto ext = [](int64_t n, int64_t s) { return (uint64_t)(n > 1 && s == 0 ? 1 : n); };
+    auto str = [](int64_t n, int64_t s) { return (uint64_t)(n > 1 && s != 0 ? s * 2 : 16); };
+    const uint64_t dims[4] = {(uint64_t)D, ext(H, x.h), ext(N, x.n), ext(B, x.b)};
+    const uint64_t strides[3] = {str(H, x.h), str(N, x.n), str(B, x.b)};
+    const uint32_t box[4] = {64, (uint32_t)heads, (uint32_t)rows, 1};
+    return encode_tensor_map_sw128(map, 4, x.p, dims, strides, box);
 }
 
 } // namespace tok

@@ -1,0 +1,831 @@
+// Gradients of cross attention on the 5th-generation tensor cores.
+//
+//   p = 2^(scale2 q k^T - lse2),  dp = go v^T,  ds = p (dp - delta),  delta = rowsum(go o)
+//   dv = p^T go,  dk = scale ds^T q,  dq = scale ds k
+//
+// Two passes that each recompute p and dp, 7 products for the 5 of the formulas: a single
+// pass would have to add up dq (or dk and dv) across CTAs, with atomics (whose order would
+// show in the result) or with a partial result per key tile (Nk / 128 times dq in fp32
+// through HBM).
+//
+// Query rows go in tiles of 128 as in the forward (G heads x 128 / G tokens of one group
+// where G is a power of two, else 128 tokens of one head).  attn_stats_kernel lays out lse2 and
+// delta in that order, padded to whole tiles (+inf and 0: p = 0 there).
+//
+// attn_dkv_kernel: one CTA per tile of 128 keys and share of the query tiles; s^T = k q^T and
+//   dp^T = v go^T have a key per tensor-memory lane, so p^T and ds^T are the A operands of
+//   dv += p^T go and dk += ds^T q as they stand.  q and go are read by two products each:
+//   [row][channel] tiles serve as K-major and as MN-major operand.  The MMA thread issues
+//   s(i+1) behind dv(i) and dp(i+1) behind dk(i): one product pair runs under the powers,
+//   the other under the ds arithmetic.  With shares, partial sums go to fp32 and
+//   attn_dkv_sum_kernel adds them in order.
+// attn_dq_kernel: one CTA per SM walks the query tiles; per key tile s, dp and dq += ds k,
+//   s double-buffered so that s(i+2), dp(i+1) and dq(i) run under the arithmetic of i+1.
+// In both, two warpgroups take half of a tile's columns each.
+#include <algorithm>
+
+#include "attention.cuh"
+
+namespace tok {
+
+static __device__ unsigned int g_attn_bwd_timeouts = 0;
+
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kThreads = 384; // warps 0-7 arithmetic, 8 MMA, 9 copies; 10 and 11 make the register split whole
+constexpr int kMathRegs = 208, kOtherRegs = 88;
+constexpr uint32_t SUB = kTile * 128; // bytes of 128 rows x 64 channels
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int DP> constexpr uint32_t tile_bytes() { return kTile * DP * 2; }
+
+struct BwdArgs {
+    AttnArgs a;
+    const float *lse2, *delta; // [B][hsets][rows]
+    float *part;               // [shares][2][B][Hkv][Nk][D]
+    int gp, hsets, rows;       // heads per tile, Hq / gp, padded query rows of a head set
+    int qtiles;                // rows / 128
+    int ktiles;                // ceil(Nk / 128)
+    int hs_kv;                 // head sets per key head
+    int shares, per;           // query tiles (over hs_kv sets) per share
+    int items;                 // dq
+    int qb, gb, kb, kh, vb, vh;
+};
+
+// lse2 and delta of every query row, in tile order: 8 lanes per row.
+__global__ void __launch_bounds__(256) attn_stats_kernel(const BwdArgs t, float *lse2, float *delta)
+{
+    const AttnArgs &a = t.a;
+    const int64_t at = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+    const int c = threadIdx.x & 7;
+    const int64_t sets = (int64_t)a.B * t.hsets;
+    if (at >= sets * t.rows)
+        return;
+    const int64_t set = at / t.rows;
+    const int r = (int)(at - set * t.rows), b = (int)(set / t.hsets), h = (int)(set - (int64_t)b * t.hsets) * t.gp + r % t.gp;
+    const int iq = r / t.gp;
+    float s = 0.0f, l = INFINITY;
+    if (iq < a.Nq) {
+        for (int d = 8 * c; d < a.D; d += 64) {
+            float x[8], y[8];
+            Row<__nv_bfloat16, 8, true>::load(a.go.row(b, iq, h) + d, x);
+            Row<__nv_bfloat16, 8, true>::load(a.o.row(b, iq, h) + d, y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s = fmaf(x[j], y[j], s);
+        }
+        l = a.lse_in[((int64_t)b * a.Hq + h) * a.Nq + iq] * kLog2e;
+        l = l == -INFINITY ? INFINITY : l; // a row without a key
+    }
+    const unsigned group = 0xFFu << (threadIdx.x & 24);
+    s += __shfl_xor_sync(group, s, 1);
+    s += __shfl_xor_sync(group, s, 2);
+    s += __shfl_xor_sync(group, s, 4);
+    if (c == 0) {
+        lse2[at] = l;
+        delta[at] = s;
+    }
+}
+
+template <int DP> struct DkvSmem {
+    static constexpr int NQ = DP == 128 ? 2 : 4, NG = NQ; // stages of q and go
+    static constexpr uint32_t TB = tile_bytes<DP>();
+    static constexpr uint32_t k = 0, v = TB, q = 2 * TB, g = q + NQ * TB, st = g + NG * TB; // stats: NQ x 1 KB
+    static constexpr size_t bytes = st + NQ * 1024 + 1024;
+};
+
+// [row][channel] tile as K-major operand, byte offset of K step k (16 channels).
+__device__ __forceinline__ constexpr uint32_t kmajor_step(int k) { return (k / 4) * SUB + (k % 4) * 32; }
+
+// Half a tile's columns of one lane: 64 columns of tensor memory.
+__device__ __forceinline__ void load_half(uint32_t col, float (&x)[64])
+{
+    tmem_ld64(col, reinterpret_cast<uint32_t(&)[64]>(x));
+    tmem_wait_ld();
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap gmap,
+                const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const BwdArgs t)
+{
+    using L = DkvSmem<DP>;
+    constexpr int NQ = L::NQ, NG = L::NG, NSUB = DP / 64;
+    constexpr uint32_t TB = L::TB;
+    __shared__ __align__(8) uint64_t kvfull, qfull[NQ], qempty[NQ], gfull[NG], gempty[NG], sfull, pfull, dpfull, dsfull,
+        done;
+    __shared__ uint32_t tmem_base_s;
+    __shared__ int abort_s;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const AttnArgs &a = t.a;
+
+    int r = blockIdx.x;
+    const int share = r % t.shares;
+    r /= t.shares;
+    const int kt = r % t.ktiles;
+    r /= t.ktiles;
+    const int hk = r % a.Hkv, b = r / a.Hkv;
+    const int len = key_count(a, b), k0 = kt * kTile;
+    const int total = t.hs_kv * t.qtiles, i0 = share * t.per, n = k0 < len ? min(total, i0 + t.per) - i0 : 0;
+    const int key = k0 + 32 * (warp & 3) + lane; // of warps 0-7
+    if (n <= 0) { // keys behind the length: zeros (with shares, the sum writes them)
+        if (t.shares == 1 && warp < 8 && key < a.Nk) {
+            __nv_bfloat16 *dst = (warp < 4 ? a.dv : a.dk).row(b, key, hk);
+            for (int d = 0; d < a.D; d += 8)
+                *reinterpret_cast<uint4 *>(dst + d) = make_uint4(0, 0, 0, 0);
+        }
+        return;
+    }
+
+    if (threadIdx.x == 0) {
+        mbar_init(smem_addr(&kvfull), 1);
+        for (int s = 0; s < NQ; ++s) {
+            mbar_init(smem_addr(&qfull[s]), 1);
+            mbar_init(smem_addr(&qempty[s]), 1);
+        }
+        for (int s = 0; s < NG; ++s) {
+            mbar_init(smem_addr(&gfull[s]), 1);
+            mbar_init(smem_addr(&gempty[s]), 1);
+        }
+        mbar_init(smem_addr(&sfull), 1);
+        mbar_init(smem_addr(&dpfull), 1);
+        mbar_init(smem_addr(&pfull), 8);
+        mbar_init(smem_addr(&dsfull), 8);
+        mbar_init(smem_addr(&done), 1);
+        abort_s = 0;
+        fence_barrier_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(smem_addr(&tmem_base_s), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+    volatile int *abort = &abort_s;
+    const uint32_t s_col = tmem, dp_col = tmem + 128, dv_col = tmem + 256, dk_col = tmem + 256 + DP;
+
+    if (warp >= 8) {
+        regs_dec<kOtherRegs>();
+        if (warp == 9 && lane == 0) {
+            auto load = [&](const CUtensorMap *map, uint32_t dst, uint32_t bar, int h, int row, int bb) {
+                for (int s = 0; s < NSUB; ++s)
+                    tma_load_4d(dst + s * SUB, map, 64 * s, h, row, bb, bar);
+            };
+            mbar_expect_tx(smem_addr(&kvfull), 2 * TB);
+            load(&kmap, base + L::k, smem_addr(&kvfull), hk * t.kh, k0, b * t.kb);
+            load(&vmap, base + L::v, smem_addr(&kvfull), hk * t.vh, k0, b * t.vb);
+            int i = 0, iq = 0, ig = 0;
+            for (; i < n; ++i) {
+                const int set = (i0 + i) / t.qtiles, qt = (i0 + i) - set * t.qtiles, hs = hk * t.hs_kv + set;
+                const int row = qt * (kTile / t.gp);
+                const uint32_t qs = i % NQ, gs = i % NG;
+                if (!wait_or_abort(smem_addr(&qempty[qs]), ((i / NQ) & 1u) ^ 1u, abort))
+                    break;
+                const uint32_t qbar = smem_addr(&qfull[qs]), st = base + L::st + qs * 1024;
+                mbar_expect_tx(qbar, TB + 1024);
+                load(&qmap, base + L::q + qs * TB, qbar, hs * t.gp, row, b * t.qb);
+                const int64_t at = ((int64_t)b * t.hsets + hs) * t.rows + qt * kTile;
+                bulk_load(st, t.lse2 + at, 512, qbar);
+                bulk_load(st + 512, t.delta + at, 512, qbar);
+                ++iq;
+                if (!wait_or_abort(smem_addr(&gempty[gs]), ((i / NG) & 1u) ^ 1u, abort))
+                    break;
+                mbar_expect_tx(smem_addr(&gfull[gs]), TB);
+                load(&gmap, base + L::g + gs * TB, smem_addr(&gfull[gs]), hs * t.gp, row, b * t.gb);
+                ++ig;
+            }
+            if (i < n) { // let the copies already issued land before the CTA exits (each wait bounded)
+                mbar_wait(smem_addr(&kvfull), 0u);
+                for (int j = max(0, iq - NQ); j < iq; ++j)
+                    mbar_wait(smem_addr(&qfull[j % NQ]), (j / NQ) & 1u);
+                for (int j = max(0, ig - NG); j < ig; ++j)
+                    mbar_wait(smem_addr(&gfull[j % NG]), (j / NG) & 1u);
+            }
+        }
+        if (warp == 8 && lane == 0) {
+            const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile), idesc_d = idesc_bf16_f32(kTile, DP) | kBTransposed;
+            const uint64_t kd = sw128_desc(base + L::k), vd = sw128_desc(base + L::v);
+            auto scores = [&](uint32_t col, uint64_t ad, uint32_t tile, uint64_t *bar) {
+                const uint64_t bd = sw128_desc(tile);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    umma_bf16(col, ad + (kmajor_step(k) >> 4), bd + (kmajor_step(k) >> 4), idesc_s, k != 0);
+                umma_commit(smem_addr(bar));
+            };
+            auto grads = [&](uint32_t col, uint32_t acol, uint32_t tile, bool add) {
+                const uint64_t bd = sw128_desc_mn(tile, SUB);
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k) // a warpgroup's 64 query columns: 32 packed ones
+                    umma_ts(col, acol + (k / 4) * 64 + (k % 4) * 8, bd + ((k * 2048) >> 4), idesc_d, add || k > 0);
+            };
+            auto full = [&](uint64_t *bars, int i, int stages) {
+                return wait_or_abort(smem_addr(&bars[i % stages]), (i / stages) & 1u, abort);
+            };
+            bool ok = wait_or_abort(smem_addr(&kvfull), 0u, abort) && full(qfull, 0, NQ);
+            if (ok) {
+                tc_fence_after();
+                scores(s_col, kd, base + L::q, &sfull);
+                ok = full(gfull, 0, NG);
+            }
+            if (ok) {
+                tc_fence_after();
+                scores(dp_col, vd, base + L::g, &dpfull);
+            }
+            for (int i = 0; i < n && ok; ++i) {
+                ok = wait_or_abort(smem_addr(&pfull), i & 1u, abort);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                grads(dv_col, s_col, base + L::g + (i % NG) * TB, i > 0);
+                umma_commit(smem_addr(&gempty[i % NG]));
+                if (i + 1 < n) {
+                    ok = full(qfull, i + 1, NQ);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    scores(s_col, kd, base + L::q + ((i + 1) % NQ) * TB, &sfull);
+                }
+                ok = wait_or_abort(smem_addr(&dsfull), i & 1u, abort);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                grads(dk_col, dp_col, base + L::q + (i % NQ) * TB, i > 0);
+                umma_commit(smem_addr(&qempty[i % NQ]));
+                if (i + 1 < n) {
+                    ok = full(gfull, i + 1, NG);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    scores(dp_col, vd, base + L::g + ((i + 1) % NG) * TB, &dpfull);
+                }
+            }
+            umma_commit(smem_addr(&done));
+            mbar_wait(smem_addr(&done), 0u); // every MMA issued has completed before tensor memory is freed
+        }
+    } else {
+        regs_inc<kMathRegs>();
+        const int half = warp >> 2;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t sc = s_col + lanes + 64 * half, dc = dp_col + lanes + 64 * half;
+        const bool live = key < len;
+        const float2 mul = make_float2(a.scale2, a.scale2);
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const uint32_t qs = i % NQ;
+            const float *stats = reinterpret_cast<const float *>(smem_raw + (base + L::st + qs * 1024 - smem_addr(smem_raw)));
+            if (!wait_or_abort(smem_addr(&sfull), i & 1u, abort) ||
+                !wait_or_abort(smem_addr(&qfull[qs]), (i / NQ) & 1u, abort)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            float p[64];
+            load_half(sc, p);
+            {
+                const float4 *l4 = reinterpret_cast<const float4 *>(stats + 64 * half);
+                uint32_t pk[32];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float4 l = l4[e];
+                    const float2 x = __ffma2_rn(make_float2(p[4 * e], p[4 * e + 1]), mul, make_float2(-l.x, -l.y));
+                    const float2 y = __ffma2_rn(make_float2(p[4 * e + 2], p[4 * e + 3]), mul, make_float2(-l.z, -l.w));
+                    p[4 * e] = live ? exp2_fast(x.x) : 0.0f;
+                    p[4 * e + 1] = live ? exp2_fast(x.y) : 0.0f;
+                    p[4 * e + 2] = live ? exp2_fast(y.x) : 0.0f;
+                    p[4 * e + 3] = live ? exp2_fast(y.y) : 0.0f;
+                    pk[2 * e] = pack_bf16x2(p[4 * e], p[4 * e + 1]);
+                    pk[2 * e + 1] = pack_bf16x2(p[4 * e + 2], p[4 * e + 3]);
+                }
+                tmem_st32(sc, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&pfull));
+            if (!wait_or_abort(smem_addr(&dpfull), i & 1u, abort)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            {
+                const float4 *d4 = reinterpret_cast<const float4 *>(stats + 128 + 64 * half);
+                float dp[64];
+                load_half(dc, dp);
+                uint32_t pk[32];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float4 d = d4[e];
+                    const float2 x = __fmul2_rn(make_float2(p[4 * e], p[4 * e + 1]),
+                                                make_float2(dp[4 * e] - d.x, dp[4 * e + 1] - d.y));
+                    const float2 y = __fmul2_rn(make_float2(p[4 * e + 2], p[4 * e + 3]),
+                                                make_float2(dp[4 * e + 2] - d.z, dp[4 * e + 3] - d.w));
+                    pk[2 * e] = live ? pack_bf16x2(x.x, x.y) : 0u;
+                    pk[2 * e + 1] = live ? pack_bf16x2(y.x, y.y) : 0u;
+                }
+                tmem_st32(dc, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&dsfull));
+        }
+        ok = ok && wait_or_abort(smem_addr(&done), 0u, abort);
+        if (ok) { // warps 0-3 store dv, 4-7 dk
+            tc_fence_after();
+            const uint32_t col = (half ? dk_col : dv_col) + lanes;
+            const float f = half ? a.scale : 1.0f;
+            float *part = t.part + ((((int64_t)share * 2 + half) * a.B + b) * a.Hkv + hk) * a.Nk * a.D +
+                          (int64_t)key * a.D;
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) {
+                uint32_t x[32];
+                tmem_ld32(col + 32 * c, x);
+                tmem_wait_ld();
+                if (key >= a.Nk)
+                    continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int d = 32 * c + 8 * e;
+                    if (d >= a.D)
+                        continue;
+                    float v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        v[k] = live ? __uint_as_float(x[8 * e + k]) * f : 0.0f;
+                    if (t.shares == 1)
+                        Row<__nv_bfloat16, 8, true>::store((half ? a.dk : a.dv).row(b, key, hk) + d, v);
+                    else
+                        Row<float, 8, true>::store(part + d, v);
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && *abort)
+        atomicAdd(&g_attn_bwd_timeouts, 1u);
+}
+
+// dv and dk of the shares' partial sums, in order; zeros behind the length (and without queries).
+__global__ void __launch_bounds__(256) attn_dkv_sum_kernel(const BwdArgs t)
+{
+    const AttnArgs &a = t.a;
+    const int64_t per = (int64_t)a.B * a.Hkv * a.Nk, chunks = a.D / 8;
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= 2 * per * chunks)
+        return;
+    const int64_t half = e / (per * chunks), r = e - half * per * chunks;
+    const int64_t at = r / chunks;
+    const int d = (int)(r - at * chunks) * 8;
+    const int key = (int)(at % a.Nk), bh = (int)(at / a.Nk), b = bh / a.Hkv, hk = bh - b * a.Hkv;
+    float v[8] = {};
+    if (key < key_count(a, b))
+        for (int s = 0; s < t.shares; ++s) {
+            float x[8];
+            Row<float, 8, true>::load(t.part + ((int64_t)s * 2 + half) * per * a.D + at * a.D + d, x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] += x[k];
+        }
+    Row<__nv_bfloat16, 8, true>::store((half ? a.dk : a.dv).row(b, key, hk) + d, v);
+}
+
+template <int DP> struct DqSmem {
+    static constexpr int NK = DP == 128 ? 3 : 4, NV = DP == 128 ? 2 : 4; // stages of k and v
+    static constexpr uint32_t TB = tile_bytes<DP>();
+    static constexpr uint32_t q = 0, g = TB, k = 2 * TB, v = k + NK * TB;
+    static constexpr size_t bytes = v + NV * TB + 1024;
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap gmap,
+               const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const BwdArgs t)
+{
+    using L = DqSmem<DP>;
+    constexpr int NK = L::NK, NV = L::NV, NSUB = DP / 64;
+    constexpr uint32_t TB = L::TB;
+    __shared__ __align__(8) uint64_t qfull, qempty, kfull[NK], kempty[NK], vfull[NV], vempty[NV], sfull[2], dpfull, dsfull,
+        dqfull, drain;
+    __shared__ uint32_t tmem_base_s;
+    __shared__ int abort_s;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const AttnArgs &a = t.a;
+    auto decode = [&](int i, int &b, int &hs, int &qt, int &len) {
+        qt = i % t.qtiles;
+        const int r = i / t.qtiles;
+        hs = r % t.hsets;
+        b = r / t.hsets;
+        len = key_count(a, b);
+    };
+
+    if (threadIdx.x == 0) {
+        for (uint64_t *bar : {&qfull, &qempty, &sfull[0], &sfull[1], &dpfull, &dqfull, &drain})
+            mbar_init(smem_addr(bar), 1);
+        mbar_init(smem_addr(&dsfull), 8);
+        for (int s = 0; s < NK; ++s) {
+            mbar_init(smem_addr(&kfull[s]), 1);
+            mbar_init(smem_addr(&kempty[s]), 1);
+        }
+        for (int s = 0; s < NV; ++s) {
+            mbar_init(smem_addr(&vfull[s]), 1);
+            mbar_init(smem_addr(&vempty[s]), 1);
+        }
+        abort_s = 0;
+        fence_barrier_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(smem_addr(&tmem_base_s), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+    volatile int *abort = &abort_s;
+    const uint32_t s_col = tmem, dp_col = tmem + 256, dq_col = tmem + 384; // s: two buffers
+
+    if (warp >= 8) {
+        regs_dec<kOtherRegs>();
+        if (warp == 9 && lane == 0) {
+            uint32_t ik = 0, iv = 0, iq = 0;
+            bool ok = true;
+            auto load = [&](const CUtensorMap *map, uint32_t dst, uint32_t bar, int h, int row, int bb) {
+                for (int s = 0; s < NSUB; ++s)
+                    tma_load_4d(dst + s * SUB, map, 64 * s, h, row, bb, bar);
+            };
+            for (int i = blockIdx.x; i < t.items && ok; i += gridDim.x) {
+                int b, hs, qt, len;
+                decode(i, b, hs, qt, len);
+                const int n = (len + kTile - 1) / kTile, hk = hs / t.hs_kv;
+                if (n == 0)
+                    continue;
+                ok = wait_or_abort(smem_addr(&qempty), (iq & 1u) ^ 1u, abort);
+                if (!ok)
+                    break;
+                mbar_expect_tx(smem_addr(&qfull), 2 * TB);
+                load(&qmap, base + L::q, smem_addr(&qfull), hs * t.gp, qt * (kTile / t.gp), b * t.qb);
+                load(&gmap, base + L::g, smem_addr(&qfull), hs * t.gp, qt * (kTile / t.gp), b * t.gb);
+                ++iq;
+                for (int j = 0; j < n && ok; ++j) {
+                    const uint32_t ks = ik % NK, vs = iv % NV;
+                    ok = wait_or_abort(smem_addr(&kempty[ks]), ((ik / NK) & 1u) ^ 1u, abort);
+                    if (!ok)
+                        break;
+                    mbar_expect_tx(smem_addr(&kfull[ks]), TB);
+                    load(&kmap, base + L::k + ks * TB, smem_addr(&kfull[ks]), hk * t.kh, j * kTile, b * t.kb);
+                    ++ik;
+                    ok = wait_or_abort(smem_addr(&vempty[vs]), ((iv / NV) & 1u) ^ 1u, abort);
+                    if (!ok)
+                        break;
+                    mbar_expect_tx(smem_addr(&vfull[vs]), TB);
+                    load(&vmap, base + L::v + vs * TB, smem_addr(&vfull[vs]), hk * t.vh, j * kTile, b * t.vb);
+                    ++iv;
+                }
+            }
+            if (!ok) { // let the copies already issued land before the CTA exits (each wait bounded)
+                if (iq)
+                    mbar_wait(smem_addr(&qfull), (iq - 1) & 1u);
+                for (uint32_t j = ik > (uint32_t)NK ? ik - NK : 0; j < ik; ++j)
+                    mbar_wait(smem_addr(&kfull[j % NK]), (j / NK) & 1u);
+                for (uint32_t j = iv > (uint32_t)NV ? iv - NV : 0; j < iv; ++j)
+                    mbar_wait(smem_addr(&vfull[j % NV]), (j / NV) & 1u);
+            }
+        }
+        if (warp == 8 && lane == 0) {
+            const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile), idesc_d = idesc_bf16_f32(kTile, DP) | kBTransposed;
+            const uint64_t qd = sw128_desc(base + L::q), gd = sw128_desc(base + L::g);
+            uint32_t it = 0, iq = 0; // key tiles, items so far
+            bool ok = true;
+            auto product = [&](uint32_t col, uint64_t ad, uint32_t tile) {
+                const uint64_t bd = sw128_desc(tile);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    umma_bf16(col, ad + (kmajor_step(k) >> 4), bd + (kmajor_step(k) >> 4), idesc_s, k != 0);
+            };
+            auto scores = [&](uint32_t x) { // s of key tile x (counted over all items)
+                if (!wait_or_abort(smem_addr(&kfull[x % NK]), (x / NK) & 1u, abort))
+                    return false;
+                tc_fence_after();
+                product(s_col + 128 * (x & 1u), qd, base + L::k + (x % NK) * TB);
+                umma_commit(smem_addr(&sfull[x & 1u]));
+                return true;
+            };
+            auto dps = [&](uint32_t x) {
+                if (!wait_or_abort(smem_addr(&vfull[x % NV]), (x / NV) & 1u, abort))
+                    return false;
+                tc_fence_after();
+                product(dp_col, gd, base + L::v + (x % NV) * TB);
+                umma_commit(smem_addr(&dpfull));
+                umma_commit(smem_addr(&vempty[x % NV]));
+                return true;
+            };
+            for (int i = blockIdx.x; i < t.items && ok; i += gridDim.x) {
+                int b, hs, qt, len;
+                decode(i, b, hs, qt, len);
+                const int n = (len + kTile - 1) / kTile;
+                if (n == 0)
+                    continue;
+                ok = wait_or_abort(smem_addr(&qfull), iq & 1u, abort) && scores(it) && dps(it) && (n == 1 || scores(it + 1));
+                if (n == 1 && ok)
+                    umma_commit(smem_addr(&qempty));
+                for (int j = 0; j < n && ok; ++j) {
+                    const uint32_t x = it + j;
+                    ok = wait_or_abort(smem_addr(&dsfull), x & 1u, abort);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint64_t bd = sw128_desc_mn(base + L::k + (x % NK) * TB, SUB);
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k) // a warpgroup's 64 key columns: 32 packed ones
+                        umma_ts(dq_col, s_col + 128 * (x & 1u) + (k / 4) * 64 + (k % 4) * 8, bd + ((k * 2048) >> 4),
+                                idesc_d, j > 0 || k > 0);
+                    umma_commit(smem_addr(&kempty[x % NK]));
+                    if (j + 1 < n) {
+                        ok = dps(x + 1) && (j + 2 >= n || scores(x + 2));
+                        if (j + 2 == n && ok)
+                            umma_commit(smem_addr(&qempty));
+                    } else
+                        umma_commit(smem_addr(&dqfull));
+                }
+                it += n;
+                ++iq;
+            }
+            umma_commit(smem_addr(&drain));
+            mbar_wait(smem_addr(&drain), 0u); // every MMA issued has completed before tensor memory is freed
+        }
+    } else {
+        regs_inc<kMathRegs>();
+        const int half = warp >> 2;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const float2 mul = make_float2(a.scale2, a.scale2);
+        uint32_t it = 0, items = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; i < t.items && ok; i += gridDim.x) {
+            int b, hs, qt, len;
+            decode(i, b, hs, qt, len);
+            const int n = (len + kTile - 1) / kTile;
+            const int row = qt * kTile + 32 * (warp & 3) + lane;
+            const int iq = row / t.gp, h = hs * t.gp + row % t.gp;
+            const int64_t at = ((int64_t)b * t.hsets + hs) * t.rows + row;
+            const float2 l2 = make_float2(-t.lse2[at], -t.lse2[at]);
+            const float delta = t.delta[at];
+            for (int j = 0; j < n; ++j, ++it) {
+                const uint32_t sc = s_col + 128 * (it & 1u) + 64 * half + lanes;
+                if (!wait_or_abort(smem_addr(&sfull[it & 1u]), (it >> 1) & 1u, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float p[64];
+                load_half(sc, p);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float2 x = __ffma2_rn(make_float2(p[2 * e], p[2 * e + 1]), mul, l2);
+                    p[2 * e] = exp2_fast(x.x);
+                    p[2 * e + 1] = exp2_fast(x.y);
+                }
+                if (!wait_or_abort(smem_addr(&dpfull), it & 1u, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int valid = len - j * kTile; // keys of this tile
+                {
+                    float dp[64];
+                    load_half(dp_col + 64 * half + lanes, dp);
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float2 x = __fmul2_rn(make_float2(p[2 * e], p[2 * e + 1]),
+                                                    make_float2(dp[2 * e] - delta, dp[2 * e + 1] - delta));
+                        pk[e] = pack_bf16x2(x.x, x.y);
+                    }
+                    if (valid < kTile) { // keys behind the length: 0, whatever their scores
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int c = 64 * half + 2 * e;
+                            pk[e] = c + 1 < valid ? pk[e] : c < valid ? pk[e] & 0xFFFFu : 0u;
+                        }
+                    }
+                    tmem_st32(sc, pk);
+                }
+                if (half == 0 && valid < kTile && len < a.Nk) { // and the k rows themselves
+                    const uint32_t ks = it % NK;
+                    if (!wait_or_abort(smem_addr(&kfull[ks]), (it / NK) & 1u, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    unsigned char *k = smem_raw + (base + L::k + ks * TB - smem_addr(smem_raw));
+                    for (int e = valid * 8 + threadIdx.x; e < kTile * 8; e += 128)
+#pragma unroll
+                        for (int sub = 0; sub < NSUB; ++sub)
+                            *reinterpret_cast<uint4 *>(k + sub * SUB + e * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&dsfull));
+            }
+            if (!ok)
+                break;
+            if (n > 0) {
+                if (!wait_or_abort(smem_addr(&dqfull), items & 1u, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                ++items;
+            }
+            // Each warpgroup stores half of the channels.
+#pragma unroll
+            for (int c = 0; c < DP / 64; ++c) {
+                uint32_t x[32] = {};
+                const int d0 = half * (DP / 2) + 32 * c;
+                if (n > 0) {
+                    tmem_ld32(dq_col + d0 + lanes, x);
+                    tmem_wait_ld();
+                }
+                if (iq >= a.Nq)
+                    continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (d0 + 8 * e >= a.D)
+                        continue;
+                    float v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        v[k] = n > 0 ? __uint_as_float(x[8 * e + k]) * a.scale : 0.0f;
+                    Row<__nv_bfloat16, 8, true>::store(a.dq.row(b, iq, h) + d0 + 8 * e, v);
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && *abort)
+        atomicAdd(&g_attn_bwd_timeouts, 1u);
+}
+
+template <typename K> tok_status prepare(K kernel, size_t smem)
+{
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) {
+        record_cuda_error(e);
+        return TOK_ERR_CUDA;
+    }
+    return TOK_OK;
+}
+
+template <int DP> tok_status launch(const BwdArgs &t, const CUtensorMap &q, const CUtensorMap &g, const CUtensorMap &k,
+                                    const CUtensorMap &v, cudaStream_t stream)
+{
+    const AttnArgs &a = t.a;
+    tok_status st = prepare(attn_dkv_kernel<DP>, DkvSmem<DP>::bytes);
+    if (st == TOK_OK)
+        st = prepare(attn_dq_kernel<DP>, DqSmem<DP>::bytes);
+    if (st != TOK_OK)
+        return st;
+    if (t.ktiles > 0) {
+        attn_dkv_kernel<DP><<<(unsigned)(a.B * a.Hkv * t.ktiles * t.shares), kThreads, DkvSmem<DP>::bytes, stream>>>(
+            q, g, k, v, t);
+        st = launch_status();
+        if (st != TOK_OK)
+            return st;
+    }
+    const int sms = sm_count();
+    attn_dq_kernel<DP><<<std::min(t.items, sms > 0 ? sms : 1), kThreads, DqSmem<DP>::bytes, stream>>>(q, g, k, v, t);
+    return launch_status();
+}
+
+// Tiles and shares of a backward call, from its extents alone.
+struct Plan {
+    int64_t gp, hsets, qtiles, rows, ktiles, hs_kv, per, shares, stat_floats, part_floats;
+    Plan(int64_t B, int64_t Nq, int64_t Nk, int64_t Hq, int64_t Hkv, int64_t D)
+    {
+        gp = attn_tc_group((int)(Hq / Hkv));
+        hsets = Hq / gp;
+        hs_kv = hsets / Hkv;
+        qtiles = (Nq * gp + kTile - 1) / kTile;
+        rows = qtiles * kTile;
+        ktiles = (Nk + kTile - 1) / kTile;
+        stat_floats = B * hsets * rows;
+        // Shares of the query tiles: the fewest that leave the SMs' last round nearly full
+        // (within 10% of the best of up to 16), each of at least 8 tiles.
+        const int64_t total = hs_kv * qtiles, base = B * Hkv * ktiles;
+        shares = 1;
+        per = total;
+        if (base > 0 && total > 0) {
+            const int64_t most = std::max<int64_t>(1, std::min<int64_t>(16, total / 8));
+            auto rounds = [&](int64_t s) { return (double)((base * s + 147) / 148) / (double)s; };
+            double best = rounds(1);
+            for (int64_t s = 2; s <= most; ++s)
+                best = std::min(best, rounds(s));
+            while (rounds(shares) > 1.1 * best)
+                ++shares;
+            per = (total + shares - 1) / shares;
+            shares = (total + per - 1) / per;
+        }
+        part_floats = shares > 1 ? shares * 2 * B * Hkv * Nk * D : 0;
+    }
+};
+
+} // namespace
+
+int64_t attn_tc_backward_workspace(int64_t B, int64_t Nq, int64_t Nk, int64_t Hq, int64_t Hkv, int64_t D)
+{
+    const Plan p(B, Nq, Nk, Hq, Hkv, D);
+    return (2 * p.stat_floats + p.part_floats) * 4;
+}
+
+tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t stream)
+{
+    const Plan p(a.B, a.Nq, a.Nk, a.Hq, a.Hkv, a.D);
+    BwdArgs t{};
+    t.a = a;
+    t.lse2 = workspace;
+    t.delta = workspace + p.stat_floats;
+    t.part = workspace + 2 * p.stat_floats;
+    t.gp = (int)p.gp;
+    t.hsets = (int)p.hsets;
+    t.rows = (int)p.rows;
+    t.qtiles = (int)p.qtiles;
+    t.ktiles = (int)p.ktiles;
+    t.hs_kv = (int)p.hs_kv;
+    t.shares = (int)p.shares;
+    t.per = (int)p.per;
+    t.items = (int)(a.B * p.hsets * p.qtiles);
+    t.qb = a.B > 1 && a.q.b == 0 ? 0 : 1;
+    t.gb = a.B > 1 && a.go.b == 0 ? 0 : 1;
+    t.kb = a.B > 1 && a.k.b == 0 ? 0 : 1;
+    t.vb = a.B > 1 && a.v.b == 0 ? 0 : 1;
+    t.kh = a.Hkv > 1 && a.k.h == 0 ? 0 : 1;
+    t.vh = a.Hkv > 1 && a.v.h == 0 ? 0 : 1;
+    const int64_t kv = (int64_t)a.B * a.Hkv * a.Nk, sum_threads = 2 * kv * (a.D / 8);
+    tok_status st = TOK_OK;
+    if (a.Nq > 0) {
+        attn_stats_kernel<<<(unsigned)((p.stat_floats + 31) / 32), 256, 0, stream>>>(t, workspace,
+                                                                                   workspace + p.stat_floats);
+        st = launch_status();
+    }
+    if (st == TOK_OK && a.Nq > 0) {
+        // Without keys the maps of k and v stand on q: no kernel reads through them.
+        const bool keys = a.Nk > 0;
+        const HeadsView none{a.q.p, 0, 0, 0};
+        CUtensorMap q, g, k, v;
+        const int qr = kTile / t.gp;
+        if (!heads_map(&q, a.q, a.B, a.Nq, a.Hq, a.D, t.gp, qr) || !heads_map(&g, a.go, a.B, a.Nq, a.Hq, a.D, t.gp, qr) ||
+            !(keys ? heads_map(&k, a.k, a.B, a.Nk, a.Hkv, a.D, 1, kTile) : heads_map(&k, none, 1, 1, 1, a.D, 1, kTile)) ||
+            !(keys ? heads_map(&v, a.v, a.B, a.Nk, a.Hkv, a.D, 1, kTile) : heads_map(&v, none, 1, 1, 1, a.D, 1, kTile)))
+            return TOK_ERR_SHAPE;
+        st = a.D <= 64 ? launch<64>(t, q, g, k, v, stream) : launch<128>(t, q, g, k, v, stream);
+    }
+    if (st == TOK_OK && kv > 0 && (t.shares > 1 || a.Nq == 0)) {
+        if (a.Nq == 0)
+            t.shares = 0; // zeros
+        attn_dkv_sum_kernel<<<(unsigned)((sum_threads + 255) / 256), 256, 0, stream>>>(t);
+        st = launch_status();
+    }
+    return st;
+}
+
+tok_status read_and_clear_attn_bwd_timeouts(cudaStream_t stream, unsigned int *count)
+{
+    unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(count, g_attn_bwd_timeouts, sizeof(unsigned int), 0,
+                                              cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(stream);
+    if (e == cudaSuccess && *count)
+        e = cudaMemcpyToSymbolAsync(g_attn_bwd_timeouts, &zero, sizeof(unsigned int), 0, cudaMemcpyHostToDevice, stream);
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) {
+        record_cuda_error(e);
+        return TOK_ERR_CUDA;
+    }
+    return TOK_OK;
+}
+
+} // namespace tok

@@ -20,7 +20,6 @@
 #include <algorithm>
 
 #include "attention.cuh"
-#include "umma.cuh"
 
 namespace tok {
 
@@ -43,7 +42,7 @@ struct TcArgs {
     int nqt;      // items per (batch, head set): 256 rows each
     int hsets;    // Hq / gp
     int items;
-    int qb, kb, kh, vb, vh, qh; // coordinate factors: 0 for a broadcast dimension
+    int qb, kb, kh, vb, vh; // coordinate factors: 0 for a broadcast dimension
 };
 
 struct Item {
@@ -66,48 +65,6 @@ __device__ __forceinline__ Item decode(const TcArgs &t, int i)
     w.ntiles = t1 - t0;
     w.kend = min(len, t1 * kTile);
     return w;
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-                 "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-                 ::"r"(taddr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-                 "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-                 "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// D[tmem] (+)= A[tmem] x B[smem], bf16: A's rows are lanes, two elements of K to a column.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
-{
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-                 "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-                 : "memory");
-}
-
-// Shared-memory descriptor of an operand stored [k][n], n contiguous ("MN-major"), in the
-// 128-byte swizzle: 64 n per 128-byte row, rows of 8 k per 1024-byte atom, atoms of the next
-// 8 k 1024 bytes on (stride field), of the next 64 n `n_bytes` on (leading field).
-__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t n_bytes)
-{
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(n_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-constexpr uint32_t kBTransposed = 1u << 16; // instruction descriptor: B is MN-major
-
-// Registers per thread of the calling warpgroup.
-template <int N> __device__ __forceinline__ void regs_inc()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N> __device__ __forceinline__ void regs_dec()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <int DP>
@@ -166,7 +123,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             auto load_q = [&](const Item &w, int i) {
                 if (!wait_or_abort(smem_addr(&qempty[i]), (nq & 1u) ^ 1u, abort))
                     return false;
-                load(&qmap, base + i * TB, smem_addr(&qfull[i]), w.hs * t.gp * t.qh, (w.row0 + i * kTile) / t.gp,
+                load(&qmap, base + i * TB, smem_addr(&qfull[i]), w.hs * t.gp, (w.row0 + i * kTile) / t.gp,
                      w.b * t.qb);
                 ++issued[i];
                 return true;
@@ -430,18 +387,6 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         atomicAdd(&g_attn_timeouts, 1u);
 }
 
-// Tensor map of a [B, N, H, D] view with boxes of 64 channels x `heads` x `rows` tokens.
-// A dimension of stride 0 becomes one of extent 1 (its coordinate factor is 0).
-bool heads_map(CUtensorMap *map, const HeadsView &x, int64_t B, int64_t N, int64_t H, int64_t D, int heads, int rows)
-{
-    auto ext = [](int64_t n, int64_t s) { return (uint64_t)(n > 1 && s == 0 ? 1 : n); };
-    auto str = [](int64_t n, int64_t s) { return (uint64_t)(n > 1 && s != 0 ? s * 2 : 16); };
-    const uint64_t dims[4] = {(uint64_t)D, ext(H, x.h), ext(N, x.n), ext(B, x.b)};
-    const uint64_t strides[3] = {str(H, x.h), str(N, x.n), str(B, x.b)};
-    const uint32_t box[4] = {64, (uint32_t)heads, (uint32_t)rows, 1};
-    return encode_tensor_map_sw128(map, 4, x.p, dims, strides, box);
-}
-
 template <int DP> tok_status launch(const TcArgs &t, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                                     cudaStream_t stream)
 {
@@ -461,11 +406,6 @@ template <int DP> tok_status launch(const TcArgs &t, const CUtensorMap &q, const
 // Heads that a 128-row tile holds: the group, where it divides the tile.
 int attn_tc_group(int G) { return G <= kTile && (G & (G - 1)) == 0 ? G : 1; }
 
-bool attn_tc_broadcast_tokens(const AttnArgs &a)
-{
-    return (a.Nq > 1 && a.q.n == 0) || (a.Nk > 1 && (a.k.n == 0 || a.v.n == 0)) || (a.Hq > 1 && a.q.h == 0);
-}
-
 tok_status attn_tc_forward(const AttnArgs &a, cudaStream_t stream)
 {
     TcArgs t{};
@@ -474,7 +414,6 @@ tok_status attn_tc_forward(const AttnArgs &a, cudaStream_t stream)
     t.hsets = a.Hq / t.gp;
     t.nqt = (int)(((int64_t)a.Nq * t.gp + 2 * kTile - 1) / (2 * kTile));
     t.items = a.B * t.hsets * t.nqt * a.splits;
-    t.qh = t.qb = t.kh = t.kb = t.vh = t.vb = 1;
     t.qb = a.B > 1 && a.q.b == 0 ? 0 : 1;
     t.kb = a.B > 1 && a.k.b == 0 ? 0 : 1;
     t.vb = a.B > 1 && a.v.b == 0 ? 0 : 1;

@@ -61,6 +61,7 @@ tok_status read_and_clear_fsq_timeouts(cudaStream_t stream, unsigned int *count)
 tok_status read_and_clear_fsq_bwd_timeouts(cudaStream_t stream, unsigned int *count);
 tok_status read_and_clear_conv_timeouts(cudaStream_t stream, unsigned int *count);
 tok_status read_and_clear_attn_timeouts(cudaStream_t stream, unsigned int *count);
+tok_status read_and_clear_attn_bwd_timeouts(cudaStream_t stream, unsigned int *count);
 
 // Remembers a CUDA error for tok_last_cuda_error().
 void record_cuda_error(cudaError_t e);

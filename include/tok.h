@@ -552,8 +552,9 @@ TOK_API tok_status tok_sample_codes(const void *logits, tok_dtype dtype, int64_t
  *
  * A tensor is a tok_heads: pointer and strides in elements of batch, token and head,
  * the D channels dense -- slices of a fused projection are read and written in place,
- * and an input's stride may be 0 (one encoder state for the whole batch; its gradient
- * is per batch entry).  Shape rule: D a multiple of 8, 8 <= D <= 128; Hq a multiple
+ * and the batch stride of an input, or the head stride of k and v, may be 0 (one encoder
+ * state for the whole batch, one key head for all; gradients are per batch entry and
+ * key head).  Token strides, and the head strides of the others, are positive.  Shape rule: D a multiple of 8, 8 <= D <= 128; Hq a multiple
  * of Hkv; B, Hq <= 65535; B * Hq * Nq, B * Hkv * Nk < 2^30.  Pointers and strides are
  * multiples of 16 bytes (TOK_ERR_ALIGN).  Outputs may interleave with inputs and each
  * other (slices of one buffer) but share no element (TOK_ERR_ALIAS).

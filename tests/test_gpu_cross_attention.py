@@ -216,6 +216,21 @@ def test_slices_of_fused_tensors(Nq, D):
     assert bool((gq[:, :, 1:] == 5.0).all())
 
 
+@pytest.mark.parametrize("Nq", [1, 300])
+def test_head_major_and_batch_inner_layouts(Nq):
+    """[B, H, N, D] and [N, B, H, D] memory: the same results as dense tensors."""
+    B, Nk, Hq, Hkv, D = 2, 333, 4, 2, 64
+    q, k, v, go = (randn(B, n, h, D, seed=s) for n, h, s in ((Nq, Hq, 1), (Nk, Hkv, 2), (Nk, Hkv, 3), (Nq, Hq, 4)))
+    o, lse = hwp.cross_attention(q, k, v, with_lse=True)
+    grads = hwp.cross_attention_backward(q, k, v, o, lse, go)
+    for perm, back in (((0, 2, 1, 3), (0, 2, 1, 3)), ((1, 0, 2, 3), (1, 0, 2, 3)), ((2, 1, 0, 3), (2, 1, 0, 3))):
+        t = [x.permute(perm).contiguous().permute(back) for x in (q, k, v, o, go)]
+        o2, lse2 = hwp.cross_attention(*t[:3], with_lse=True)
+        assert torch.equal(o2, o) and torch.equal(lse2, lse)
+        for a, b in zip(hwp.cross_attention_backward(*t[:4], lse, t[4]), grads):
+            assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("Nq", [1, 200])
 def test_broadcast_encoder_state(Nq):
     """One encoder state for the whole batch (stride 0), one key head shared by expansion."""

@@ -132,7 +132,8 @@ def attend(lib, q=Q, k=K, v=V, o=O, lse=LSE, lens=0, B=3, Nq=10, Nk=20, Hq=4, Hk
 def test_cross_attention_rules(lib):
     for kw in (dict(D=4), dict(D=12), dict(D=136), dict(D=0), dict(Hq=3), dict(Hkv=0), dict(B=-1), dict(Nq=-1), dict(Nk=-1),
                dict(Nq=1 << 30), dict(B=65536), dict(Hq=1 << 17), dict(so=(0, 256, 64)), dict(so=(2560, 256, 32)),
-               dict(sk=(2560, -128, 64)), dict(sq=(1 << 40, 256, 64)), dict(B=1, Nq=1, Nk=100000, wb=16)):
+               dict(sk=(2560, -128, 64)), dict(sq=(1 << 40, 256, 64)), dict(B=1, Nq=1, Nk=100000, wb=16), dict(sq=(2560, 0, 64)),
+               dict(sq=(2560, 256, 0)), dict(sk=(2560, 0, 64))):
         assert attend(lib, **kw) == hwp.TOK_ERR_SHAPE, kw
     for kw in (dict(q=0), dict(k=0), dict(v=0), dict(o=0), dict(B=1, Nq=1, Nk=100000, ws=0)):
         assert attend(lib, **kw) == hwp.TOK_ERR_NULL, kw
