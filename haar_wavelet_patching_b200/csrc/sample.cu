@@ -581,16 +581,16 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs g,
     // degree 4 (|f ln 2 / 64| <= 0.0055: what is left out is below 2^-44 relative).
     const double per_t = 64.0 / 0.6931471805599453 / (double)T1, xmax_d = infinite ? 0.0 : (double)xmax;
     const float xcut = infinite ? INFINITY : fmaxf(xmax - reach, kLowest); // no weight below
-    auto weight_d = [&](float x) -> double { // x >= xcut
+    auto weight_at = [&](double d) -> double { // of d = x - xmax
         constexpr double kMagic = 6755399441055744.0; // 1.5 2^52: a sum's low bits are its integer part
         constexpr double c1 = 0.6931471805599453 / 64, c2 = c1 * c1 / 2, c3 = c2 * c1 / 3, c4 = c3 * c1 / 4;
-        const double d = infinite ? 0.0 : (double)x - xmax_d, kd = fma(d, per_t, kMagic),
-                     f = fma(d, per_t, kMagic - kd);
+        const double kd = fma(d, per_t, kMagic), f = fma(d, per_t, kMagic - kd);
         const int k = __double2loint(kd);
         const double q = fma(fma(fma(c4, f, c3), f, c2), f, c1) * f, t = sh.table[k & 63];
         const double w = fma(t, q, t);
         return __hiloint2double(__double2hiint(w) + ((k >> 6) << 20), __double2loint(w));
     };
+    auto weight_d = [&](float x) { return weight_at(infinite ? 0.0 : (double)x - xmax_d); }; // x >= xcut
     auto to_fixed = [](double w) -> uint64_t { // nearest integer of 0 <= w < 2^51
         return (uint64_t)__double_as_longlong(w + 4503599627370496.0) & 0xFFFFFFFFFFFFFull;
     };
@@ -727,7 +727,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs g,
         // Sums of the bits of 2^52 + w: the number of terms times the bits of 2^52 is taken off at the end.
         // A token without a weight (-inf, NaN or below xcut) counts as one at xcut, which rounds to 0.
         constexpr uint64_t kBias = 0x4330000000000000ull;
-        uint64_t sum_all = 0, sum_above = 0, n_all = 0, n_above = 0, n_mine = 0;
+        uint64_t sum_all = 0, sum_above = 0;
+        uint32_t n_all = 0, n_above = 0, n_mine = 0;
         auto pick = [&](float x, int idx) {
             const uint32_t to = atomicAdd(&sh.pub[2], 1u);
             if (to < (uint32_t)kCap) {
@@ -737,13 +738,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs g,
         };
         auto weigh = [&](float x0) -> bool { // whether the token is one of the bin's
             const float x = fmaxf(x0, xcut);
-            const double wd = weight_d(x);
+            const double wd = weight_at((double)x - xmax_d);
             const uint64_t bits = (uint64_t)__double_as_longlong(wd + 4503599627370496.0);
             sum_all += bits;
-            ++n_all;
             const bool in = x >= above;
-            sum_above += in ? bits : 0ull;
-            n_above += in;
+            if (in) {
+                sum_above += bits;
+                ++n_above;
+            }
             if (floor_w > 0.0) {
                 mine += in && wd >= floor_w ? bits : 0ull;
                 n_mine += in && wd >= floor_w;
@@ -756,6 +758,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs g,
                 float x[N];
                 Vec<T>::split(v, x);
                 uint32_t m = 0;
+                n_all += N;
 #pragma unroll
                 for (int k = 0; k < N; ++k)
                     m |= (uint32_t)weigh(x[k]) << k;
@@ -765,6 +768,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs g,
                 }
             },
             [&](float x, int idx) {
+                ++n_all;
                 if (weigh(x))
                     pick(x, idx);
             });
