@@ -581,6 +581,23 @@ def tok_fsq_decode_backward(idx, w, grad_out, grad_codes, grad_w, workspace, str
 
 
 # ---------------------------------------------------------------------------
+# Calls of the token-model operators: on the tensors' device, whichever is current.
+# ---------------------------------------------------------------------------
+def _call(name, device, stream, *args):
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        s = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = getattr(_lib or lib(), name)(*args, s)
+    else:
+        with torch.cuda.device(device):
+            status = getattr(_lib or lib(), name)(*args, s)
+    if status != TOK_OK:
+        raise TokError(status, name)
+
+
+# ---------------------------------------------------------------------------
 # Rotary positions of the axes (time, height, width).
 # ---------------------------------------------------------------------------
 def _triple(v):
@@ -596,21 +613,19 @@ def rope_table(sizes, dims, base=10000.0, scale=1.0, device="cuda", stream=None)
     if torch.device(device).type != "cuda":
         raise ValueError("the table must be on a CUDA device (there is no CPU path)")
     table = _new(nt * dt + nh * dh + nw * dw, torch.float32, device, stream)
-    with torch.cuda.device(table.device):
-        _check(lib().tok_rope_table(_ptr(table), nt, nh, nw, dt, dh, dw, *_triple(base), *_triple(scale),
-                                    _stream(table, stream)), "tok_rope_table")
+    _call("tok_rope_table", table.device, stream, table.data_ptr(), nt, nh, nw, dt, dh, dw, *_triple(base),
+          *_triple(scale))
     return table
 
 
 def _rope_check(x, y, table, sizes, dims):
-    if not (x.is_cuda and y.is_cuda and table.is_cuda):
-        raise ValueError("x, y and table must be CUDA tensors (there is no CPU path)")
-    if x.device != y.device or x.device != table.device:
-        raise ValueError("x, y and table must be on one device")
+    dev = x.device
+    if dev.type != "cuda" or y.device != dev or table.device != dev:
+        raise ValueError("x, y and table must be CUDA tensors on one device (there is no CPU path)")
     if x.shape != y.shape or x.dtype != y.dtype:
         raise ValueError("x and y must have the same shape and dtype")
-    (nt, nh, nw), (dt, dh, dw) = sizes, dims
-    if table.dtype != torch.float32 or not table.is_contiguous() or table.numel() != nt * dt + nh * dh + nw * dw:
+    if table.dtype != torch.float32 or table.numel() != sizes[0] * dims[0] + sizes[1] * dims[1] + sizes[2] * dims[2] \
+            or not table.is_contiguous():
         raise ValueError("table must be the float32 rope_table of these sizes and dims")
     if x.shape[-1] > 1 and (x.stride(-1) != 1 or y.stride(-1) != 1):
         raise ValueError("the channels of x and y must be dense")
@@ -618,6 +633,8 @@ def _rope_check(x, y, table, sizes, dims):
 
 def _token_stride(t: torch.Tensor, name: str) -> int:
     """The one stride of the leading dimensions of [..., heads, D] taken as one index."""
+    if t.is_contiguous():
+        return t.shape[-1] * t.shape[-2]
     stride = None
     for n, s in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
         if n != 1:
@@ -634,10 +651,9 @@ def _rope_grid(name, x, y, table, sizes, dims, origin, interleaved, stream):
     if x.dim() != 6:
         raise ValueError("the tensors must be [B, T, h, w, heads, D]")
     B, T, h, w, H, D = x.shape
-    with torch.cuda.device(x.device):
-        _check(getattr(lib(), name)(x.data_ptr(), y.data_ptr(), table.data_ptr(), _dtype_code(x), B, T, h, w, H, D,
-                                    _token_stride(x, "x"), x.stride(4), _token_stride(y, "y"), y.stride(4), *origin,
-                                    *sizes, *dims, bool(interleaved), _stream(x, stream)), name)
+    _call(name, x.device, stream, x.data_ptr(), y.data_ptr(), table.data_ptr(), _dtype_code(x), B, T, h, w, H, D,
+          _token_stride(x, "x"), x.stride(4), _token_stride(y, "y"), y.stride(4), *origin, *sizes, *dims,
+          bool(interleaved))
     return y
 
 
@@ -656,21 +672,18 @@ def _rope_positions(name, x, y, pos, table, sizes, dims, interleaved, bad_count,
     _rope_check(x, y, table, sizes, dims)
     if x.dim() < 3:
         raise ValueError("the tensors must be [..., heads, D]")
-    if not pos.is_cuda or pos.device != x.device or pos.dtype != torch.int32 or not pos.is_contiguous() \
+    if pos.device != x.device or pos.dtype != torch.int32 or not pos.is_contiguous() \
             or pos.shape != x.shape[:-2] + (3,):
         raise ValueError("pos must be a contiguous int32 CUDA tensor [..., 3] of (t, h, w)")
-    if bad_count is not None and (not bad_count.is_cuda or bad_count.device != x.device
-                                  or bad_count.dtype != torch.int32 or bad_count.numel() < 1):
+    if bad_count is not None and (bad_count.device != x.device or bad_count.dtype != torch.int32 or bad_count.numel() < 1):
         raise ValueError("bad_count must be an int32 CUDA tensor")
     H, D = x.shape[-2:]
     N = 1
     for n in x.shape[:-2]:
         N *= n
-    with torch.cuda.device(x.device):
-        _check(getattr(lib(), name)(x.data_ptr(), y.data_ptr(), pos.data_ptr(), table.data_ptr(),
-                                    None if bad_count is None else bad_count.data_ptr(), _dtype_code(x), N, H, D,
-                                    _token_stride(x, "x"), x.stride(-2), _token_stride(y, "y"), y.stride(-2), *sizes,
-                                    *dims, bool(interleaved), _stream(x, stream)), name)
+    _call(name, x.device, stream, x.data_ptr(), y.data_ptr(), pos.data_ptr(), table.data_ptr(),
+          None if bad_count is None else bad_count.data_ptr(), _dtype_code(x), N, H, D, _token_stride(x, "x"),
+          x.stride(-2), _token_stride(y, "y"), y.stride(-2), *sizes, *dims, bool(interleaved))
     return y
 
 
@@ -689,12 +702,11 @@ def tok_rope_positions_adjoint(gy, gx, pos, table, sizes, dims, interleaved=Fals
 # ---------------------------------------------------------------------------
 # Drawing codes from logits.
 # ---------------------------------------------------------------------------
-def _setting(v, name, dtype, logits):
+def _setting(v, name, dtype, rows, device):
     """A sampling setting: (device pointer or None, value for every row)."""
     if not isinstance(v, torch.Tensor):
         return None, v
-    if not v.is_cuda or v.device != logits.device or v.dtype != dtype or v.numel() != logits.numel() // logits.shape[-1] \
-            or not v.is_contiguous():
+    if v.device != device or v.dtype != dtype or v.numel() != rows or not v.is_contiguous():
         raise ValueError(f"{name} must be a number or a contiguous {dtype} CUDA tensor with one value per row")
     return v.data_ptr(), 0
 
@@ -704,27 +716,26 @@ def tok_sample_codes(logits, u, idx, logprob=None, temperature=1.0, top_k=0, top
     (-1 for a row of -inf) and, if given, logprob [...] fp32 under the filtered distribution.  The settings
     are numbers or tensors with one value per row (float32; top_k int32).  Filters: top_k largest, then the
     top_p nucleus, then weight >= min_p of the largest; ties to the lower index; temperature 0 is greedy."""
-    if not logits.is_cuda:
+    dev = logits.device
+    if dev.type != "cuda":
         raise ValueError("logits must be a CUDA tensor (there is no CPU path)")
     if logits.dim() < 1 or logits.shape[-1] < 1:
         raise ValueError("logits must be [..., V] with V >= 1")
-    V = logits.shape[-1]
+    lead, V = logits.shape[:-1], logits.shape[-1]
     if V > 1 and logits.stride(-1) != 1:
         raise ValueError("the last dimension of logits must be dense")
     for t, name, dtype in ((u, "u", torch.float32), (idx, "idx", torch.int32), (logprob, "logprob", torch.float32)):
-        if t is not None and (not t.is_cuda or t.device != logits.device or t.dtype != dtype
-                              or t.shape != logits.shape[:-1] or not t.is_contiguous()):
+        if t is not None and (t.device != dev or t.dtype != dtype or t.shape != lead or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor with one value per row")
-    tp, ta = _setting(temperature, "temperature", torch.float32, logits)
-    kp, ka = _setting(top_k, "top_k", torch.int32, logits)
-    pp, pa = _setting(top_p, "top_p", torch.float32, logits)
-    mp, ma = _setting(min_p, "min_p", torch.float32, logits)
-    stride = _token_stride(logits.unsqueeze(-2), "logits")
-    with torch.cuda.device(logits.device):
-        _check(lib().tok_sample_codes(logits.data_ptr(), _dtype_code(logits), u.numel(), V, stride, u.data_ptr(), tp,
-                                      ta, kp, max(-1, min(ka, 2 ** 31 - 1)), pp, pa, mp, ma, idx.data_ptr(),
-                                      None if logprob is None else logprob.data_ptr(), _stream(logits, stream)),
-               "tok_sample_codes")
+    R = u.numel()
+    tp, ta = _setting(temperature, "temperature", torch.float32, R, dev)
+    kp, ka = _setting(top_k, "top_k", torch.int32, R, dev)
+    pp, pa = _setting(top_p, "top_p", torch.float32, R, dev)
+    mp, ma = _setting(min_p, "min_p", torch.float32, R, dev)
+    stride = V if logits.is_contiguous() else _token_stride(logits.unsqueeze(-2), "logits")
+    _call("tok_sample_codes", dev, stream, logits.data_ptr(), _dtype_code(logits), R, V, stride, u.data_ptr(), tp, ta,
+          kp, max(-1, min(ka, 2 ** 31 - 1)), pp, pa, mp, ma, idx.data_ptr(),
+          None if logprob is None else logprob.data_ptr())
     return idx, logprob
 
 
@@ -732,8 +743,8 @@ def tok_sample_codes(logits, u, idx, logprob=None, temperature=1.0, top_k=0, top
 # Cross attention.
 # ---------------------------------------------------------------------------
 def _heads(t: torch.Tensor) -> _Heads:
-    s = t.stride()
-    return _Heads(t.data_ptr(), s[0], s[1], s[2])
+    b, n, h, _ = t.stride()
+    return _Heads(t.data_ptr(), b, n, h)
 
 
 def _attn_dims(q, k, v, k_lens, others):
@@ -744,16 +755,16 @@ def _attn_dims(q, k, v, k_lens, others):
     B, Nq, Hq, D = q.shape
     Nk, Hkv = k.shape[1], k.shape[2]
     sq, sk = q.shape, torch.Size((B, Nk, Hkv, D))
+    if dev.type != "cuda":
+        raise ValueError("q must be a CUDA tensor (there is no CPU path)")
     for t, name, like_q in ((q, "q", True), (k, "k", False), (v, "v", False), *others):
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
         if t.dtype != torch.bfloat16 or t.device != dev:
-            raise ValueError(f"{name} must be bfloat16, on the device of q")
+            raise ValueError(f"{name} must be a bfloat16 CUDA tensor on the device of q")
         if t.shape != (sq if like_q else sk):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(sq if like_q else sk)}")
         if t.stride(3) != 1:
             raise ValueError(f"the channels of {name} must be dense")
-    if k_lens is not None and (not k_lens.is_cuda or k_lens.device != dev or k_lens.dtype != torch.int32
+    if k_lens is not None and (k_lens.device != dev or k_lens.dtype != torch.int32
                                or k_lens.shape != (B,) or not k_lens.is_contiguous()):
         raise ValueError("k_lens must be a contiguous int32 CUDA tensor [B]")
     return B, Nq, Nk, Hq, Hkv, D
@@ -761,8 +772,7 @@ def _attn_dims(q, k, v, k_lens, others):
 
 def _stats(t, name, dims, device):
     B, Nq, _, Hq, _, _ = dims
-    if t is not None and (not t.is_cuda or t.device != device or t.dtype != torch.float32
-                          or t.shape != (B, Hq, Nq) or not t.is_contiguous()):
+    if t is not None and (t.device != device or t.dtype != torch.float32 or t.shape != (B, Hq, Nq) or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous float32 CUDA tensor [B, Hq, Nq]")
 
 
@@ -796,14 +806,10 @@ def tok_cross_attention(q, k, v, o, lse=None, k_lens=None, scale=None, workspace
     default; workspace: cross_attention_workspace_size bytes, allocated if None."""
     dims = _attn_dims(q, k, v, k_lens, ((o, "o", True),))
     _stats(lse, "lse", dims, q.device)
-    L = lib()
-    ws = _attn_workspace(L.tok_cross_attention_workspace_size, dims, workspace, q.device, stream)
-    with torch.cuda.device(q.device):
-        _check(L.tok_cross_attention(_heads(q), _heads(k), _heads(v), _heads(o),
-                                     None if lse is None else lse.data_ptr(),
-                                     None if k_lens is None else k_lens.data_ptr(), *dims,
-                                     dims[5] ** -0.5 if scale is None else scale, *_bytes(ws), _stream(q, stream)),
-               "tok_cross_attention")
+    ws = _attn_workspace(lib().tok_cross_attention_workspace_size, dims, workspace, q.device, stream)
+    _call("tok_cross_attention", q.device, stream, _heads(q), _heads(k), _heads(v), _heads(o),
+          None if lse is None else lse.data_ptr(), None if k_lens is None else k_lens.data_ptr(), *dims,
+          dims[5] ** -0.5 if scale is None else scale, *_bytes(ws))
     return o
 
 
@@ -813,14 +819,10 @@ def tok_cross_attention_backward(q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v
     dims = _attn_dims(q, k, v, k_lens, ((o, "o", True), (grad_o, "grad_o", True), (grad_q, "grad_q", True),
                                         (grad_k, "grad_k", False), (grad_v, "grad_v", False)))
     _stats(lse, "lse", dims, q.device)
-    L = lib()
-    ws = _attn_workspace(L.tok_cross_attention_backward_workspace_size, dims, workspace, q.device, stream)
-    with torch.cuda.device(q.device):
-        _check(L.tok_cross_attention_backward(_heads(q), _heads(k), _heads(v), _heads(o), lse.data_ptr(),
-                                              _heads(grad_o), None if k_lens is None else k_lens.data_ptr(),
-                                              _heads(grad_q), _heads(grad_k), _heads(grad_v), *dims,
-                                              dims[5] ** -0.5 if scale is None else scale, *_bytes(ws),
-                                              _stream(q, stream)), "tok_cross_attention_backward")
+    ws = _attn_workspace(lib().tok_cross_attention_backward_workspace_size, dims, workspace, q.device, stream)
+    _call("tok_cross_attention_backward", q.device, stream, _heads(q), _heads(k), _heads(v), _heads(o), lse.data_ptr(),
+          _heads(grad_o), None if k_lens is None else k_lens.data_ptr(), _heads(grad_q), _heads(grad_k), _heads(grad_v),
+          *dims, dims[5] ** -0.5 if scale is None else scale, *_bytes(ws))
     return grad_q, grad_k, grad_v
 
 
