@@ -4,11 +4,13 @@
 // with more run on the 5th-generation tensor cores, attention_tc.cu and attention_bwd_tc.cu).
 //
 // attn_rows_kernel: with few query rows the call is bound by reading the keys and values, so
-// it runs on warp-level m16n8k16 tiles whose fragments come straight from global memory as
-// 16-byte loads (attention.cuh), without staging.  16 query rows of one key head (queries x the heads of its
-// group) per CTA; its 4 warps take 16 keys each in turn with a running maximum and sum of
-// their own, joined through shared memory.  The keys are split over `splits` CTAs; with
-// more than one, attn_join_kernel adds up their partial results in split order.
+// it runs on warp-level m16n8k16 tiles.  16 query rows of one key head (queries x the heads of
+// its group) per CTA; its 4 warps take 16 keys each in turn with a running maximum and sum of
+// their own, joined through shared memory at the end.  Each warp keeps a ring of its own in
+// shared memory, kStages - 1 steps of keys and values on their way (cp.async): two CTAs of 96 KB
+// in flight per SM cover HBM's latency.  The keys are split over `splits` CTAs; with more than one,
+// attn_join_kernel (launched early, it waits for the grid before it) adds up their partial
+// results in split order.
 #include <algorithm>
 #include <initializer_list>
 
@@ -30,13 +32,36 @@ __device__ __forceinline__ void split_range(int len, int splits, int s, int &beg
     end = min(len, begin + per * unit);
 }
 
-// NP = ceil(D / 64).
+// 16 bytes global -> shared, zeros where !ok.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src, bool ok)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// NP = ceil(D / 64).  Rows of the ring are padded by 16 bytes (value fragments then meet no bank
+// conflict, key fragments two-way ones).
+template <int NP> struct Ring {
+    static constexpr int stages = NP == 2 ? 3 : 4;
+    static constexpr int row = NP * 128 + 16, tile = kKeyStep * row; // bytes
+    static constexpr int stage = 2 * tile, warp = stages * stage;
+    static constexpr int join = kFwdWarps * kRows * NP * 64 * 4; // the warps' results, over the rings
+    static constexpr int bytes = kFwdWarps * warp > join ? kFwdWarps * warp : join;
+};
+
+__device__ __forceinline__ uint4 shared16(const unsigned char *p) { return *reinterpret_cast<const uint4 *>(p); }
+
 template <int NP>
-__global__ void __launch_bounds__(kFwdWarps * 32) attn_rows_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(kFwdWarps * 32, 2) attn_rows_kernel(const AttnArgs a)
 {
     constexpr int NC = 2 * NP;
+    using R = Ring<NP>;
+    extern __shared__ __align__(16) unsigned char ring_raw[];
     __shared__ float sm[kFwdWarps][kRows], sl[kFwdWarps][kRows];
-    __shared__ float so[kFwdWarps][kRows][NP * 64];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const int tiles = (a.Nq * a.G + kRows - 1) / kRows;
     const int split = blockIdx.x % a.splits, tile = (int)(blockIdx.x / a.splits) % tiles;
@@ -44,7 +69,33 @@ __global__ void __launch_bounds__(kFwdWarps * 32) attn_rows_kernel(const AttnArg
     const int rows = a.Nq * a.G, r0 = tile * kRows;
     int k0, k1;
     split_range(key_count(a, b), a.splits, split, k0, k1);
+    asm volatile("griddepcontrol.launch_dependents;");
 
+    unsigned char *ring = ring_raw + warp * R::warp;
+    const uint32_t ring_s = smem_addr(ring);
+    // One step: 16 keys and values, 16 bytes per lane and copy, whole rows together.
+    const __nv_bfloat16 *kbase = a.k.row(b, 0, hk), *vbase = a.v.row(b, 0, hk);
+    constexpr int kChunks = NP * 8, kCopies = kKeyStep * kChunks / 32; // per tile and lane
+    auto fetch = [&](int kk, int stage) {
+        const uint32_t dst = ring_s + stage * R::stage;
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int e = i * 32 + lane, r = e / kChunks, ch = e % kChunks;
+            const bool ok = kk + r < k1 && ch * 8 < a.D;
+            const int64_t key = ok ? kk + r : k0;
+            const int d = ok ? ch * 8 : 0;
+            copy16_async(dst + r * R::row + ch * 16, kbase + key * a.k.n + d, ok);
+            copy16_async(dst + R::tile + r * R::row + ch * 16, vbase + key * a.v.n + d, ok);
+        }
+    };
+    constexpr int kRound = kFwdWarps * kKeyStep;
+    const int first = k0 + warp * kKeyStep, steps = first < k1 ? (k1 - first + kRound - 1) / kRound : 0;
+#pragma unroll
+    for (int s = 0; s < R::stages - 1; ++s) {
+        if (s < steps)
+            fetch(first + s * kRound, s);
+        copies_commit();
+    }
     uint4 qlo[NC], qhi[NC];
     {
         const int lo = r0 + g, hi = lo + 8;
@@ -53,25 +104,23 @@ __global__ void __launch_bounds__(kFwdWarps * 32) attn_rows_kernel(const AttnArg
     }
     float acc[NP][8][4] = {};
     float mlo = -INFINITY, mhi = -INFINITY, llo = 0.0f, lhi = 0.0f;
-    for (int kk = k0 + warp * kKeyStep; kk < k1; kk += kFwdWarps * kKeyStep) {
-        uint4 kf[2][NC];
-        RowFrag vf[NP];
+    for (int step = 0; step < steps; ++step) {
+        const int kk = first + step * kRound;
+        copies_wait<R::stages - 2>(); // this lane's copies of the step
+        __syncwarp();                 // every lane's; and every lane is done with the stage refilled next
+        if (step + R::stages - 1 < steps)
+            fetch(kk + (R::stages - 1) * kRound, (step + R::stages - 1) % R::stages);
+        copies_commit();
+        const unsigned char *kt = ring + step % R::stages * R::stage, *vt = kt + R::tile;
+        float s[2][4] = {};
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const int key = kk + 8 * t + g;
-            load_chan<NC>(kf[t], a.k.row(b, key, hk), key < k1, 8 * c, a.D);
-        }
+            uint4 kf[NC];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int key = kk + 2 * c + (i & 1) + 8 * (i >> 1);
-            const __nv_bfloat16 *row = a.v.row(b, key, hk);
-#pragma unroll
-            for (int p = 0; p < NP; ++p)
-                vf[p].r[i] = load16(row + 64 * p + 8 * g, key < k1 && 64 * p + 8 * g < a.D);
+            for (int i = 0; i < NC; ++i)
+                kf[i] = shared16(kt + (8 * t + g) * R::row + 64 * i + 16 * c);
+            mma_chan<NC>(s[t], qlo, qhi, kf);
         }
-        float s[2][4] = {};
-        mma_chan<NC>(s[0], qlo, qhi, kf[0]);
-        mma_chan<NC>(s[1], qlo, qhi, kf[1]);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -111,9 +160,17 @@ __global__ void __launch_bounds__(kFwdWarps * 32) attn_rows_kernel(const AttnArg
         const uint32_t pa[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
                                 pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])};
 #pragma unroll
-        for (int p = 0; p < NP; ++p)
-            mma_rows(acc[p], pa, vf[p]);
+        for (int p = 0; p < NP; ++p) {
+            RowFrag vf;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                vf.r[i] = shared16(vt + (2 * c + (i & 1) + 8 * (i >> 1)) * R::row + 128 * p + 16 * g);
+            mma_rows(acc[p], pa, vf);
+        }
     }
+    copies_wait<0>();
+    __syncthreads(); // every warp is done with its ring: the results go over them
+    float(*so)[kRows][NP * 64] = reinterpret_cast<float(*)[kRows][NP * 64]>(ring_raw);
     llo = quad_sum(llo);
     lhi = quad_sum(lhi);
     if (c == 0) {
@@ -180,31 +237,41 @@ __global__ void __launch_bounds__(kFwdWarps * 32) attn_rows_kernel(const AttnArg
 }
 
 // One warp per query row and head: the splits' partial results in split order.
+constexpr int kMaxSplits = 32; // a lane each
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory"); // the grid before has written its parts
     const int64_t nstat = (int64_t)a.B * a.Hq * a.Nq;
     const int64_t stat = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (stat >= nstat)
         return;
     const float *ml = a.part + a.splits * nstat * a.D;
-    float m = -INFINITY, l = 0.0f;
-    for (int s = 0; s < a.splits; ++s)
-        m = fmaxf(m, ml[2 * (s * nstat + stat)]);
-    float v[4] = {};
+    float ms = -INFINITY, ls = 0.0f;
+    if (lane < a.splits) {
+        const float2 x = *reinterpret_cast<const float2 *>(ml + 2 * (lane * nstat + stat));
+        ms = x.x;
+        ls = x.y;
+    }
+    float m = ms;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    const float f = ms == -INFINITY ? 0.0f : exp2_fast(ms - m);
+    float l = f * ls, v[4] = {};
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        l += __shfl_xor_sync(~0u, l, o);
     const int d = 4 * lane;
+#pragma unroll 8
     for (int s = 0; s < a.splits; ++s) {
-        const float ms = ml[2 * (s * nstat + stat)];
-        if (ms == -INFINITY)
-            continue;
-        const float f = exp2_fast(ms - m);
-        l += f * ml[2 * (s * nstat + stat) + 1];
-        if (d < a.D) {
+        const float fs = __shfl_sync(~0u, f, s);
+        if (d < a.D && fs != 0.0f) { // (a split without keys has written nothing)
             float x[4];
             Row<float, 4, true>::load(a.part + (s * nstat + stat) * a.D + d, x);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                v[j] += f * x[j];
+                v[j] += fs * x[j];
         }
     }
     const int iq = (int)(stat % a.Nq), bh = (int)(stat / a.Nq), b = bh / a.Hq, h = bh - b * a.Hq;
@@ -217,6 +284,39 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a)
     }
     if (lane == 0 && a.lse)
         a.lse[stat] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int NP> tok_status launch_rows(const AttnArgs &a, int64_t blocks, cudaStream_t stream)
+{
+    const cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Ring<NP>::bytes);
+    if (e != cudaSuccess) {
+        record_cuda_error(e);
+        return TOK_ERR_CUDA;
+    }
+    attn_rows_kernel<NP><<<(unsigned)blocks, kFwdWarps * 32, Ring<NP>::bytes, stream>>>(a);
+    return launch_status();
+}
+
+// The join's CTAs may start while the grid before still runs; they wait for its end.
+tok_status launch_join(const AttnArgs &a, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.B * a.Hq * a.Nq + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_join_kernel, a);
+    if (e != cudaSuccess) {
+        record_cuda_error(e);
+        cudaGetLastError();
+        return TOK_ERR_CUDA;
+    }
+    return launch_status();
 }
 
 // ---------------------------------------------------------------------------
@@ -319,14 +419,14 @@ int64_t fwd_splits(const Dims &d)
         const int64_t gp = attn_tc_group((int)G), items = d.B * (d.Hq / gp) * ((d.Nq * gp + 255) / 256);
         if (items == 0)
             return 1;
-        return std::max<int64_t>(1, std::min(148 / items, d.Nk / 512));
+        return std::max<int64_t>(1, std::min(std::min(148 / items, d.Nk / 512), (int64_t)kMaxSplits));
     }
     // Four CTAs per SM, each with at least four rounds of its warps.
     const int64_t tiles = (d.Nq * G + kRows - 1) / kRows, units = d.B * d.Hkv * tiles;
     if (units == 0)
         return 1;
     const int64_t want = (148 * 4 + units - 1) / units, most = d.Nk / (4 * kFwdWarps * kKeyStep);
-    return std::max<int64_t>(1, std::min(std::min(want, most), (int64_t)64));
+    return std::max<int64_t>(1, std::min(std::min(want, most), (int64_t)kMaxSplits));
 }
 
 } // namespace
@@ -405,20 +505,11 @@ extern "C" tok_status tok_cross_attention(const tok_heads *q, const tok_heads *k
     a.scale = scale;
     a.scale2 = (float)((double)scale * 1.4426950408889634);
     const int64_t blocks = B * Hkv * ((Nq * a.G + kRows - 1) / kRows) * splits;
-    tok_status st;
-    if (wants_tc(dim)) {
-        st = attn_tc_forward(a, stream);
-    } else if (D <= 64) {
-        attn_rows_kernel<1><<<(unsigned)blocks, kFwdWarps * 32, 0, stream>>>(a);
-        st = launch_status();
-    } else {
-        attn_rows_kernel<2><<<(unsigned)blocks, kFwdWarps * 32, 0, stream>>>(a);
-        st = launch_status();
-    }
-    if (st == TOK_OK && splits > 1) {
-        attn_join_kernel<<<(unsigned)((B * Hq * Nq + 3) / 4), 128, 0, stream>>>(a);
-        st = launch_status();
-    }
+    tok_status st = wants_tc(dim) ? attn_tc_forward(a, stream)
+                    : D <= 64     ? launch_rows<1>(a, blocks, stream)
+                                  : launch_rows<2>(a, blocks, stream);
+    if (st == TOK_OK && splits > 1)
+        st = launch_join(a, stream);
     return st;
 }
 
