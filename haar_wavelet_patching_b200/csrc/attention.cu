@@ -421,11 +421,13 @@ int64_t fwd_splits(const Dims &d)
             return 1;
         return std::max<int64_t>(1, std::min(std::min(148 / items, d.Nk / 512), (int64_t)kMaxSplits));
     }
-    // Four CTAs per SM, each with at least four rounds of its warps.
+    // Two CTAs per SM, as many as are resident, each with at least four rounds of its warps (8 x 3520 keys,
+    // ragged, 8 key heads: 20.0 us; with half as many CTAs 24, twice as many 23; a cluster of 8
+    // CTAs that joins through distributed shared memory instead of the workspace: 30).
     const int64_t tiles = (d.Nq * G + kRows - 1) / kRows, units = d.B * d.Hkv * tiles;
     if (units == 0)
         return 1;
-    const int64_t want = (148 * 4 + units - 1) / units, most = d.Nk / (4 * kFwdWarps * kKeyStep);
+    const int64_t want = (148 * 2 + units - 1) / units, most = d.Nk / (4 * kFwdWarps * kKeyStep);
     return std::max<int64_t>(1, std::min(std::min(want, most), (int64_t)kMaxSplits));
 }
 
