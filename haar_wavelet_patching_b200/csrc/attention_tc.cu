@@ -34,7 +34,11 @@ constexpr float kGrow = 8.0f; // log2 of the growth of the maximum that the weig
 
 template <int DP> constexpr uint32_t tile_bytes() { return kTile * DP * 2; }
 template <int DP> constexpr int stages() { return DP == 128 ? 4 : 8; }
-template <int DP> constexpr size_t smem_bytes() { return (2 + stages<DP>()) * (size_t)tile_bytes<DP>() + 1024; }
+constexpr uint32_t kStage = kTile * 128; // output staging of a warpgroup: 128 rows x 64 channels
+template <int DP> constexpr size_t smem_bytes()
+{
+    return (2 + stages<DP>()) * (size_t)tile_bytes<DP>() + 2 * kStage + 1024;
+}
 
 struct TcArgs {
     AttnArgs a;
@@ -70,7 +74,7 @@ __device__ __forceinline__ Item decode(const TcArgs &t, int i)
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                const __grid_constant__ CUtensorMap vmap, const TcArgs t)
+                const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap, const TcArgs t)
 {
     constexpr int NST = stages<DP>(), NSUB = DP / 64;
     constexpr uint32_t TB = tile_bytes<DP>(), SUB = kTile * 128;
@@ -335,32 +339,54 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 it += 2 * w.ntiles;
             }
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            if (a.splits == 1) {
+                // 64 channels at a time through the warp's 32 rows of the staging buffer, whole lines to HBM.
+                const uint32_t stage = kvbase + NST * TB + r * kStage + (warp & 3) * 4096u;
+                unsigned char *stage_ptr = smem_raw + (stage - smem_addr(smem_raw));
 #pragma unroll
-            for (int c = 0; c < DP / 32; ++c) {
-                uint32_t o[32] = {};
-                if (w.ntiles > 0) {
+                for (int c = 0; c < NSUB; ++c) {
+                    uint32_t o[64] = {};
+                    if (w.ntiles > 0) {
+                        tmem_ld64(oc + 64 * c, o);
+                        tmem_wait_ld();
+                    }
+                    if (c == NSUB - 1)
+                        tc_fence_before();
+                    if (lane == 0)
+                        bulk_wait_read<0>(); // the store that last used the rows has read them
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = w.ntiles > 0 ? pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * inv,
+                                                              __uint_as_float(o[8 * e + 2 * k + 1]) * inv)
+                                                : 0u;
+                        *reinterpret_cast<uint4 *>(stage_ptr + sw128_offset((uint32_t)lane, 8u * e)) =
+                            make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        const int row_w = w.row0 + r * kTile + 32 * (warp & 3);
+                        // (rows of one token lie in one warp where a tile has at most 32 heads; the box is
+                        // 32 rows: min(gp, 32) heads x 32 / gp tokens)
+                        if (64 * c < a.D && row_w / t.gp < a.Nq)
+                            tma_store_4d(&omap, 64 * c, w.hs * t.gp + row_w % t.gp, row_w / t.gp, w.b, stage);
+                        bulk_commit();
+                    }
+                }
+            } else if (w.ntiles > 0) { // (a split without keys has m = -inf: its o is not read)
+#pragma unroll
+                for (int c = 0; c < DP / 32; ++c) {
+                    uint32_t o[32];
                     tmem_ld32(oc + 32 * c, o);
                     tmem_wait_ld();
-                }
-                if (!live)
-                    continue;
-                if (a.splits == 1) {
-                    __nv_bfloat16 *dst = a.o.row(w.b, iq, h) + 32 * c;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (32 * c + 8 * e < a.D) {
-                            float v[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                v[k] = w.ntiles > 0 ? __uint_as_float(o[8 * e + k]) * inv : 0.0f;
-                            Row<__nv_bfloat16, 8, true>::store(dst + 8 * e, v);
-                        }
-                    }
-                } else if (w.ntiles > 0) { // (a split without keys has m = -inf: its o is not read)
                     float *dst = a.part + (w.split * nstat + stat) * a.D + 32 * c;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (32 * c + 8 * e < a.D)
+                        if (live && 32 * c + 8 * e < a.D)
                             Row<float, 8, true>::store(dst + 8 * e, reinterpret_cast<const float *>(o) + 8 * e);
                 }
             }
@@ -376,6 +402,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 }
             }
         }
+        if (lane == 0)
+            bulk_wait_all(); // the stores have completed before the CTA exits
     }
     tc_fence_before();
     __syncthreads();
@@ -388,7 +416,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
 }
 
 template <int DP> tok_status launch(const TcArgs &t, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                                    cudaStream_t stream)
+                                    const CUtensorMap &o, cudaStream_t stream)
 {
     const cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem_bytes<DP>());
@@ -397,7 +425,7 @@ template <int DP> tok_status launch(const TcArgs &t, const CUtensorMap &q, const
         return TOK_ERR_CUDA;
     }
     const int sms = sm_count();
-    attn_fwd_kernel<DP><<<std::min(t.items, sms > 0 ? sms : 1), kThreads, smem_bytes<DP>(), stream>>>(q, k, v, t);
+    attn_fwd_kernel<DP><<<std::min(t.items, sms > 0 ? sms : 1), kThreads, smem_bytes<DP>(), stream>>>(q, k, v, o, t);
     return launch_status();
 }
 
@@ -419,11 +447,12 @@ tok_status attn_tc_forward(const AttnArgs &a, cudaStream_t stream)
     t.vb = a.B > 1 && a.v.b == 0 ? 0 : 1;
     t.kh = a.Hkv > 1 && a.k.h == 0 ? 0 : 1;
     t.vh = a.Hkv > 1 && a.v.h == 0 ? 0 : 1;
-    CUtensorMap q, k, v;
-    if (!heads_map(&q, a.q, a.B, a.Nq, a.Hq, a.D, t.gp, kTile / t.gp) ||
+    CUtensorMap q, k, v, o;
+    if (!heads_map(&o, a.o, a.B, a.Nq, a.Hq, a.D, std::min(t.gp, 32), std::max(1, 32 / t.gp)) ||
+        !heads_map(&q, a.q, a.B, a.Nq, a.Hq, a.D, t.gp, kTile / t.gp) ||
         !heads_map(&k, a.k, a.B, a.Nk, a.Hkv, a.D, 1, kTile) || !heads_map(&v, a.v, a.B, a.Nk, a.Hkv, a.D, 1, kTile))
         return TOK_ERR_SHAPE;
-    return a.D <= 64 ? launch<64>(t, q, k, v, stream) : launch<128>(t, q, k, v, stream);
+    return a.D <= 64 ? launch<64>(t, q, k, v, o, stream) : launch<128>(t, q, k, v, o, stream);
 }
 
 tok_status read_and_clear_attn_timeouts(cudaStream_t stream, unsigned int *count)
