@@ -308,6 +308,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_addr(&pfull));
+            __syncwarp(); // the arrival goes out before any lane begins to wait
             if (!wait_or_abort(smem_addr(&dpfull), i & 1u, abort)) {
                 ok = false;
                 break;
@@ -335,6 +336,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_addr(&dsfull));
+            __syncwarp(); // the arrival goes out before any lane begins to wait
         }
         ok = ok && wait_or_abort(smem_addr(&done), 0u, abort);
         if (ok) { // warps 0-3 store dv, 4-7 dk
@@ -642,6 +644,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_addr(&dsfull));
+                __syncwarp(); // the arrival goes out before any lane begins to wait
             }
             if (!ok)
                 break;

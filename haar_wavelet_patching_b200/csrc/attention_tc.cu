@@ -252,29 +252,36 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 for (int c = 0; c < 4; ++c)
                     tmem_ld32(sc + 32 * c, reinterpret_cast<uint32_t(&)[32]>(s[32 * c]));
                 tmem_wait_ld();
-                if (odd_scale) {
+                if (__builtin_expect(odd_scale, 0)) { // (the seldom taken blocks out of the loop's code)
 #pragma unroll
                     for (int c = 0; c < kTile; ++c)
                         s[c] *= a.scale2;
                 }
                 const int valid = w.kend - (w.k0 + j * kTile);
-                if (valid < kTile) {
+                if (__builtin_expect(valid < kTile, 0)) {
 #pragma unroll
                     for (int c = 0; c < kTile; ++c)
                         s[c] = c < valid ? s[c] : -INFINITY;
                 }
-                float mx[4] = {s[0], s[1], s[2], s[3]};
+                float mx[8];
 #pragma unroll
-                for (int c = 4; c < kTile; c += 4)
+                for (int e = 0; e < 8; ++e)
+                    mx[e] = s[e];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx[e] = fmaxf(mx[e], s[c + e]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+                for (int c = 8; c < kTile - 8; c += 16) // (two new values to a three-operand maximum)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        mx[e] = fmaxf(fmaxf(mx[e], s[c + e]), s[c + 8 + e]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    mx[e] = fmaxf(mx[e], s[kTile - 8 + e]);
+                const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                        fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * mul;
                 if (j == 0)
                     m = top == -INFINITY ? 0.0f : top;
                 else {
                     const bool grow = top > m + kGrow;
-                    if (__any_sync(~0u, grow)) {
+                    if (__builtin_expect(__any_sync(~0u, grow), 0)) {
                         const float f = grow ? exp2_fast(m - top) : 1.0f;
                         m = grow ? top : m;
                         l *= f;
@@ -307,7 +314,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 }
                 sum[0] = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
                 l += sum[0].x + sum[0].y;
-                if (r == 0 && valid < kTile && w.kend < a.Nk) { // v rows behind the length
+                if (__builtin_expect(r == 0 && valid < kTile && w.kend < a.Nk, 0)) { // v rows behind the length
                     const uint32_t pos = it + 2 * j + 1, vs = pos % NST;
                     if (!wait_or_abort(smem_addr(&kvfull[vs]), (pos / NST) & 1u, abort)) {
                         ok = false;
@@ -326,6 +333,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_addr(&pfull[r]));
+                __syncwarp(); // the arrival goes out before any lane begins to wait
             }
             if (!ok)
                 break;
