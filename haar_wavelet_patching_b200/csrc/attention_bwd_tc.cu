@@ -53,38 +53,47 @@ struct BwdArgs {
     int qb, gb, kb, kh, vb, vh;
 };
 
-// lse2 and delta of every query row, in tile order: 8 lanes per row.
+// lse2 and delta of every query row, in tile order: 8 lanes per row, kStatRows rows in flight per lane.
+constexpr int kStatRows = 4;
 __global__ void __launch_bounds__(256) attn_stats_kernel(const BwdArgs t, float *lse2, float *delta)
 {
     const AttnArgs &a = t.a;
-    const int64_t at = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
     const int c = threadIdx.x & 7;
-    const int64_t sets = (int64_t)a.B * t.hsets;
-    if (at >= sets * t.rows)
-        return;
-    const int64_t set = at / t.rows;
-    const int r = (int)(at - set * t.rows), b = (int)(set / t.hsets), h = (int)(set - (int64_t)b * t.hsets) * t.gp + r % t.gp;
-    const int iq = r / t.gp;
-    float s = 0.0f, l = INFINITY;
-    if (iq < a.Nq) {
-        for (int d = 8 * c; d < a.D; d += 64) {
-            float x[8], y[8];
-            Row<__nv_bfloat16, 8, true>::load(a.go.row(b, iq, h) + d, x);
-            Row<__nv_bfloat16, 8, true>::load(a.o.row(b, iq, h) + d, y);
+    const int64_t total = (int64_t)a.B * t.hsets * t.rows, at0 = (int64_t)blockIdx.x * 32 * kStatRows + (threadIdx.x >> 3);
+    uint4 x[kStatRows][2], y[kStatRows][2];
+    float l[kStatRows];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                s = fmaf(x[j], y[j], s);
+    for (int k = 0; k < kStatRows; ++k) {
+        const int64_t at = at0 + 32 * k, set = at / t.rows;
+        const int r = (int)(at - set * t.rows), b = (int)(set / t.hsets);
+        const int h = (int)(set - (int64_t)b * t.hsets) * t.gp + r % t.gp, iq = r / t.gp;
+        const bool live = at < total && iq < a.Nq;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int d = 8 * c + 64 * e;
+            x[k][e] = load16(a.go.row(b, iq, h) + d, live && d < a.D);
+            y[k][e] = load16(a.o.row(b, iq, h) + d, live && d < a.D);
         }
-        l = a.lse_in[((int64_t)b * a.Hq + h) * a.Nq + iq] * kLog2e;
-        l = l == -INFINITY ? INFINITY : l; // a row without a key
+        l[k] = live && c == 0 ? a.lse_in[((int64_t)b * a.Hq + h) * a.Nq + iq] * kLog2e : INFINITY;
     }
-    const unsigned group = 0xFFu << (threadIdx.x & 24);
-    s += __shfl_xor_sync(group, s, 1);
-    s += __shfl_xor_sync(group, s, 2);
-    s += __shfl_xor_sync(group, s, 4);
-    if (c == 0) {
-        lse2[at] = l;
-        delta[at] = s;
+#pragma unroll
+    for (int k = 0; k < kStatRows; ++k) {
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                s = fmaf(bf16_lo(word(x[k][e], w)), bf16_lo(word(y[k][e], w)), s);
+                s = fmaf(bf16_hi(word(x[k][e], w)), bf16_hi(word(y[k][e], w)), s);
+            }
+        s += __shfl_xor_sync(~0u, s, 1);
+        s += __shfl_xor_sync(~0u, s, 2);
+        s += __shfl_xor_sync(~0u, s, 4);
+        const int64_t at = at0 + 32 * k;
+        if (c == 0 && at < total) {
+            lse2[at] = l[k] == -INFINITY ? INFINITY : l[k]; // (a row without a key)
+            delta[at] = s;
+        }
     }
 }
 
@@ -734,19 +743,25 @@ struct Plan {
         rows = qtiles * kTile;
         ktiles = (Nk + kTile - 1) / kTile;
         stat_floats = B * hsets * rows;
-        // Shares of the query tiles: the fewest that leave the SMs' last round nearly full
-        // (within 10% of the best of up to 16), each of at least 8 tiles.
+        // Shares of the query tiles: the least of an estimate in us.  A share costs its tiles (1.8 us each,
+        // 1.6 with narrow heads) and 5 us around them; the last round of the SMs is half full on
+        // average (batch entries end early); partial sums are written and read once.  (2 x 28
+        // tiles of 3520 keys, 16 heads: 1 share, 2 cost 60 us more; 4 x 4 tiles of 512 ragged
+        // keys over 220 query tiles: 8, against 1.8 times as long with 1.)
         const int64_t total = hs_kv * qtiles, base = B * Hkv * ktiles;
         shares = 1;
         per = total;
         if (base > 0 && total > 0) {
-            const int64_t most = std::max<int64_t>(1, std::min<int64_t>(16, total / 8));
-            auto rounds = [&](int64_t s) { return (double)((base * s + 147) / 148) / (double)s; };
-            double best = rounds(1);
-            for (int64_t s = 2; s <= most; ++s)
-                best = std::min(best, rounds(s));
-            while (rounds(shares) > 1.1 * best)
-                ++shares;
+            const double tile_us = D > 64 ? 1.8 : 1.6, part_us = 2.0 * 2 * 4 * B * Hkv * Nk * D / 6.0e6;
+            double best = 0;
+            for (int64_t s = 1; s <= 16 && s <= std::max<int64_t>(1, total / 4); ++s) {
+                const double rounds = std::max(1.0, (double)(base * s) / 148 + 0.5);
+                const double us = rounds * ((double)((total + s - 1) / s) * tile_us + 5) + (s > 1 ? 4 + s * part_us : 0);
+                if (s == 1 || us < best) {
+                    best = us;
+                    shares = s;
+                }
+            }
             per = (total + shares - 1) / shares;
             shares = (total + per - 1) / per;
         }
@@ -788,8 +803,8 @@ tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t st
     const int64_t kv = (int64_t)a.B * a.Hkv * a.Nk, sum_threads = 2 * kv * (a.D / 8);
     tok_status st = TOK_OK;
     if (a.Nq > 0) {
-        attn_stats_kernel<<<(unsigned)((p.stat_floats + 31) / 32), 256, 0, stream>>>(t, workspace,
-                                                                                   workspace + p.stat_floats);
+        attn_stats_kernel<<<(unsigned)((p.stat_floats + 32 * kStatRows - 1) / (32 * kStatRows)), 256, 0, stream>>>(
+            t, workspace, workspace + p.stat_floats);
         st = launch_status();
     }
     if (st == TOK_OK && a.Nq > 0) {
