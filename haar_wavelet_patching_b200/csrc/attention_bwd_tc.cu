@@ -15,9 +15,9 @@
 // attn_dkv_kernel: one CTA per tile of 128 keys and share of the query tiles; s^T = k q^T and
 //   dp^T = v go^T have a key per tensor-memory lane, so p^T and ds^T are the A operands of
 //   dv += p^T go and dk += ds^T q as they stand.  q and go are read by two products each:
-//   [row][channel] tiles serve as K-major and as MN-major operand.  The MMA thread issues
-//   s(i+1) behind dv(i) and dp(i+1) behind dk(i): one product pair runs under the powers,
-//   the other under the ds arithmetic.  With shares, partial sums go to fp32 and
+//   [row][channel] tiles serve as K-major and as MN-major operand.  Once dp^T is in registers, p^T and
+//   ds^T both go over its columns, so that s(i+1) can follow as soon as s(i) has been read; the powers
+//   of i+1 run under dv(i), dk(i) and dp(i+1).  With shares, partial sums go to fp32 and
 //   attn_dkv_sum_kernel adds them in order.
 // attn_dq_kernel: one CTA per SM walks the query tiles; per key tile s, dp and dq += ds k,
 //   s double-buffered so that s(i+2), dp(i+1) and dq(i) run under the arithmetic of i+1.
@@ -53,21 +53,23 @@ struct BwdArgs {
     int qb, gb, kb, kh, vb, vh;
 };
 
-// lse2 and delta of every query row, in tile order: 8 lanes per row, kStatRows rows in flight per lane.
-constexpr int kStatRows = 4;
+// lse2 and delta of every query row, in tile order: a block per tile of 128, 8 lanes per row, four rows in
+// flight per lane.
+constexpr int kStatRows = kTile / 32;
 __global__ void __launch_bounds__(256) attn_stats_kernel(const BwdArgs t, float *lse2, float *delta)
 {
     const AttnArgs &a = t.a;
     const int c = threadIdx.x & 7;
-    const int64_t total = (int64_t)a.B * t.hsets * t.rows, at0 = (int64_t)blockIdx.x * 32 * kStatRows + (threadIdx.x >> 3);
+    const int set = (int)blockIdx.x / t.qtiles, tile = (int)blockIdx.x - set * t.qtiles;
+    const int b = set / t.hsets, h0 = (set - b * t.hsets) * t.gp, lgp = 31 - __clz(t.gp);
+    const int r0 = tile * kTile + (int)(threadIdx.x >> 3);
+    const int64_t at0 = (int64_t)blockIdx.x * kTile + (threadIdx.x >> 3);
     uint4 x[kStatRows][2], y[kStatRows][2];
     float l[kStatRows];
 #pragma unroll
     for (int k = 0; k < kStatRows; ++k) {
-        const int64_t at = at0 + 32 * k, set = at / t.rows;
-        const int r = (int)(at - set * t.rows), b = (int)(set / t.hsets);
-        const int h = (int)(set - (int64_t)b * t.hsets) * t.gp + r % t.gp, iq = r / t.gp;
-        const bool live = at < total && iq < a.Nq;
+        const int r = r0 + 32 * k, h = h0 + (r & (t.gp - 1)), iq = r >> lgp;
+        const bool live = iq < a.Nq;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int d = 8 * c + 64 * e;
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(256) attn_stats_kernel(const BwdArgs t, float 
         s += __shfl_xor_sync(~0u, s, 2);
         s += __shfl_xor_sync(~0u, s, 4);
         const int64_t at = at0 + 32 * k;
-        if (c == 0 && at < total) {
+        if (c == 0) {
             lse2[at] = l[k] == -INFINITY ? INFINITY : l[k]; // (a row without a key)
             delta[at] = s;
         }
@@ -122,7 +124,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     using L = DkvSmem<DP>;
     constexpr int NQ = L::NQ, NG = L::NG, NSUB = DP / 64;
     constexpr uint32_t TB = L::TB;
-    __shared__ __align__(8) uint64_t kvfull, qfull[NQ], qempty[NQ], gfull[NG], gempty[NG], sfull, pfull, dpfull, dsfull,
+    __shared__ __align__(8) uint64_t kvfull, qfull[NQ], qempty[NQ], gfull[NG], gempty[NG], sfull, sread, dpfull, pfull,
         done;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
@@ -161,8 +163,8 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         }
         mbar_init(smem_addr(&sfull), 1);
         mbar_init(smem_addr(&dpfull), 1);
+        mbar_init(smem_addr(&sread), 8);
         mbar_init(smem_addr(&pfull), 8);
-        mbar_init(smem_addr(&dsfull), 8);
         mbar_init(smem_addr(&done), 1);
         abort_s = 0;
         fence_barrier_init();
@@ -246,24 +248,20 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 scores(dp_col, vd, base + L::g, &dpfull);
             }
             for (int i = 0; i < n && ok; ++i) {
-                ok = wait_or_abort(smem_addr(&pfull), i & 1u, abort);
-                if (!ok)
-                    break;
-                tc_fence_after();
-                grads(dv_col, s_col, base + L::g + (i % NG) * TB, i > 0);
-                umma_commit(smem_addr(&gempty[i % NG]));
-                if (i + 1 < n) {
-                    ok = full(qfull, i + 1, NQ);
+                if (i + 1 < n) { // s(i + 1) as soon as s(i) is in registers
+                    ok = full(qfull, i + 1, NQ) && wait_or_abort(smem_addr(&sread), i & 1u, abort);
                     if (!ok)
                         break;
                     tc_fence_after();
                     scores(s_col, kd, base + L::q + ((i + 1) % NQ) * TB, &sfull);
                 }
-                ok = wait_or_abort(smem_addr(&dsfull), i & 1u, abort);
+                ok = wait_or_abort(smem_addr(&pfull), i & 1u, abort);
                 if (!ok)
                     break;
                 tc_fence_after();
-                grads(dk_col, dp_col, base + L::q + (i % NQ) * TB, i > 0);
+                grads(dv_col, dp_col, base + L::g + (i % NG) * TB, i > 0);
+                umma_commit(smem_addr(&gempty[i % NG]));
+                grads(dk_col, dp_col + 32, base + L::q + (i % NQ) * TB, i > 0);
                 umma_commit(smem_addr(&qempty[i % NQ]));
                 if (i + 1 < n) {
                     ok = full(gfull, i + 1, NG);
@@ -295,39 +293,39 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             tc_fence_after();
             float p[64];
             load_half(sc, p);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&sread));
+            __syncwarp();
             {
                 const float4 *l4 = reinterpret_cast<const float4 *>(stats + 64 * half);
-                uint32_t pk[32];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const float4 l = l4[e];
                     const float2 x = __ffma2_rn(make_float2(p[4 * e], p[4 * e + 1]), mul, make_float2(-l.x, -l.y));
                     const float2 y = __ffma2_rn(make_float2(p[4 * e + 2], p[4 * e + 3]), mul, make_float2(-l.z, -l.w));
-                    p[4 * e] = live ? exp2_fast(x.x) : 0.0f;
-                    p[4 * e + 1] = live ? exp2_fast(x.y) : 0.0f;
-                    p[4 * e + 2] = live ? exp2_fast(y.x) : 0.0f;
-                    p[4 * e + 3] = live ? exp2_fast(y.y) : 0.0f;
-                    pk[2 * e] = pack_bf16x2(p[4 * e], p[4 * e + 1]);
-                    pk[2 * e + 1] = pack_bf16x2(p[4 * e + 2], p[4 * e + 3]);
+                    p[4 * e] = exp2_fast(x.x);
+                    p[4 * e + 1] = exp2_fast(x.y);
+                    p[4 * e + 2] = exp2_fast(y.x);
+                    p[4 * e + 3] = exp2_fast(y.y);
                 }
-                tmem_st32(sc, pk);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_addr(&pfull));
-            __syncwarp(); // the arrival goes out before any lane begins to wait
             if (!wait_or_abort(smem_addr(&dpfull), i & 1u, abort)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             {
+                // p and ds go over this half of dp: 32 packed columns each.
                 const float4 *d4 = reinterpret_cast<const float4 *>(stats + 128 + 64 * half);
                 float dp[64];
                 load_half(dc, dp);
                 uint32_t pk[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    pk[e] = live ? pack_bf16x2(p[2 * e], p[2 * e + 1]) : 0u;
+                tmem_st32(dc, pk);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const float4 d = d4[e];
@@ -338,13 +336,13 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     pk[2 * e] = live ? pack_bf16x2(x.x, x.y) : 0u;
                     pk[2 * e + 1] = live ? pack_bf16x2(y.x, y.y) : 0u;
                 }
-                tmem_st32(dc, pk);
+                tmem_st32(dc + 32, pk);
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(smem_addr(&dsfull));
+                mbar_arrive(smem_addr(&pfull));
             __syncwarp(); // the arrival goes out before any lane begins to wait
         }
         ok = ok && wait_or_abort(smem_addr(&done), 0u, abort);
@@ -803,7 +801,7 @@ tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t st
     const int64_t kv = (int64_t)a.B * a.Hkv * a.Nk, sum_threads = 2 * kv * (a.D / 8);
     tok_status st = TOK_OK;
     if (a.Nq > 0) {
-        attn_stats_kernel<<<(unsigned)((p.stat_floats + 32 * kStatRows - 1) / (32 * kStatRows)), 256, 0, stream>>>(
+        attn_stats_kernel<<<(unsigned)(p.stat_floats / kTile), 256, 0, stream>>>(
             t, workspace, workspace + p.stat_floats);
         st = launch_status();
     }
