@@ -21,6 +21,9 @@
 //   attn_dkv_sum_kernel adds them in order.
 // attn_dq_kernel: one CTA per SM walks the query tiles; per key tile s, dp and dq += ds k,
 //   s double-buffered so that s(i+2), dp(i+1) and dq(i) run under the arithmetic of i+1.
+// delta comes from the rounded o, an error of up to 2^-8 |go| |o| that averages out over many keys but
+// not over few: where a batch entry has at most 128 keys, attn_dq_kernel (which runs first) has
+// all of a row's p and dp at hand and takes delta = sum p dp from them.
 // In both, two warpgroups take half of a tile's columns each.
 #include <algorithm>
 
@@ -42,7 +45,8 @@ template <int DP> constexpr uint32_t tile_bytes() { return kTile * DP * 2; }
 
 struct BwdArgs {
     AttnArgs a;
-    const float *lse2, *delta; // [B][hsets][rows]
+    const float *lse2; // [B][hsets][rows]
+    float *delta;      // likewise
     float *part;               // [shares][2][B][Hkv][Nk][D]
     int gp, hsets, rows;       // heads per tile, Hq / gp, padded query rows of a head set
     int qtiles;                // rows / 128
@@ -427,7 +431,8 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     constexpr int NK = L::NK, NV = L::NV, NSUB = DP / 64;
     constexpr uint32_t TB = L::TB;
     __shared__ __align__(8) uint64_t qfull, qempty, kfull[NK], kempty[NK], vfull[NV], vempty[NV], sfull[2], dpfull, dsfull,
-        dqfull, drain;
+        dqfull, xfull[4], drain;
+    __shared__ float row_sum[2][kTile];
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
     extern __shared__ uint8_t smem_raw[];
@@ -446,6 +451,8 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         for (uint64_t *bar : {&qfull, &qempty, &sfull[0], &sfull[1], &dpfull, &dqfull, &drain})
             mbar_init(smem_addr(bar), 1);
         mbar_init(smem_addr(&dsfull), 8);
+        for (int i = 0; i < 4; ++i)
+            mbar_init(smem_addr(&xfull[i]), 2);
         for (int s = 0; s < NK; ++s) {
             mbar_init(smem_addr(&kfull[s]), 1);
             mbar_init(smem_addr(&kempty[s]), 1);
@@ -582,7 +589,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         const int half = warp >> 2;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const float2 mul = make_float2(a.scale2, a.scale2);
-        uint32_t it = 0, items = 0;
+        uint32_t it = 0, items = 0, nx = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < t.items && ok; i += gridDim.x) {
             int b, hs, qt, len;
@@ -592,7 +599,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             const int iq = row / t.gp, h = hs * t.gp + row % t.gp;
             const int64_t at = ((int64_t)b * t.hsets + hs) * t.rows + row;
             const float2 l2 = make_float2(-t.lse2[at], -t.lse2[at]);
-            const float delta = t.delta[at];
+            float delta = t.delta[at];
             for (int j = 0; j < n; ++j, ++it) {
                 const uint32_t sc = s_col + 128 * (it & 1u) + 64 * half + lanes;
                 if (!wait_or_abort(smem_addr(&sfull[it & 1u]), (it >> 1) & 1u, abort)) {
@@ -617,6 +624,25 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 {
                     float dp[64];
                     load_half(dp_col + 64 * half + lanes, dp);
+                    if (n == 1) { // all keys are here: delta = sum p dp, for attn_dkv_kernel as well
+                        float sum[4] = {};
+#pragma unroll
+                        for (int e = 0; e < 64; ++e)
+                            sum[e & 3] += 64 * half + e < valid ? p[e] * dp[e] : 0.0f;
+                        const int lrow = 32 * (warp & 3) + lane;
+                        row_sum[half][lrow] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(smem_addr(&xfull[warp & 3]));
+                        __syncwarp();
+                        if (!wait_or_abort(smem_addr(&xfull[warp & 3]), nx++ & 1u, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        delta = row_sum[0][lrow] + row_sum[1][lrow];
+                        if (half == 0)
+                            t.delta[at] = delta;
+                    }
                     uint32_t pk[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
@@ -717,16 +743,15 @@ template <int DP> tok_status launch(const BwdArgs &t, const CUtensorMap &q, cons
         st = prepare(attn_dq_kernel<DP>, DqSmem<DP>::bytes);
     if (st != TOK_OK)
         return st;
-    if (t.ktiles > 0) {
+    const int sms = sm_count();
+    attn_dq_kernel<DP><<<std::min(t.items, sms > 0 ? sms : 1), kThreads, DqSmem<DP>::bytes, stream>>>(q, g, k, v, t);
+    st = launch_status();
+    if (st == TOK_OK && t.ktiles > 0) {
         attn_dkv_kernel<DP><<<(unsigned)(a.B * a.Hkv * t.ktiles * t.shares), kThreads, DkvSmem<DP>::bytes, stream>>>(
             q, g, k, v, t);
         st = launch_status();
-        if (st != TOK_OK)
-            return st;
     }
-    const int sms = sm_count();
-    attn_dq_kernel<DP><<<std::min(t.items, sms > 0 ? sms : 1), kThreads, DqSmem<DP>::bytes, stream>>>(q, g, k, v, t);
-    return launch_status();
+    return st;
 }
 
 // Tiles and shares of a backward call, from its extents alone.
