@@ -612,7 +612,7 @@ def rope_table(sizes, dims, base=10000.0, scale=1.0, device="cuda", stream=None)
         raise ValueError("sizes and dims must not be negative")
     if torch.device(device).type != "cuda":
         raise ValueError("the table must be on a CUDA device (there is no CPU path)")
-    table = _new(nt * dt + nh * dh + nw * dw, torch.float32, device, stream)
+    table = _new(torch.empty(0, device=device), nt * dt + nh * dh + nw * dw, torch.float32, stream)
     _call("tok_rope_table", table.device, stream, table.data_ptr(), nt, nh, nw, dt, dh, dw, *_triple(base),
           *_triple(scale))
     return table
@@ -757,11 +757,11 @@ def _attn_dims(q, k, v, k_lens, others):
     sq, sk = q.shape, torch.Size((B, Nk, Hkv, D))
     if dev.type != "cuda":
         raise ValueError("q must be a CUDA tensor (there is no CPU path)")
-    for t, name, like_q in ((q, "q", True), (k, "k", False), (v, "v", False), *others):
+    for t, name, shape in ((q, "q", sq), (k, "k", sk), (v, "v", sk), *((t, n, sq if lq else sk) for t, n, lq in others)):
         if t.dtype != torch.bfloat16 or t.device != dev:
             raise ValueError(f"{name} must be a bfloat16 CUDA tensor on the device of q")
-        if t.shape != (sq if like_q else sk):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(sq if like_q else sk)}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if t.stride(3) != 1:
             raise ValueError(f"the channels of {name} must be dense")
     if k_lens is not None and (k_lens.device != dev or k_lens.dtype != torch.int32
@@ -776,14 +776,14 @@ def _stats(t, name, dims, device):
         raise ValueError(f"{name} must be a contiguous float32 CUDA tensor [B, Hq, Nq]")
 
 
-def _attn_workspace(f, dims, workspace, device, stream):
+def _attn_workspace(f, dims, workspace, like, stream):
     need = f(*dims)
     if need < 0:
         raise ValueError(f"no cross attention for (B, Nq, Nk, Hq, Hkv, D) = {dims}: D a multiple of 8, at most 128; "
                          "Hq a multiple of Hkv")
     if workspace is None:
-        return _new(need, torch.uint8, device, stream) if need else None
-    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        return _new(like, need, torch.uint8, stream) if need else None
+    if workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the device of q")
     return workspace
 
@@ -806,7 +806,7 @@ def tok_cross_attention(q, k, v, o, lse=None, k_lens=None, scale=None, workspace
     default; workspace: cross_attention_workspace_size bytes, allocated if None."""
     dims = _attn_dims(q, k, v, k_lens, ((o, "o", True),))
     _stats(lse, "lse", dims, q.device)
-    ws = _attn_workspace(lib().tok_cross_attention_workspace_size, dims, workspace, q.device, stream)
+    ws = _attn_workspace(lib().tok_cross_attention_workspace_size, dims, workspace, q, stream)
     _call("tok_cross_attention", q.device, stream, _heads(q), _heads(k), _heads(v), _heads(o),
           None if lse is None else lse.data_ptr(), None if k_lens is None else k_lens.data_ptr(), *dims,
           dims[5] ** -0.5 if scale is None else scale, *_bytes(ws))
@@ -819,7 +819,7 @@ def tok_cross_attention_backward(q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v
     dims = _attn_dims(q, k, v, k_lens, ((o, "o", True), (grad_o, "grad_o", True), (grad_q, "grad_q", True),
                                         (grad_k, "grad_k", False), (grad_v, "grad_v", False)))
     _stats(lse, "lse", dims, q.device)
-    ws = _attn_workspace(lib().tok_cross_attention_backward_workspace_size, dims, workspace, q.device, stream)
+    ws = _attn_workspace(lib().tok_cross_attention_backward_workspace_size, dims, workspace, q, stream)
     _call("tok_cross_attention_backward", q.device, stream, _heads(q), _heads(k), _heads(v), _heads(o), lse.data_ptr(),
           _heads(grad_o), None if k_lens is None else k_lens.data_ptr(), _heads(grad_q), _heads(grad_k), _heads(grad_v),
           *dims, dims[5] ** -0.5 if scale is None else scale, *_bytes(ws))
@@ -918,16 +918,19 @@ def fsq_decode_backward(idx: torch.Tensor, w: torch.Tensor, grad_out: torch.Tens
     return tok_fsq_decode_backward(idx, w, grad_out, grad_codes, grad_w, _workspace(B, C, S, idx.device), stream)
 
 
-def _new(shape, dtype, device, stream):
-    """A tensor for work on `stream` (memory that no other stream may still be using)."""
+def _new(like, shape, dtype, stream):
+    """A tensor on the device of `like` for work on `stream` (memory that no other stream may still be using)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _dense(x, stream):
-    return _new(x.shape, x.dtype, x.device, stream)
+    if stream is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def rope_grid(x, table, sizes, dims, origin=(0, 0, 0), interleaved=False, stream=None) -> torch.Tensor:
@@ -949,8 +952,8 @@ def rope_positions_adjoint(gy, pos, table, sizes, dims, interleaved=False, bad_c
 
 def sample_codes(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, with_logprob=False, stream=None):
     """idx, or (idx, logprob): see tok_sample_codes.  idx feeds fsq_decode where V is the FSQ codebook."""
-    idx = _new(logits.shape[:-1], torch.int32, logits.device, stream)
-    logprob = _new(logits.shape[:-1], torch.float32, logits.device, stream) if with_logprob else None
+    idx = _new(logits, logits.shape[:-1], torch.int32, stream)
+    logprob = _new(logits, logits.shape[:-1], torch.float32, stream) if with_logprob else None
     tok_sample_codes(logits, u, idx, logprob, temperature, top_k, top_p, min_p, stream)
     return (idx, logprob) if with_logprob else idx
 
@@ -958,7 +961,7 @@ def sample_codes(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, with
 def cross_attention(q, k, v, k_lens=None, scale=None, with_lse=False, stream=None):
     """o, or (o, lse): see tok_cross_attention."""
     o = _dense(q, stream)
-    lse = _new((q.shape[0], q.shape[2], q.shape[1]), torch.float32, q.device, stream) if with_lse else None
+    lse = _new(q, (q.shape[0], q.shape[2], q.shape[1]), torch.float32, stream) if with_lse else None
     tok_cross_attention(q, k, v, o, lse, k_lens, scale, None, stream)
     return (o, lse) if with_lse else o
 
