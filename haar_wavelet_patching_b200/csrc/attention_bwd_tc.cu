@@ -19,7 +19,8 @@
 //   ds^T both go over its columns, so that s(i+1) can follow as soon as s(i) has been read; the powers
 //   of i+1 run under dv(i), dk(i) and dp(i+1).  With shares, partial sums go to fp32 and
 //   attn_dkv_sum_kernel adds them in order.
-// attn_dq_kernel: one CTA per SM walks the query tiles; per key tile s, dp and dq += ds k,
+// attn_dq_kernel: one CTA per SM walks the query tiles (and, with few of them, shares of the keys, added up
+//   by attn_dq_sum_kernel); per key tile s, dp and dq += ds k,
 //   s double-buffered so that s(i+2), dp(i+1) and dq(i) run under the arithmetic of i+1.
 // delta comes from the rounded o, an error of up to 2^-8 |go| |o| that averages out over many keys but
 // not over few: where a batch entry has at most 128 keys, attn_dq_kernel (which runs first) has
@@ -54,6 +55,8 @@ struct BwdArgs {
     int hs_kv;                 // head sets per key head
     int shares, per;           // query tiles (over hs_kv sets) per share
     int items;                 // dq
+    int dq_shares, dq_per;     // dq: key tiles per share
+    float *dq_part;            // [dq_shares][B][Hq][Nq][D]
     int qb, gb, kb, kh, vb, vh;
 };
 
@@ -415,6 +418,29 @@ __global__ void __launch_bounds__(256) attn_dkv_sum_kernel(const BwdArgs t)
     Row<__nv_bfloat16, 8, true>::store((half ? a.dk : a.dv).row(b, key, hk) + d, v);
 }
 
+// dq of the shares' partial sums, in order.
+__global__ void __launch_bounds__(256) attn_dq_sum_kernel(const BwdArgs t)
+{
+    const AttnArgs &a = t.a;
+    const int chunks = a.D / 8;
+    const int64_t rows = (int64_t)a.B * a.Hq * a.Nq, e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= rows * chunks)
+        return;
+    const int64_t at = e / chunks;
+    const int d = (int)(e - at * chunks) * 8;
+    const int iq = (int)(at % a.Nq), bh = (int)(at / a.Nq), b = bh / a.Hq, h = bh - b * a.Hq;
+    const int tiles = (key_count(a, b) + kTile - 1) / kTile, live = (tiles + t.dq_per - 1) / t.dq_per;
+    float v[8] = {};
+    for (int s = 0; s < live; ++s) {
+        float x[8];
+        Row<float, 8, true>::load(t.dq_part + (s * rows + at) * a.D + d, x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] += x[k];
+    }
+    Row<__nv_bfloat16, 8, true>::store(a.dq.row(b, iq, h) + d, v);
+}
+
 template <int DP> struct DqSmem {
     static constexpr int NK = DP == 128 ? 3 : 4, NV = DP == 128 ? 2 : 4; // stages of k and v
     static constexpr uint32_t TB = tile_bytes<DP>();
@@ -439,12 +465,23 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const AttnArgs &a = t.a;
-    auto decode = [&](int i, int &b, int &hs, int &qt, int &len) {
-        qt = i % t.qtiles;
-        const int r = i / t.qtiles;
-        hs = r % t.hsets;
-        b = r / t.hsets;
-        len = key_count(a, b);
+    // Item i: query tile qt of head set hs of batch entry b, over key tiles [j0, j0 + n) of its share.
+    struct Item {
+        int b, hs, qt, share, len, tiles, j0, n;
+    };
+    auto decode = [&](int i) {
+        Item w;
+        w.share = i % t.dq_shares;
+        int r = i / t.dq_shares;
+        w.qt = r % t.qtiles;
+        r /= t.qtiles;
+        w.hs = r % t.hsets;
+        w.b = r / t.hsets;
+        w.len = key_count(a, w.b);
+        w.tiles = (w.len + kTile - 1) / kTile;
+        w.j0 = min(w.tiles, w.share * t.dq_per);
+        w.n = min(w.tiles, w.j0 + t.dq_per) - w.j0;
+        return w;
     };
 
     if (threadIdx.x == 0) {
@@ -485,9 +522,8 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     tma_load_4d(dst + s * SUB, map, 64 * s, h, row, bb, bar);
             };
             for (int i = blockIdx.x; i < t.items && ok; i += gridDim.x) {
-                int b, hs, qt, len;
-                decode(i, b, hs, qt, len);
-                const int n = (len + kTile - 1) / kTile, hk = hs / t.hs_kv;
+                const Item w = decode(i);
+                const int b = w.b, hs = w.hs, qt = w.qt, n = w.n, hk = hs / t.hs_kv;
                 if (n == 0)
                     continue;
                 ok = wait_or_abort(smem_addr(&qempty), (iq & 1u) ^ 1u, abort);
@@ -503,13 +539,13 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     if (!ok)
                         break;
                     mbar_expect_tx(smem_addr(&kfull[ks]), TB);
-                    load(&kmap, base + L::k + ks * TB, smem_addr(&kfull[ks]), hk * t.kh, j * kTile, b * t.kb);
+                    load(&kmap, base + L::k + ks * TB, smem_addr(&kfull[ks]), hk * t.kh, (w.j0 + j) * kTile, b * t.kb);
                     ++ik;
                     ok = wait_or_abort(smem_addr(&vempty[vs]), ((iv / NV) & 1u) ^ 1u, abort);
                     if (!ok)
                         break;
                     mbar_expect_tx(smem_addr(&vfull[vs]), TB);
-                    load(&vmap, base + L::v + vs * TB, smem_addr(&vfull[vs]), hk * t.vh, j * kTile, b * t.vb);
+                    load(&vmap, base + L::v + vs * TB, smem_addr(&vfull[vs]), hk * t.vh, (w.j0 + j) * kTile, b * t.vb);
                     ++iv;
                 }
             }
@@ -551,9 +587,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 return true;
             };
             for (int i = blockIdx.x; i < t.items && ok; i += gridDim.x) {
-                int b, hs, qt, len;
-                decode(i, b, hs, qt, len);
-                const int n = (len + kTile - 1) / kTile;
+                const int n = decode(i).n;
                 if (n == 0)
                     continue;
                 ok = wait_or_abort(smem_addr(&qfull), iq & 1u, abort) && scores(it) && dps(it) && (n == 1 || scores(it + 1));
@@ -592,9 +626,8 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         uint32_t it = 0, items = 0, nx = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < t.items && ok; i += gridDim.x) {
-            int b, hs, qt, len;
-            decode(i, b, hs, qt, len);
-            const int n = (len + kTile - 1) / kTile;
+            const Item w = decode(i);
+            const int b = w.b, hs = w.hs, qt = w.qt, len = w.len, n = w.n;
             const int row = qt * kTile + 32 * (warp & 3) + lane;
             const int iq = row / t.gp, h = hs * t.gp + row % t.gp;
             const int64_t at = ((int64_t)b * t.hsets + hs) * t.rows + row;
@@ -620,11 +653,11 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     break;
                 }
                 tc_fence_after();
-                const int valid = len - j * kTile; // keys of this tile
+                const int valid = len - (w.j0 + j) * kTile; // keys of this tile
                 {
                     float dp[64];
                     load_half(dp_col + 64 * half + lanes, dp);
-                    if (n == 1) { // all keys are here: delta = sum p dp, for attn_dkv_kernel as well
+                    if (w.tiles == 1) { // all keys are here: delta = sum p dp, for attn_dkv_kernel as well
                         float sum[4] = {};
 #pragma unroll
                         for (int e = 0; e < 64; ++e)
@@ -689,7 +722,8 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 tc_fence_after();
                 ++items;
             }
-            // Each warpgroup stores half of the channels.
+            // Each warpgroup stores half of the channels; with shares, the partial sum.
+            float *part = t.dq_part + ((((int64_t)w.share * a.B + b) * a.Hq + h) * a.Nq + iq) * a.D;
 #pragma unroll
             for (int c = 0; c < DP / 64; ++c) {
                 uint32_t x[32] = {};
@@ -698,7 +732,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     tmem_ld32(dq_col + d0 + lanes, x);
                     tmem_wait_ld();
                 }
-                if (iq >= a.Nq)
+                if (iq >= a.Nq || (t.dq_shares > 1 && n == 0)) // (a share without keys is not read)
                     continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -708,7 +742,10 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         v[k] = n > 0 ? __uint_as_float(x[8 * e + k]) * a.scale : 0.0f;
-                    Row<__nv_bfloat16, 8, true>::store(a.dq.row(b, iq, h) + d0 + 8 * e, v);
+                    if (t.dq_shares == 1)
+                        Row<__nv_bfloat16, 8, true>::store(a.dq.row(b, iq, h) + d0 + 8 * e, v);
+                    else
+                        Row<float, 8, true>::store(part + d0 + 8 * e, v);
                 }
             }
             tc_fence_before();
@@ -746,6 +783,11 @@ template <int DP> tok_status launch(const BwdArgs &t, const CUtensorMap &q, cons
     const int sms = sm_count();
     attn_dq_kernel<DP><<<std::min(t.items, sms > 0 ? sms : 1), kThreads, DqSmem<DP>::bytes, stream>>>(q, g, k, v, t);
     st = launch_status();
+    if (st == TOK_OK && t.dq_shares > 1) {
+        const int64_t threads = (int64_t)a.B * a.Hq * a.Nq * (a.D / 8);
+        attn_dq_sum_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(t);
+        st = launch_status();
+    }
     if (st == TOK_OK && t.ktiles > 0) {
         attn_dkv_kernel<DP><<<(unsigned)(a.B * a.Hkv * t.ktiles * t.shares), kThreads, DkvSmem<DP>::bytes, stream>>>(
             q, g, k, v, t);
@@ -756,7 +798,7 @@ template <int DP> tok_status launch(const BwdArgs &t, const CUtensorMap &q, cons
 
 // Tiles and shares of a backward call, from its extents alone.
 struct Plan {
-    int64_t gp, hsets, qtiles, rows, ktiles, hs_kv, per, shares, stat_floats, part_floats;
+    int64_t gp, hsets, qtiles, rows, ktiles, hs_kv, per, shares, stat_floats, part_floats, dq_per, dq_shares, dq_floats;
     Plan(int64_t B, int64_t Nq, int64_t Nk, int64_t Hq, int64_t Hkv, int64_t D)
     {
         gp = attn_tc_group((int)(Hq / Hkv));
@@ -789,6 +831,16 @@ struct Plan {
             shares = (total + per - 1) / per;
         }
         part_floats = shares > 1 ? shares * 2 * B * Hkv * Nk * D : 0;
+        // Shares of the key tiles for dq, where there are fewer query tiles than SMs: as many as fill
+        // them, each of at least four tiles.
+        const int64_t items = B * hsets * qtiles;
+        dq_per = std::max<int64_t>(1, ktiles);
+        if (items > 0) {
+            const int64_t s = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(148 / items, ktiles / 4), 32));
+            dq_per = std::max<int64_t>(1, (ktiles + s - 1) / s);
+        }
+        dq_shares = std::max<int64_t>(1, (ktiles + dq_per - 1) / dq_per);
+        dq_floats = dq_shares > 1 ? dq_shares * B * Hq * Nq * D : 0;
     }
 };
 
@@ -797,7 +849,7 @@ struct Plan {
 int64_t attn_tc_backward_workspace(int64_t B, int64_t Nq, int64_t Nk, int64_t Hq, int64_t Hkv, int64_t D)
 {
     const Plan p(B, Nq, Nk, Hq, Hkv, D);
-    return (2 * p.stat_floats + p.part_floats) * 4;
+    return (2 * p.stat_floats + p.part_floats + p.dq_floats) * 4;
 }
 
 tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t stream)
@@ -808,6 +860,9 @@ tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t st
     t.lse2 = workspace;
     t.delta = workspace + p.stat_floats;
     t.part = workspace + 2 * p.stat_floats;
+    t.dq_part = t.part + p.part_floats;
+    t.dq_shares = (int)p.dq_shares;
+    t.dq_per = (int)p.dq_per;
     t.gp = (int)p.gp;
     t.hsets = (int)p.hsets;
     t.rows = (int)p.rows;
@@ -816,7 +871,7 @@ tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t st
     t.hs_kv = (int)p.hs_kv;
     t.shares = (int)p.shares;
     t.per = (int)p.per;
-    t.items = (int)(a.B * p.hsets * p.qtiles);
+    t.items = (int)(a.B * p.hsets * p.qtiles * p.dq_shares);
     t.qb = a.B > 1 && a.q.b == 0 ? 0 : 1;
     t.gb = a.B > 1 && a.go.b == 0 ? 0 : 1;
     t.kb = a.B > 1 && a.k.b == 0 ? 0 : 1;

@@ -49,6 +49,7 @@ constexpr int kSmall = 1024;                         // largest top_k that picks
 constexpr int kMaxCluster = 8;
 constexpr int64_t kMaxV = 1 << 18;
 constexpr double kOne = 17592186044416.0; // 2^44
+constexpr uint64_t kBias = 0x4330000000000000ull; // the bits of 2^52
 constexpr float kReach = 31.25f;          // exp(-31.25) 2^44 < 1/2: no weight beyond
 constexpr float kLowest = -3.402823466e+38f; // tokens that are not at least this (-inf, NaN) do not count
 
@@ -547,7 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
                 by_k = listed > top_k;
             } else
                 barrier(); // pub is read by others until here
-        }
+        } else
+            barrier(); // (likewise: the extremes are published anew below)
     }
 
     // ---- The largest token; what weights are relative to. ----
@@ -730,7 +732,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         __syncthreads();
         // Sums of the bits of 2^52 + w: the number of terms times the bits of 2^52 is taken off at the end.
         // A token without a weight (-inf, NaN or below xcut) counts as one at xcut, which rounds to 0.
-        constexpr uint64_t kBias = 0x4330000000000000ull;
         uint64_t sum_all = 0, sum_above = 0;
         uint32_t n_all = 0, n_above = 0, n_mine = 0;
         auto pick = [&](float x, int idx) TOK_INLINE {
@@ -1052,7 +1053,28 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
             emit(value((uint32_t)sh.sorted[tid]), (int)~(uint32_t)(sh.sorted[tid] >> 32), total);
         return;
     }
-    if (!have_mine) {
+    if (!have_mine && cut == 0 && !infinite && xmax - reach >= kLowest) {
+        // No rank limit: as in the exact pass above, without a branch per token.
+        uint32_t count = 0;
+        auto sum = [&](float x0) TOK_INLINE {
+            const double w = weight_at((double)fmaxf(x0, xcut) - xmax_d);
+            const bool in = w >= floor_w;
+            mine += in ? (uint64_t)__double_as_longlong(w + 4503599627370496.0) : 0ull;
+            count += in;
+        };
+        mine = 0;
+        vectors(
+            1,
+            [&](const uint4 &v, int) {
+                float x[N];
+                Vec<T>::split(v, x);
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    sum(x[k]);
+            },
+            [&](float x, int) { sum(x); });
+        mine -= count * kBias;
+    } else if (!have_mine) {
         mine = 0;
         tokens([&](float x, int idx) { mine += kept_weight(x, idx); });
     }

@@ -228,3 +228,39 @@ def test_feeds_fsq_decode():
     out = hwp.fsq_decode(idx, torch.randn(6, 16, device="cuda"), bad)
     assert int(bad) == 1 and out.shape == (1, 16, 3, 4)
     assert out[0, :, 0, 3].isnan().all() and out.isnan().sum() == 16
+
+
+@pytest.mark.parametrize("R", [1, 9, 400])
+@pytest.mark.parametrize("V", [V0, 5000])
+def test_samples_that_mislead(R, V):
+    """Rows whose sampled part says nothing about the rest: all of it ruled out, or infinite, or the
+    largest tokens all elsewhere; and rows with few tokens left."""
+    x, u = data(R, V, seed=11)
+    step = torch.arange(V, device="cuda")
+    x[0, step % 2048 < 256] = -math.inf
+    compare(x[:1], u[:1], top_k=100, top_p=0.9)
+    x[0] = torch.where(step % 2048 < 256, -5.0, 5.0) + 0.1 * x[0].nan_to_num(0.0, 0.0, 0.0)
+    compare(x[:1], u[:1], top_k=300)
+    x[0, V // 2] = math.inf
+    x[0, 3] = math.inf
+    compare(x[:1], u[:1], top_k=300, top_p=0.9)
+    x[0] = -math.inf
+    x[0, V - 1] = x[0, V // 3] = 1.0
+    idx = compare(x[:3], u[:3], top_k=50, top_p=0.4)
+    compare(x[:3], u[:3], top_p=0.4)
+    compare(x[:3], u[:3], top_k=2000, top_p=0.4)
+    if R > 3:
+        assert torch.equal(hwp.sample_codes(x, u, top_k=50, top_p=0.4)[:3], idx[:3])
+
+
+def test_two_streams_at_once():
+    """Calls on two streams at the same time, with settings per row, give what each gives alone."""
+    a, b = data(40, V0, dtype=torch.bfloat16, seed=12), data(300, 9000, seed=13)
+    k = torch.randint(1, 900, (300,), dtype=torch.int32, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    want = hwp.sample_codes(*a, top_p=0.8), hwp.sample_codes(*b, top_k=k)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        x, y = hwp.sample_codes(*a, top_p=0.8, stream=s1), hwp.sample_codes(*b, top_k=k, stream=s2)
+        torch.cuda.synchronize()
+        assert torch.equal(x, want[0]) and torch.equal(y, want[1])
