@@ -52,6 +52,24 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// 16 bf16 of a row (8 words), or 8 where only 8 channels are left: whole 32-byte sectors with one store where
+// the row is so aligned (`wide`).  A lane stores a row of its own, so a warp's store meets 32 lines
+// whatever its width: fewer, wider ones are what counts.
+__device__ __forceinline__ void store16(__nv_bfloat16 *p, const uint32_t (&v)[8], int left, bool wide)
+{
+    if (left <= 0)
+        return;
+    if (wide && left >= 16) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+        return;
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(v[0], v[1], v[2], v[3]);
+    if (left >= 16)
+        *reinterpret_cast<uint4 *>(p + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+}
+
 // D += A B on one 16 x 8 x 16 tile.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1)

@@ -11,8 +11,9 @@
 //                   product; at the end o / sum -> HBM.  The accumulator is rescaled only
 //                   when the maximum has grown by more than 2^8 (every term carries the
 //                   same factor, so the quotient is unchanged; 2^8 is far from overflow).
-//   warp 8          one thread issues the MMAs: o_i += p_i v_j, then s_i = q_i k_(j+1), for
-//                   i = 0, 1 in turn, so that one tile's MMAs run under the other's softmax;
+//   warp 8          one thread issues the MMAs: o_i += p_i v_j, then s_i = q_i k_(j+1) (of the next
+//                   item where j was the last), for i = 0, 1 in turn, so that one tile's MMAs run
+//                   under the other's softmax and an item's first scores under the stores of the one before;
 //   warp 9          tensor copies of q, k, v into 128-byte-swizzled tiles (zero-filled
 //                   past the tensor: D below the tile's width needs no other care).
 // The v rows behind a batch entry's length are zeroed in shared memory (a weight of 0 times
@@ -34,15 +35,15 @@ constexpr float kGrow = 8.0f; // log2 of the growth of the maximum that the weig
 
 template <int DP> constexpr uint32_t tile_bytes() { return kTile * DP * 2; }
 template <int DP> constexpr int stages() { return DP == 128 ? 4 : 8; }
-constexpr uint32_t kStage = kTile * 128; // output staging of a warpgroup: 128 rows x 64 channels
 template <int DP> constexpr size_t smem_bytes()
 {
-    return (2 + stages<DP>()) * (size_t)tile_bytes<DP>() + 2 * kStage + 1024;
+    return (2 + stages<DP>()) * (size_t)tile_bytes<DP>() + 1024;
 }
 
 struct TcArgs {
     AttnArgs a;
-    int gp;       // heads of a row tile
+    int gp, lgp;  // heads of a row tile (a power of two)
+    int wide;     // rows of o start on 32 bytes
     int nqt;      // items per (batch, head set): 256 rows each
     int hsets;    // Hq / gp
     int items;
@@ -74,7 +75,7 @@ __device__ __forceinline__ Item decode(const TcArgs &t, int i)
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap, const TcArgs t)
+                const __grid_constant__ CUtensorMap vmap, const TcArgs t)
 {
     constexpr int NST = stages<DP>(), NSUB = DP / 64;
     constexpr uint32_t TB = tile_bytes<DP>(), SUB = kTile * 128;
@@ -127,7 +128,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             auto load_q = [&](const Item &w, int i) {
                 if (!wait_or_abort(smem_addr(&qempty[i]), (nq & 1u) ^ 1u, abort))
                     return false;
-                load(&qmap, base + i * TB, smem_addr(&qfull[i]), w.hs * t.gp, (w.row0 + i * kTile) / t.gp,
+                load(&qmap, base + i * TB, smem_addr(&qfull[i]), w.hs * t.gp, (w.row0 + i * kTile) >> t.lgp,
                      w.b * t.qb);
                 ++issued[i];
                 return true;
@@ -173,26 +174,35 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 }
                 umma_commit(smem_addr(&sfull[i]));
             };
-            for (int i = blockIdx.x; i < t.items && ok; i += gridDim.x) {
-                const Item w = decode(t, i);
-                if (w.ntiles == 0)
-                    continue;
-                const uint32_t ks = it % NST;
-                ok = wait_or_abort(smem_addr(&kvfull[ks]), (it / NST) & 1u, abort);
+            // The item after i that has keys: its number of key tiles (0: there is none).
+            auto next = [&](int &i) {
+                for (i += gridDim.x; i < t.items; i += gridDim.x) {
+                    const int n = decode(t, i).ntiles;
+                    if (n)
+                        return n;
+                }
+                return 0;
+            };
+            int i = (int)blockIdx.x - (int)gridDim.x, n = next(i);
+            if (n) { // the first scores; those of a later item follow the last products of the one before
+                ok = wait_or_abort(smem_addr(&kvfull[0]), 0u, abort);
                 for (int r = 0; r < 2 && ok; ++r) {
-                    ok = wait_or_abort(smem_addr(&qfull[r]), nq & 1u, abort);
+                    ok = wait_or_abort(smem_addr(&qfull[r]), 0u, abort);
                     if (!ok)
                         break;
                     tc_fence_after();
-                    scores(r, ks);
-                    if (w.ntiles == 1)
+                    scores(r, 0);
+                    if (n == 1)
                         umma_commit(smem_addr(&qempty[r]));
                 }
                 if (ok)
-                    umma_commit(smem_addr(&kvempty[ks]));
-                ++it;
-                for (int j = 0; j < w.ntiles && ok; ++j, ++np) {
-                    const bool more = j + 1 < w.ntiles;
+                    umma_commit(smem_addr(&kvempty[0]));
+                it = nq = 1;
+            }
+            while (n && ok) {
+                const int n2 = next(i);
+                for (int j = 0; j < n && ok; ++j, ++np, it += 2) {
+                    const bool last = j + 1 == n, more = !last || n2;
                     const uint32_t vs = it % NST, kn = (it + 1) % NST;
                     ok = wait_or_abort(smem_addr(&kvfull[vs]), (it / NST) & 1u, abort) &&
                          (!more || wait_or_abort(smem_addr(&kvfull[kn]), ((it + 1) / NST) & 1u, abort));
@@ -207,18 +217,25 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                                     j > 0 || k > 0);
                         if (r == 1)
                             umma_commit(smem_addr(&kvempty[vs]));
-                        if (more) {
-                            scores(r, kn);
-                            if (j + 2 == w.ntiles)
-                                umma_commit(smem_addr(&qempty[r]));
-                        } else
+                        if (last)
                             umma_commit(smem_addr(&ofull[r]));
+                        if (!more)
+                            continue;
+                        if (last) {
+                            ok = wait_or_abort(smem_addr(&qfull[r]), nq & 1u, abort);
+                            if (!ok)
+                                break;
+                            tc_fence_after();
+                        }
+                        scores(r, kn);
+                        if (last ? n2 == 1 : j + 2 == n)
+                            umma_commit(smem_addr(&qempty[r]));
                     }
                     if (ok && more)
                         umma_commit(smem_addr(&kvempty[kn]));
-                    it += more ? 2 : 1;
                 }
                 ++nq;
+                n = n2;
             }
             // Every MMA issued has completed before tensor memory is freed.
             umma_commit(smem_addr(&drain));
@@ -237,7 +254,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         for (int i = blockIdx.x; i < t.items && ok; i += gridDim.x) {
             const Item w = decode(t, i);
             const int row = w.row0 + r * kTile + 32 * (warp & 3) + lane;
-            const int iq = row / t.gp, h = w.hs * t.gp + row % t.gp;
+            const int iq = row >> t.lgp, h = w.hs * t.gp + (row & (t.gp - 1));
             const bool live = iq < a.Nq;
             const int64_t stat = ((int64_t)w.b * a.Hq + h) * a.Nq + iq;
             float m = -INFINITY, l = 0.0f; // maximum (log2 units) that the weights are relative to; their sum
@@ -348,42 +365,23 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             }
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
             if (a.splits == 1) {
-                // 64 channels at a time through the warp's 32 rows of the staging buffer, whole lines to HBM.
-                const uint32_t stage = kvbase + NST * TB + r * kStage + (warp & 3) * 4096u;
-                unsigned char *stage_ptr = smem_raw + (stage - smem_addr(smem_raw));
+                uint32_t o[DP] = {};
+                if (w.ntiles > 0) {
 #pragma unroll
-                for (int c = 0; c < NSUB; ++c) {
-                    uint32_t o[64] = {};
-                    if (w.ntiles > 0) {
-                        tmem_ld64(oc + 64 * c, o);
-                        tmem_wait_ld();
-                    }
-                    if (c == NSUB - 1)
-                        tc_fence_before();
-                    if (lane == 0)
-                        bulk_wait_read<0>(); // the store that last used the rows has read them
-                    __syncwarp();
+                    for (int c = 0; c < NSUB; ++c)
+                        tmem_ld64(oc + 64 * c, reinterpret_cast<uint32_t(&)[64]>(o[64 * c]));
+                    tmem_wait_ld();
+                }
+                __nv_bfloat16 *dst = a.o.row(w.b, iq, h);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        uint32_t v[4];
+                for (int c = 0; c < DP / 16; ++c) {
+                    uint32_t v[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            v[k] = w.ntiles > 0 ? pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * inv,
-                                                              __uint_as_float(o[8 * e + 2 * k + 1]) * inv)
-                                                : 0u;
-                        *reinterpret_cast<uint4 *>(stage_ptr + sw128_offset((uint32_t)lane, 8u * e)) =
-                            make_uint4(v[0], v[1], v[2], v[3]);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        const int row_w = w.row0 + r * kTile + 32 * (warp & 3);
-                        // (rows of one token lie in one warp where a tile has at most 32 heads; the box is
-                        // 32 rows: min(gp, 32) heads x 32 / gp tokens)
-                        if (64 * c < a.D && row_w / t.gp < a.Nq)
-                            tma_store_4d(&omap, 64 * c, w.hs * t.gp + row_w % t.gp, row_w / t.gp, w.b, stage);
-                        bulk_commit();
-                    }
+                    for (int k = 0; k < 8; ++k)
+                        v[k] = pack_bf16x2(__uint_as_float(o[16 * c + 2 * k]) * inv,
+                                           __uint_as_float(o[16 * c + 2 * k + 1]) * inv);
+                    if (live)
+                        store16(dst + 16 * c, v, a.D - 16 * c, t.wide);
                 }
             } else if (w.ntiles > 0) { // (a split without keys has m = -inf: its o is not read)
 #pragma unroll
@@ -410,8 +408,6 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 }
             }
         }
-        if (lane == 0)
-            bulk_wait_all(); // the stores have completed before the CTA exits
     }
     tc_fence_before();
     __syncthreads();
@@ -424,7 +420,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
 }
 
 template <int DP> tok_status launch(const TcArgs &t, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                                    const CUtensorMap &o, cudaStream_t stream)
+                                    cudaStream_t stream)
 {
     const cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)smem_bytes<DP>());
@@ -433,7 +429,7 @@ template <int DP> tok_status launch(const TcArgs &t, const CUtensorMap &q, const
         return TOK_ERR_CUDA;
     }
     const int sms = sm_count();
-    attn_fwd_kernel<DP><<<std::min(t.items, sms > 0 ? sms : 1), kThreads, smem_bytes<DP>(), stream>>>(q, k, v, o, t);
+    attn_fwd_kernel<DP><<<std::min(t.items, sms > 0 ? sms : 1), kThreads, smem_bytes<DP>(), stream>>>(q, k, v, t);
     return launch_status();
 }
 
@@ -447,6 +443,9 @@ tok_status attn_tc_forward(const AttnArgs &a, cudaStream_t stream)
     TcArgs t{};
     t.a = a;
     t.gp = attn_tc_group(a.G);
+    while (t.gp >> t.lgp > 1)
+        ++t.lgp;
+    t.wide = aligned(a.o.p, 32) && (a.B <= 1 || a.o.b % 16 == 0) && a.o.n % 16 == 0 && (a.Hq <= 1 || a.o.h % 16 == 0);
     t.hsets = a.Hq / t.gp;
     t.nqt = (int)(((int64_t)a.Nq * t.gp + 2 * kTile - 1) / (2 * kTile));
     t.items = a.B * t.hsets * t.nqt * a.splits;
@@ -455,12 +454,11 @@ tok_status attn_tc_forward(const AttnArgs &a, cudaStream_t stream)
     t.vb = a.B > 1 && a.v.b == 0 ? 0 : 1;
     t.kh = a.Hkv > 1 && a.k.h == 0 ? 0 : 1;
     t.vh = a.Hkv > 1 && a.v.h == 0 ? 0 : 1;
-    CUtensorMap q, k, v, o;
-    if (!heads_map(&o, a.o, a.B, a.Nq, a.Hq, a.D, std::min(t.gp, 32), std::max(1, 32 / t.gp)) ||
-        !heads_map(&q, a.q, a.B, a.Nq, a.Hq, a.D, t.gp, kTile / t.gp) ||
+    CUtensorMap q, k, v;
+    if (!heads_map(&q, a.q, a.B, a.Nq, a.Hq, a.D, t.gp, kTile / t.gp) ||
         !heads_map(&k, a.k, a.B, a.Nk, a.Hkv, a.D, 1, kTile) || !heads_map(&v, a.v, a.B, a.Nk, a.Hkv, a.D, 1, kTile))
         return TOK_ERR_SHAPE;
-    return a.D <= 64 ? launch<64>(t, q, k, v, o, stream) : launch<128>(t, q, k, v, o, stream);
+    return a.D <= 64 ? launch<64>(t, q, k, v, stream) : launch<128>(t, q, k, v, stream);
 }
 
 tok_status read_and_clear_attn_timeouts(cudaStream_t stream, unsigned int *count)

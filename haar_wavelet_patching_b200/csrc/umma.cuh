@@ -192,13 +192,6 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The same without ordering the thread's memory accesses: for handing over tensor memory, which
-// tcgen05.fence::before_thread_sync orders.
-__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
 // Non-blocking test of phase `parity` (no suspension when the phase is still open).
 __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity)
 {
