@@ -237,53 +237,16 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 2) attn_rows_kernel(const Attn
 }
 
 // One warp per query row and head: the splits' partial results in split order.
-constexpr int kMaxSplits = 32; // a lane each
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory"); // the grid before has written its parts
     const int64_t nstat = (int64_t)a.B * a.Hq * a.Nq;
     const int64_t stat = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
     if (stat >= nstat)
         return;
-    const float *ml = a.part + a.splits * nstat * a.D;
-    float ms = -INFINITY, ls = 0.0f;
-    if (lane < a.splits) {
-        const float2 x = *reinterpret_cast<const float2 *>(ml + 2 * (lane * nstat + stat));
-        ms = x.x;
-        ls = x.y;
-    }
-    float m = ms;
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    const float f = ms == -INFINITY ? 0.0f : exp2_fast(ms - m);
-    float l = f * ls, v[4] = {};
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        l += __shfl_xor_sync(~0u, l, o);
-    const int d = 4 * lane;
-#pragma unroll 8
-    for (int s = 0; s < a.splits; ++s) {
-        const float fs = __shfl_sync(~0u, f, s);
-        if (d < a.D && fs != 0.0f) { // (a split without keys has written nothing)
-            float x[4];
-            Row<float, 4, true>::load(a.part + (s * nstat + stat) * a.D + d, x);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] += fs * x[j];
-        }
-    }
     const int iq = (int)(stat % a.Nq), bh = (int)(stat / a.Nq), b = bh / a.Hq, h = bh - b * a.Hq;
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    if (d < a.D) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v[j] *= inv;
-        Row<__nv_bfloat16, 4, true>::store(a.o.row(b, iq, h) + d, v);
-    }
-    if (lane == 0 && a.lse)
-        a.lse[stat] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    join_parts(a.part + stat * a.D, reinterpret_cast<const float2 *>(a.part + a.splits * nstat * a.D) + stat, nstat,
+               a.splits, a.D, a.o.row(b, iq, h), a.lse ? a.lse + stat : nullptr);
 }
 
 template <int NP> tok_status launch_rows(const AttnArgs &a, int64_t blocks, cudaStream_t stream)
@@ -295,27 +258,6 @@ template <int NP> tok_status launch_rows(const AttnArgs &a, int64_t blocks, cuda
         return TOK_ERR_CUDA;
     }
     attn_rows_kernel<NP><<<(unsigned)blocks, kFwdWarps * 32, Ring<NP>::bytes, stream>>>(a);
-    return launch_status();
-}
-
-// The join's CTAs may start while the grid before still runs; they wait for its end.
-tok_status launch_join(const AttnArgs &a, cudaStream_t stream)
-{
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(((int64_t)a.B * a.Hq * a.Nq + 3) / 4));
-    cfg.blockDim = dim3(128);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_join_kernel, a);
-    if (e != cudaSuccess) {
-        record_cuda_error(e);
-        cudaGetLastError();
-        return TOK_ERR_CUDA;
-    }
     return launch_status();
 }
 
@@ -411,16 +353,10 @@ constexpr int64_t kTcRows = 64;
 
 bool wants_tc(const Dims &d) { return d.Nq * (d.Hq / d.Hkv) > kTcRows && d.Nk > 0; }
 
-// CTAs that the keys of one row tile are split over.
-int64_t fwd_splits(const Dims &d)
+// CTAs that the keys of one 16-row tile are split over.
+int64_t rows_splits(const Dims &d)
 {
     const int64_t G = d.Hq / d.Hkv;
-    if (wants_tc(d)) { // one CTA per SM, each with at least four key tiles
-        const int64_t gp = attn_tc_group((int)G), items = d.B * (d.Hq / gp) * ((d.Nq * gp + 255) / 256);
-        if (items == 0)
-            return 1;
-        return std::max<int64_t>(1, std::min(std::min(148 / items, d.Nk / 512), (int64_t)kMaxSplits));
-    }
     // Two CTAs per SM, as many as are resident, each with at least four rounds of its warps (8 x 3520 keys,
     // ragged, 8 key heads: 20.0 us; with half as many CTAs 24, twice as many 23; a cluster of 8
     // CTAs that joins through distributed shared memory instead of the workspace: 30).
@@ -440,7 +376,9 @@ extern "C" int64_t tok_cross_attention_workspace_size(int64_t B, int64_t Nq, int
     const tok::Dims d{B, Nq, Nk, Hq, Hkv, D};
     if (!d.ok())
         return -1;
-    const int64_t s = tok::fwd_splits(d);
+    if (tok::wants_tc(d))
+        return tok::attn_tc_workspace(B, Nq, Nk, Hq, Hkv, D);
+    const int64_t s = tok::rows_splits(d);
     return s > 1 ? s * B * Hq * Nq * (D + 2) * 4 : 0;
 }
 
@@ -464,7 +402,7 @@ extern "C" tok_status tok_cross_attention(const tok_heads *q, const tok_heads *k
         return TOK_OK;
     if (!q || !k || !v || !o || !q->ptr || !o->ptr || (Nk > 0 && (!k->ptr || !v->ptr)))
         return TOK_ERR_NULL;
-    const int64_t splits = fwd_splits(dim), need = tok_cross_attention_workspace_size(B, Nq, Nk, Hq, Hkv, D);
+    const int64_t need = tok_cross_attention_workspace_size(B, Nq, Nk, Hq, Hkv, D);
     const View vq{q, B, Nq, Hq, D, false}, vk{k, B, Nk, Hkv, D, true}, vv{v, B, Nk, Hkv, D, true},
         vo{o, B, Nq, Hq, D, false};
     for (const View &x : {vq, vk, vv, vo})
@@ -503,16 +441,14 @@ extern "C" tok_status tok_cross_attention(const tok_heads *q, const tok_heads *k
     a.Hkv = (int)Hkv;
     a.G = (int)(Hq / Hkv);
     a.D = (int)D;
-    a.splits = (int)splits;
     a.scale = scale;
     a.scale2 = (float)((double)scale * 1.4426950408889634);
-    const int64_t blocks = B * Hkv * ((Nq * a.G + kRows - 1) / kRows) * splits;
-    tok_status st = wants_tc(dim) ? attn_tc_forward(a, stream)
-                    : D <= 64     ? launch_rows<1>(a, blocks, stream)
-                                  : launch_rows<2>(a, blocks, stream);
-    if (st == TOK_OK && splits > 1)
-        st = launch_join(a, stream);
-    return st;
+    if (wants_tc(dim))
+        return attn_tc_forward(a, stream);
+    a.splits = (int)rows_splits(dim);
+    const int64_t blocks = B * Hkv * ((Nq * a.G + kRows - 1) / kRows) * a.splits;
+    const tok_status st = D <= 64 ? launch_rows<1>(a, blocks, stream) : launch_rows<2>(a, blocks, stream);
+    return st == TOK_OK && a.splits > 1 ? launch_join(attn_join_kernel, B * Hq * Nq, a, stream) : st;
 }
 
 extern "C" tok_status tok_cross_attention_backward(const tok_heads *q, const tok_heads *k, const tok_heads *v,
@@ -597,7 +533,6 @@ extern "C" tok_status tok_cross_attention_backward(const tok_heads *q, const tok
     a.Hkv = (int)Hkv;
     a.G = (int)(Hq / Hkv);
     a.D = (int)D;
-    a.splits = 1;
     a.scale = scale;
     a.scale2 = (float)((double)scale * 1.4426950408889634);
     return attn_tc_backward(a, static_cast<float *>(workspace), stream);

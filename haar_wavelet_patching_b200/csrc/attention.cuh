@@ -32,9 +32,112 @@ struct AttnArgs {
     float scale, scale2; // scale2 = scale * log2(e)
 };
 
+// 2^x, 2 ulp; 0 for -inf.
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// How many of a grid's equal items run whole: the last, unfull round of the SMs (all of them, where
+// there are fewer than SMs) is split into `shares` of an item's `steps` where that is estimated to be
+// faster, the shares' partial results being added up by a second kernel.  In us: a step, what
+// an item costs around its steps, writing and reading one partial result.
+struct Rounds {
+    int64_t whole, tail, shares, per; // items whole, items split, shares of each, steps of a share
+    Rounds(int64_t items, int64_t steps, int64_t most, double step_us, double item_us, double part_us)
+        : whole(items), tail(0), shares(1), per(steps > 0 ? steps : 1)
+    {
+        constexpr int64_t sms = 148;
+        constexpr double join_us = 6; // a second kernel
+        const int64_t last = items % sms;
+        double best = steps * step_us + item_us;
+        for (int64_t s = 2; last > 0 && s <= most && s <= steps; ++s) {
+            const int64_t p = (steps + s - 1) / s;
+            const double us = (double)((last * s + sms - 1) / sms) * (p * step_us + item_us) + join_us + last * s * part_us;
+            if (us < best) {
+                best = us;
+                whole = items - last;
+                tail = last;
+                shares = (steps + p - 1) / p; // (none without steps)
+                per = p;
+            }
+        }
+    }
+};
+
+// The partial results of one query row, `n` of them `stride` rows apart, joined in order by one warp:
+// lane s holds the statistics of part s, all lanes 4 channels each.
+__device__ __forceinline__ void join_parts(const float *part, const float2 *ml, int64_t stride, int n, int D,
+                                           __nv_bfloat16 *o, float *lse)
+{
+    const int lane = threadIdx.x & 31;
+    float ms = -INFINITY, ls = 0.0f;
+    if (lane < n) {
+        const float2 x = ml[lane * stride];
+        ms = x.x;
+        ls = x.y;
+    }
+    float m = ms;
+#pragma unroll
+    for (int i = 16; i; i >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(~0u, m, i));
+    const float f = ms == -INFINITY ? 0.0f : exp2_fast(ms - m);
+    float l = f * ls, v[4] = {};
+#pragma unroll
+    for (int i = 16; i; i >>= 1)
+        l += __shfl_xor_sync(~0u, l, i);
+    const int d = 4 * lane;
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) {
+        const float fs = __shfl_sync(~0u, f, s);
+        if (d < D && fs != 0.0f) { // (a part without keys has written nothing)
+            float x[4];
+            Row<float, 4, true>::load(part + s * stride * D + d, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] += fs * x[j];
+        }
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    if (d < D) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] *= inv;
+        Row<__nv_bfloat16, 4, true>::store(o + d, v);
+    }
+    if (lane == 0 && lse)
+        *lse = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+constexpr int kMaxSplits = 32; // parts of a query row: a lane of the join each
+
+// A join's CTAs may start while the grid before still runs; they wait for its end (griddepcontrol.wait).
+template <class Args> tok_status launch_join(void (*kernel)(Args), int64_t rows, const Args &args, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
+    if (e != cudaSuccess) {
+        record_cuda_error(e);
+        cudaGetLastError();
+        return TOK_ERR_CUDA;
+    }
+    return launch_status();
+}
+
 // The forward on the 5th-generation tensor cores (attention_tc.cu): query heads per row tile
-// for groups of G, and the call.  Backward (attention_bwd_tc.cu): workspace bytes and the call.
+// for groups of G, workspace bytes, and the call.  Backward (attention_bwd_tc.cu): likewise.
 int attn_tc_group(int G);
+int64_t attn_tc_workspace(int64_t B, int64_t Nq, int64_t Nk, int64_t Hq, int64_t Hkv, int64_t D);
 tok_status attn_tc_forward(const AttnArgs &a, cudaStream_t stream);
 int64_t attn_tc_backward_workspace(int64_t B, int64_t Nq, int64_t Nk, int64_t Hq, int64_t Hkv, int64_t D);
 tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t stream);
@@ -42,14 +145,6 @@ tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t st
 __device__ __forceinline__ int key_count(const AttnArgs &a, int b)
 {
     return a.lens ? min(max(a.lens[b], 0), a.Nk) : a.Nk;
-}
-
-// 2^x, 2 ulp; 0 for -inf.
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // 16 bf16 of a row (8 words), or 8 where only 8 channels are left: whole 32-byte sectors with one store where

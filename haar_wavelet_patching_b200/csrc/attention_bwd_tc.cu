@@ -48,15 +48,17 @@ struct BwdArgs {
     AttnArgs a;
     const float *lse2; // [B][hsets][rows]
     float *delta;      // likewise
-    float *part;               // [shares][2][B][Hkv][Nk][D]
+    float *part;               // [shares][2][tail][128][D]
     int gp, hsets, rows;       // heads per tile, Hq / gp, padded query rows of a head set
     int qtiles;                // rows / 128
     int ktiles;                // ceil(Nk / 128)
     int hs_kv;                 // head sets per key head
-    int shares, per;           // query tiles (over hs_kv sets) per share
-    int items;                 // dq
-    int dq_shares, dq_per;     // dq: key tiles per share
-    float *dq_part;            // [dq_shares][B][Hq][Nq][D]
+    int whole, tail;           // dkv: key tiles that one CTA takes, then ones that several share
+    int shares, per;           // of these: shares, query tiles (over hs_kv sets) of a share
+    int dq_whole, dq_tail;     // dq: likewise query tiles,
+    int dq_shares, dq_per;     // and key tiles of a share
+    int dq_items;              // dq_whole + dq_tail * dq_shares
+    float *dq_part;            // [dq_shares][dq_tail][128][D]
     int qb, gb, kb, kh, vb, vh;
 };
 
@@ -140,17 +142,16 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const AttnArgs &a = t.a;
 
-    int r = blockIdx.x;
-    const int share = r % t.shares;
-    r /= t.shares;
-    const int kt = r % t.ktiles;
-    r /= t.ktiles;
-    const int hk = r % a.Hkv, b = r / a.Hkv;
+    const bool split = (int)blockIdx.x >= t.whole;
+    const int share = split ? ((int)blockIdx.x - t.whole) % t.shares : 0;
+    const int item = split ? t.whole + ((int)blockIdx.x - t.whole) / t.shares : blockIdx.x;
+    const int kt = item % t.ktiles, hk = item / t.ktiles % a.Hkv, b = item / t.ktiles / a.Hkv;
     const int len = key_count(a, b), k0 = kt * kTile;
-    const int total = t.hs_kv * t.qtiles, i0 = share * t.per, n = k0 < len ? min(total, i0 + t.per) - i0 : 0;
+    const int total = t.hs_kv * t.qtiles, per = split ? t.per : total, i0 = share * per;
+    const int n = k0 < len ? min(total, i0 + per) - i0 : 0;
     const int key = k0 + 32 * (warp & 3) + lane; // of warps 0-7
     if (n <= 0) { // keys behind the length: zeros (with shares, the sum writes them)
-        if (t.shares == 1 && warp < 8 && key < a.Nk) {
+        if (!split && warp < 8 && key < a.Nk) {
             __nv_bfloat16 *dst = (warp < 4 ? a.dv : a.dk).row(b, key, hk);
             for (int d = 0; d < a.D; d += 8)
                 *reinterpret_cast<uint4 *>(dst + d) = make_uint4(0, 0, 0, 0);
@@ -357,8 +358,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             tc_fence_after();
             const uint32_t col = (half ? dk_col : dv_col) + lanes;
             const float f = half ? a.scale : 1.0f;
-            float *part = t.part + ((((int64_t)share * 2 + half) * a.B + b) * a.Hkv + hk) * a.Nk * a.D +
-                          (int64_t)key * a.D;
+            float *part = t.part + ((((int64_t)share * 2 + half) * t.tail + item - t.whole) * kTile + key - k0) * a.D;
 #pragma unroll
             for (int c = 0; c < DP / 32; ++c) {
                 uint32_t x[32];
@@ -375,7 +375,7 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         v[k] = live ? __uint_as_float(x[8 * e + k]) * f : 0.0f;
-                    if (t.shares == 1)
+                    if (!split)
                         Row<__nv_bfloat16, 8, true>::store((half ? a.dk : a.dv).row(b, key, hk) + d, v);
                     else
                         Row<float, 8, true>::store(part + d, v);
@@ -394,18 +394,21 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         atomicAdd(&g_attn_bwd_timeouts, 1u);
 }
 
-// dv and dk of the shares' partial sums, in order; zeros behind the length (and without queries).
+// dv and dk of the shared tiles' partial sums, in order; zeros behind the length (and without queries).
 __global__ void __launch_bounds__(256) attn_dkv_sum_kernel(const BwdArgs t)
 {
     const AttnArgs &a = t.a;
-    const int64_t per = (int64_t)a.B * a.Hkv * a.Nk, chunks = a.D / 8;
+    const int64_t per = (int64_t)t.tail * kTile, chunks = a.D / 8;
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (e >= 2 * per * chunks)
         return;
     const int64_t half = e / (per * chunks), r = e - half * per * chunks;
     const int64_t at = r / chunks;
     const int d = (int)(r - at * chunks) * 8;
-    const int key = (int)(at % a.Nk), bh = (int)(at / a.Nk), b = bh / a.Hkv, hk = bh - b * a.Hkv;
+    const int item = t.whole + (int)(at / kTile);
+    const int key = item % t.ktiles * kTile + (int)(at % kTile), hk = item / t.ktiles % a.Hkv, b = item / t.ktiles / a.Hkv;
+    if (key >= a.Nk)
+        return;
     float v[8] = {};
     if (key < key_count(a, b))
         for (int s = 0; s < t.shares; ++s) {
@@ -418,17 +421,21 @@ __global__ void __launch_bounds__(256) attn_dkv_sum_kernel(const BwdArgs t)
     Row<__nv_bfloat16, 8, true>::store((half ? a.dk : a.dv).row(b, key, hk) + d, v);
 }
 
-// dq of the shares' partial sums, in order.
+// dq of the shared tiles' partial sums, in order.
 __global__ void __launch_bounds__(256) attn_dq_sum_kernel(const BwdArgs t)
 {
     const AttnArgs &a = t.a;
     const int chunks = a.D / 8;
-    const int64_t rows = (int64_t)a.B * a.Hq * a.Nq, e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t rows = (int64_t)t.dq_tail * kTile, e = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (e >= rows * chunks)
         return;
     const int64_t at = e / chunks;
     const int d = (int)(e - at * chunks) * 8;
-    const int iq = (int)(at % a.Nq), bh = (int)(at / a.Nq), b = bh / a.Hq, h = bh - b * a.Hq;
+    const int item = t.dq_whole + (int)(at / kTile);
+    const int row = item % t.qtiles * kTile + (int)(at % kTile), hs = item / t.qtiles % t.hsets, b = item / t.qtiles / t.hsets;
+    const int iq = row / t.gp, h = hs * t.gp + row % t.gp;
+    if (iq >= a.Nq)
+        return;
     const int tiles = (key_count(a, b) + kTile - 1) / kTile, live = (tiles + t.dq_per - 1) / t.dq_per;
     float v[8] = {};
     for (int s = 0; s < live; ++s) {
@@ -465,14 +472,21 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const AttnArgs &a = t.a;
-    // Item i: query tile qt of head set hs of batch entry b, over key tiles [j0, j0 + n) of its share.
+    // Item i: query tile qt of head set hs of batch entry b, over key tiles [j0, j0 + n); of a shared tile,
+    // its index among these (else -1) and the share.
     struct Item {
-        int b, hs, qt, share, len, tiles, j0, n;
+        int b, hs, qt, part, share, len, tiles, j0, n;
     };
     auto decode = [&](int i) {
         Item w;
-        w.share = i % t.dq_shares;
-        int r = i / t.dq_shares;
+        w.part = -1;
+        w.share = 0;
+        int r = i;
+        if (i >= t.dq_whole) {
+            w.part = (i - t.dq_whole) / t.dq_shares;
+            w.share = (i - t.dq_whole) - w.part * t.dq_shares;
+            r = t.dq_whole + w.part;
+        }
         w.qt = r % t.qtiles;
         r /= t.qtiles;
         w.hs = r % t.hsets;
@@ -480,7 +494,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         w.len = key_count(a, w.b);
         w.tiles = (w.len + kTile - 1) / kTile;
         w.j0 = min(w.tiles, w.share * t.dq_per);
-        w.n = min(w.tiles, w.j0 + t.dq_per) - w.j0;
+        w.n = (w.part < 0 ? w.tiles : min(w.tiles, w.j0 + t.dq_per)) - w.j0;
         return w;
     };
 
@@ -521,7 +535,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 for (int s = 0; s < NSUB; ++s)
                     tma_load_4d(dst + s * SUB, map, 64 * s, h, row, bb, bar);
             };
-            for (int i = blockIdx.x; i < t.items && ok; i += gridDim.x) {
+            for (int i = blockIdx.x; i < t.dq_items && ok; i += gridDim.x) {
                 const Item w = decode(i);
                 const int b = w.b, hs = w.hs, qt = w.qt, n = w.n, hk = hs / t.hs_kv;
                 if (n == 0)
@@ -586,7 +600,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 umma_commit(smem_addr(&vempty[x % NV]));
                 return true;
             };
-            for (int i = blockIdx.x; i < t.items && ok; i += gridDim.x) {
+            for (int i = blockIdx.x; i < t.dq_items && ok; i += gridDim.x) {
                 const int n = decode(i).n;
                 if (n == 0)
                     continue;
@@ -625,7 +639,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         const float2 mul = make_float2(a.scale2, a.scale2);
         uint32_t it = 0, items = 0, nx = 0;
         bool ok = true;
-        for (int i = blockIdx.x; i < t.items && ok; i += gridDim.x) {
+        for (int i = blockIdx.x; i < t.dq_items && ok; i += gridDim.x) {
             const Item w = decode(i);
             const int b = w.b, hs = w.hs, qt = w.qt, len = w.len, n = w.n;
             const int row = qt * kTile + 32 * (warp & 3) + lane;
@@ -723,7 +737,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 ++items;
             }
             // Each warpgroup stores half of the channels; with shares, the partial sum.
-            float *part = t.dq_part + ((((int64_t)w.share * a.B + b) * a.Hq + h) * a.Nq + iq) * a.D;
+            float *part = t.dq_part + (((int64_t)w.share * t.dq_tail + w.part) * kTile + row - qt * kTile) * a.D;
 #pragma unroll
             for (int c = 0; c < DP / 64; ++c) {
                 uint32_t x[32] = {};
@@ -732,7 +746,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     tmem_ld32(dq_col + d0 + lanes, x);
                     tmem_wait_ld();
                 }
-                if (iq >= a.Nq || (t.dq_shares > 1 && n == 0)) // (a share without keys is not read)
+                if (iq >= a.Nq || (w.part >= 0 && n == 0)) // (a share without keys is not read)
                     continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -742,7 +756,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         v[k] = n > 0 ? __uint_as_float(x[8 * e + k]) * a.scale : 0.0f;
-                    if (t.dq_shares == 1)
+                    if (w.part < 0)
                         Row<__nv_bfloat16, 8, true>::store(a.dq.row(b, iq, h) + d0 + 8 * e, v);
                     else
                         Row<float, 8, true>::store(part + d0 + 8 * e, v);
@@ -781,15 +795,15 @@ template <int DP> tok_status launch(const BwdArgs &t, const CUtensorMap &q, cons
     if (st != TOK_OK)
         return st;
     const int sms = sm_count();
-    attn_dq_kernel<DP><<<std::min(t.items, sms > 0 ? sms : 1), kThreads, DqSmem<DP>::bytes, stream>>>(q, g, k, v, t);
+    attn_dq_kernel<DP><<<std::min(t.dq_items, sms > 0 ? sms : 1), kThreads, DqSmem<DP>::bytes, stream>>>(q, g, k, v, t);
     st = launch_status();
-    if (st == TOK_OK && t.dq_shares > 1) {
-        const int64_t threads = (int64_t)a.B * a.Hq * a.Nq * (a.D / 8);
+    if (st == TOK_OK && t.dq_tail > 0) {
+        const int64_t threads = (int64_t)t.dq_tail * kTile * (a.D / 8);
         attn_dq_sum_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(t);
         st = launch_status();
     }
     if (st == TOK_OK && t.ktiles > 0) {
-        attn_dkv_kernel<DP><<<(unsigned)(a.B * a.Hkv * t.ktiles * t.shares), kThreads, DkvSmem<DP>::bytes, stream>>>(
+        attn_dkv_kernel<DP><<<(unsigned)(t.whole + t.tail * t.shares), kThreads, DkvSmem<DP>::bytes, stream>>>(
             q, g, k, v, t);
         st = launch_status();
     }
@@ -798,7 +812,9 @@ template <int DP> tok_status launch(const BwdArgs &t, const CUtensorMap &q, cons
 
 // Tiles and shares of a backward call, from its extents alone.
 struct Plan {
-    int64_t gp, hsets, qtiles, rows, ktiles, hs_kv, per, shares, stat_floats, part_floats, dq_per, dq_shares, dq_floats;
+    int64_t gp, hsets, qtiles, rows, ktiles, hs_kv, stat_floats;
+    int64_t whole, tail, shares, per, part_floats;
+    int64_t dq_whole, dq_tail, dq_shares, dq_per, dq_floats;
     Plan(int64_t B, int64_t Nq, int64_t Nk, int64_t Hq, int64_t Hkv, int64_t D)
     {
         gp = attn_tc_group((int)(Hq / Hkv));
@@ -814,33 +830,40 @@ struct Plan {
         // tiles of 3520 keys, 16 heads: 1 share, 2 cost 60 us more; 4 x 4 tiles of 512 ragged
         // keys over 220 query tiles: 8, against 1.8 times as long with 1.)
         const int64_t total = hs_kv * qtiles, base = B * Hkv * ktiles;
+        const double tile_us = D > 64 ? 1.8 : 1.6, part_us = 2.0 * kTile * 4 * D / 6.0e6;
+        whole = base;
+        tail = 0;
         shares = 1;
-        per = total;
-        if (base > 0 && total > 0) {
-            const double tile_us = D > 64 ? 1.8 : 1.6, part_us = 2.0 * 2 * 4 * B * Hkv * Nk * D / 6.0e6;
-            double best = 0;
-            for (int64_t s = 1; s <= 16 && s <= std::max<int64_t>(1, total / 4); ++s) {
-                const double rounds = std::max(1.0, (double)(base * s) / 148 + 0.5);
-                const double us = rounds * ((double)((total + s - 1) / s) * tile_us + 5) + (s > 1 ? 4 + s * part_us : 0);
-                if (s == 1 || us < best) {
-                    best = us;
-                    shares = s;
-                }
+        per = std::max<int64_t>(1, total);
+        double best = 0;
+        for (int64_t s = 1; base > 0 && s <= 16 && s <= std::max<int64_t>(1, total / 4); ++s) {
+            const double rounds = std::max(1.0, (double)(base * s) / 148 + 0.5);
+            const double us = rounds * ((double)((total + s - 1) / s) * tile_us + 5) +
+                              (s > 1 ? 4 + (double)(s * base) * 2 * part_us : 0);
+            if (s == 1 || us < best) {
+                best = us;
+                shares = s;
             }
+        }
+        if (shares > 1) {
+            whole = 0;
+            tail = base;
             per = (total + shares - 1) / shares;
             shares = (total + per - 1) / per;
+        } else if (base > 148) { // one each pays; the last round's may be shared all the same
+            const Rounds r(base, total, 16, tile_us, 5, 2 * part_us);
+            whole = r.whole;
+            tail = r.tail;
+            shares = r.shares;
+            per = r.per;
         }
-        part_floats = shares > 1 ? shares * 2 * B * Hkv * Nk * D : 0;
-        // Shares of the key tiles for dq, where there are fewer query tiles than SMs: as many as fill
-        // them, each of at least four tiles.
-        const int64_t items = B * hsets * qtiles;
-        dq_per = std::max<int64_t>(1, ktiles);
-        if (items > 0) {
-            const int64_t s = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(148 / items, ktiles / 4), 32));
-            dq_per = std::max<int64_t>(1, (ktiles + s - 1) / s);
-        }
-        dq_shares = std::max<int64_t>(1, (ktiles + dq_per - 1) / dq_per);
-        dq_floats = dq_shares > 1 ? dq_shares * B * Hq * Nq * D : 0;
+        part_floats = tail * shares * 2 * kTile * D;
+        const Rounds r(B * hsets * qtiles, ktiles, 32, 1.6, 4, part_us);
+        dq_whole = r.whole;
+        dq_tail = r.tail;
+        dq_shares = r.shares;
+        dq_per = r.per;
+        dq_floats = dq_tail * dq_shares * kTile * D;
     }
 };
 
@@ -861,6 +884,9 @@ tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t st
     t.delta = workspace + p.stat_floats;
     t.part = workspace + 2 * p.stat_floats;
     t.dq_part = t.part + p.part_floats;
+    t.dq_whole = (int)p.dq_whole;
+    t.dq_tail = (int)p.dq_tail;
+    t.dq_items = (int)(p.dq_whole + p.dq_tail * p.dq_shares);
     t.dq_shares = (int)p.dq_shares;
     t.dq_per = (int)p.dq_per;
     t.gp = (int)p.gp;
@@ -869,16 +895,16 @@ tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t st
     t.qtiles = (int)p.qtiles;
     t.ktiles = (int)p.ktiles;
     t.hs_kv = (int)p.hs_kv;
+    t.whole = (int)p.whole;
+    t.tail = (int)p.tail;
     t.shares = (int)p.shares;
     t.per = (int)p.per;
-    t.items = (int)(a.B * p.hsets * p.qtiles * p.dq_shares);
     t.qb = a.B > 1 && a.q.b == 0 ? 0 : 1;
     t.gb = a.B > 1 && a.go.b == 0 ? 0 : 1;
     t.kb = a.B > 1 && a.k.b == 0 ? 0 : 1;
     t.vb = a.B > 1 && a.v.b == 0 ? 0 : 1;
     t.kh = a.Hkv > 1 && a.k.h == 0 ? 0 : 1;
     t.vh = a.Hkv > 1 && a.v.h == 0 ? 0 : 1;
-    const int64_t kv = (int64_t)a.B * a.Hkv * a.Nk, sum_threads = 2 * kv * (a.D / 8);
     tok_status st = TOK_OK;
     if (a.Nq > 0) {
         attn_stats_kernel<<<(unsigned)(p.stat_floats / kTile), 256, 0, stream>>>(
@@ -897,9 +923,12 @@ tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t st
             return TOK_ERR_SHAPE;
         st = a.D <= 64 ? launch<64>(t, q, g, k, v, stream) : launch<128>(t, q, g, k, v, stream);
     }
-    if (st == TOK_OK && kv > 0 && (t.shares > 1 || a.Nq == 0)) {
-        if (a.Nq == 0)
-            t.shares = 0; // zeros
+    if (a.Nq == 0) { // zeros: sums of no shares
+        t.tail = a.B * a.Hkv * t.ktiles;
+        t.whole = t.shares = 0;
+    }
+    if (st == TOK_OK && t.tail > 0) {
+        const int64_t sum_threads = (int64_t)t.tail * kTile * 2 * (a.D / 8);
         attn_dkv_sum_kernel<<<(unsigned)((sum_threads + 255) / 256), 256, 0, stream>>>(t);
         st = launch_status();
     }

@@ -46,25 +46,38 @@ struct TcArgs {
     int wide;     // rows of o start on 32 bytes
     int nqt;      // items per (batch, head set): 256 rows each
     int hsets;    // Hq / gp
-    int items;
+    int items;    // CTAs' worth: whole ones, then the shares of the others
+    int whole, tail;
     int qb, kb, kh, vb, vh; // coordinate factors: 0 for a broadcast dimension
 };
 
 struct Item {
-    int b, hs, row0, k0, ntiles, kend, split;
+    int b, hs, row0, k0, ntiles, kend, split, part; // part: index among the split items, or -1
 };
 
-__device__ __forceinline__ Item decode(const TcArgs &t, int i)
+__device__ __forceinline__ void place(const TcArgs &t, int r, Item &w)
 {
-    Item w;
-    w.split = i % t.a.splits;
-    int r = i / t.a.splits;
     w.row0 = r % t.nqt * (2 * kTile);
     r /= t.nqt;
     w.hs = r % t.hsets;
     w.b = r / t.hsets;
+}
+
+__device__ __forceinline__ Item decode(const TcArgs &t, int i)
+{
+    Item w;
+    int splits = 1;
+    w.split = 0;
+    w.part = -1;
+    if (i >= t.whole) {
+        splits = t.a.splits;
+        w.part = (i - t.whole) / splits;
+        w.split = (i - t.whole) - w.part * splits;
+        i = t.whole + w.part;
+    }
+    place(t, i, w);
     const int len = key_count(t.a, w.b), tiles = (len + kTile - 1) / kTile;
-    const int per = (tiles + t.a.splits - 1) / t.a.splits;
+    const int per = (tiles + splits - 1) / splits;
     const int t0 = min(tiles, w.split * per), t1 = min(tiles, t0 + per);
     w.k0 = t0 * kTile;
     w.ntiles = t1 - t0;
@@ -246,7 +259,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         const int r = warp >> 2;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t sc = s_col[r] + lanes, oc = o_col[r] + lanes;
-        const int64_t nstat = (int64_t)a.B * a.Hq * a.Nq;
+        const int64_t part_rows = (int64_t)t.tail * (2 * kTile); // of one split
         const bool odd_scale = !(a.scale2 > 0.0f);
         const float mul = odd_scale ? 1.0f : a.scale2;
         uint32_t it = 0, ns = 0, nitem = 0;
@@ -257,6 +270,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             const int iq = row >> t.lgp, h = w.hs * t.gp + (row & (t.gp - 1));
             const bool live = iq < a.Nq;
             const int64_t stat = ((int64_t)w.b * a.Hq + h) * a.Nq + iq;
+            const int64_t part_row = w.split * part_rows + (int64_t)w.part * (2 * kTile) + (row - w.row0);
             float m = -INFINITY, l = 0.0f; // maximum (log2 units) that the weights are relative to; their sum
             for (int j = 0; j < w.ntiles; ++j, ++ns) {
                 if (!wait_or_abort(smem_addr(&sfull[r]), ns & 1u, abort)) {
@@ -364,7 +378,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 it += 2 * w.ntiles;
             }
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            if (a.splits == 1) {
+            if (w.part < 0) {
                 uint32_t o[DP] = {};
                 if (w.ntiles > 0) {
 #pragma unroll
@@ -389,7 +403,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     uint32_t o[32];
                     tmem_ld32(oc + 32 * c, o);
                     tmem_wait_ld();
-                    float *dst = a.part + (w.split * nstat + stat) * a.D + 32 * c;
+                    float *dst = a.part + part_row * a.D + 32 * c;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (live && 32 * c + 8 * e < a.D)
@@ -398,13 +412,12 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             }
             tc_fence_before();
             if (live) {
-                if (a.splits == 1) {
+                if (w.part < 0) {
                     if (a.lse)
                         a.lse[stat] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
                 } else {
-                    float *ml = a.part + a.splits * nstat * a.D + 2 * (w.split * nstat + stat);
-                    ml[0] = w.ntiles > 0 ? m : -INFINITY;
-                    ml[1] = l;
+                    reinterpret_cast<float2 *>(a.part + a.splits * part_rows * a.D)[part_row] =
+                        make_float2(w.ntiles > 0 ? m : -INFINITY, l);
                 }
             }
         }
@@ -419,6 +432,30 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         atomicAdd(&g_attn_timeouts, 1u);
 }
 
+// One warp per query row of a split item.
+__global__ void __launch_bounds__(128) attn_tail_join_kernel(const TcArgs t)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory"); // the grid before has written its parts
+    const AttnArgs &a = t.a;
+    const int64_t rows = (int64_t)t.tail * (2 * kTile), at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    Item w;
+    place(t, t.whole + (int)(at / (2 * kTile)), w);
+    const int row = w.row0 + (int)(at % (2 * kTile)), iq = row >> t.lgp, h = w.hs * t.gp + (row & (t.gp - 1));
+    if (iq >= a.Nq)
+        return;
+    join_parts(a.part + at * a.D, reinterpret_cast<const float2 *>(a.part + a.splits * rows * a.D) + at, rows, a.splits,
+               a.D, a.o.row(w.b, iq, h), a.lse ? a.lse + ((int64_t)w.b * a.Hq + h) * a.Nq + iq : nullptr);
+}
+
+// Items of 256 query rows, the last round's split over the keys.  (2 x 3520 x 3520, 16 heads: 448 items,
+// 4 of them shared: 186 us, 225 without.)
+Rounds plan(int64_t B, int64_t Nq, int64_t Nk, int64_t Hq, int64_t Hkv, int64_t D)
+{
+    const int64_t gp = attn_tc_group((int)(Hq / Hkv));
+    return Rounds(B * (Hq / gp) * ((Nq * gp + 2 * kTile - 1) / (2 * kTile)), (Nk + kTile - 1) / kTile, kMaxSplits,
+                  D > 64 ? 2.0 : 1.75, 3, 2.0 * 2 * kTile * 4 * D / 6.0e6);
+}
+
 template <int DP> tok_status launch(const TcArgs &t, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                                     cudaStream_t stream)
 {
@@ -430,10 +467,17 @@ template <int DP> tok_status launch(const TcArgs &t, const CUtensorMap &q, const
     }
     const int sms = sm_count();
     attn_fwd_kernel<DP><<<std::min(t.items, sms > 0 ? sms : 1), kThreads, smem_bytes<DP>(), stream>>>(q, k, v, t);
-    return launch_status();
+    const tok_status st = launch_status();
+    return st == TOK_OK && t.tail > 0 ? launch_join(attn_tail_join_kernel, (int64_t)t.tail * (2 * kTile), t, stream) : st;
 }
 
 } // namespace
+
+int64_t attn_tc_workspace(int64_t B, int64_t Nq, int64_t Nk, int64_t Hq, int64_t Hkv, int64_t D)
+{
+    const Rounds r = plan(B, Nq, Nk, Hq, Hkv, D);
+    return r.tail * r.shares * 2 * kTile * (D + 2) * 4;
+}
 
 // Heads that a 128-row tile holds: the group, where it divides the tile.
 int attn_tc_group(int G) { return G <= kTile && (G & (G - 1)) == 0 ? G : 1; }
@@ -448,7 +492,11 @@ tok_status attn_tc_forward(const AttnArgs &a, cudaStream_t stream)
     t.wide = aligned(a.o.p, 32) && (a.B <= 1 || a.o.b % 16 == 0) && a.o.n % 16 == 0 && (a.Hq <= 1 || a.o.h % 16 == 0);
     t.hsets = a.Hq / t.gp;
     t.nqt = (int)(((int64_t)a.Nq * t.gp + 2 * kTile - 1) / (2 * kTile));
-    t.items = a.B * t.hsets * t.nqt * a.splits;
+    const Rounds r = plan(a.B, a.Nq, a.Nk, a.Hq, a.Hkv, a.D);
+    t.a.splits = (int)r.shares;
+    t.whole = (int)r.whole;
+    t.tail = (int)r.tail;
+    t.items = (int)(r.whole + r.tail * r.shares);
     t.qb = a.B > 1 && a.q.b == 0 ? 0 : 1;
     t.kb = a.B > 1 && a.k.b == 0 ? 0 : 1;
     t.vb = a.B > 1 && a.v.b == 0 ? 0 : 1;

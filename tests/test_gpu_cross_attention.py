@@ -109,6 +109,8 @@ FORWARD = [  # B, Nq, Nk, Hq, Hkv, D, lens
     (2, 255, 1, 2, 2, 128, None), (1, 515, 1030, 3, 1, 120, None), (5, 200, 260, 2, 2, 56, "wild"),
     (1, 5, 0, 2, 2, 64, None), (2, 300, 0, 2, 2, 128, None), (4, 400, 257, 8, 2, 72, "empty"),
     (1, 700, 129, 16, 1, 128, None), (2, 128, 256, 2, 2, 128, None), (1, 256, 2048, 2, 2, 128, None),
+    # a last round of the SMs that is shared: forward, both backward passes
+    (1, 2437, 1500, 16, 16, 128, None), (2, 1300, 900, 16, 4, 64, "ragged"), (3, 700, 2100, 18, 18, 80, "wild"),
 ]
 
 
