@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "tma.cuh"
 #include "tok_common.cuh"
 #include "tok_internal.h"
 #include "umma.cuh"
@@ -163,6 +164,12 @@ __device__ __forceinline__ void store16(__nv_bfloat16 *p, const uint32_t (&v)[8]
     *reinterpret_cast<uint4 *>(p) = make_uint4(v[0], v[1], v[2], v[3]);
     if (left >= 16)
         *reinterpret_cast<uint4 *>(p + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+}
+
+// Whether every row of a tensor starts on 32 bytes.
+inline bool rows_wide(const HeadsView &v, int64_t B, int64_t N, int64_t H)
+{
+    return aligned(v.p, 32) && (B <= 1 || v.b % 16 == 0) && (N <= 1 || v.n % 16 == 0) && (H <= 1 || v.h % 16 == 0);
 }
 
 // D += A B on one 16 x 8 x 16 tile.

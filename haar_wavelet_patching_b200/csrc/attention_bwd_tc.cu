@@ -49,8 +49,11 @@ struct BwdArgs {
     const float *lse2; // [B][hsets][rows]
     float *delta;      // likewise
     float *part;               // [shares][2][tail][128][D]
-    int gp, hsets, rows;       // heads per tile, Hq / gp, padded query rows of a head set
+    int gp, lgp;               // heads per tile: a power of two
+    int hsets, rows;           // Hq / gp, padded query rows of a head set
     int qtiles;                // rows / 128
+    FastDiv qtiles_div, hsets_div;
+    int wide, dq_wide;         // rows of dk and dv, of dq start on 32 bytes
     int ktiles;                // ceil(Nk / 128)
     int hs_kv;                 // head sets per key head
     int whole, tail;           // dkv: key tiles that one CTA takes, then ones that several share
@@ -114,6 +117,27 @@ template <int DP> struct DkvSmem {
     static constexpr uint32_t k = 0, v = TB, q = 2 * TB, g = q + NQ * TB, st = g + NG * TB; // stats: NQ x 1 KB
     static constexpr size_t bytes = st + NQ * 1024 + 1024;
 };
+
+struct Words8 {
+    uint32_t w[8];
+};
+__device__ __forceinline__ Words8 packed(const uint32_t *x) // 16 fp32 -> bf16
+{
+    Words8 r;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        r.w[k] = pack_bf16x2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+    return r;
+}
+__device__ __forceinline__ void store16(__nv_bfloat16 *p, const Words8 &v, int left, bool wide) { tok::store16(p, v.w, left, wide); }
+__device__ __forceinline__ void store16(float *p, const uint32_t *x, int left)
+{
+    const float *v = reinterpret_cast<const float *>(x);
+    if (left > 0)
+        Row<float, 8, true>::store(p, v);
+    if (left >= 16)
+        Row<float, 8, true>::store(p + 8, v + 8);
+}
 
 // [row][channel] tile as K-major operand, byte offset of K step k (16 channels).
 __device__ __forceinline__ constexpr uint32_t kmajor_step(int k) { return (k / 4) * SUB + (k % 4) * 32; }
@@ -367,19 +391,15 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 if (key >= a.Nk)
                     continue;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int d = 32 * c + 8 * e;
-                    if (d >= a.D)
-                        continue;
-                    float v[8];
+                for (int e = 0; e < 32; ++e)
+                    x[e] = live ? __float_as_uint(__uint_as_float(x[e]) * f) : 0u;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        v[k] = live ? __uint_as_float(x[8 * e + k]) * f : 0.0f;
+                for (int e = 0; e < 2; ++e) // 16 channels
                     if (!split)
-                        Row<__nv_bfloat16, 8, true>::store((half ? a.dk : a.dv).row(b, key, hk) + d, v);
+                        store16((half ? a.dk : a.dv).row(b, key, hk) + 32 * c + 16 * e, packed(x + 16 * e),
+                                a.D - 32 * c - 16 * e, t.wide);
                     else
-                        Row<float, 8, true>::store(part + d, v);
-                }
+                        store16(part + 32 * c + 16 * e, x + 16 * e, a.D - 32 * c - 16 * e);
             }
             tc_fence_before();
         }
@@ -449,9 +469,10 @@ __global__ void __launch_bounds__(256) attn_dq_sum_kernel(const BwdArgs t)
 }
 
 template <int DP> struct DqSmem {
-    static constexpr int NK = DP == 128 ? 3 : 4, NV = DP == 128 ? 2 : 4; // stages of k and v
+    static constexpr int NQ = DP == 128 ? 1 : 2;                         // stages of q and go,
+    static constexpr int NK = DP == 128 ? 3 : 4, NV = DP == 128 ? 2 : 4; // of k and v
     static constexpr uint32_t TB = tile_bytes<DP>();
-    static constexpr uint32_t q = 0, g = TB, k = 2 * TB, v = k + NK * TB;
+    static constexpr uint32_t q = 0, g = TB, k = 2 * NQ * TB, v = k + NK * TB; // (q and go of a stage side by side)
     static constexpr size_t bytes = v + NV * TB + 1024;
 };
 
@@ -461,9 +482,9 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const BwdArgs t)
 {
     using L = DqSmem<DP>;
-    constexpr int NK = L::NK, NV = L::NV, NSUB = DP / 64;
+    constexpr int NQ = L::NQ, NK = L::NK, NV = L::NV, NSUB = DP / 64;
     constexpr uint32_t TB = L::TB;
-    __shared__ __align__(8) uint64_t qfull, qempty, kfull[NK], kempty[NK], vfull[NV], vempty[NV], sfull[2], dpfull, dsfull,
+    __shared__ __align__(8) uint64_t qfull[NQ], qempty[NQ], kfull[NK], kempty[NK], vfull[NV], vempty[NV], sfull[2], dpfull, dsfull,
         dqfull, xfull[4], drain;
     __shared__ float row_sum[2][kTile];
     __shared__ uint32_t tmem_base_s;
@@ -487,10 +508,10 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             w.share = (i - t.dq_whole) - w.part * t.dq_shares;
             r = t.dq_whole + w.part;
         }
-        w.qt = r % t.qtiles;
-        r /= t.qtiles;
-        w.hs = r % t.hsets;
-        w.b = r / t.hsets;
+        const int sets = t.qtiles_div.div(r);
+        w.qt = r - sets * t.qtiles;
+        w.b = t.hsets_div.div(sets);
+        w.hs = sets - w.b * t.hsets;
         w.len = key_count(a, w.b);
         w.tiles = (w.len + kTile - 1) / kTile;
         w.j0 = min(w.tiles, w.share * t.dq_per);
@@ -499,7 +520,11 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     };
 
     if (threadIdx.x == 0) {
-        for (uint64_t *bar : {&qfull, &qempty, &sfull[0], &sfull[1], &dpfull, &dqfull, &drain})
+        for (int s = 0; s < NQ; ++s) {
+            mbar_init(smem_addr(&qfull[s]), 1);
+            mbar_init(smem_addr(&qempty[s]), 1);
+        }
+        for (uint64_t *bar : {&sfull[0], &sfull[1], &dpfull, &dqfull, &drain})
             mbar_init(smem_addr(bar), 1);
         mbar_init(smem_addr(&dsfull), 8);
         for (int i = 0; i < 4; ++i)
@@ -540,12 +565,13 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 const int b = w.b, hs = w.hs, qt = w.qt, n = w.n, hk = hs / t.hs_kv;
                 if (n == 0)
                     continue;
-                ok = wait_or_abort(smem_addr(&qempty), (iq & 1u) ^ 1u, abort);
+                const uint32_t qs = iq % NQ, at = base + qs * 2 * TB, qbar = smem_addr(&qfull[qs]);
+                ok = wait_or_abort(smem_addr(&qempty[qs]), ((iq / NQ) & 1u) ^ 1u, abort);
                 if (!ok)
                     break;
-                mbar_expect_tx(smem_addr(&qfull), 2 * TB);
-                load(&qmap, base + L::q, smem_addr(&qfull), hs * t.gp, qt * (kTile / t.gp), b * t.qb);
-                load(&gmap, base + L::g, smem_addr(&qfull), hs * t.gp, qt * (kTile / t.gp), b * t.gb);
+                mbar_expect_tx(qbar, 2 * TB);
+                load(&qmap, at + L::q, qbar, hs * t.gp, qt * (kTile / t.gp), b * t.qb);
+                load(&gmap, at + L::g, qbar, hs * t.gp, qt * (kTile / t.gp), b * t.gb);
                 ++iq;
                 for (int j = 0; j < n && ok; ++j) {
                     const uint32_t ks = ik % NK, vs = iv % NV;
@@ -564,8 +590,8 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 }
             }
             if (!ok) { // let the copies already issued land before the CTA exits (each wait bounded)
-                if (iq)
-                    mbar_wait(smem_addr(&qfull), (iq - 1) & 1u);
+                for (uint32_t j = iq > (uint32_t)NQ ? iq - NQ : 0; j < iq; ++j)
+                    mbar_wait(smem_addr(&qfull[j % NQ]), (j / NQ) & 1u);
                 for (uint32_t j = ik > (uint32_t)NK ? ik - NK : 0; j < ik; ++j)
                     mbar_wait(smem_addr(&kfull[j % NK]), (j / NK) & 1u);
                 for (uint32_t j = iv > (uint32_t)NV ? iv - NV : 0; j < iv; ++j)
@@ -583,32 +609,49 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 for (int k = 0; k < DP / 16; ++k)
                     umma_bf16(col, ad + (kmajor_step(k) >> 4), bd + (kmajor_step(k) >> 4), idesc_s, k != 0);
             };
-            auto scores = [&](uint32_t x) { // s of key tile x (counted over all items)
+            auto scores = [&](uint32_t x, uint32_t m) { // s of key tile x (counted over all items) for item m
                 if (!wait_or_abort(smem_addr(&kfull[x % NK]), (x / NK) & 1u, abort))
                     return false;
                 tc_fence_after();
-                product(s_col + 128 * (x & 1u), qd, base + L::k + (x % NK) * TB);
+                product(s_col + 128 * (x & 1u), qd + ((m % NQ * 2 * TB) >> 4), base + L::k + (x % NK) * TB);
                 umma_commit(smem_addr(&sfull[x & 1u]));
                 return true;
             };
-            auto dps = [&](uint32_t x) {
+            auto first = [&](uint32_t x, uint32_t m) {
+                return wait_or_abort(smem_addr(&qfull[m % NQ]), (m / NQ) & 1u, abort) && scores(x, m);
+            };
+            auto dps = [&](uint32_t x, uint32_t m) {
                 if (!wait_or_abort(smem_addr(&vfull[x % NV]), (x / NV) & 1u, abort))
                     return false;
                 tc_fence_after();
-                product(dp_col, gd, base + L::v + (x % NV) * TB);
+                product(dp_col, gd + ((m % NQ * 2 * TB) >> 4), base + L::v + (x % NV) * TB);
                 umma_commit(smem_addr(&dpfull));
                 umma_commit(smem_addr(&vempty[x % NV]));
                 return true;
             };
-            for (int i = blockIdx.x; i < t.dq_items && ok; i += gridDim.x) {
-                const int n = decode(i).n;
-                if (n == 0)
-                    continue;
-                ok = wait_or_abort(smem_addr(&qfull), iq & 1u, abort) && scores(it) && dps(it) && (n == 1 || scores(it + 1));
+            // The item after i that has keys: its number of key tiles (0: there is none).
+            auto next = [&](int &i) {
+                for (i += gridDim.x; i < t.dq_items; i += gridDim.x) {
+                    const int n = decode(i).n;
+                    if (n)
+                        return n;
+                }
+                return 0;
+            };
+            int i = (int)blockIdx.x - (int)gridDim.x, n = next(i);
+            ok = n == 0 || first(0, 0);
+            while (n && ok) { // the first scores of the item have been issued
+                const int n2 = next(i);
+                ok = dps(it, iq) && (n == 1 || scores(it + 1, iq));
                 if (n == 1 && ok)
-                    umma_commit(smem_addr(&qempty));
+                    umma_commit(smem_addr(&qempty[iq % NQ]));
                 for (int j = 0; j < n && ok; ++j) {
                     const uint32_t x = it + j;
+                    // With two stages of q: the next item's first scores under this item's last arithmetic.
+                    if (NQ == 2 && j + 1 == n && n2 && !first(x + 1, iq + 1)) {
+                        ok = false;
+                        break;
+                    }
                     ok = wait_or_abort(smem_addr(&dsfull), x & 1u, abort);
                     if (!ok)
                         break;
@@ -620,14 +663,17 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                                 idesc_d, j > 0 || k > 0);
                     umma_commit(smem_addr(&kempty[x % NK]));
                     if (j + 1 < n) {
-                        ok = dps(x + 1) && (j + 2 >= n || scores(x + 2));
+                        ok = dps(x + 1, iq) && (j + 2 >= n || scores(x + 2, iq));
                         if (j + 2 == n && ok)
-                            umma_commit(smem_addr(&qempty));
+                            umma_commit(smem_addr(&qempty[iq % NQ]));
                     } else
                         umma_commit(smem_addr(&dqfull));
                 }
                 it += n;
                 ++iq;
+                if (NQ == 1 && n2 && ok)
+                    ok = first(it, iq);
+                n = n2;
             }
             umma_commit(smem_addr(&drain));
             mbar_wait(smem_addr(&drain), 0u); // every MMA issued has completed before tensor memory is freed
@@ -639,14 +685,17 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         const float2 mul = make_float2(a.scale2, a.scale2);
         uint32_t it = 0, items = 0, nx = 0;
         bool ok = true;
+        auto stat_at = [&](const Item &w) {
+            return ((int64_t)w.b * t.hsets + w.hs) * t.rows + w.qt * kTile + 32 * (warp & 3) + lane;
+        };
+        Item w = decode(min((int)blockIdx.x, t.dq_items - 1));
+        float lse2 = t.lse2[stat_at(w)], delta = t.delta[stat_at(w)];
         for (int i = blockIdx.x; i < t.dq_items && ok; i += gridDim.x) {
-            const Item w = decode(i);
             const int b = w.b, hs = w.hs, qt = w.qt, len = w.len, n = w.n;
             const int row = qt * kTile + 32 * (warp & 3) + lane;
-            const int iq = row / t.gp, h = hs * t.gp + row % t.gp;
-            const int64_t at = ((int64_t)b * t.hsets + hs) * t.rows + row;
-            const float2 l2 = make_float2(-t.lse2[at], -t.lse2[at]);
-            float delta = t.delta[at];
+            const int iq = row >> t.lgp, h = hs * t.gp + (row & (t.gp - 1));
+            const int64_t at = stat_at(w);
+            const float2 l2 = make_float2(-lse2, -lse2);
             for (int j = 0; j < n; ++j, ++it) {
                 const uint32_t sc = s_col + 128 * (it & 1u) + 64 * half + lanes;
                 if (!wait_or_abort(smem_addr(&sfull[it & 1u]), (it >> 1) & 1u, abort)) {
@@ -728,6 +777,13 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             }
             if (!ok)
                 break;
+            // The next item's statistics are on their way while this one's products end.
+            const Item done = w;
+            if (i + gridDim.x < t.dq_items) {
+                w = decode(i + gridDim.x);
+                lse2 = t.lse2[stat_at(w)];
+                delta = t.delta[stat_at(w)];
+            }
             if (n > 0) {
                 if (!wait_or_abort(smem_addr(&dqfull), items & 1u, abort)) {
                     ok = false;
@@ -737,7 +793,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 ++items;
             }
             // Each warpgroup stores half of the channels; with shares, the partial sum.
-            float *part = t.dq_part + (((int64_t)w.share * t.dq_tail + w.part) * kTile + row - qt * kTile) * a.D;
+            float *part = t.dq_part + (((int64_t)done.share * t.dq_tail + done.part) * kTile + row - qt * kTile) * a.D;
 #pragma unroll
             for (int c = 0; c < DP / 64; ++c) {
                 uint32_t x[32] = {};
@@ -746,21 +802,17 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     tmem_ld32(dq_col + d0 + lanes, x);
                     tmem_wait_ld();
                 }
-                if (iq >= a.Nq || (w.part >= 0 && n == 0)) // (a share without keys is not read)
+                if (iq >= a.Nq || (done.part >= 0 && n == 0)) // (a share without keys is not read)
                     continue;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (d0 + 8 * e >= a.D)
-                        continue;
-                    float v[8];
+                for (int e = 0; e < 32; ++e)
+                    x[e] = n > 0 ? __float_as_uint(__uint_as_float(x[e]) * a.scale) : 0u;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        v[k] = n > 0 ? __uint_as_float(x[8 * e + k]) * a.scale : 0.0f;
-                    if (w.part < 0)
-                        Row<__nv_bfloat16, 8, true>::store(a.dq.row(b, iq, h) + d0 + 8 * e, v);
+                for (int e = 0; e < 2; ++e) // 16 channels
+                    if (done.part < 0)
+                        store16(a.dq.row(b, iq, h) + d0 + 16 * e, packed(x + 16 * e), a.D - d0 - 16 * e, t.dq_wide);
                     else
-                        Row<float, 8, true>::store(part + d0 + 8 * e, v);
-                }
+                        store16(part + d0 + 16 * e, x + 16 * e, a.D - d0 - 16 * e);
             }
             tc_fence_before();
         }
@@ -890,7 +942,13 @@ tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t st
     t.dq_shares = (int)p.dq_shares;
     t.dq_per = (int)p.dq_per;
     t.gp = (int)p.gp;
+    while (t.gp >> t.lgp > 1)
+        ++t.lgp;
     t.hsets = (int)p.hsets;
+    t.qtiles_div = FastDiv((uint32_t)std::max<int64_t>(1, p.qtiles));
+    t.hsets_div = FastDiv((uint32_t)p.hsets);
+    t.dq_wide = rows_wide(a.dq, a.B, a.Nq, a.Hq);
+    t.wide = rows_wide(a.dk, a.B, a.Nk, a.Hkv) && rows_wide(a.dv, a.B, a.Nk, a.Hkv);
     t.rows = (int)p.rows;
     t.qtiles = (int)p.qtiles;
     t.ktiles = (int)p.ktiles;

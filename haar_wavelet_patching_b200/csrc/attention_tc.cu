@@ -46,6 +46,7 @@ struct TcArgs {
     int wide;     // rows of o start on 32 bytes
     int nqt;      // items per (batch, head set): 256 rows each
     int hsets;    // Hq / gp
+    FastDiv nqt_div, hsets_div;
     int items;    // CTAs' worth: whole ones, then the shares of the others
     int whole, tail;
     int qb, kb, kh, vb, vh; // coordinate factors: 0 for a broadcast dimension
@@ -57,10 +58,10 @@ struct Item {
 
 __device__ __forceinline__ void place(const TcArgs &t, int r, Item &w)
 {
-    w.row0 = r % t.nqt * (2 * kTile);
-    r /= t.nqt;
-    w.hs = r % t.hsets;
-    w.b = r / t.hsets;
+    const int sets = t.nqt_div.div(r);
+    w.row0 = (r - sets * t.nqt) * (2 * kTile);
+    w.b = t.hsets_div.div(sets);
+    w.hs = sets - w.b * t.hsets;
 }
 
 __device__ __forceinline__ Item decode(const TcArgs &t, int i)
@@ -489,9 +490,11 @@ tok_status attn_tc_forward(const AttnArgs &a, cudaStream_t stream)
     t.gp = attn_tc_group(a.G);
     while (t.gp >> t.lgp > 1)
         ++t.lgp;
-    t.wide = aligned(a.o.p, 32) && (a.B <= 1 || a.o.b % 16 == 0) && a.o.n % 16 == 0 && (a.Hq <= 1 || a.o.h % 16 == 0);
+    t.wide = rows_wide(a.o, a.B, a.Nq, a.Hq);
     t.hsets = a.Hq / t.gp;
     t.nqt = (int)(((int64_t)a.Nq * t.gp + 2 * kTile - 1) / (2 * kTile));
+    t.nqt_div = FastDiv((uint32_t)t.nqt);
+    t.hsets_div = FastDiv((uint32_t)t.hsets);
     const Rounds r = plan(a.B, a.Nq, a.Nk, a.Hq, a.Hkv, a.D);
     t.a.splits = (int)r.shares;
     t.whole = (int)r.whole;
