@@ -68,22 +68,23 @@ struct BwdArgs {
 // lse2 and delta of every query row, in tile order: a block per tile of 128, 8 lanes per row, four rows in
 // flight per lane.
 constexpr int kStatRows = kTile / 32;
-__global__ void __launch_bounds__(256) attn_stats_kernel(const BwdArgs t, float *lse2, float *delta)
+template <int DP> __global__ void __launch_bounds__(256) attn_stats_kernel(const BwdArgs t, float *lse2, float *delta)
 {
     const AttnArgs &a = t.a;
     const int c = threadIdx.x & 7;
-    const int set = (int)blockIdx.x / t.qtiles, tile = (int)blockIdx.x - set * t.qtiles;
-    const int b = set / t.hsets, h0 = (set - b * t.hsets) * t.gp, lgp = 31 - __clz(t.gp);
+    const int set = t.qtiles_div.div(blockIdx.x), tile = (int)blockIdx.x - set * t.qtiles;
+    const int b = t.hsets_div.div(set), h0 = (set - b * t.hsets) * t.gp, lgp = t.lgp;
     const int r0 = tile * kTile + (int)(threadIdx.x >> 3);
     const int64_t at0 = (int64_t)blockIdx.x * kTile + (threadIdx.x >> 3);
-    uint4 x[kStatRows][2], y[kStatRows][2];
+    constexpr int NSUB = DP / 64;
+    uint4 x[kStatRows][NSUB], y[kStatRows][NSUB];
     float l[kStatRows];
 #pragma unroll
     for (int k = 0; k < kStatRows; ++k) {
         const int r = r0 + 32 * k, h = h0 + (r & (t.gp - 1)), iq = r >> lgp;
         const bool live = iq < a.Nq;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < NSUB; ++e) {
             const int d = 8 * c + 64 * e;
             x[k][e] = load16(a.go.row(b, iq, h) + d, live && d < a.D);
             y[k][e] = load16(a.o.row(b, iq, h) + d, live && d < a.D);
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(256) attn_stats_kernel(const BwdArgs t, float 
     for (int k = 0; k < kStatRows; ++k) {
         float s = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < NSUB; ++e)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 s = fmaf(bf16_lo(word(x[k][e], w)), bf16_lo(word(y[k][e], w)), s);
@@ -965,8 +966,8 @@ tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t st
     t.vh = a.Hkv > 1 && a.v.h == 0 ? 0 : 1;
     tok_status st = TOK_OK;
     if (a.Nq > 0) {
-        attn_stats_kernel<<<(unsigned)(p.stat_floats / kTile), 256, 0, stream>>>(
-            t, workspace, workspace + p.stat_floats);
+        const auto stats = a.D <= 64 ? attn_stats_kernel<64> : attn_stats_kernel<128>;
+        stats<<<(unsigned)(p.stat_floats / kTile), 256, 0, stream>>>(t, workspace, workspace + p.stat_floats);
         st = launch_status();
     }
     if (st == TOK_OK && a.Nq > 0) {

@@ -86,6 +86,16 @@ __device__ __forceinline__ Item decode(const TcArgs &t, int i)
     return w;
 }
 
+// Row of a split item in the partial results, and these' statistics (maximum, sum).
+__device__ __forceinline__ int64_t part_row(const TcArgs &t, const Item &w, int row)
+{
+    return ((int64_t)w.split * t.tail + w.part) * (2 * kTile) + (row - w.row0);
+}
+__device__ __forceinline__ float2 *part_stats(const TcArgs &t)
+{
+    return reinterpret_cast<float2 *>(t.a.part + (int64_t)t.a.splits * t.tail * (2 * kTile) * t.a.D);
+}
+
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -260,7 +270,6 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         const int r = warp >> 2;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t sc = s_col[r] + lanes, oc = o_col[r] + lanes;
-        const int64_t part_rows = (int64_t)t.tail * (2 * kTile); // of one split
         const bool odd_scale = !(a.scale2 > 0.0f);
         const float mul = odd_scale ? 1.0f : a.scale2;
         uint32_t it = 0, ns = 0, nitem = 0;
@@ -271,7 +280,6 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             const int iq = row >> t.lgp, h = w.hs * t.gp + (row & (t.gp - 1));
             const bool live = iq < a.Nq;
             const int64_t stat = ((int64_t)w.b * a.Hq + h) * a.Nq + iq;
-            const int64_t part_row = w.split * part_rows + (int64_t)w.part * (2 * kTile) + (row - w.row0);
             float m = -INFINITY, l = 0.0f; // maximum (log2 units) that the weights are relative to; their sum
             for (int j = 0; j < w.ntiles; ++j, ++ns) {
                 if (!wait_or_abort(smem_addr(&sfull[r]), ns & 1u, abort)) {
@@ -379,7 +387,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 it += 2 * w.ntiles;
             }
             const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            if (w.part < 0) {
+            if (__builtin_expect(w.part < 0, 1)) {
                 uint32_t o[DP] = {};
                 if (w.ntiles > 0) {
 #pragma unroll
@@ -404,7 +412,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     uint32_t o[32];
                     tmem_ld32(oc + 32 * c, o);
                     tmem_wait_ld();
-                    float *dst = a.part + part_row * a.D + 32 * c;
+                    float *dst = a.part + part_row(t, w, row) * a.D + 32 * c;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (live && 32 * c + 8 * e < a.D)
@@ -417,8 +425,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     if (a.lse)
                         a.lse[stat] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
                 } else {
-                    reinterpret_cast<float2 *>(a.part + a.splits * part_rows * a.D)[part_row] =
-                        make_float2(w.ntiles > 0 ? m : -INFINITY, l);
+                    part_stats(t)[part_row(t, w, row)] = make_float2(w.ntiles > 0 ? m : -INFINITY, l);
                 }
             }
         }
@@ -444,8 +451,7 @@ __global__ void __launch_bounds__(128) attn_tail_join_kernel(const TcArgs t)
     const int row = w.row0 + (int)(at % (2 * kTile)), iq = row >> t.lgp, h = w.hs * t.gp + (row & (t.gp - 1));
     if (iq >= a.Nq)
         return;
-    join_parts(a.part + at * a.D, reinterpret_cast<const float2 *>(a.part + a.splits * rows * a.D) + at, rows, a.splits,
-               a.D, a.o.row(w.b, iq, h), a.lse ? a.lse + ((int64_t)w.b * a.Hq + h) * a.Nq + iq : nullptr);
+    join_parts(a.part + at * a.D, part_stats(t) + at, rows, a.splits, a.D, a.o.row(w.b, iq, h), a.lse ? a.lse + ((int64_t)w.b * a.Hq + h) * a.Nq + iq : nullptr);
 }
 
 // Items of 256 query rows, the last round's split over the keys.  (2 x 3520 x 3520, 16 heads: 448 items,
