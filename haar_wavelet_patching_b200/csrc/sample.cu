@@ -28,6 +28,9 @@
 //     kCap tokens is narrowed on the bits of x, to a single value if need be, whose ties
 //     are counted in index order.
 // With few rows a cluster of up to 8 CTAs shares one, a contiguous slice each.
+// Measured, rows of 64,000: 4 with all filters 17 us; 255 in fp32 under top_p 0.9 75 us (65 MB: 10 us
+// of HBM); 880 in bf16 under top_k 500 63 us (17 us of HBM).  Sorting every picked token outright
+// instead of the limit's bin only: 19 and 86 us for the first and the last.
 #include <algorithm>
 
 #include "tma.cuh"
