@@ -1,4 +1,5 @@
-"""B200 Haar patcher / unpatcher and FSQ quantizer: Python binding of libtok.so.
+"""B200 Haar patcher / unpatcher, FSQ quantizer and operators of a model over the tokens (rotary
+positions, cross attention, drawing codes): Python binding of libtok.so.
 
 The functions named like the C ABI (``tok_haar_fwd`` ...) marshal torch CUDA
 tensors into the C calls of ``include/tok.h`` and nothing else: every step of
@@ -6,7 +7,7 @@ the computation runs in the library's sm_100a kernels.  There is no CPU path;
 a missing library or a CPU tensor raises.
 
 Convenience wrappers (``haar_fwd``, ``haar_inv``, ``fsq_encode``,
-``fsq_decode``) allocate outputs with torch and call the same entry points.
+``fsq_decode``, ``cross_attention``, ``sample_codes`` ...) allocate outputs with torch and call the same entry points.
 """
 import ctypes
 import os

@@ -333,6 +333,29 @@ def test_caller_workspace_and_untouched_surroundings(Nk):
         assert e.value.status == hwp.TOK_ERR_SHAPE
 
 
+@pytest.mark.parametrize("B,Nq,Nk,Hq,Hkv,D", [(4, 1, 3000, 8, 2, 128), (1, 2437, 1500, 16, 16, 128), (2, 1300, 900, 16, 4, 64)])
+def test_two_streams_at_once(B, Nq, Nk, Hq, Hkv, D):
+    """Calls that run beside each other on two streams, each with partial results in a workspace of its own."""
+    data = [[randn(B, n, h, D, seed=10 * i + s) for s, (n, h) in enumerate(((Nq, Hq), (Nk, Hkv), (Nk, Hkv), (Nq, Hq)))]
+            for i in range(2)]
+    def call(q, k, v, go):
+        o, lse = hwp.cross_attention(q, k, v, with_lse=True)
+        return (o, lse) + tuple(hwp.cross_attention_backward(q, k, v, o, lse, go))
+    want = [call(*d) for d in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(call(*data[i]))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for run in runs:
+            assert all(torch.equal(a, b) for a, b in zip(w, run))
+    hwp.tok_check_device()
+
+
 def test_empty_calls():
     e = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
     assert hwp.cross_attention(e(0, 3, 2, 64), e(0, 5, 2, 64), e(0, 5, 2, 64)).numel() == 0
