@@ -349,8 +349,10 @@ HeadsView view(const tok_heads *t)
     return HeadsView{static_cast<__nv_bfloat16 *>(t->ptr), t->batch, t->token, t->head};
 }
 
-// Query rows per key head from which the tensor-core kernel takes a call.
-constexpr int64_t kTcRows = 64;
+// Query rows per key head up to which the kernel for few rows takes a call.  Its time grows with every 16 rows, the
+// tensor cores' hardly at all (us, few rows / tensor cores, at 48, 64 and 96 rows: 8 x 3520 keys, 32
+// heads of 128 on 8: 36 / 38, 45 / 39, 56 / 39; 32 x 300 keys, 16 heads of 64: 22 / 27, 27 / 27, 37 / 27).
+constexpr int64_t kTcRows = 48;
 
 bool wants_tc(const Dims &d) { return d.Nq * (d.Hq / d.Hkv) > kTcRows && d.Nk > 0; }
 
