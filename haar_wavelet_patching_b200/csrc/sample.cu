@@ -1061,7 +1061,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         uint32_t count = 0;
         auto sum = [&](float x0) TOK_INLINE {
             const double w = weight_at((double)fmaxf(x0, xcut) - xmax_d);
-            const bool in = w >= floor_w;
+            // (xcut is rounded and may be xmax itself: what lies below it has no weight, whatever w is there)
+            const bool in = x0 >= xcut && w >= floor_w;
             mine += in ? (uint64_t)__double_as_longlong(w + 4503599627370496.0) : 0ull;
             count += in;
         };

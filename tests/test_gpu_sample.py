@@ -264,3 +264,54 @@ def test_two_streams_at_once():
         x, y = hwp.sample_codes(*a, top_p=0.8, stream=s1), hwp.sample_codes(*b, top_k=k, stream=s2)
         torch.cuda.synchronize()
         assert torch.equal(x, want[0]) and torch.equal(y, want[1])
+
+
+def drawn(x, u, temperature, min_p, idx, lp, label):
+    """One draw without a rank limit against the running sum in 64 bits.  Weights are off by at most half a
+    unit of 2^-44 and 2^-44 of themselves (the exponential), so the sums before and through the drawn token are
+    off by at most V 2^-45 + 2^-44 total, and so is u times the total: a slack of twice both; a token below half a unit
+    has no weight at all."""
+    x = np.where(np.isnan(x), -np.inf, x.astype(np.float64))
+    t, floor = float(np.float32(temperature)), float(np.float32(min_p))
+    w = np.exp((x - x.max()) / t)
+    w[w < floor] = 0.0
+    c = np.cumsum(w)
+    slack = 2 * (len(x) * 2.0 ** -45 + 2.0 ** -44 * c[-1])
+    assert 0 <= idx < len(x), f"{label}: index {idx}"
+    assert w[idx] > 2.0 ** -45 * (1 - 2.0 ** -40), f"{label}: drew {idx}, whose weight is {w[idx]}"
+    at = min(max(float(u), 0.0), 1.0) * c[-1]
+    assert c[idx] - w[idx] - slack <= at <= c[idx] + slack, f"{label}: drew {idx}"
+    want = math.log(w[idx] / c[-1])
+    assert abs(lp - want) <= 2.0 ** -24 * abs(want) + 2.0 ** -26, f"{label}: {lp}, expected {want}"
+
+
+COLD = [1e-4, 1e-5, 1e-6, 1e-7, 1e-8, 1e-12, 1e-38, 1e-45]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [V0, 4097])
+@pytest.mark.parametrize("R", [4, 40, 320])
+@pytest.mark.parametrize("min_p", [0.0, 0.3])
+def test_temperatures_next_to_zero(R, V, dtype, min_p):
+    """Temperatures at which a token's reach is below a step of the largest logit: tokens far below it, -inf
+    and NaN, in front, behind and between, have no weight, whatever u is."""
+    for top in (1.0, 9.0, 24.0, 100.0, 200.0, 1000.0):
+        x, _ = data(R, V, dtype=torch.float32, seed=int(top))
+        x = top - 0.02 * top - 0.1 * x.abs()
+        x[:, : V // 8] = -math.inf
+        x[:, V - V // 8:] = math.nan
+        x[1::2, V - V // 8:] = -math.inf
+        x[:, V // 2: V // 2 + 40: 8] = top
+        x[2::3, V // 3] = top * (1 - 2.0 ** -23)  # one step below
+        x = x.to(dtype)
+        temperature = torch.tensor([COLD[r % len(COLD)] for r in range(R)], device="cuda")
+        u = torch.tensor([(0.0, 0.5, 1 - 2.0 ** -24, 1.0, 0.3)[r // len(COLD) % 5] if R > 4 else (0.0, 0.5, 1.0, 0.3)[r]
+                          for r in range(R)], device="cuda")
+        if R == 4:
+            temperature = temperature.roll(int(top) % 4) * 1e-2
+        idx = torch.full((R,), -7, dtype=torch.int32, device="cuda")
+        lp = torch.full((R,), 7.0, device="cuda")
+        hwp.tok_sample_codes(x, u, idx, lp, temperature=temperature, min_p=min_p)
+        xs, i, p, t, us = x.float().cpu().numpy(), idx.tolist(), lp.tolist(), temperature.tolist(), u.tolist()
+        for r in range(R if R < 320 else 120):
+            drawn(xs[r], us[r], t[r], min_p, i[r], p[r], f"top {top} row {r} T {t[r]} u {us[r]}")
