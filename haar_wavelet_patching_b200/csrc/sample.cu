@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
             sh.pub[2] = 0;
         __syncthreads();
         // Sums of the bits of 2^52 + w: the number of terms times the bits of 2^52 is taken off at the end.
-        // A token without a weight (-inf, NaN or below xcut) counts as one at xcut, which rounds to 0.
+        // A token without a weight (-inf, NaN or below xcut, which is rounded and may be xmax) counts as 2^52 + 0.
         uint64_t sum_all = 0, sum_above = 0;
         uint32_t n_all = 0, n_above = 0, n_mine = 0;
         auto pick = [&](float x, int idx) TOK_INLINE {
@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         auto weigh = [&](float x0) TOK_INLINE -> bool { // whether the token is one of the bin's
             const float x = fmaxf(x0, xcut);
             const double wd = weight_at((double)x - xmax_d);
-            const uint64_t bits = (uint64_t)__double_as_longlong(wd + 4503599627370496.0);
+            const uint64_t bits = x0 >= xcut ? (uint64_t)__double_as_longlong(wd + 4503599627370496.0) : kBias;
             sum_all += bits;
             const bool in = x >= above;
             if (in) {

@@ -315,3 +315,24 @@ def test_temperatures_next_to_zero(R, V, dtype, min_p):
         xs, i, p, t, us = x.float().cpu().numpy(), idx.tolist(), lp.tolist(), temperature.tolist(), u.tolist()
         for r in range(R if R < 320 else 120):
             drawn(xs[r], us[r], t[r], min_p, i[r], p[r], f"top {top} row {r} T {t[r]} u {us[r]}")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R", [3, 60, 320])
+def test_cold_nucleus_of_equal_values(R, dtype):
+    """Many equal largest values under top_p: the tokens below them do not count in its total."""
+    V, n = 600, 401
+    g = torch.Generator(device="cuda").manual_seed(14)
+    for top in (1.0, 24.0, 1000.0):
+        x = torch.full((R, V), top, device="cuda")
+        for r in range(R):
+            x[r, torch.randperm(V, generator=g, device="cuda")[: V - n]] = (0.5 * top, -math.inf, math.nan)[r % 3]
+        u = torch.rand(R, generator=g, device="cuda")
+        for t in (1e-6, 1e-8, 1e-38):
+            for top_p in (0.3, 0.5, 0.6):
+                for s in (dict(), dict(min_p=0.2)):
+                    compare(x.to(dtype)[:60], u[:60], f"top {top}", temperature=t, top_p=top_p, **s)
+                    if R > 60:
+                        want = hwp.sample_codes(x[:60].to(dtype), u[:60].contiguous(), temperature=t, top_p=top_p, **s)
+                        got = hwp.sample_codes(x.to(dtype), u, temperature=t, top_p=top_p, **s)
+                        assert torch.equal(got[:60], want)
