@@ -394,3 +394,25 @@ def test_a_step_of_a_code_model():
     assert bool((logits.float().gather(1, idx.long()[:, None])[:, 0] >= top).all())
     latent = hwp.fsq_decode(idx.view(2, 1, h, w), torch.randn(6, 16, device="cuda"))
     assert latent.shape == (2, 16, 1, h, w) and bool(latent.isfinite().all())
+
+
+@pytest.mark.parametrize("Nq,Nk,H,D,dead", [(3, 400, 2, 64, 130), (2, 6000, 2, 128, 3000), (300, 400, 2, 64, 130),
+                                            (300, 400, 2, 128, 256), (1200, 2600, 5, 128, 1900), (260, 700, 3, 64, 700)])
+@pytest.mark.parametrize("low", [-math.inf, torch.finfo(torch.bfloat16).min])
+@pytest.mark.parametrize("level", [-150.0, 0.0, 90.0])
+def test_keys_masked_through_a_channel(Nq, Nk, H, D, dead, low, level):
+    """Keys ruled out by a channel of their own (1 in the queries, -inf or the lowest number in the keys): whole
+    tiles of them before keys whose scores lie at any level."""
+    q, k, v = (randn(1, n, H, D, seed=s, spread=f) for n, s, f in ((Nq, 1, 1.0), (Nk, 2, 0.3), (Nk, 3, 1.0)))
+    q[..., 0], q[..., 1] = 1.0, 1.0
+    k[..., 0], k[..., 1] = 0.0, level
+    live = k[:, dead:].contiguous(), v[:, dead:].contiguous()
+    k[:, :dead, :, 0] = low
+    o, lse = hwp.cross_attention(q, k, v, scale=1.0, with_lse=True)
+    if dead == Nk:
+        if low == -math.inf:
+            assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+        return
+    ref = reference(q, *live, None, 1.0)
+    check(o, ref, "o")
+    check(lse, ref, "lse")
