@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 2) attn_rows_kernel(const Attn
     const int iq = r / a.G, h = hk * a.G + r % a.G;
     const int64_t stat = ((int64_t)b * a.Hq + h) * a.Nq + iq;
     const int64_t nstat = (int64_t)a.B * a.Hq * a.Nq;
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l; // (a sum of NaN gives NaN, no key 0)
     for (int d = 8 * (threadIdx.x & 7); d < a.D; d += 64) {
         float v[8];
 #pragma unroll
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 2) attn_rows_kernel(const Attn
     if ((threadIdx.x & 7) == 0) {
         if (a.splits == 1) {
             if (a.lse)
-                a.lse[stat] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                a.lse[stat] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         } else {
             float *ml = a.part + a.splits * nstat * a.D + 2 * (split * nstat + stat);
             ml[0] = m;

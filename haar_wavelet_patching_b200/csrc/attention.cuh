@@ -84,7 +84,7 @@ __device__ __forceinline__ void join_parts(const float *part, const float2 *ml, 
 #pragma unroll
     for (int i = 16; i; i >>= 1)
         m = fmaxf(m, __shfl_xor_sync(~0u, m, i));
-    const float f = ms == -INFINITY ? 0.0f : exp2_fast(ms - m);
+    const float f = ms == -INFINITY ? ls : exp2_fast(ms - m); // (ls is 0 there, or NaN: no number was the largest)
     float l = f * ls, v[4] = {};
 #pragma unroll
     for (int i = 16; i; i >>= 1)
@@ -101,7 +101,7 @@ __device__ __forceinline__ void join_parts(const float *part, const float2 *ml, 
                 v[j] += fs * x[j];
         }
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     if (d < D) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -109,7 +109,7 @@ __device__ __forceinline__ void join_parts(const float *part, const float2 *ml, 
         Row<__nv_bfloat16, 4, true>::store(o + d, v);
     }
     if (lane == 0 && lse)
-        *lse = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        *lse = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 constexpr int kMaxSplits = 32; // parts of a query row: a lane of the join each

@@ -392,7 +392,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 ++nitem;
                 it += 2 * w.ntiles;
             }
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l; // (a sum of NaN gives NaN, no key 0)
             if (__builtin_expect(w.part < 0, 1)) {
                 uint32_t o[DP] = {};
                 if (w.ntiles > 0) {
@@ -429,7 +429,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             if (live) {
                 if (w.part < 0) {
                     if (a.lse)
-                        a.lse[stat] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                        a.lse[stat] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
                 } else {
                     part_stats(t)[part_row(t, w, row)] = make_float2(w.ntiles > 0 ? m : -INFINITY, l);
                 }

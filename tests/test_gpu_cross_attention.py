@@ -416,3 +416,26 @@ def test_keys_masked_through_a_channel(Nq, Nk, H, D, dead, low, level):
     ref = reference(q, *live, None, 1.0)
     check(o, ref, "o")
     check(lse, ref, "lse")
+
+
+@pytest.mark.parametrize("B,Nq,Nk,H,D", [(1, 3, 90, 2, 64), (1, 2, 6000, 2, 128), (1, 300, 300, 2, 64),
+                                         (1, 1200, 2600, 5, 128)])
+def test_nan_in_live_places_shows(B, Nq, Nk, H, D):
+    """A query, or a key within the length, of NaN: what the formula makes NaN is NaN, the statistics as well, and
+    nothing else changes."""
+    q, k, v, go = (randn(B, n, H, D, seed=s) for n, s in ((Nq, 1), (Nk, 2), (Nk, 3), (Nq, 4)))
+    clean, clean_lse = hwp.cross_attention(q, k, v, with_lse=True)
+    row = Nq // 2
+    q[0, row, 1] = math.nan
+    o, lse = hwp.cross_attention(q, k, v, with_lse=True)
+    assert bool(o[0, row, 1].isnan().all()) and bool(lse[0, 1, row].isnan())
+    o[0, row, 1], lse[0, 1, row] = clean[0, row, 1], clean_lse[0, 1, row]
+    assert torch.equal(o, clean) and torch.equal(lse, clean_lse)
+    q[0, row, 1] = 1.0
+    k[0, Nk - 2, 0, 5] = math.nan
+    o, lse = hwp.cross_attention(q, k, v, with_lse=True)
+    assert bool(o[:, :, 0].isnan().all()) and bool(lse[:, 0].isnan().all())
+    assert bool(o[:, :, 1].isfinite().all()) and bool(lse[:, 1].isfinite().all())
+    dq, dk, dv = hwp.cross_attention_backward(q, k, v, o, lse, go)
+    for g in (dq, dk, dv):
+        assert bool(g[:, :, 0].isnan().all()) and bool(g[:, :, 1].isfinite().all())
