@@ -38,7 +38,8 @@ struct RopeArgs {
     int units, rot_units; // units of V pairs per head: rotated ones, then copied ones (2V channels each)
     FastDiv units_div, groups_div;
     int H, hg; // heads, heads per thread
-    int64_t items; // units * head groups * tokens
+    uint32_t n0;   // first token of the launch
+    uint32_t items; // units * head groups * tokens of the launch
     float sign;
 };
 
@@ -81,14 +82,14 @@ constexpr int kThreads = 128; // (256: 153 us instead of 146 on the 16x44x80 gri
 template <typename T, int V, bool IL>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs g)
 {
-    const int64_t item = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const uint32_t item = blockIdx.x * kThreads + threadIdx.x;
     if (item >= g.items)
         return;
-    // item = (token * groups + group) * units + unit; 32-bit items (checked by the launcher).
-    const uint32_t tg = g.units_div.div((uint32_t)item);
-    const int unit = (int)((uint32_t)item - tg * (uint32_t)g.units);
-    const uint32_t n = g.groups_div.div(tg);
-    const int h0 = (int)(tg - n * g.groups_div.d) * g.hg, h1 = min(h0 + g.hg, g.H);
+    // item = (token * groups + group) * units + unit; below 2^31 in a launch.
+    const uint32_t tg = g.units_div.div(item);
+    const int unit = (int)(item - tg * (uint32_t)g.units);
+    const uint32_t ln = g.groups_div.div(tg), n = g.n0 + ln;
+    const int h0 = (int)(tg - ln * g.groups_div.d) * g.hg, h1 = h0 + min(g.hg, g.H - h0);
     const T *x = static_cast<const T *>(g.x) + (int64_t)n * g.xt;
     T *y = static_cast<T *>(g.y) + (int64_t)n * g.yt;
 
@@ -306,20 +307,25 @@ tok_status rope_apply(const RopeCall &c, cudaStream_t stream)
     hg = (c.H + (c.H + hg - 1) / hg - 1) / ((c.H + hg - 1) / hg);
     int64_t groups = (c.H + hg - 1) / hg;
     while (threads * groups >= kMax && hg < c.H) { // items are 32-bit
-        hg *= 2;
+        hg = std::min(2 * hg, c.H);
         groups = (c.H + hg - 1) / hg;
     }
-    if (threads * groups >= kMax)
-        return TOK_ERR_SHAPE;
     g.hg = (int)hg;
     g.groups_div = FastDiv((uint32_t)groups);
-    g.items = threads * groups;
     g.sign = c.adjoint ? -1.0f : 1.0f;
-    if (c.dtype == TOK_F32)
-        il ? launch_v<float, true>(v, g, stream) : launch_v<float, false>(v, g, stream);
-    else
-        il ? launch_v<__nv_bfloat16, true>(v, g, stream) : launch_v<__nv_bfloat16, false>(v, g, stream);
-    return launch_status();
+    // (One group where a launch does not hold all tokens; a token has at most 2^15 units then.)
+    const int64_t per_token = g.units * groups, most = (kMax - 1) / per_token;
+    tok_status st = TOK_OK;
+    for (int64_t n0 = 0; n0 < n && st == TOK_OK; n0 += most) {
+        g.n0 = (uint32_t)n0;
+        g.items = (uint32_t)(std::min(most, n - n0) * per_token);
+        if (c.dtype == TOK_F32)
+            il ? launch_v<float, true>(v, g, stream) : launch_v<float, false>(v, g, stream);
+        else
+            il ? launch_v<__nv_bfloat16, true>(v, g, stream) : launch_v<__nv_bfloat16, false>(v, g, stream);
+        st = launch_status();
+    }
+    return st;
 }
 
 } // namespace

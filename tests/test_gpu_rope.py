@@ -190,3 +190,19 @@ def test_empty_other_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, 2 * want)
+
+
+def test_more_than_2_31_thread_items():
+    """A broadcast token turned at every place of a grid of 755 million, three pairs each and no vector that
+    divides them (9 GB)."""
+    dims, sizes, D = (2, 2, 2), (1024, 1024, 720), 6
+    x = randn(1, 1, 1, 1, 1, D, dtype=torch.bfloat16)
+    table = hwp.rope_table(sizes, dims)
+    y = hwp.rope_grid(x.expand(1, *sizes, 1, D), table, sizes, dims)
+    for t in range(0, 1024, 64):
+        part = hwp.rope_grid(x.expand(1, 64, *sizes[1:], 1, D), table, sizes, dims, origin=(t, 0, 0))
+        assert torch.equal(y[:, t:t + 64], part), t
+    tokens = torch.tensor([[0, 0, 0], [970, 1023, 719], [971, 0, 0], [1023, 1023, 719]])
+    got = y[0, tokens[:, 0], tokens[:, 1], tokens[:, 2]]
+    ref, tol = reference(x[0, 0, 0].expand(4, 1, D), [tokens[:, a].double().cuda() for a in range(3)], dims, False)
+    check(got, ref, tol, "far tokens")
