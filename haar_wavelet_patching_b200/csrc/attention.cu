@@ -13,7 +13,6 @@
 // results in split order.  Measured: 8 x 1 query, up to 3520 ragged keys, 32 heads on 8, D 128: 20 us,
 // of them 5 for the join; its 65 MB take 10 at HBM's rate.
 #include <algorithm>
-#include <initializer_list>
 
 #include "attention.cuh"
 
@@ -278,29 +277,6 @@ struct Dims {
                prod_ok({Hq, Nq}, &p) && p <= kIntMax / 2;
     }
 };
-
-struct Axis {
-    int64_t n, s;
-};
-
-// No element of the strided dims (dense block of D) is met twice: each stride leaves room
-// for everything of smaller stride.
-bool nested(std::initializer_list<Axis> dims, int64_t D)
-{
-    Axis a[4];
-    int n = 0;
-    for (const Axis &x : dims)
-        if (x.n > 1)
-            a[n++] = x;
-    std::sort(a, a + n, [](const Axis &x, const Axis &y) { return x.s < y.s; });
-    int64_t span = D;
-    for (int i = 0; i < n; ++i) {
-        if (a[i].s < span)
-            return false;
-        span += (a[i].n - 1) * a[i].s;
-    }
-    return true;
-}
 
 struct View {
     const tok_heads *t;

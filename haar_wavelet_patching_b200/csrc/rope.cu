@@ -15,6 +15,7 @@
 // 6.3 TB/s; fp32 pairs side by side, 10,395 x 12 x 80: 18 us, 4.5 TB/s (a ramp: about two rounds of
 // the SMs); 16 tokens: 2 us.
 #include <algorithm>
+#include <cstdlib>
 
 #include "tma.cuh"
 #include "tok_common.cuh"
@@ -183,16 +184,6 @@ struct RopeCall {
     bool adjoint;
 };
 
-// [n, H, D] with strides (sn, sh, 1): no element twice, either index the outer one.
-bool distinct(int64_t n, int64_t sn, int64_t H, int64_t sh, int64_t D)
-{
-    if (n <= 1)
-        return H <= 1 || sh >= D;
-    if (H <= 1)
-        return sn >= D;
-    return (sh >= D && sn >= (H - 1) * sh + D) || (sn >= D && sh >= (n - 1) * sn + D);
-}
-
 // Bytes from the first to the last element of [n, H, D]; false on overflow or a negative stride.
 bool extent(int64_t n, int64_t sn, int64_t H, int64_t sh, int64_t D, int64_t size, int64_t *out)
 {
@@ -242,7 +233,7 @@ tok_status rope_apply(const RopeCall &c, cudaStream_t stream)
         return TOK_OK;
     int64_t xb, yb;
     if (c.xt < 0 || c.xh < 0 || c.yt < 0 || c.yh < 0 || !extent(n, c.xt, c.H, c.xh, c.D, size, &xb) ||
-        !extent(n, c.yt, c.H, c.yh, c.D, size, &yb) || !distinct(n, c.yt, c.H, c.yh, c.D))
+        !extent(n, c.yt, c.H, c.yh, c.D, size, &yb) || !nested({{n, c.yt}, {c.H, c.yh}}, c.D))
         return TOK_ERR_SHAPE;
     const bool by_pos = c.pos != nullptr;
     if (!c.x || !c.y || (R > 0 && !c.table))
@@ -250,8 +241,11 @@ tok_status rope_apply(const RopeCall &c, cudaStream_t stream)
     if (!aligned(c.x, size) || !aligned(c.y, size) || !aligned(c.table, 8) || !aligned(c.pos, 4) ||
         !aligned(c.bad_count, 4))
         return TOK_ERR_ALIGN;
-    const bool in_place = c.x == c.y && (n == 1 || c.xt == c.yt) && (c.H == 1 || c.xh == c.yh);
-    if ((!in_place && overlaps(c.x, xb, c.y, yb)) || overlaps(c.table, table_floats * 4, c.y, yb) ||
+    // x and y with equal strides are in place, or slices of one buffer whose distance fits into the gaps.
+    const bool alike = (n == 1 || c.xt == c.yt) && (c.H == 1 || c.xh == c.yh);
+    const int64_t apart = std::abs(((const char *)c.y - (const char *)c.x) / size);
+    const bool fits = alike && (apart == 0 || nested({{n, c.yt}, {c.H, c.yh}, {2, apart}}, c.D));
+    if ((overlaps(c.x, xb, c.y, yb) && !fits) || overlaps(c.table, table_floats * 4, c.y, yb) ||
         (by_pos && overlaps(c.pos, n * 12, c.y, yb)) ||
         (c.bad_count && (overlaps(c.bad_count, 4, c.y, yb) || overlaps(c.bad_count, 4, c.x, xb) ||
                          overlaps(c.bad_count, 4, c.table, table_floats * 4) ||

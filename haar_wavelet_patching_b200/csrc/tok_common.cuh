@@ -6,6 +6,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <initializer_list>
+
 #include "tok.h"
 
 namespace tok {
@@ -36,6 +39,30 @@ inline bool overlaps(const void *a, int64_t abytes, const void *b, int64_t bbyte
 {
     const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
     return a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
+}
+
+// A strided dimension: extent and stride in elements.
+struct Axis {
+    int64_t n, s;
+};
+
+// No element of the strided dims (at most four, over a dense block of D) is met twice: each stride leaves room
+// for everything of smaller stride.
+inline bool nested(std::initializer_list<Axis> dims, int64_t D)
+{
+    Axis a[4];
+    int n = 0;
+    for (const Axis &x : dims)
+        if (x.n > 1)
+            a[n++] = x;
+    std::sort(a, a + n, [](const Axis &x, const Axis &y) { return x.s < y.s; });
+    int64_t span = D;
+    for (int i = 0; i < n; ++i) {
+        if (a[i].s < span)
+            return false;
+        span += (a[i].n - 1) * a[i].s;
+    }
+    return true;
 }
 
 inline bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p % n) == 0; }

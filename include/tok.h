@@ -478,7 +478,9 @@ TOK_API tok_status tok_fsq_decode_backward(const int32_t *idx, const float *w, c
  * tok_rope_grid -- every token of a grid: x [B, T, h, w, heads, D] -> y, token
  *   ((b*T + t)*h + i)*w + j at position (t0 + t, h0 + i, w0 + j).  Token and head
  *   strides are given (so the queries and keys of one fused projection are one
- *   call); y == x with equal strides turns in place.
+ *   call); y == x with equal strides turns in place.  With equal strides x and y may also
+ *   be slices of one buffer that share no element; any other meeting of their address
+ *   ranges is TOK_ERR_ALIAS.
  * tok_rope_positions -- x [N, heads, D] with pos [N, 3] int32 (t, h, w) of each
  *   token.  A token with a position outside the table gets NaN in its rotated
  *   channels and adds 1 to bad_count (device int32 or NULL; the caller zeroes it).

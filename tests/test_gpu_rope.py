@@ -206,3 +206,20 @@ def test_more_than_2_31_thread_items():
     got = y[0, tokens[:, 0], tokens[:, 1], tokens[:, 2]]
     ref, tol = reference(x[0, 0, 0].expand(4, 1, D), [tokens[:, a].double().cuda() for a in range(3)], dims, False)
     check(got, ref, tol, "far tokens")
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_into_another_slice_of_the_same_rows(interleaved):
+    """Queries of a fused projection turned into its third part: slices of one buffer that share no element."""
+    dims, sizes, H, D = (16, 24, 24), (3, 4, 5), 4, 64
+    rows = randn(2, 3, 4, 5, 3 * H, D, dtype=torch.bfloat16)
+    before = rows.clone()
+    x, y = rows[..., :H, :], rows[..., 2 * H:, :]
+    table = hwp.rope_table(sizes, dims)
+    want = hwp.rope_grid(x.contiguous(), table, sizes, dims, interleaved=interleaved)
+    hwp.tok_rope_grid(x, y, table, sizes, dims, interleaved=interleaved)
+    assert torch.equal(y, want) and torch.equal(rows[..., : 2 * H, :], before[..., : 2 * H, :])
+    rows.copy_(before)  # and the adjoint the other way
+    want = hwp.rope_grid_adjoint(y.contiguous(), table, sizes, dims, interleaved=interleaved)
+    hwp.tok_rope_grid_adjoint(y, x, table, sizes, dims, interleaved=interleaved)
+    assert torch.equal(x, want) and torch.equal(rows[..., H:, :], before[..., H:, :])
