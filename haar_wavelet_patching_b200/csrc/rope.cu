@@ -94,6 +94,16 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs g)
     const T *x = static_cast<const T *>(g.x) + (int64_t)n * g.xt;
     T *y = static_cast<T *>(g.y) + (int64_t)n * g.yt;
 
+    int pt, ph, pw;
+    bool ok = true;
+    if (g.pos && (unit == 0 || unit < g.rot_units)) { // (unit 0 counts, whether it is rotated or not)
+        pt = g.pos[(int64_t)n * 3];
+        ph = g.pos[(int64_t)n * 3 + 1];
+        pw = g.pos[(int64_t)n * 3 + 2];
+        ok = (uint32_t)pt < (uint32_t)g.nt && (uint32_t)ph < (uint32_t)g.nh && (uint32_t)pw < (uint32_t)g.nw;
+        if (!ok && unit == 0 && h0 == 0 && g.bad_count)
+            atomicAdd(g.bad_count, 1);
+    }
     if (unit >= g.rot_units) { // channels that are not rotated
         const int c = 2 * g.P + (unit - g.rot_units) * 2 * V;
         for (int h = h0; h < h1; ++h) {
@@ -106,16 +116,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs g)
         return;
     }
 
-    int pt, ph, pw;
-    bool ok = true;
-    if (g.pos) {
-        pt = g.pos[(int64_t)n * 3];
-        ph = g.pos[(int64_t)n * 3 + 1];
-        pw = g.pos[(int64_t)n * 3 + 2];
-        ok = (uint32_t)pt < (uint32_t)g.nt && (uint32_t)ph < (uint32_t)g.nh && (uint32_t)pw < (uint32_t)g.nw;
-        if (!ok && unit == 0 && h0 == 0 && g.bad_count)
-            atomicAdd(g.bad_count, 1);
-    } else {
+    if (!g.pos) {
         const uint32_t r = g.w.div(n), q = g.h.div(r), s = g.t.div(q);
         pw = g.w0 + (int)(n - r * g.w.d);
         ph = g.h0 + (int)(r - q * g.h.d);

@@ -223,3 +223,11 @@ def test_into_another_slice_of_the_same_rows(interleaved):
     want = hwp.rope_grid_adjoint(y.contiguous(), table, sizes, dims, interleaved=interleaved)
     hwp.tok_rope_grid_adjoint(y, x, table, sizes, dims, interleaved=interleaved)
     assert torch.equal(x, want) and torch.equal(rows[..., H:, :], before[..., H:, :])
+
+
+def test_bad_positions_are_counted_without_rotated_channels():
+    x = randn(4, 3, 8, dtype=torch.float32)
+    pos = torch.tensor([[0, 0, 0], [2, 0, 0], [0, -1, 0], [1, 2, 3]], dtype=torch.int32, device="cuda")
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = hwp.rope_positions(x, pos, hwp.rope_table((2, 3, 4), (0, 0, 0)), (2, 3, 4), (0, 0, 0), bad_count=bad)
+    assert torch.equal(y, x) and int(bad) == 2
