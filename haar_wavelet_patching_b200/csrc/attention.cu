@@ -285,9 +285,9 @@ struct View {
     bool kv; // keys or values: heads may be broadcast, as batch entries may in all tensors
     bool strides_ok() const
     {
-        constexpr int64_t kMax = (int64_t)1 << 38; // elements: byte strides and spans stay far inside 64 bits
+        constexpr int64_t kMax = (int64_t)1 << 38; // elements of one dimension's span: far inside 64 bits as bytes
         for (const Axis &x : {Axis{B, t->batch}, Axis{N, t->token}, Axis{H, t->head}})
-            if (x.n > 1 && (x.s < 0 || x.s >= kMax))
+            if (x.n > 1 && (x.s < 0 || x.s >= kMax / (x.n - 1)))
                 return false;
         return (N <= 1 || t->token > 0) && (H <= 1 || t->head > 0 || kv);
     }

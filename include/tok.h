@@ -557,7 +557,7 @@ TOK_API tok_status tok_sample_codes(const void *logits, tok_dtype dtype, int64_t
  * and the batch stride of an input, or the head stride of k and v, may be 0 (one encoder
  * state for the whole batch, one key head for all; gradients are per batch entry and
  * key head).  Token strides, and the head strides of the others, are positive.  Shape rule: D a multiple of 8, 8 <= D <= 128; Hq a multiple
- * of Hkv; B, Hq <= 65535; B * Hq * Nq, B * Hkv * Nk < 2^30.  Pointers and strides are
+ * of Hkv; B, Hq <= 65535; B * Hq * Nq, B * Hkv * Nk < 2^30; no dimension spans 2^38 elements.  Pointers and strides are
  * multiples of 16 bytes (TOK_ERR_ALIGN).  Outputs may interleave with inputs and each
  * other (slices of one buffer) but share no element (TOK_ERR_ALIAS).
  *

@@ -174,3 +174,13 @@ def test_cross_attention_binding_refuses():
     x = torch.zeros(1, 2, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         hwp.cross_attention(x, x, x)
+
+
+def test_cross_attention_spans(lib):
+    """Strides that fit each for itself, but whose span over all tokens does not fit into an address."""
+    far = dict(B=1, Nq=1, Nk=1 << 29, Hq=1, Hkv=1, wb=1 << 60)
+    for s in ((0, 1 << 35, 64), (0, 1 << 37, 64), ((1 << 38) - 8, (1 << 38) - 8, 64)):
+        assert attend(lib, sk=s, **far) == hwp.TOK_ERR_SHAPE, s
+        assert attend(lib, sv=s, **far) == hwp.TOK_ERR_SHAPE, s
+    for s in ((0, 1 << 35, 64), (0, 1 << 37, 64)):
+        assert backward(lib, sgk=s, B=1, Nq=1, Nk=1 << 29, Hq=1, Hkv=1, wb=1 << 60) == hwp.TOK_ERR_SHAPE, s
