@@ -819,6 +819,8 @@ def tok_cross_attention_backward(q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v
     """Gradients of tok_cross_attention into grad_q, grad_k, grad_v, from its inputs, o and lse."""
     dims = _attn_dims(q, k, v, k_lens, ((o, "o", True), (grad_o, "grad_o", True), (grad_q, "grad_q", True),
                                         (grad_k, "grad_k", False), (grad_v, "grad_v", False)))
+    if lse is None:
+        raise ValueError("lse must be what tok_cross_attention gave (with_lse)")
     _stats(lse, "lse", dims, q.device)
     ws = _attn_workspace(lib().tok_cross_attention_backward_workspace_size, dims, workspace, q, stream)
     _call("tok_cross_attention_backward", q.device, stream, _heads(q), _heads(k), _heads(v), _heads(o), lse.data_ptr(),

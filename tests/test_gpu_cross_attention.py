@@ -439,3 +439,9 @@ def test_nan_in_live_places_shows(B, Nq, Nk, H, D):
     dq, dk, dv = hwp.cross_attention_backward(q, k, v, o, lse, go)
     for g in (dq, dk, dv):
         assert bool(g[:, :, 0].isnan().all()) and bool(g[:, :, 1].isfinite().all())
+
+
+def test_gradients_ask_for_the_statistics():
+    x = randn(1, 2, 2, 64)
+    with pytest.raises(ValueError, match="lse"):
+        hwp.cross_attention_backward(x, x, x, x, None, x)
