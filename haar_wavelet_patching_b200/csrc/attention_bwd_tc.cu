@@ -419,7 +419,20 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         atomicAdd(&g_attn_bwd_timeouts, 1u);
 }
 
-// dv and dk of the shared tiles' partial sums, in order; zeros behind the length (and without queries).
+// Without queries: dv and dk are zeros.
+__global__ void __launch_bounds__(256) attn_dkv_zero_kernel(const AttnArgs a)
+{
+    const int64_t chunks = a.D / 8, rows = (int64_t)a.B * a.Nk * a.Hkv;
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= 2 * rows * chunks)
+        return;
+    const int64_t half = e / (rows * chunks), r = e - half * rows * chunks, at = r / chunks;
+    const int d = (int)(r - at * chunks) * 8;
+    const int64_t hk = at % a.Hkv, n = at / a.Hkv;
+    *reinterpret_cast<uint4 *>((half ? a.dk : a.dv).row(n / a.Nk, n % a.Nk, hk) + d) = make_uint4(0, 0, 0, 0);
+}
+
+// dv and dk of the shared tiles' partial sums, in order; zeros behind the length.
 __global__ void __launch_bounds__(256) attn_dkv_sum_kernel(const BwdArgs t)
 {
     const AttnArgs &a = t.a;
@@ -986,9 +999,10 @@ tok_status attn_tc_backward(const AttnArgs &a, float *workspace, cudaStream_t st
             return TOK_ERR_SHAPE;
         st = a.D <= 64 ? launch<64>(t, q, g, k, v, stream) : launch<128>(t, q, g, k, v, stream);
     }
-    if (a.Nq == 0) { // zeros: sums of no shares
-        t.tail = a.B * a.Hkv * t.ktiles;
-        t.whole = t.shares = 0;
+    if (a.Nq == 0) {
+        const int64_t threads = (int64_t)a.B * a.Nk * a.Hkv * 2 * (a.D / 8);
+        attn_dkv_zero_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(a);
+        return launch_status();
     }
     if (st == TOK_OK && t.tail > 0) {
         const int64_t sum_threads = (int64_t)t.tail * kTile * 2 * (a.D / 8);

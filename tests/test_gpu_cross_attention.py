@@ -445,3 +445,17 @@ def test_gradients_ask_for_the_statistics():
     x = randn(1, 2, 2, 64)
     with pytest.raises(ValueError, match="lse"):
         hwp.cross_attention_backward(x, x, x, x, None, x)
+
+
+def test_no_queries_and_very_many_key_heads():
+    """Gradients of 134 million rows of keys and values without a query (69 GB): zeros."""
+    B, H, D = 8192, 16400, 128
+    e = torch.empty(B, 0, H, D, dtype=torch.bfloat16, device="cuda")
+    k = randn(1, 1, 1, D).expand(B, 1, H, D)
+    dk, dv = (torch.full((B, 1, H, D), 1.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    hwp.tok_cross_attention_backward(e, k, k, e, torch.empty(B, H, 0, device="cuda"), e, e, dk, dv)
+    for g in (dk, dv):
+        bits = g.view(torch.int32)
+        assert int(bits.max()) == 0 and int(bits.min()) == 0
+    del dk, dv, g, bits
+    torch.cuda.empty_cache()
