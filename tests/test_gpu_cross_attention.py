@@ -459,3 +459,36 @@ def test_no_queries_and_very_many_key_heads():
         assert int(bits.max()) == 0 and int(bits.min()) == 0
     del dk, dv, g, bits
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("case", [  # few query rows in more than one tile of 16, keys in more than one split
+    (1, 40, 3000, 2, 2, 128, None), (2, 12, 2000, 12, 4, 80, "ragged"), (1, 17, 4000, 1, 1, 64, None),
+    (3, 11, 1500, 8, 2, 72, "wild"),
+    # on both sides of the border between the two kernels: 48 and 49, 64 query rows of a key head
+    (2, 12, 1500, 8, 2, 128, "ragged"), (1, 48, 1000, 2, 2, 64, None), (1, 49, 1000, 2, 2, 64, None),
+    (2, 16, 1500, 8, 2, 128, "ragged"), (2, 7, 900, 14, 2, 96, "empty")])
+def test_rows_by_tiles_and_splits(case):
+    test_forward(case)
+    test_backward(case)
+
+
+@pytest.mark.parametrize("B,Nq,Nk,Hq,Hkv,D", [(1, 2, 4000, 2, 2, 64), (1, 2, 40000, 2, 2, 64), (1, 2437, 1500, 16, 16, 128)])
+def test_workspaces_are_taken_and_checked(B, Nq, Nk, Hq, Hkv, D):
+    """Split calls in a workspace of the caller's, with nothing to spare; one byte less is refused."""
+    q, k, v, go = randn(B, Nq, Hq, D), randn(B, Nk, Hkv, D, seed=2), randn(B, Nk, Hkv, D, seed=3), randn(B, Nq, Hq, D, seed=4)
+    o, lse = hwp.cross_attention(q, k, v, with_lse=True)
+    grads = hwp.cross_attention_backward(q, k, v, o, lse, go)
+    dims = B, Nq, Nk, Hq, Hkv, D
+    need, back = hwp.cross_attention_workspace_size(*dims), hwp.cross_attention_backward_workspace_size(*dims)
+    assert need > 0 and back > 0
+    buf = torch.full((max(need, back) + 512,), 77, dtype=torch.uint8, device="cuda")
+    for n, call, want in (
+            (need, lambda ws: (hwp.tok_cross_attention(q, k, v, torch.empty_like(q), workspace=ws),), (o,)),
+            (back, lambda ws: hwp.tok_cross_attention_backward(q, k, v, o, lse, go, torch.empty_like(q), torch.empty_like(k),
+                                                               torch.empty_like(v), workspace=ws), grads)):
+        buf.fill_(77)
+        assert all(torch.equal(a, b) for a, b in zip(call(buf[256:256 + n]), want))
+        assert bool((buf[:256] == 77).all()) and bool((buf[256 + n:] == 77).all())
+        with pytest.raises(hwp.TokError) as e:
+            call(buf[256:256 + n - 1])
+        assert e.value.status == hwp.TOK_ERR_SHAPE

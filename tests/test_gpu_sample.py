@@ -336,3 +336,87 @@ def test_cold_nucleus_of_equal_values(R, dtype):
                         want = hwp.sample_codes(x[:60].to(dtype), u[:60].contiguous(), temperature=t, top_p=top_p, **s)
                         got = hwp.sample_codes(x.to(dtype), u, temperature=t, top_p=top_p, **s)
                         assert torch.equal(got[:60], want)
+
+
+def check_some(x, u, rows, label="", **settings):
+    """One call over all rows; `rows` of them against the reference."""
+    dev = {k: (torch.as_tensor(v, device="cuda") if isinstance(v, np.ndarray) else v) for k, v in settings.items()}
+    idx, lp = hwp.sample_codes(x, u, with_logprob=True, **dev)
+    sub, uu, idx, lp = x[rows].float().cpu().numpy(), u[rows].tolist(), idx[rows].tolist(), lp[rows].tolist()
+    skipped = 0
+    for i, r in enumerate(rows):
+        row = {k: (v[r] if isinstance(v, np.ndarray) else v) for k, v in settings.items()}
+        want, want_lp, near = reference(sub[i], uu[i], **row)
+        if near < 2.0 ** -26:
+            skipped += 1
+            continue
+        assert idx[i] == want, f"{label} row {r}: drew {idx[i]}, expected {want} ({row})"
+        if math.isinf(want_lp):
+            assert lp[i] == want_lp
+        else:
+            assert abs(lp[i] - want_lp) <= 2.0 ** -24 * abs(want_lp) + 2.0 ** -26, f"{label} row {r}"
+    assert skipped <= len(rows) // 4
+
+
+MANY = 320  # rows: more than two to an SM, which take blocks of 256 threads
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("settings", SETTINGS + [dict(top_k=500), dict(top_k=900, top_p=0.9), dict(top_k=1025)])
+@pytest.mark.parametrize("V", [V0, 4097, 257])
+def test_filters_with_many_rows(V, settings, dtype):
+    x, u = data(MANY, V, dtype=dtype, seed=15)
+    check_some(x, u, [0, 1, 2, 147, 148, 149, 295, 296, 297, 318, 319], **settings)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("settings", [dict(top_k=37), dict(top_p=0.37), dict(top_k=3000, top_p=0.7), dict(top_k=1),
+                                      dict(temperature=0.0), dict(), dict(top_k=700)])
+def test_ties_narrow_and_special_with_many_rows(settings, dtype):
+    V = 9001
+    x, _ = data(MANY, V, dtype=torch.float32, seed=16)
+    g = torch.Generator(device="cuda").manual_seed(17)
+    x[:9] = torch.randint(0, 3, (9, V), generator=g, device="cuda").float()
+    x[1] = 1.5
+    x[2] = torch.where(torch.arange(V, device="cuda") == 17, 2.0, -1.0)
+    x[3, ::2], x[3, 1::2] = 0.0, -0.0
+    x[10:14] = 20.0 + 1e-3 * x[10:14]
+    x[12:14, 0] = 35.0
+    x[14, 10:] = -1e9
+    x[15, 10:] = torch.finfo(torch.float32).min
+    x[16, : V // 2] -= 25.0
+    x[300] = -math.inf
+    x[301] = math.nan
+    x[302, 5:] = -math.inf
+    x[303, ::3] = math.nan
+    x[304, 100] = x[304, 7] = math.inf
+    x[305, 1:] = math.nan
+    u = torch.linspace(0.0101, 0.9897, MANY, device="cuda")
+    check_some(x.to(dtype), u, list(range(20)) + list(range(298, 308)), "special", **settings)
+
+
+def test_settings_per_row_with_many_rows():
+    x, u = data(MANY, 5000, seed=18)
+    rng = np.random.RandomState(1)
+    check_some(x, u, list(range(0, MANY, 8)), temperature=np.float32([0.0, 1.0, 0.5, 2.0, 0.8] * 64),
+               top_k=rng.choice([0, -3, 1, 5, 400, 900, 5000, 9999], MANY).astype(np.int32),
+               top_p=rng.choice([1.0, 0.3, 0.9, 0.0, 1.5], MANY).astype(np.float32),
+               min_p=rng.choice([0.0, 0.05, -1.0], MANY).astype(np.float32))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("settings", [dict(top_k=50), dict(top_k=2000), dict(top_p=0.7), dict(top_k=3, top_p=0.9),
+                                      dict(top_k=2000, top_p=0.45, min_p=0.1)])
+@pytest.mark.parametrize("R", [24, 320])
+def test_cold_draws_under_filters(R, settings, dtype):
+    """Five equal largest tokens far above the rest, at temperatures next to zero."""
+    V = 5000
+    g = torch.Generator(device="cuda").manual_seed(19)
+    for top in (1.0, 24.0, 1000.0):
+        x = 0.5 * top - torch.rand(R, V, generator=g, device="cuda")
+        x[:, 100::1000] = top
+        x[:, :50] = -math.inf
+        x[:, V - 50:] = math.nan
+        u = torch.rand(R, generator=g, device="cuda")
+        check_some(x.to(dtype), u, list(range(24)), f"top {top}",
+                   temperature=np.float32([COLD[r % len(COLD)] for r in range(R)]), **settings)
