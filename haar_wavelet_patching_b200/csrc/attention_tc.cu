@@ -323,7 +323,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                         fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * mul;
                 if (j == 0)
-                    m = top; // (-inf where every score so far is: any later one moves it)
+                    m = fmaxf(top, -3.402823466e+38f); // (where every score is -inf, any later one moves it)
                 else {
                     const bool grow = top > m + kGrow;
                     if (__builtin_expect(__any_sync(~0u, grow), 0)) {
@@ -342,8 +342,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                         }
                     }
                 }
-                const float off = m == -INFINITY ? 0.0f : -m;
-                const float2 mul2 = make_float2(mul, mul), neg = make_float2(off, off);
+                const float2 mul2 = make_float2(mul, mul), neg = make_float2(-m, -m);
                 float2 sum[4] = {};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
