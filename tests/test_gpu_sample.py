@@ -420,3 +420,16 @@ def test_cold_draws_under_filters(R, settings, dtype):
         u = torch.rand(R, generator=g, device="cuda")
         check_some(x.to(dtype), u, list(range(24)), f"top {top}",
                    temperature=np.float32([COLD[r % len(COLD)] for r in range(R)]), **settings)
+
+
+@pytest.mark.parametrize("R", [2, 400])
+def test_one_value_everywhere(R):
+    """The longest row, all equal: every token in one bin of the histograms, whose 32-bit sums wrap."""
+    V = 1 << 18
+    x = torch.full((R, V), -3.0, dtype=torch.bfloat16, device="cuda")
+    u = (torch.arange(R, device="cuda") + 0.37) / R
+    for top_p in (1.0, 0.25 + 2.0 ** -12, 1e-6, 0.999):
+        n = V if top_p >= 1 else math.ceil(float(np.float32(top_p)) * V)
+        idx, lp = hwp.sample_codes(x, u, top_p=top_p, with_logprob=True)
+        assert idx.tolist() == [int(float(np.float32(t)) * n) for t in u.tolist()], top_p
+        assert float((lp + math.log(n)).abs().max()) <= 2.0 ** -24 * math.log(n) + 2.0 ** -26
