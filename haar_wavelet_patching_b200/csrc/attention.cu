@@ -7,8 +7,8 @@
 // it runs on warp-level m16n8k16 tiles.  16 query rows of one key head (queries x the heads of
 // its group) per CTA; its 4 warps take 16 keys each in turn with a running maximum and sum of
 // their own, joined through shared memory at the end.  Each warp keeps a ring of its own in
-// shared memory, kStages - 1 steps of keys and values on their way (cp.async): two CTAs of 96 KB
-// in flight per SM cover HBM's latency.  The keys are split over `splits` CTAs; with more than one,
+// shared memory, all stages but one on their way (cp.async): two CTAs per SM, with 64 KB each in flight
+// at 128 channels, cover HBM's latency.  The keys are split over `splits` CTAs; with more than one,
 // attn_join_kernel (launched early, it waits for the grid before it) adds up their partial
 // results in split order.  Measured: 8 x 1 query, up to 3520 ragged keys, 32 heads on 8, D 128: 20 us,
 // of them 5 for the join; its 65 MB take 10 at HBM's rate.
@@ -336,8 +336,8 @@ bool wants_tc(const Dims &d) { return d.Nq * (d.Hq / d.Hkv) > kTcRows && d.Nk > 
 int64_t rows_splits(const Dims &d)
 {
     const int64_t G = d.Hq / d.Hkv;
-    // Two CTAs per SM, as many as are resident, each with at least four rounds of its warps (8 x 3520 keys,
-    // ragged, 8 key heads: 20.0 us; with half as many CTAs 24, twice as many 23; a cluster of 8
+    // Two CTAs per SM, rounded up to equal splits, each with at least four rounds of its warps (8 x 3520 keys,
+    // ragged, 8 key heads: 5 splits, 320 CTAs for the 296 that are resident: 20.0 us; with half as many CTAs 24, twice as many 23; a cluster of 8
     // CTAs that joins through distributed shared memory instead of the workspace: 30).
     const int64_t tiles = (d.Nq * G + kRows - 1) / kRows, units = d.B * d.Hkv * tiles;
     if (units == 0)

@@ -22,7 +22,7 @@
 // attn_dq_kernel: one CTA per SM walks the query tiles (and, with few of them, shares of the keys, added up
 //   by attn_dq_sum_kernel); per key tile s, dp and dq += ds k,
 //   s double-buffered so that s(i+2), dp(i+1) and dq(i) run under the arithmetic of i+1.
-// delta comes from the rounded o, an error of up to 2^-8 |go| |o| that averages out over many keys but
+// delta comes from the o that is given, rounded to bf16, an error of up to 2^-8 |go| |o| that averages out over many keys but
 // not over few: where a batch entry has at most 128 keys, attn_dq_kernel (which runs first) has
 // all of a row's p and dp at hand and takes delta = sum p dp from them.
 // In both, two warpgroups take half of a tile's columns each.

@@ -18,8 +18,8 @@
 //                   past the tensor: D below the tile's width needs no other care).
 // What bounds it: the 16 exponentials an SM takes per cycle (1,024 cycles for a tile of scores) and the chain
 // scores -> softmax -> product of a row tile, which two row tiles in turn do not hide in full.  Measured, 16
-// heads of 128: 56,320 queries x 512 keys 247 us (957 TFLOP/s), 14,080 x 2048 210 us; of 64: 217
-// and 182 us.  Rows of o go straight from registers to HBM, one per thread, in 32-byte sectors: through a
+// heads of 128: 56,320 queries x 512 keys 249 us (947 TFLOP/s), 14,080 x 2048 203 us; of 64: 213
+// and 179 us.  Rows of o go straight from registers to HBM, one per thread, in 32-byte sectors: through a
 // staging buffer and tensor stores an item of one key tile took 7% (64 channels) longer.
 // The v rows behind a batch entry's length are zeroed in shared memory (a weight of 0 times
 // NaN would be NaN); scores behind it are -inf.  All waits are bounded as in the convolutions.

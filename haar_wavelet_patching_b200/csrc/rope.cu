@@ -12,7 +12,7 @@
 // in and once out and is bound by HBM.  A thread owns V pairs of one token, reads their
 // 2V table values once and turns them in several heads (16-byte loads and stores where
 // the layout allows).  Measured: 56,320 tokens x 32 heads (of 48 in a row) x 128, bf16: 146 us,
-// 6.3 TB/s; fp32 pairs side by side, 10,395 x 12 x 80: 18 us, 4.5 TB/s (a ramp: about two rounds of
+// 6.3 TB/s; fp32 pairs side by side, 10,395 x 12 x 80: 18 us, 4.4 TB/s (a ramp: 1,625 blocks, less than one round of
 // the SMs); 16 tokens: 2 us.
 #include <algorithm>
 #include <cstdlib>

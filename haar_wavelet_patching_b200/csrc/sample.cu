@@ -14,7 +14,8 @@
 // depend on their order, so neither the split over threads and CTAs nor the order of
 // the histogram's atomics shows in the result.
 //
-// The kernel is bound by instructions per token and by the chain of short steps of a row, so
+// The kernel is bound by latency: the chain of short steps of a row between barriers, at 40% of an SM's
+// warps (1.6 to 2.1 instructions a cycle of 4; HBM and the issue slots are half idle or more).  So
 // rows are streamed (re-reads come from L2), several to an SM, in few and short passes:
 //   top_k up to kSmall: a histogram of a sample gives a value that a little more than top_k
 //     tokens should reach; one pass picks these out (their count says whether they hold the top_k),
@@ -28,7 +29,7 @@
 //     kCap tokens is narrowed on the bits of x, to a single value if need be, whose ties
 //     are counted in index order.
 // With few rows a cluster of up to 8 CTAs shares one, a contiguous slice each.
-// Measured, rows of 64,000: 4 with all filters 17 us; 255 in fp32 under top_p 0.9 75 us (65 MB: 10 us
+// Measured, rows of 64,000: 4 with all filters 17 us; 255 in fp32 under top_p 0.9 76 us (65 MB: 10 us
 // of HBM); 880 in bf16 under top_k 500 63 us (17 us of HBM).  Sorting every picked token outright
 // instead of the limit's bin only: 19 and 86 us for the first and the last.
 #include <algorithm>
@@ -587,7 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(const
         sh.table[tid] = kOne * exp2((double)tid / 64.0);
     // 2^44 exp((x - xmax) / T1) in 64 bits: with y = 64 log2(e) (x - xmax) / T1 = k + f,
     // 2^(k / 64) from a table and the exponent, 2^(f / 64) by its Taylor polynomial of
-    // degree 4 (|f ln 2 / 64| <= 0.0055: what is left out is below 2^-44 relative).
+    // degree 4 (|f ln 2 / 64| <= 0.0055: what is left out is below 2^-44.5 relative, beside the
+    // half unit, 2^-45, of rounding to an integer).
     const double per_t = 64.0 / 0.6931471805599453 / (double)T1, xmax_d = infinite ? 0.0 : (double)xmax;
     const float xcut = infinite ? INFINITY : fmaxf(xmax - reach, kLowest); // no weight below
     auto weight_at = [&](double d) TOK_INLINE -> double { // of d = x - xmax
