@@ -335,6 +335,13 @@ attn_dkv_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             if (lane == 0)
                 mbar_arrive(smem_addr(&sread));
             __syncwarp();
+            // Query rows behind the last one are zeros, of which a key of -inf makes NaN: a number in its place,
+            // and their lse2 of +inf, give the weight 0.  (A NaN of a query's own is in its lse2 as well.)
+            if (__builtin_expect(stats[64 * half + 63] == INFINITY, 0)) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                    p[e] = fmaxf(p[e], -3.402823466e+38f);
+            }
             {
                 const float4 *l4 = reinterpret_cast<const float4 *>(stats + 64 * half);
 #pragma unroll
@@ -754,7 +761,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                             break;
                         }
                         delta = row_sum[0][lrow] + row_sum[1][lrow];
-                        if (half == 0)
+                        if (half == 0 && iq < a.Nq) // (0 behind the last row)
                             t.delta[at] = delta;
                     }
                     uint32_t pk[32];

@@ -492,3 +492,25 @@ def test_workspaces_are_taken_and_checked(B, Nq, Nk, Hq, Hkv, D):
         with pytest.raises(hwp.TokError) as e:
             call(buf[256:256 + n - 1])
         assert e.value.status == hwp.TOK_ERR_SHAPE
+
+
+@pytest.mark.parametrize("Nq,Nk,Hq,Hkv,D,dead", [(3, 100, 2, 2, 64, 40), (1, 400, 6, 2, 128, 130), (300, 400, 2, 2, 64, 130),
+                                                 (256, 400, 2, 1, 128, 256), (1201, 2600, 4, 2, 128, 1900)])
+@pytest.mark.parametrize("low", [-math.inf, torch.finfo(torch.bfloat16).min])
+def test_gradients_of_keys_masked_through_a_channel(Nq, Nk, Hq, Hkv, D, dead, low):
+    """Keys ruled out by a channel of their own get no gradient, whether or not the queries fill their tiles; the
+    others get what they get alone.  (That channel of grad_q is 0 times -inf: NaN by the formula.)"""
+    q, k, v, go = (randn(1, n, h, D, seed=s, spread=f)
+                   for n, h, s, f in ((Nq, Hq, 1, 1.0), (Nk, Hkv, 2, 0.3), (Nk, Hkv, 3, 1.0), (Nq, Hq, 4, 1.0)))
+    q[..., 0], k[..., 0] = 1.0, 0.0
+    ref = reference(q, k[:, dead:].contiguous(), v[:, dead:].contiguous(), None, 1.0, go)
+    k[:, :dead, :, 0] = low
+    o, lse = hwp.cross_attention(q, k, v, scale=1.0, with_lse=True)
+    dq, dk, dv = hwp.cross_attention_backward(q, k, v, o, lse, go, scale=1.0)
+    assert bool((dk[:, :dead] == 0).all()) and bool((dv[:, :dead] == 0).all())
+    check(dk[:, dead:], ref, "dk")
+    check(dv[:, dead:], ref, "dv")
+    if low == -math.inf:
+        assert bool(dq[..., 0].isnan().all())
+        dq[..., 0] = ref["dq"][0][..., 0].to(dq.dtype)
+    check(dq, ref, "dq")
