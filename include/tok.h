@@ -547,7 +547,8 @@ TOK_API tok_status tok_sample_codes(const void *logits, tok_dtype dtype, int64_t
  * reading key head h / (Hq / Hkv).  Batch entry b has the keys [0, k_lens[b])
  * (clamped to [0, Nk]; NULL: all Nk); what lies behind them is not read into any
  * result, NaN included.  A query without a key (or whose scores are all -inf) has o = 0
- * and lse = -inf, and gives no gradient; one with a score of NaN or +inf has NaN in both.  Products accumulate in fp32, the softmax is fp32; its weights (and
+ * and lse = -inf, and gives no gradient; one with a score of NaN or +inf has NaN in both.
+ * (Scores are taken times log2(e), in fp32: one below that range counts as -inf.)  Products accumulate in fp32, the softmax is fp32; its weights (and
  * in the backward the score gradients) are rounded to bf16 once, as operands of the
  * second product, and outputs once; the backward takes the row sums of grad_o * o from the
  * rounded o where a batch entry has more than 128 keys.  Results do not depend on the device's timing
