@@ -1,5 +1,5 @@
-"""B200 Haar patcher / unpatcher, FSQ quantizer and operators of a model over the tokens (rotary
-positions, cross attention, drawing codes): Python binding of libtok.so.
+"""B200 Haar patcher / unpatcher, FSQ quantizer and operators of a model over the tokens (embedding of codes, rotary
+positions, cross attention, a paged cache with its attention, drawing codes, verifying drafts): Python binding of libtok.so.
 
 The functions named like the C ABI (``tok_haar_fwd`` ...) marshal torch CUDA
 tensors into the C calls of ``include/tok.h`` and nothing else: every step of
@@ -33,7 +33,10 @@ ABI_SYMBOLS = ("tok_abi_version", "tok_status_str", "tok_last_cuda_error", "tok_
                "tok_fsq_encode_backward", "tok_fsq_encode_backward_noalloc", "tok_fsq_decode_backward",
                "tok_rope_table", "tok_rope_grid", "tok_rope_grid_adjoint", "tok_rope_positions",
                "tok_rope_positions_adjoint", "tok_sample_codes", "tok_cross_attention_workspace_size",
-               "tok_cross_attention", "tok_cross_attention_backward_workspace_size", "tok_cross_attention_backward")
+               "tok_cross_attention", "tok_cross_attention_backward_workspace_size", "tok_cross_attention_backward",
+               "tok_embed_codes", "tok_embed_codes_backward_workspace_size", "tok_embed_codes_backward",
+               "tok_page_tables", "tok_page_release", "tok_paged_write", "tok_paged_attention_workspace_size",
+               "tok_paged_attention", "tok_verify_codes")
 
 _lib = None
 
@@ -41,6 +44,12 @@ _lib = None
 class _Heads(ctypes.Structure):
     """tok_heads: a [B, N, H, D] tensor with dense channels."""
     _fields_ = [("ptr", ctypes.c_void_p), ("batch", ctypes.c_int64), ("token", ctypes.c_int64),
+                ("head", ctypes.c_int64)]
+
+
+class _Pages(ctypes.Structure):
+    """tok_pages: a [P, page_size, H, D] tensor with dense channels."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("page", ctypes.c_int64), ("token", ctypes.c_int64),
                 ("head", ctypes.c_int64)]
 
 
@@ -128,6 +137,25 @@ def lib():
         L.tok_sample_codes.argtypes = [vp, i32, i64, i64, i64, vp, vp, f32, vp, i32, vp, f32, vp, f32, vp, vp, vp]
         L.tok_fsq_decode.restype = i32
         L.tok_fsq_decode.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp]
+        L.tok_embed_codes.restype = i32
+        L.tok_embed_codes.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, i64, i64, f32, vp]
+        L.tok_embed_codes_backward_workspace_size.restype = i64
+        L.tok_embed_codes_backward_workspace_size.argtypes = [i64] * 3
+        L.tok_embed_codes_backward.restype = i32
+        L.tok_embed_codes_backward.argtypes = [vp, vp, vp, i32, i32] + [i64] * 5 + [f32, vp, i64, vp]
+        L.tok_page_tables.restype = i32
+        L.tok_page_tables.argtypes = [vp] * 10 + [i64] * 6 + [vp]
+        L.tok_page_release.restype = i32
+        L.tok_page_release.argtypes = [vp] * 8 + [i64] * 5 + [vp]
+        pp = ctypes.POINTER(_Pages)
+        L.tok_paged_write.restype = i32
+        L.tok_paged_write.argtypes = [hp, hp, vp, pp, pp, vp] + [i64] * 6 + [vp]
+        L.tok_paged_attention_workspace_size.restype = i64
+        L.tok_paged_attention_workspace_size.argtypes = [i64] * 5
+        L.tok_paged_attention.restype = i32
+        L.tok_paged_attention.argtypes = [hp, pp, pp, vp, vp, vp, hp, vp] + [i64] * 9 + [f32, vp, i64, vp]
+        L.tok_verify_codes.restype = i32
+        L.tok_verify_codes.argtypes = [vp, vp, i32, vp, vp, vp, vp, f32, vp, vp] + [i64] * 7 + [vp]
         _lib = L
     return _lib
 
@@ -830,6 +858,241 @@ def tok_cross_attention_backward(q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v
 
 
 # ---------------------------------------------------------------------------
+# Embedding of codes.
+# ---------------------------------------------------------------------------
+def _check_on(dev, dtype, shape, **tensors):
+    """Contiguous tensors of one dtype and shape on `dev`; None is left out."""
+    for name, t in tensors.items():
+        if t is not None and (t.device != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {dev}")
+
+
+def _counter(t, dev, name="bad_count"):
+    if t is not None and (t.device != dev or t.dtype != torch.int32 or t.numel() < 1):
+        raise ValueError(f"{name} must be an int32 CUDA tensor")
+    return None if t is None else t.data_ptr()
+
+
+def _row_stride(t, name):
+    """The stride of the rows of [..., D], dense in D, its leading dimensions taken as one index."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be dense")
+    return t.shape[-1] if t.is_contiguous() else _token_stride(t.unsqueeze(-2), name)
+
+
+def _codes(codes, rows, name):
+    if codes.device.type != "cuda":
+        raise ValueError("codes must be a CUDA tensor (there is no CPU path)")
+    if codes.dtype != torch.int32 or not codes.is_contiguous():
+        raise ValueError("codes must be a contiguous int32 CUDA tensor")
+    if rows.device != codes.device or rows.shape[:-1] != codes.shape or rows.dim() < 1:
+        raise ValueError(f"{name} must be [..., D] on the device of codes [...]")
+
+
+def tok_embed_codes(codes, table, y, scale=1.0, bad_count=None, stream=None):
+    """y[..., :] = scale * table[codes]: codes [...] int32, table [V, D], y [..., D] (float32 or bfloat16, rows
+    strided).  A code outside the table gives a row of NaN and adds 1 to bad_count (int32 CUDA tensor)."""
+    _codes(codes, y, "y")
+    if table.dim() != 2 or table.device != codes.device or table.dtype != y.dtype or table.shape[1] != y.shape[-1]:
+        raise ValueError("table must be [V, D] with the dtype, device and D of y")
+    V, D = table.shape
+    _call("tok_embed_codes", codes.device, stream, codes.data_ptr(), table.data_ptr(), y.data_ptr(),
+          _counter(bad_count, codes.device), _dtype_code(y), codes.numel(), V, D, _row_stride(table, "table"),
+          _row_stride(y, "y"), scale)
+    return y
+
+
+def embed_codes_backward_workspace_size(N, V, D) -> int:
+    return int(lib().tok_embed_codes_backward_workspace_size(N, V, D))
+
+
+def tok_embed_codes_backward(grad_y, codes, grad_table, scale=1.0, workspace=None, stream=None):
+    """Gradient of tok_embed_codes into grad_table [V, D] (overwritten): grad_y [..., D], codes [...]; the two
+    gradients' dtypes are their own.  workspace: embed_codes_backward_workspace_size bytes, allocated if None."""
+    _codes(codes, grad_y, "grad_y")
+    dev = codes.device
+    if grad_table.dim() != 2 or grad_table.device != dev or grad_table.shape[1] != grad_y.shape[-1]:
+        raise ValueError("grad_table must be [V, D] with the device and D of grad_y")
+    N, (V, D) = codes.numel(), grad_table.shape
+    ws = _workspace_of(embed_codes_backward_workspace_size(N, V, D), workspace, codes, stream,
+                       f"no embedding for (N, V, D) = {(N, V, D)}: V at most 2^18, D at most 65536")
+    _call("tok_embed_codes_backward", dev, stream, codes.data_ptr(), grad_y.data_ptr(), grad_table.data_ptr(),
+          _dtype_code(grad_y), _dtype_code(grad_table), N, V, D, _row_stride(grad_y, "grad_y"),
+          _row_stride(grad_table, "grad_table"), scale, *_bytes(ws))
+    return grad_table
+
+
+def _workspace_of(need, workspace, like, stream, what):
+    if need < 0:
+        raise ValueError(what)
+    if workspace is None:
+        return _new(like, need, torch.uint8, stream) if need else None
+    if workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the device of the inputs")
+    return workspace
+
+
+# ---------------------------------------------------------------------------
+# Pages of a cache of keys and values.
+# ---------------------------------------------------------------------------
+def _tables_check(lens, held, free, pages, table, held_out, free_out):
+    dev = lens.device
+    if dev.type != "cuda":
+        raise ValueError("lens must be a CUDA tensor (there is no CPU path)")
+    if lens.dim() != 1 or table.dim() != 2 or pages.dim() != 1:
+        raise ValueError("lens must be [B], table [B, M], pages [F]")
+    _check_on(dev, torch.int32, lens.shape, lens=lens, held=held, held_out=held_out)
+    _check_on(dev, torch.int32, torch.Size((1,)), free=free, free_out=free_out)
+    _check_on(dev, torch.int32, pages.shape, pages=pages)
+    if table.device != dev or table.dtype != torch.int32 or table.shape[0] != lens.shape[0] \
+            or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("table must be an int32 CUDA tensor [B, M] with dense rows")
+    return lens.shape[0], table.shape[1], pages.shape[0]
+
+
+def tok_page_tables(lens, fresh, held, free, pages, table, slots, held_out, free_out, page_size, bad_count=None,
+                    stream=None):
+    """Room for new tokens: stream b has lens[b] tokens and gets fresh[b] more (None: all of slots' columns).  Pages
+    come off the end of pages[:free] in the order of streams and go into table [B, M]; slots [B, N] gets
+    page * page_size + row of each new token (-1 behind them), held_out and free_out the new counts (they may be
+    held and free).  A stream without room gets slots of -1 and adds 1 to bad_count.  All int32."""
+    B, M, F = _tables_check(lens, held, free, pages, table, held_out, free_out)
+    if slots.dim() != 2 or slots.shape[0] != B:
+        raise ValueError("slots must be [B, N]")
+    _check_on(lens.device, torch.int32, slots.shape, slots=slots)
+    _check_on(lens.device, torch.int32, lens.shape, fresh=fresh)
+    _call("tok_page_tables", lens.device, stream, lens.data_ptr(), None if fresh is None else fresh.data_ptr(),
+          held.data_ptr(), free.data_ptr(), pages.data_ptr(), table.data_ptr(), slots.data_ptr(), held_out.data_ptr(),
+          free_out.data_ptr(), _counter(bad_count, lens.device), B, slots.shape[1], M, F, page_size,
+          table.stride(0) if B > 1 else M)
+    return slots
+
+
+def tok_page_release(lens, held, free, pages, table, held_out, free_out, page_size, bad_count=None, stream=None):
+    """Give back the pages that lens[b] tokens do not need: onto pages[free:], their table entries become -1; held_out and
+    free_out get the new counts (they may be held and free)."""
+    B, M, F = _tables_check(lens, held, free, pages, table, held_out, free_out)
+    _call("tok_page_release", lens.device, stream, lens.data_ptr(), held.data_ptr(), free.data_ptr(), pages.data_ptr(),
+          table.data_ptr(), held_out.data_ptr(), free_out.data_ptr(), _counter(bad_count, lens.device), B, M, F,
+          page_size, table.stride(0) if B > 1 else M)
+
+
+def _pool(t: torch.Tensor) -> _Pages:
+    p, n, h, _ = t.stride()
+    return _Pages(t.data_ptr(), p, n, h)
+
+
+def _pools_check(k_pages, v_pages, heads, channels, dev):
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must be [P, page_size, H, D], alike")
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if t.dtype != torch.bfloat16 or t.device != dev:
+            raise ValueError(f"{name} must be a bfloat16 CUDA tensor on the device of the tokens")
+        if t.stride(3) != 1:
+            raise ValueError(f"the channels of {name} must be dense")
+    if k_pages.shape[3] != channels or (heads is not None and k_pages.shape[2] != heads):
+        raise ValueError(f"the pages have (H, D) = {tuple(k_pages.shape[2:])}, the tokens {(heads, channels)}")
+
+
+def paged_write(k, v, k_pages, v_pages, slots, bad_count=None, stream=None):
+    """Keys and values k, v [B, N, H, D] (dense channels, other strides free) into the pages [P, page_size, H, D] at
+    slots [B, N] int32 (page * page_size + row; below 0: left out), all bfloat16.  A slot behind the pool is left
+    out and adds 1 to bad_count.  Slots must differ."""
+    dev = k.device
+    if dev.type != "cuda":
+        raise ValueError("k must be a CUDA tensor (there is no CPU path)")
+    if k.dim() != 4 or k.shape != v.shape:
+        raise ValueError("k and v must be [B, N, H, D], alike")
+    for t, name in ((k, "k"), (v, "v")):
+        if t.dtype != torch.bfloat16 or t.device != dev:
+            raise ValueError(f"{name} must be a bfloat16 CUDA tensor on the device of k")
+        if t.stride(3) != 1:
+            raise ValueError(f"the channels of {name} must be dense")
+    B, N, H, D = k.shape
+    _pools_check(k_pages, v_pages, H, D, dev)
+    _check_on(dev, torch.int32, torch.Size((B, N)), slots=slots)
+    _call("tok_paged_write", dev, stream, _heads(k), _heads(v), slots.data_ptr(), _pool(k_pages), _pool(v_pages),
+          _counter(bad_count, dev), B, N, H, D, k_pages.shape[0], k_pages.shape[1])
+
+
+tok_paged_write = paged_write
+
+
+def paged_attention_workspace_size(B, Nq, Hq, Hkv, D) -> int:
+    return int(lib().tok_paged_attention_workspace_size(B, Nq, Hq, Hkv, D))
+
+
+def tok_paged_attention(q, k_pages, v_pages, table, k_lens, o, lse=None, q_lens=None, scale=None, workspace=None,
+                        stream=None):
+    """Attention of new tokens over pages: q, o [B, Nq, Hq, D], pages [P, page_size, Hkv, D] bfloat16 (dense
+    channels, other strides free), table [B, M], k_lens [B], q_lens [B] or None (Nq) int32.  Query i < q_lens[b] is token
+    k_lens[b] - q_lens[b] + i of its stream and sees the tokens up to itself; the others get o = 0, lse = -inf.
+    lse [B, Hq, Nq] fp32 or None; scale: 1/sqrt(D) by default; workspace: paged_attention_workspace_size bytes,
+    allocated if None."""
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("q must be a CUDA tensor (there is no CPU path)")
+    if q.dim() != 4 or o.shape != q.shape:
+        raise ValueError("q and o must be [B, Nq, Hq, D], alike")
+    for t, name in ((q, "q"), (o, "o")):
+        if t.dtype != torch.bfloat16 or t.device != dev:
+            raise ValueError(f"{name} must be a bfloat16 CUDA tensor on the device of q")
+        if t.stride(3) != 1:
+            raise ValueError(f"the channels of {name} must be dense")
+    B, Nq, Hq, D = q.shape
+    _pools_check(k_pages, v_pages, None, D, dev)
+    P, page_size, Hkv, _ = k_pages.shape
+    if table.device != dev or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B \
+            or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("table must be an int32 CUDA tensor [B, M] with dense rows")
+    if k_lens is None:
+        raise ValueError("k_lens must be a contiguous int32 CUDA tensor [B]")
+    _check_on(dev, torch.int32, torch.Size((B,)), k_lens=k_lens, q_lens=q_lens)
+    _stats(lse, "lse", (B, Nq, 0, Hq, Hkv, D), dev)
+    ws = _workspace_of(paged_attention_workspace_size(B, Nq, Hq, Hkv, D), workspace, q, stream,
+                       f"no paged attention for (B, Nq, Hq, Hkv, D) = {(B, Nq, Hq, Hkv, D)}: D a multiple of 8, at "
+                       "most 128; Hq a multiple of Hkv; Nq at most 64")
+    M = table.shape[1]
+    _call("tok_paged_attention", dev, stream, _heads(q), _pool(k_pages), _pool(v_pages), table.data_ptr(),
+          k_lens.data_ptr(), None if q_lens is None else q_lens.data_ptr(), _heads(o),
+          None if lse is None else lse.data_ptr(), B, Nq, Hq, Hkv, D, P, page_size, M, table.stride(0) if B > 1 else M,
+          D ** -0.5 if scale is None else scale, *_bytes(ws))
+    return o
+
+
+# ---------------------------------------------------------------------------
+# Verifying drafted codes.
+# ---------------------------------------------------------------------------
+def tok_verify_codes(logits, codes, u, out, accepted, draft_logits=None, n_draft=None, temperature=1.0, stream=None):
+    """Which drafted codes stand, and the code behind them: logits [B, K + 1, V] (float32 or bfloat16), draft_logits
+    [B, K, V] or None (each draft was certain), codes [B, K] int32, u [B, K + 1] fp32 in [0, 1), n_draft [B] int32 or
+    None (K), temperature a number or fp32 [B] -> out [B, K + 1] int32 (the codes that stand, the drawn one, then -1),
+    accepted [B] int32.  Draft i stands if u q(x) < p(x); the code behind is drawn with u[:, K] from max(p - q, 0), or
+    from p behind all drafts."""
+    dev = logits.device
+    if dev.type != "cuda":
+        raise ValueError("logits must be a CUDA tensor (there is no CPU path)")
+    if logits.dim() != 3 or logits.shape[1] < 1 or logits.shape[2] < 1:
+        raise ValueError("logits must be [B, K + 1, V] with V >= 1")
+    B, K, V = logits.shape[0], logits.shape[1] - 1, logits.shape[2]
+    for t, name, rows in ((logits, "logits", K + 1), (draft_logits, "draft_logits", K)):
+        if t is not None and (t.device != dev or t.dtype != logits.dtype or t.shape != (B, rows, V)
+                              or (V > 1 and t.stride(2) != 1)):
+            raise ValueError(f"{name} must be [B, {rows}, V] with the dtype and device of logits, dense in V")
+    _check_on(dev, torch.int32, torch.Size((B, K)), codes=codes)
+    _check_on(dev, torch.float32, torch.Size((B, K + 1)), u=u)
+    _check_on(dev, torch.int32, torch.Size((B, K + 1)), out=out)
+    _check_on(dev, torch.int32, torch.Size((B,)), n_draft=n_draft, accepted=accepted)
+    tp, ta = _setting(temperature, "temperature", torch.float32, B, dev)
+    drafted = draft_logits is not None and K > 0
+    _call("tok_verify_codes", dev, stream, logits.data_ptr(), draft_logits.data_ptr() if drafted else None,
+          _dtype_code(logits), codes.data_ptr(), u.data_ptr(), None if n_draft is None else n_draft.data_ptr(), tp, ta,
+          out.data_ptr(), accepted.data_ptr(), B, K, V, logits.stride(0), logits.stride(1),
+          draft_logits.stride(0) if drafted else 0, draft_logits.stride(1) if drafted else 0)
+    return out, accepted
+
+
+# ---------------------------------------------------------------------------
 # Allocating wrappers.
 # ---------------------------------------------------------------------------
 def haar_fwd(x: torch.Tensor, stream=None) -> torch.Tensor:
@@ -973,3 +1236,41 @@ def cross_attention_backward(q, k, v, o, lse, grad_o, k_lens=None, scale=None, s
     """(grad_q, grad_k, grad_v): see tok_cross_attention_backward."""
     return tok_cross_attention_backward(q, k, v, o, lse, grad_o, _dense(q, stream), _dense(k, stream),
                                         _dense(v, stream), k_lens, scale, None, stream)
+
+
+def embed_codes(codes, table, scale=1.0, bad_count=None, stream=None) -> torch.Tensor:
+    """y [..., D]: see tok_embed_codes."""
+    y = _new(table, codes.shape + table.shape[1:], table.dtype, stream)
+    return tok_embed_codes(codes, table, y, scale, bad_count, stream)
+
+
+def embed_codes_backward(grad_y, codes, V, scale=1.0, dtype=None, stream=None) -> torch.Tensor:
+    """grad_table [V, D] of `dtype` (that of grad_y by default): see tok_embed_codes_backward."""
+    grad = _new(grad_y, (V, grad_y.shape[-1]), grad_y.dtype if dtype is None else dtype, stream)
+    return tok_embed_codes_backward(grad_y, codes, grad, scale, None, stream)
+
+
+def page_tables(lens, fresh, n, held, free, pages, table, page_size, bad_count=None, stream=None) -> torch.Tensor:
+    """slots [B, n]; held, free and table are updated in place: see tok_page_tables."""
+    slots = _new(lens, (lens.shape[0], n), torch.int32, stream)
+    return tok_page_tables(lens, fresh, held, free, pages, table, slots, held, free, page_size, bad_count, stream)
+
+
+def page_release(lens, held, free, pages, table, page_size, bad_count=None, stream=None):
+    """held, free, pages and table are updated in place: see tok_page_release."""
+    tok_page_release(lens, held, free, pages, table, held, free, page_size, bad_count, stream)
+
+
+def paged_attention(q, k_pages, v_pages, table, k_lens, q_lens=None, scale=None, with_lse=False, stream=None):
+    """o, or (o, lse): see tok_paged_attention."""
+    o = _dense(q, stream)
+    lse = _new(q, (q.shape[0], q.shape[2], q.shape[1]), torch.float32, stream) if with_lse else None
+    tok_paged_attention(q, k_pages, v_pages, table, k_lens, o, lse, q_lens, scale, None, stream)
+    return (o, lse) if with_lse else o
+
+
+def verify_codes(logits, codes, u, draft_logits=None, n_draft=None, temperature=1.0, stream=None):
+    """(out, accepted): see tok_verify_codes.  out feeds embed_codes where V is the table's."""
+    out = _new(logits, logits.shape[:2], torch.int32, stream)
+    accepted = _new(logits, logits.shape[:1], torch.int32, stream)
+    return tok_verify_codes(logits, codes, u, out, accepted, draft_logits, n_draft, temperature, stream)

@@ -278,53 +278,6 @@ struct Dims {
     }
 };
 
-struct View {
-    const tok_heads *t;
-    int64_t B, N, H, D;
-    int64_t span() const { return (B - 1) * t->batch + (N - 1) * t->token + (H - 1) * t->head + D; }
-    bool kv; // keys or values: heads may be broadcast, as batch entries may in all tensors
-    bool strides_ok() const
-    {
-        constexpr int64_t kMax = (int64_t)1 << 38; // elements of one dimension's span: far inside 64 bits as bytes
-        for (const Axis &x : {Axis{B, t->batch}, Axis{N, t->token}, Axis{H, t->head}})
-            if (x.n > 1 && (x.s < 0 || x.s >= kMax / (x.n - 1)))
-                return false;
-        return (N <= 1 || t->token > 0) && (H <= 1 || t->head > 0 || kv);
-    }
-    bool distinct() const { return nested({{B, t->batch}, {N, t->token}, {H, t->head}}, D); }
-    bool aligned16() const
-    {
-        for (const Axis &x : {Axis{B, t->batch}, Axis{N, t->token}, Axis{H, t->head}})
-            if (x.n > 1 && x.s % 8)
-                return false;
-        return aligned(t->ptr, 16);
-    }
-};
-
-// Whether two views may share an element: their ranges meet, and they are not slices that
-// interleave (equal strides, and the distance between them fits into the gaps).
-bool meet(const View &a, const View &b)
-{
-    if (!overlaps(a.t->ptr, a.span() * 2, b.t->ptr, b.span() * 2))
-        return false;
-    const int64_t off = ((const char *)b.t->ptr - (const char *)a.t->ptr) / 2;
-    auto same = [](int64_t na, int64_t sa, int64_t nb, int64_t sb) { return na <= 1 || nb <= 1 || sa == sb; };
-    if (!same(a.B, a.t->batch, b.B, b.t->batch) || !same(a.N, a.t->token, b.N, b.t->token) ||
-        !same(a.H, a.t->head, b.H, b.t->head))
-        return true;
-    auto ax = [](int64_t na, int64_t sa, int64_t nb, int64_t sb) { return Axis{std::max(na, nb), na > 1 ? sa : sb}; };
-    return !nested({ax(a.B, a.t->batch, b.B, b.t->batch), ax(a.N, a.t->token, b.N, b.t->token),
-                    ax(a.H, a.t->head, b.H, b.t->head), Axis{2, off < 0 ? -off : off}},
-                   a.D);
-}
-
-bool meets(const View &a, const void *p, int64_t bytes) { return p && overlaps(a.t->ptr, a.span() * 2, p, bytes); }
-
-HeadsView view(const tok_heads *t)
-{
-    return HeadsView{static_cast<__nv_bfloat16 *>(t->ptr), t->batch, t->token, t->head};
-}
-
 // Query rows per key head up to which the kernel for few rows takes a call.  Its time grows with every 16 rows, the
 // tensor cores' hardly at all (us, few rows / tensor cores, at 48, 64 and 96 rows: 8 x 3520 keys, 32
 // heads of 128 on 8: 36 / 38, 45 / 39, 56 / 39; 32 x 300 keys, 16 heads of 64: 22 / 27, 27 / 27, 37 / 27).

@@ -1,0 +1,62 @@
+// Keys or values in pages: [P, page_size, H, D], strides in elements, channels dense.
+#pragma once
+
+#include "attention.cuh"
+
+namespace tok {
+
+struct PagesView {
+    __nv_bfloat16 *p;
+    int64_t pg, t, h;
+    __device__ __forceinline__ __nv_bfloat16 *row(int64_t page, int64_t in, int64_t ih) const
+    {
+        return p + page * pg + in * t + ih * h;
+    }
+};
+
+inline PagesView view(const tok_pages *t)
+{
+    return PagesView{static_cast<__nv_bfloat16 *>(t->ptr), t->page, t->token, t->head};
+}
+
+// Host: argument rules.
+struct PoolView {
+    const tok_pages *t;
+    int64_t P, N, H, D;
+    int64_t span() const
+    {
+        return (std::max<int64_t>(P, 1) - 1) * t->page + (N - 1) * t->token + (H - 1) * t->head + D;
+    }
+    bool strides_ok() const
+    {
+        constexpr int64_t kMax = (int64_t)1 << 38; // elements of one dimension's span: far inside 64 bits as bytes
+        for (const Axis &x : {Axis{P, t->page}, Axis{N, t->token}, Axis{H, t->head}})
+            if (x.n > 1 && (x.s < 0 || x.s >= kMax / (x.n - 1)))
+                return false;
+        return true;
+    }
+    bool distinct() const { return nested({{P, t->page}, {N, t->token}, {H, t->head}}, D); }
+    bool aligned16() const
+    {
+        for (const Axis &x : {Axis{P, t->page}, Axis{N, t->token}, Axis{H, t->head}})
+            if (x.n > 1 && x.s % 8)
+                return false;
+        return aligned(t->ptr, 16);
+    }
+    bool meets(const void *p, int64_t bytes) const { return p && overlaps(t->ptr, span() * 2, p, bytes); }
+};
+
+// Whether two pools of the same extents may share an element: their ranges meet, and they are not slices
+// that interleave (equal strides, and the distance between them fits into the gaps).
+inline bool pools_meet(const PoolView &a, const PoolView &b)
+{
+    if (!overlaps(a.t->ptr, a.span() * 2, b.t->ptr, b.span() * 2))
+        return false;
+    if ((a.P > 1 && a.t->page != b.t->page) || (a.N > 1 && a.t->token != b.t->token) ||
+        (a.H > 1 && a.t->head != b.t->head))
+        return true;
+    const int64_t off = ((const char *)b.t->ptr - (const char *)a.t->ptr) / 2;
+    return !nested({{a.P, a.t->page}, {a.N, a.t->token}, {a.H, a.t->head}, {2, off < 0 ? -off : off}}, a.D);
+}
+
+} // namespace tok

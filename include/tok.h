@@ -593,6 +593,132 @@ TOK_API tok_status tok_cross_attention_backward(const tok_heads *q, const tok_he
                                                 float scale, void *workspace, int64_t workspace_bytes,
                                                 cudaStream_t stream);
 
+/*
+ * Embedding of codes: y[n] = scale * table[codes[n]], and its gradient.
+ *   codes    : [N] int32 (input).  A code outside [0, V) gives a row of NaN, adds 1 to
+ *              bad_count (device int32 or NULL; the caller zeroes it) and nothing to the gradient.
+ *   table, y : [V, D] and [N, D] of `dtype`, rows table_row and y_row elements apart, channels dense;
+ *              computed in fp32, rounded once.
+ * tok_embed_codes_backward -- grad_table[v] = scale * the sum of grad_y[n] over the tokens n
+ *   with code v (overwritten; zero for a code without a token).  grad_y and grad_table have dtypes
+ *   of their own.  Sums are fp32 and added in an order that depends on N, V, D, the dtypes, the
+ *   alignment of the two tensors and the codes alone: tokens are sorted by code first, in rising order within a code.
+ *   workspace: 16-byte-aligned device memory of tok_embed_codes_backward_workspace_size()
+ *   bytes, overwritten; calls that may overlap need one each.  The size is -1 for an invalid shape.
+ * Shape rule: 0 <= N < 2^30, 1 <= V <= 2^18, 1 <= D <= 65536; row strides at least D and below 2^38 / rows.
+ * Outputs overlap no input, the workspace neither (TOK_ERR_ALIAS).
+ */
+TOK_API tok_status tok_embed_codes(const int32_t *codes, const void *table, void *y, int32_t *bad_count,
+                                   tok_dtype dtype, int64_t N, int64_t V, int64_t D, int64_t table_row, int64_t y_row,
+                                   float scale, cudaStream_t stream);
+TOK_API int64_t tok_embed_codes_backward_workspace_size(int64_t N, int64_t V, int64_t D);
+TOK_API tok_status tok_embed_codes_backward(const int32_t *codes, const void *grad_y, void *grad_table,
+                                            tok_dtype grad_dtype, tok_dtype table_dtype, int64_t N, int64_t V,
+                                            int64_t D, int64_t grad_row, int64_t table_row, float scale,
+                                            void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Pages: a cache of keys and values whose streams grow, in pages of page_size tokens from one pool.
+ * Stream b holds held[b] pages, table[b][0 .. held[b]), token t of it being row t % page_size of page
+ * table[b][t / page_size]; its slot is that page times page_size plus that row.  pages [F] lists the pages
+ * that no stream holds: the first *free_count of them.
+ *
+ * tok_page_tables -- room for new tokens.  Stream b has lens[b] tokens and gets fresh[b] (NULL: N; clamped to
+ *   [0, N]) more.  Pages that it still needs come off the end of the list, in the order of streams, then of
+ *   their pages, and are added to its row of the table; slots [B, N] gets the slots of its new tokens, and -1
+ *   behind them.  A stream for which the list is too short (all streams before it served or not), the
+ *   table's row too narrow (M pages) or whose length is negative gets no page and slots of -1, and adds 1 to
+ *   bad_count (device int32 or NULL; the caller zeroes it).  A slot of 2^31 or more, or of a page below 0, is -1.
+ *   held_out [B] and free_out [1] get the new counts; they may be held and free_count themselves.
+ * tok_page_release -- the pages that lens[b] tokens (negative: 0) do not need go back to the list, so that taking
+ *   them anew gives each stream the same ones; their table entries become -1.  A list without room for all of them
+ *   (F) stays as it is, as does everything else, and bad_count gets 1.
+ * free_count is clamped to [0, F], held to [0, M].
+ * Shape rule: 0 <= B <= 65535, 0 <= N, M, F < 2^31, page_size >= 1, M * page_size < 2^31, B * N, B * M < 2^31; table
+ * rows table_row >= M elements apart, below 2^38 / B.
+ */
+TOK_API tok_status tok_page_tables(const int32_t *lens, const int32_t *fresh, const int32_t *held,
+                                   const int32_t *free_count, const int32_t *pages, int32_t *table, int32_t *slots,
+                                   int32_t *held_out, int32_t *free_out, int32_t *bad_count, int64_t B, int64_t N,
+                                   int64_t M, int64_t F, int64_t page_size, int64_t table_row, cudaStream_t stream);
+TOK_API tok_status tok_page_release(const int32_t *lens, const int32_t *held, const int32_t *free_count,
+                                    int32_t *pages, int32_t *table, int32_t *held_out, int32_t *free_out,
+                                    int32_t *bad_count, int64_t B, int64_t M, int64_t F, int64_t page_size,
+                                    int64_t table_row, cudaStream_t stream);
+
+/*
+ * Keys or values in pages: [P, page_size, H, D] bf16, pointer and strides in elements of page, token and
+ * head, the D channels dense (so keys and values may be slices of one pool).
+ */
+typedef struct {
+    void *ptr;
+    int64_t page, token, head; /* strides in elements */
+} tok_pages;
+
+/*
+ * tok_paged_write -- k and v [B, N, H, D] bf16 into the pages: token n of stream b goes to slot slots[b][n]
+ *   (page slot / page_size, row slot % page_size).  Slots below 0 are left out; one behind the pool
+ *   is left out and adds 1 to bad_count (device int32 or NULL; the caller zeroes it).  Of several tokens with the same slot
+ *   the last one, in the order of (b, n), need not win: the row is a mix of theirs.
+ * Shape rule: D a multiple of 8, 8 <= D <= 128; B, H <= 65535; B * N, P * page_size < 2^31; as tok_cross_attention
+ * for strides and alignment (pointers and strides multiples of 16 bytes).
+ */
+TOK_API tok_status tok_paged_write(const tok_heads *k, const tok_heads *v, const int32_t *slots,
+                                   const tok_pages *k_pages, const tok_pages *v_pages, int32_t *bad_count, int64_t B,
+                                   int64_t N, int64_t H, int64_t D, int64_t P, int64_t page_size,
+                                   cudaStream_t stream);
+
+/*
+ * tok_paged_attention -- attention of a few new tokens of each stream over its keys and values in pages.
+ *   q, o [B, Nq, Hq, D] bf16; k_pages, v_pages [P, page_size, Hkv, D] bf16; table [B, M] int32, rows
+ *   table_row elements apart: token t of stream b is row t % page_size of page table[b][t / page_size].
+ * Stream b has k_lens[b] tokens (clamped to [0, M * page_size]), the new ones among them: query i, for i < q_lens[b]
+ * (NULL: Nq; clamped to [0, Nq]), is token k_lens[b] - q_lens[b] + i and sees the tokens up to itself. The keys and values
+ * that it does not see show nowhere in its result, NaN included.  A query without a token (i >= q_lens[b], or
+ * a token before the first) has o = 0 and lse = -inf.  Formulas, head groups, roundings and the values that are not numbers are
+ * tok_cross_attention's; so are the rules for q and o.  An entry of the table outside [0, P) that one of the k_lens[b]
+ * tokens needs makes o and lse of the stream's queries NaN (of those with a token).
+ * lse [B, Hq, Nq] fp32 or NULL.  workspace: 16-byte-aligned device memory of
+ * tok_paged_attention_workspace_size() bytes, overwritten; calls that may overlap need one each.
+ * Results do not depend on the device's timing (every sum has a fixed order).
+ * Shape rule: D a multiple of 8, 8 <= D <= 128; Hq a multiple of Hkv; 0 <= Nq <= 64; B, Hq <= 65535; B * Hq * Nq <
+ * 2^30; P * page_size, M * page_size < 2^31; the size is -1 for an invalid shape.
+ */
+TOK_API int64_t tok_paged_attention_workspace_size(int64_t B, int64_t Nq, int64_t Hq, int64_t Hkv, int64_t D);
+TOK_API tok_status tok_paged_attention(const tok_heads *q, const tok_pages *k_pages, const tok_pages *v_pages,
+                                       const int32_t *table, const int32_t *k_lens, const int32_t *q_lens,
+                                       const tok_heads *o, float *lse, int64_t B, int64_t Nq, int64_t Hq, int64_t Hkv,
+                                       int64_t D, int64_t P, int64_t page_size, int64_t M, int64_t table_row,
+                                       float scale, void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * tok_verify_codes -- which of the drafted codes stand, and the code that follows them, from given numbers in [0, 1).
+ *   logits       : [B, K + 1, V] of `dtype` (input), the model's logits for each drafted code and for the one behind them
+ *   draft_logits : [B, K, V] of `dtype`, the logits that the drafts were drawn from, or NULL: each draft was certain
+ *   codes        : [B, K] int32, the drafted codes (input; may be NULL for K = 0)
+ *   u            : [B, K + 1] fp32 in [0, 1) (input)
+ *   n_draft      : [B] int32, drafted codes of each stream (clamped to [0, K]), or NULL: K
+ *   temperature  : [B], of both logits, or NULL: temperature_all for every stream
+ *   out          : [B, K + 1] int32 (output): the codes that stand, the drawn one, then -1
+ *   accepted     : [B] int32 (output): how many stand
+ * p_i = softmax(logits[b][i] / T), q_i = softmax(draft_logits[b][i] / T) (or 1 at the drafted code).  Draft i
+ * stands if all before it do and u[b][i] q_i(x_i) < p_i(x_i); behind the last that stands, a code is drawn with
+ * u[b][K]: from max(p_i - q_i, 0) where draft i does not stand (from p_i where that is 0 throughout), from p_i behind
+ * all drafts.  Drawn is the first code, in index order, at which the running sum exceeds u times the total; u is
+ * clamped to [0, 1) (NaN: 0).  So the codes are distributed as draws from p.  temperature <= 0 (or NaN): p and q are 1 at the
+ * first of the largest logits.  Logits of NaN count as -inf; where a logit is +inf only these count, alike.  A row of
+ * logits all -inf refuses the draft and draws -1.  A drafted code outside [0, V) does not stand.
+ * Probabilities are taken and added up in 64 bits, in a fixed order; a draft's test is decided in 32 bits where these
+ * leave no doubt.
+ * Shape rule: 0 <= B <= 2^20, 0 <= K <= 63, 1 <= V <= 2^18; rows logits_row apart, streams logits_batch apart
+ * (draft_row, draft_batch), 0 <= strides < 2^40.
+ */
+TOK_API tok_status tok_verify_codes(const void *logits, const void *draft_logits, tok_dtype dtype,
+                                    const int32_t *codes, const float *u, const int32_t *n_draft,
+                                    const float *temperature, float temperature_all, int32_t *out, int32_t *accepted,
+                                    int64_t B, int64_t K, int64_t V, int64_t logits_batch, int64_t logits_row,
+                                    int64_t draft_batch, int64_t draft_row, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
