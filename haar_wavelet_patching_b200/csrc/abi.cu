@@ -105,7 +105,7 @@ extern "C" int tok_last_cuda_error(void) { return tok::g_last_cuda_error; }
 
 extern "C" tok_status tok_check_device(cudaStream_t stream)
 {
-    unsigned int nh = 0, nf = 0, nb = 0, nc = 0, na = 0, nab = 0;
+    unsigned int nh = 0, nf = 0, nb = 0, nc = 0, na = 0, nab = 0, np = 0;
     tok_status st = tok::read_and_clear_haar_timeouts(stream, &nh);
     if (st == TOK_OK)
         st = tok::read_and_clear_fsq_timeouts(stream, &nf);
@@ -117,9 +117,11 @@ extern "C" tok_status tok_check_device(cudaStream_t stream)
         st = tok::read_and_clear_attn_timeouts(stream, &na);
     if (st == TOK_OK)
         st = tok::read_and_clear_attn_bwd_timeouts(stream, &nab);
+    if (st == TOK_OK)
+        st = tok::read_and_clear_paged_timeouts(stream, &np);
     if (st != TOK_OK)
         return st;
-    return (nh || nf || nb || nc || na || nab) ? TOK_ERR_TIMEOUT : TOK_OK;
+    return (nh || nf || nb || nc || na || nab || np) ? TOK_ERR_TIMEOUT : TOK_OK;
 }
 
 extern "C" const char *tok_status_str(tok_status status)

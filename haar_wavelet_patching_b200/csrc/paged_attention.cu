@@ -1,41 +1,55 @@
 // Attention of a few new tokens of each stream over its keys and values in pages.
 //
-// The call is bound by reading the keys and values once.  16 query rows (queries x the heads of a group) of one key
-// head are a unit; its keys come in rounds of 64, 16 to each of a CTA's 4 warps, on warp-level m16n8k16 tiles with a running maximum
-// and sum per warp.  Streams differ in length, so the rounds of all units of all streams, in order, are one sequence,
-// which two CTAs per SM share out in equal contiguous parts.  A CTA that has a unit whole writes its
-// result; of a unit that several CTAs have parts of, partial results (fp32) go to the workspace, at most two per CTA,
-// and join_kernel, launched early, adds them up in order.
+// The call is bound by reading the keys and values once.  Up to 64 query rows (queries x the heads of a group) of one key
+// head are a unit; its keys come in rounds of 128.  Streams differ in length, so the rounds of all units of all
+// streams, in order, are one sequence, which the SMs' CTAs share out in equal contiguous parts.  A CTA that
+// has a unit whole writes its result; of a unit that several CTAs have parts of, partial results (fp32) go to the
+// workspace, at most two per CTA, and paged_join_kernel, launched early, adds them up in order.
 //
-// Each warp keeps a ring of its own in shared memory, all stages but one on their way (cp.async, 16 bytes a lane, so
-// that pages of any size and stride are read whole rows at a time); the ring runs on from one unit
-// into the next.  A table entry is loaded one step before its rows.
+// There are few query rows and many keys, so the products are taken transposed, with the 128 rows of the tensor
+// cores' tiles for keys and for channels: scores^T = K Q^T (128 keys x N queries), then o^T += V^T P^T
+// (channels x N), and no thread touches a key or a value.  A CTA's warps:
+//   warps 0-3  softmax, a key to a thread (its lane of tensor memory): scores -> weights, rounded to bf16, into shared
+//              memory as the second product's operand.  All keys of a unit share a row's maximum, which is moved only when a
+//              score exceeds it by more than 2^8; sums stay with the threads.  At a unit's end: o / sum -> HBM;
+//   warp 4     tensor copies of keys and values into a ring of 128-byte-swizzled tiles: boxes of as many rows as divide
+//              both a page and a round, a box to a lane, on from one unit into the next;
+//   warp 5     one thread issues the MMAs: the next round's scores before this round's second product;
+//   warp 6     copies of the units' queries, one unit ahead.
+// A round may read rows behind a stream's last token: their scores are masked and their values zeroed in shared memory.
+// All waits are bounded as in the convolutions.
 #include <algorithm>
 
 #include "pages.cuh"
 
 namespace tok {
+
+static __device__ unsigned int g_paged_timeouts = 0;
+
 namespace {
 
-constexpr int kRows = 16; // query rows of a unit
-constexpr int kWarps = 4;
-constexpr int kStep = 16;               // keys of a warp's step
-constexpr int kRound = kWarps * kStep;  // keys of a CTA's
-constexpr int kMinRounds = 2;           // fewest rounds of a CTA
-constexpr int kCtas = 148 * 2;
+constexpr int kRound = 128;    // keys of a round
+constexpr int kMinRounds = 2;  // fewest rounds of a CTA
+constexpr int kCtas = 148;
 constexpr int64_t kMaxNq = 64;
+constexpr int kThreads = 7 * 32;
+constexpr float kGrow = 8.0f;  // log2 of the growth of the maximum that the weights absorb
+constexpr float kLowest = -3.402823466e+38f;
 
 struct PagedArgs {
     HeadsView q, o;
     PagesView k, v;
     const int32_t *table, *k_lens, *q_lens;
     float *lse;
-    float *part;   // [kCtas][2][kRows][D]: unit begun before the CTA's part, unit going on behind it
-    float2 *stats; // [kCtas][2][kRows]: their maximum and sum
+    float *part;   // [kCtas][2][rows][D]: unit begun before the CTA's part, unit going on behind it
+    float2 *stats; // [kCtas][2][rows]: their maximum and sum
+    float *side;   // [kCtas][64][rows]: scores of keys whose values are no numbers
     int2 *spans;   // [units]: first and last CTA of a unit, or (-1, .) of one that a CTA has whole
     int64_t table_row;
-    int B, Nq, Hq, Hkv, G, D, tiles, units, P, tokens; // row tiles; units of a stream; tokens of a table row
+    int B, Nq, Hq, Hkv, G, D, rows, tiles, units, P, tokens; // rows of a unit; row tiles; units of a stream; tokens of a table row
     FastDiv page;
+    int box_rows;     // rows of a tensor copy
+    int kh, vh;       // coordinate factors: 0 for broadcast heads
     float scale2;
 };
 
@@ -44,16 +58,61 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok) /
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
 
-// NP = ceil(D / 64).  Row r of a tile of 16 keeps its 16-byte chunk c at c ^ mix(r): the 8 lanes that a shared-memory
-// read serves at a time (key fragments: 2 rows x 4 chunks; value fragments: 4 rows of one parity x 2 chunks) then meet 8
-// different banks.
-template <int NP> struct Ring {
-    static constexpr int stages = NP == 2 ? 3 : 4;
-    static constexpr int row = NP * 128, tile = kStep * row, stage = 2 * tile, warp = stages * stage; // bytes
-    static constexpr int join = 32 * NP * 32 * 4; // a warp's result
-    static constexpr int bytes = kWarps * warp + 2 * join;
-};
-__device__ __forceinline__ int mix(int r) { return (r & 6) ^ ((r & 1) << 2); }
+// Barrier of the softmax warps; `any`: whether one of their threads says so.
+__device__ __forceinline__ void softmax_sync()
+{
+    __syncwarp();
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+__device__ __forceinline__ bool softmax_any(bool v)
+{
+    uint32_t r;
+    __syncwarp();
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+                 : "=r"(r)
+                 : "r"((uint32_t)v)
+                 : "memory");
+    return r != 0;
+}
+
+// One value of each of 16 rows per lane -> the rows' maxima (or sums) over the warp: lane 2 i has row i's.
+template <bool kMax> __device__ __forceinline__ float reduce16(float (&v)[16])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 8; o; o >>= 1) { // o rows left of 2 o: the upper ones go to the lane with bit 2 o set
+        const bool up = lane & (2 * o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < o) {
+                const float keep = up ? v[i + o] : v[i], give = up ? v[i] : v[i + o];
+                const float x = __shfl_xor_sync(~0u, give, 2 * o);
+                v[i] = kMax ? fmaxf(keep, x) : keep + x;
+            }
+    }
+    const float x = __shfl_xor_sync(~0u, v[0], 1);
+    return kMax ? fmaxf(v[0], x) : v[0] + x;
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+                 "%15}, [%16];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+                   "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+                 "%15, %16};" ::"r"(taddr),
+                 "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]),
+                 "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
+                 : "memory");
+}
+
+constexpr uint32_t kATransposed = 1u << 15; // instruction descriptor: A is MN-major
 
 __device__ __forceinline__ int rounds_of(const PagedArgs &a, int b, int &len)
 {
@@ -78,17 +137,56 @@ struct Place {
     int b, unit, round, rounds, len;
 };
 
-template <int NP>
-__global__ void __launch_bounds__(kWarps * 32, 2) paged_kernel(const PagedArgs a)
+// Shared memory of a CTA: DP channels, N query rows; `ring` rounds of keys and values.
+template <int DP, int N> struct Smem {
+    static constexpr int sub = kRound * 128;     // 64 channels of a round's keys
+    static constexpr int tile = DP / 64 * sub;   // keys or values of a round
+    static constexpr int q = DP / 64 * N * 128;  // a unit's queries
+    static constexpr int p = 2 * N * 128;        // a round's weights
+    static constexpr int ring = DP == 64 ? (N == 16 ? 6 : N == 32 ? 5 : 4) : N == 16 ? 3 : 2;
+    static constexpr int at_q = 2 * ring * tile, at_p = at_q + 2 * q;
+    static constexpr int bytes = at_p + 2 * p + 1024;
+    static_assert(bytes <= 227 * 1024 - 4096, "4 KB are for the static part");
+};
+
+template <int DP, int N>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PagedArgs a)
 {
-    constexpr int NC = 2 * NP;
-    using R = Ring<NP>;
-    extern __shared__ __align__(128) unsigned char ring_raw[];
-    __shared__ float sm[kWarps][kRows], sl[kWarps][kRows];
-    __shared__ int64_t s_sum[kWarps];
+    using S = Smem<DP, N>;
+    constexpr int NB = 2 * S::ring, kChunks = N / 16;
+    constexpr uint32_t kColumns = N == 16 ? 64 : N == 32 ? 128 : 256;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full[NB], empty[NB], qfull[2], qempty[2], sfull[2], pfull[2], pfree[2], ofull, drain;
+    __shared__ uint32_t tmem_base_s;
+    __shared__ int abort_s;
+    __shared__ int64_t s_sum[kThreads / 32];
     __shared__ Place s_first;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    __shared__ float s_m[N], s_inv[N], s_scale[N], s_red[4][N];
+    __shared__ int s_lim[N];
+    __shared__ int64_t s_out[N];
+    __shared__ unsigned long long s_odd; // keys behind lim_first whose values are no numbers
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     asm volatile("griddepcontrol.launch_dependents;");
+
+    if (tid == 0) {
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(smem_addr(&full[i]), 1);
+            mbar_init(smem_addr(&empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&qfull[i]), 1);
+            mbar_init(smem_addr(&qempty[i]), 1);
+            mbar_init(smem_addr(&sfull[i]), 1);
+            mbar_init(smem_addr(&pfull[i]), 4);
+            mbar_init(smem_addr(&pfree[i]), 1);
+        }
+        mbar_init(smem_addr(&ofull), 1);
+        mbar_init(smem_addr(&drain), 1);
+        abort_s = 0;
+        fence_barrier_init();
+    }
 
     // ---- This CTA's part [pos, end) of the rounds. ----
     auto block_sum = [&](int64_t v, int64_t &before) { // sum over the block; `before`: of the threads before
@@ -106,38 +204,47 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_kernel(const PagedArgs a
         before = x - v;
         int64_t all = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < kThreads / 32; ++w) {
             before += w < warp ? s_sum[w] : 0;
             all += s_sum[w];
         }
         return all;
     };
     int64_t total = 0, before;
-    for (int b0 = 0; b0 < a.B; b0 += kWarps * 32) {
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         int len;
         total += block_sum(b0 + tid < a.B ? (int64_t)rounds_of(a, b0 + tid, len) * a.units : 0, before);
     }
     const int64_t ctas = min((int64_t)kCtas, max((int64_t)1, total / kMinRounds)), cta = blockIdx.x;
     if (cta >= ctas)
         return;
-    int64_t pos = total * cta / ctas;
-    const int64_t end = total * (cta + 1) / ctas;
+    const int64_t pos0 = total * cta / ctas, end = total * (cta + 1) / ctas;
     int64_t run = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kWarps * 32) {
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + tid;
         int len = 0;
         const int rounds = b < a.B ? rounds_of(a, b, len) : 0;
         const int64_t mine = (int64_t)rounds * a.units, all = block_sum(mine, before), at = run + before;
-        if (pos >= at && pos < at + mine) {
-            const int64_t in = pos - at;
+        if (pos0 >= at && pos0 < at + mine) {
+            const int64_t in = pos0 - at;
             s_first = Place{b, (int)(in / rounds), (int)(in % rounds), rounds, len};
         }
         run += all;
-        if (run > pos)
+        if (run > pos0)
             break;
     }
+    if (warp == 5) {
+        tmem_alloc(smem_addr(&tmem_base_s), kColumns);
+        tmem_relinquish();
+    }
+    tc_fence_before();
     __syncthreads();
-    Place now = s_first, ahead = now;
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+    const uint32_t s_col[2] = {tmem, tmem + N}, o_col = tmem + 2 * N;
+    volatile int *abort = &abort_s;
+    Place now = s_first;
+    const int64_t count = end - pos0; // rounds of this CTA
     auto advance = [&](Place &p) {
         if (++p.round < p.rounds)
             return;
@@ -148,322 +255,403 @@ __global__ void __launch_bounds__(kWarps * 32, 2) paged_kernel(const PagedArgs a
         if (++p.b < a.B)
             p.rounds = rounds_of(a, p.b, p.len);
     };
+    auto ends_unit = [&](const Place &p, int64_t j) { return p.round + 1 == p.rounds || j + 1 == count; };
 
-    // ---- Copies: `ahead` is the round whose table entry is at hand. ----
-    unsigned char *ring = ring_raw + warp * R::warp;
-    const uint32_t ring_s = smem_addr(ring);
-    constexpr int kChunks = NP * 8, kCopies = kStep * kChunks / 32; // per tile and lane
-    int entry = -1, in_page = 0; // lane r (and r + 16): of key r of the step; -1: there is none, -2: not a page
-    auto look_up = [&]() {
-        const int key = ahead.round * kRound + warp * kStep + (lane & 15);
-        entry = -1;
-        if (key < ahead.len) {
-            const uint32_t p = a.page.div((uint32_t)key);
-            in_page = (int)(key - p * a.page.d);
-            entry = a.table[ahead.b * a.table_row + p];
-        }
-    };
-    int64_t left = end - pos; // rounds not yet fetched
-    uint32_t bad = 0;         // stages with a key of no page
-    auto fetch = [&](int stage) {
-        if (left > 0) {
-            const bool none = entry == -1 && ahead.round * kRound + warp * kStep + (lane & 15) >= ahead.len;
-            const bool out = !none && (uint32_t)entry >= (uint32_t)a.P;
-            if (__any_sync(~0u, out))
-                bad |= 1u << stage;
-            const int page = none || out ? -1 : entry;
-            const int64_t head = ahead.unit / a.tiles;
-            const __nv_bfloat16 *kbase = a.k.p + head * a.k.h, *vbase = a.v.p + head * a.v.h;
-            const uint32_t dst = ring_s + stage * R::stage;
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const int e = i * 32 + lane, r = e / kChunks, ch = e % kChunks;
-                const int pg = __shfl_sync(~0u, page, r), in = __shfl_sync(~0u, in_page, r);
-                const bool ok = pg >= 0 && ch * 8 < a.D;
-                const uint32_t to = dst + r * R::row + ((ch ^ mix(r)) << 4);
-                copy16(to, ok ? kbase + (pg * a.k.pg + in * a.k.t + ch * 8) : a.q.p, ok);
-                copy16(to + R::tile, ok ? vbase + (pg * a.v.pg + in * a.v.t + ch * 8) : a.q.p, ok);
-            }
-            if (--left > 0) {
-                advance(ahead);
-                look_up();
-            }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    look_up();
-#pragma unroll
-    for (int s = 0; s < R::stages - 1; ++s)
-        fetch(s);
-
-    // ---- Rounds. ----
-    uint4 qlo[NC], qhi[NC];
-    float acc[NP][8][4];
-    float mlo, mhi, llo, lhi;
-    int lim_lo = 0, lim_hi = 0, lim_first = 0; // keys seen by this lane's rows; by all of the unit's
-    bool unit_bad = false, whole = false;
-    int stage = 0;
-    bool fresh = true;
-    for (; pos < end; ++pos) {
-        const int hk = now.unit / a.tiles, r0 = (now.unit - hk * a.tiles) * kRows;
-        if (fresh) {
-            fresh = false;
-            whole = now.round == 0;
-            const int queries = query_count(a, now.b), lo = r0 + g, hi = lo + 8, rows = a.Nq * a.G;
-            lim_lo = limit_of(a, lo, now.len, queries);
-            lim_hi = limit_of(a, hi, now.len, queries);
-            lim_first = limit_of(a, r0, now.len, queries);
-            load_chan<NC>(qlo, a.q.row(now.b, lo / a.G, hk * a.G + lo % a.G), lo < rows, 8 * c, a.D);
-            load_chan<NC>(qhi, a.q.row(now.b, hi / a.G, hk * a.G + hi % a.G), hi < rows, 8 * c, a.D);
-#pragma unroll
-            for (int p = 0; p < NP; ++p)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[p][j][e] = 0.0f;
-            mlo = mhi = -INFINITY;
-            llo = lhi = 0.0f;
-            unit_bad = false;
-        }
-        asm volatile("cp.async.wait_group %0;" ::"n"(R::stages - 2) : "memory"); // this lane's copies of the round
-        __syncwarp(); // every lane's; and every lane is done with the stage refilled next
-        const int kk = now.round * kRound + warp * kStep;
-        unit_bad = unit_bad || (bad >> stage & 1);
-        bad &= ~(1u << stage);
-        fetch(stage == 0 ? R::stages - 1 : stage - 1);
-        const unsigned char *kt = ring + stage * R::stage, *vt = kt + R::tile;
-        stage = stage + 1 == R::stages ? 0 : stage + 1;
-        if (kk < now.len) {
-            float s[2][4] = {};
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                uint4 kf[NC];
-#pragma unroll
-                for (int i = 0; i < NC; ++i)
-                    kf[i] = *reinterpret_cast<const uint4 *>(kt + (8 * t + g) * R::row + (((4 * i + c) ^ mix(g)) << 4));
-                mma_chan<NC>(s[t], qlo, qhi, kf);
-            }
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[t][e] = kk + 8 * t + 2 * c + (e & 1) < (e < 2 ? lim_lo : lim_hi) ? s[t][e] * a.scale2 : -INFINITY;
-            const float nlo = fmaxf(mlo, quad_max(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]))));
-            const float nhi = fmaxf(mhi, quad_max(fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]))));
-            if (__any_sync(~0u, nlo > mlo || nhi > mhi)) {
-                const float flo = nlo == -INFINITY ? 1.0f : exp2_fast(mlo - nlo);
-                const float fhi = nhi == -INFINITY ? 1.0f : exp2_fast(mhi - nhi);
-                llo *= flo;
-                lhi *= fhi;
-#pragma unroll
-                for (int p = 0; p < NP; ++p)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        acc[p][j][0] *= flo;
-                        acc[p][j][1] *= flo;
-                        acc[p][j][2] *= fhi;
-                        acc[p][j][3] *= fhi;
-                    }
-                mlo = nlo;
-                mhi = nhi;
-            }
-            const float zlo = mlo == -INFINITY ? 0.0f : mlo, zhi = mhi == -INFINITY ? 0.0f : mhi;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                s[t][0] = exp2_fast(s[t][0] - zlo);
-                s[t][1] = exp2_fast(s[t][1] - zlo);
-                s[t][2] = exp2_fast(s[t][2] - zhi);
-                s[t][3] = exp2_fast(s[t][3] - zhi);
-                llo += s[t][0] + s[t][1];
-                lhi += s[t][2] + s[t][3];
-            }
-            // The weights enter the second product as bf16 (its operands share one type).
-            const uint32_t pa[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
-                                    pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])};
-            // A value that some rows see and others do not meets weights of 0; where it is no finite
-            // number, the products are taken key by key, with the rows that see the key.
-            bool careful = false;
-            if (kk + kStep > lim_first) {
-                uint32_t odd = 0;
-#pragma unroll
-                for (int i = 0; i < kStep * kChunks / 32; ++i) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(vt + (i * 32 + lane) * 16);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        odd |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
+    if (warp == 4) {
+        // ---- Keys and values. ----
+        const int boxes = kRound / a.box_rows; // of a round's keys, per 64 channels
+        constexpr int kSubs = DP / 64;
+        uint32_t n = 0; // tiles
+        bool ok = true;
+        for (int64_t j = 0; j < count && ok; ++j) {
+            const int head = now.unit / a.tiles;
+            for (int kv = 0; kv < 2 && ok; ++kv, ++n) {
+                const uint32_t slot = n % NB, bar = smem_addr(&full[slot]), dst = base + slot * S::tile;
+                if (lane == 0) {
+                    ok = wait_or_abort(smem_addr(&empty[slot]), ((n / NB) & 1u) ^ 1u, abort);
+                    if (ok)
+                        mbar_expect_tx(bar, S::tile);
                 }
-                careful = __any_sync(~0u, odd);
-            }
-            if (!careful) {
-#pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    RowFrag vf;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 2 * c + (i & 1) + 8 * (i >> 1);
-                        vf.r[i] = *reinterpret_cast<const uint4 *>(vt + r * R::row + (((8 * p + g) ^ mix(r & 7)) << 4));
+                ok = __shfl_sync(~0u, ok, 0);
+                if (!ok)
+                    break;
+                for (int i = lane; i < boxes * kSubs; i += 32) {
+                    const int sub = i / boxes, box = i - sub * boxes, key = now.round * kRound + box * a.box_rows;
+                    int page = a.P, in = 0; // (behind the pool: zeros)
+                    if (key < now.len) {
+                        const uint32_t p = a.page.div((uint32_t)key);
+                        const int entry = a.table[now.b * a.table_row + p];
+                        in = (int)(key - p * a.page.d);
+                        page = (uint32_t)entry < (uint32_t)a.P ? entry : a.P;
                     }
-                    mma_rows(acc[p], pa, vf);
+                    tma_load_4d(dst + sub * S::sub + box * a.box_rows * 128, kv ? &vmap : &kmap, 64 * sub, in,
+                                head * (kv ? a.vh : a.kh), page, bar);
                 }
-            } else {
-#pragma unroll 1
-                for (int k = 0; k < kStep; ++k) { // key k's weights are in lane k % 8 / 2 of a row's four
-                    const int from = (lane & ~3) | (k & 7) >> 1;
-                    const uint32_t plo = __shfl_sync(~0u, k < 8 ? pa[0] : pa[2], from);
-                    const uint32_t phi = __shfl_sync(~0u, k < 8 ? pa[1] : pa[3], from);
-                    const float wlo = k & 1 ? bf16_hi(plo) : bf16_lo(plo), whi = k & 1 ? bf16_hi(phi) : bf16_lo(phi);
+                __syncwarp();
+            }
+            advance(now);
+        }
+        if (!ok && lane == 0) // let the copies already issued land before the CTA exits (each wait bounded)
+            for (uint32_t t = n > (uint32_t)NB ? n - NB : 0; t < n; ++t)
+                mbar_wait(smem_addr(&full[t % NB]), (t / NB) & 1u);
+    } else if (warp == 6) {
+        // ---- Queries. ----
+        constexpr int kPieces = DP / 8;
+        uint32_t u = 0; // units
+        bool ok = true;
+        for (int64_t j = 0; j < count && ok; ++u) {
+            ok = wait_or_abort(smem_addr(&qempty[u & 1]), ((u >> 1) & 1u) ^ 1u, abort);
+            ok = __all_sync(~0u, ok);
+            if (!ok)
+                break;
+            const int hk = now.unit / a.tiles, first = (now.unit - hk * a.tiles) * N;
+#pragma unroll 4
+            for (int i = lane; i < N * kPieces; i += 32) {
+                const int r = i / kPieces, ch = i % kPieces, row = first + r;
+                const bool have = ch * 8 < a.D && row < a.Nq * a.G;
+                copy16(base + S::at_q + (u & 1) * S::q + (ch >> 3) * (N * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                       have ? a.q.row(now.b, row / a.G, hk * a.G + row % a.G) + ch * 8 : a.q.p, have);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&qfull[u & 1]));
+            j += now.rounds - now.round; // to the next unit
+            now.round = now.rounds - 1;
+            advance(now);
+        }
+    } else if (warp == 5) {
+        if (lane == 0) {
+            const uint32_t idesc_s = idesc_bf16_f32(kRound, N), idesc_o = idesc_bf16_f32(DP, N) | kATransposed;
+            const uint64_t kdesc = sw128_desc(base), qdesc = sw128_desc(base + S::at_q);
+            const uint64_t vdesc = sw128_desc_mn(base, S::sub), pdesc = sw128_desc(base + S::at_p);
+            bool ok = true;
+            Place next = now; // of the round whose scores come next
+            int unit_s = 0;
+            auto scores = [&](int64_t j) { // s_j = k_j q^T
+                const uint32_t n = (uint32_t)(2 * j), slot = n % NB;
+                ok = wait_or_abort(smem_addr(&qfull[unit_s & 1]), (uint32_t)(unit_s >> 1) & 1u, abort) &&
+                     wait_or_abort(smem_addr(&full[slot]), (n / NB) & 1u, abort);
+                if (!ok)
+                    return;
+                tc_fence_after();
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        float x[2][8];
+                for (int k = 0; k < DP / 16; ++k)
+                    umma_bf16(s_col[j & 1], kdesc + ((slot * S::tile + (k / 4) * S::sub + (k % 4) * 32) >> 4),
+                              qdesc + (((unit_s & 1) * S::q + (k / 4) * (N * 128) + (k % 4) * 32) >> 4), idesc_s,
+                              k != 0);
+                umma_commit(smem_addr(&sfull[j & 1]));
+                umma_commit(smem_addr(&empty[slot]));
+                if (ends_unit(next, j)) {
+                    umma_commit(smem_addr(&qempty[unit_s & 1]));
+                    ++unit_s;
+                }
+                advance(next);
+            };
+            scores(0);
+            bool fresh = true;
+            for (int64_t j = 0; j < count && ok; ++j) {
+                if (j + 1 < count)
+                    scores(j + 1); // (s_(j - 1) has been read: its weights were there)
+                const uint32_t n = (uint32_t)(2 * j + 1), slot = n % NB;
+                ok = ok && wait_or_abort(smem_addr(&full[slot]), (n / NB) & 1u, abort) &&
+                     wait_or_abort(smem_addr(&pfull[j & 1]), (uint32_t)(j >> 1) & 1u, abort);
+                if (!ok)
+                    break;
+                tc_fence_after();
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            Row<__nv_bfloat16, 8, true>::load(
-                                reinterpret_cast<const __nv_bfloat16 *>(vt + k * R::row + (((8 * p + 2 * c + h) ^ mix(k & 7)) << 4)),
-                                x[h]);
+                for (int k = 0; k < kRound / 16; ++k)
+                    umma_bf16(o_col, vdesc + ((slot * S::tile + k * 2048) >> 4),
+                              pdesc + (((j & 1) * S::p + (k / 4) * (N * 128) + (k % 4) * 32) >> 4), idesc_o,
+                              !fresh || k > 0);
+                umma_commit(smem_addr(&empty[slot]));
+                umma_commit(smem_addr(&pfree[j & 1]));
+                fresh = ends_unit(now, j);
+                if (fresh)
+                    umma_commit(smem_addr(&ofull));
+                advance(now);
+            }
+            // Every MMA issued has completed before tensor memory is freed.
+            umma_commit(smem_addr(&drain));
+            mbar_wait(smem_addr(&drain), 0u);
+        }
+    } else {
+        // ---- Softmax: thread = key. ----
+        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+        constexpr bool kHold = N == 16; // a row's scores and maxima stay in registers
+        float l[N], m[kHold ? N : 1];
+        const uint32_t pbase = base + S::at_p + (tid >> 6) * (N * 128) + (tid & 7) * 2;
+        const int chunk = (tid >> 3) & 7;
+        float *side = a.side + cta * 64 * N;
+        bool ok = true, fresh = true, whole = false;
+        int lim_first = 0, units_done = 0;
+        int entry = 0; // of this thread's key, one round ahead; 0 (or what was) where it is none of the stream's
+        auto look_up = [&](const Place &p) {
+            const int key = p.round * kRound + tid;
+            if (key < p.len)
+                entry = a.table[p.b * a.table_row + a.page.div((uint32_t)key)];
+        };
+        look_up(now);
+        // (No thread leaves before the others know: a wait that has run out shows in the next round's vote.)
+        for (int64_t j = 0; j < count; ++j) {
+            const int hk = now.unit / a.tiles, r0 = (now.unit - hk * a.tiles) * N;
+            const bool first = fresh;
+            if (fresh) {
+                const int queries = query_count(a, now.b);
+                whole = now.round == 0;
+                // (the fewest keys that a row with a token sees; without such rows it is of no account)
+                lim_first = r0 / a.G < queries ? limit_of(a, r0, now.len, queries) : now.len;
+                softmax_sync(); // (the numbers of the unit before are still being read)
+                if (tid < N) {
+                    const int row = r0 + tid;
+                    s_lim[tid] = limit_of(a, row, now.len, queries);
+                    s_out[tid] = row < a.Nq * a.G
+                                     ? now.b * a.o.b + (row / a.G) * a.o.n + (hk * a.G + row % a.G) * a.o.h
+                                     : -1;
+                }
+                if (tid == 0)
+                    s_odd = 0;
+                softmax_sync();
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            if (kk + k < lim_lo) {
-                                acc[p][j][0] += wlo * x[0][j];
-                                acc[p][j][1] += wlo * x[1][j];
-                            }
-                            if (kk + k < lim_hi) {
-                                acc[p][j][2] += whi * x[0][j];
-                                acc[p][j][3] += whi * x[1][j];
-                            }
+                for (int r = 0; r < N; ++r)
+                    l[r] = 0.0f;
+            }
+            ok = wait_or_abort(smem_addr(&sfull[j & 1]), (uint32_t)(j >> 1) & 1u, abort) && ok;
+            __syncwarp();
+            tc_fence_after();
+            const int key = now.round * kRound + tid;
+            const bool none = key < now.len && (uint32_t)entry >= (uint32_t)a.P; // a key of no page: its score is no number
+            if (j + 1 < count) {
+                Place then = now;
+                advance(then);
+                look_up(then);
+            }
+            const bool edge = (now.round + 1) * kRound > lim_first; // some row does not see some key
+            const uint32_t sc = s_col[j & 1] + lanes;
+            float s[16];
+            auto load = [&](int c) { // 16 rows' scores times log2 e, -inf where the key is not seen
+                tmem_ld16(sc + 16 * c, s);
+                tmem_wait_ld();
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    s[r] = none ? __int_as_float(0x7FC00000) : s[r] * a.scale2;
+                if (edge) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        s[r] = key < s_lim[16 * c + r] ? s[r] : -INFINITY;
+                }
+            };
+            bool grow = false;
+            if (!first) {
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    load(c);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        grow |= s[r] > (kHold ? m[kHold ? r : 0] : s_m[16 * c + r]) + kGrow;
+                }
+            }
+            grow = softmax_any(grow || !ok);
+            if (grow && softmax_any(!ok))
+                break;
+            if (first || grow) { // the rows' maxima over the round's keys (and the one before)
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    if (!kHold || first)
+                        load(c);
+                    float x[16];
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        x[r] = s[r];
+                    const float top = reduce16<true>(x);
+                    if (!(lane & 1))
+                        s_red[warp][16 * c + (lane >> 1)] = top;
+                }
+                softmax_sync();
+                float to = kLowest, from = kLowest; // of row tid
+                if (tid < N) {
+                    to = fmaxf(fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), kLowest);
+                    if (!first) {
+                        from = s_m[tid];
+                        to = to > from + kGrow ? to : from;
+                    }
+                }
+                softmax_sync();
+                if (tid < N) {
+                    s_m[tid] = to;
+                    s_scale[tid] = exp2_fast(from - to); // (of the first round: not used)
+                }
+                softmax_sync();
+                if (!first) { // what is there already is relative to the maximum before
+                    ok = wait_or_abort(smem_addr(&pfree[(j - 1) & 1]), (uint32_t)((j - 1) >> 1) & 1u, abort) && ok;
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        float o[16];
+                        tmem_ld16(o_col + lanes + 16 * c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            o[r] *= s_scale[16 * c + r];
+                            l[16 * c + r] *= s_scale[16 * c + r];
                         }
+                        tmem_st16(o_col + lanes + 16 * c, o);
                     }
+                    tmem_wait_st();
+                }
+                if constexpr (kHold)
+#pragma unroll
+                    for (int r = 0; r < N; ++r)
+                        m[r] = s_m[r];
+            }
+            if (j >= 2)
+                ok = wait_or_abort(smem_addr(&pfree[j & 1]), (uint32_t)((j - 2) >> 1) & 1u, abort) && ok;
+            // A value that some rows see and others do not meets weights of 0: where it is no finite number,
+            // its row is taken out, and what it adds to the rows that see it comes at the unit's end.  What lies
+            // behind the stream's last token is nobody's.
+            bool odd = false;
+            if (edge && key >= lim_first) {
+                const uint32_t n = (uint32_t)(2 * j + 1), slot = n % NB;
+                if (!wait_or_abort(smem_addr(&full[slot]), (n / NB) & 1u, abort))
+                    ok = false;
+                else {
+                    unsigned char *row = smem_raw + (base - smem_addr(smem_raw)) + slot * S::tile + tid * 128;
+                    for (int i = 0; i < DP / 8; ++i) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(row + (i >> 3) * S::sub + (i & 7) * 16);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            odd |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
+                    }
+                    if (odd && key < now.len)
+                        atomicOr(&s_odd, 1ull << (key - lim_first));
+                    if (odd) {
+                        for (int i = 0; i < DP / 8; ++i)
+                            *reinterpret_cast<uint4 *>(row + (i >> 3) * S::sub + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    odd = odd && key < now.len;
                 }
             }
-        }
-        const bool done = now.round + 1 == now.rounds;
-        if (!done && pos + 1 < end) {
-            ++now.round;
-            continue;
-        }
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                if constexpr (!kHold)
+                    load(c);
+                if (odd) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        side[(key - lim_first) * N + 16 * c + r] = s[r];
+                }
+                __syncwarp();
+                const uint32_t to = pbase + (j & 1) * S::p + 16 * c * 128;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float e = exp2_fast(s[r] - (kHold ? m[kHold ? r : 0] : s_m[16 * c + r]));
+                    l[16 * c + r] += e;
+                    // (an operand of the second product: bf16, as the values are)
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + r * 128 + ((chunk ^ (r & 7)) << 4)),
+                                 "h"(__bfloat16_as_ushort(__float2bfloat16_rn(e)))
+                                 : "memory");
+                }
+            }
+            tc_fence_before();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&pfull[j & 1]));
+            fresh = ends_unit(now, j);
+            if (!fresh) {
+                ++now.round;
+                continue;
+            }
 
-        // ---- The unit's end, or that of this CTA's part: the warps' results added up. ----
-        fresh = true;
-        llo = quad_sum(llo); // (all lanes, whatever their rows see)
-        lhi = quad_sum(lhi);
-        llo = lim_lo == 0 ? 0.0f : unit_bad ? __int_as_float(0x7FC00000) : llo;
-        lhi = lim_hi == 0 ? 0.0f : unit_bad ? __int_as_float(0x7FC00000) : lhi;
-        if (c == 0) {
-            sm[warp][g] = mlo;
-            sm[warp][g + 8] = mhi;
-            sl[warp][g] = llo;
-            sl[warp][g + 8] = lhi;
-        }
-        __syncthreads();
-        float all_lo = sm[0][g], all_hi = sm[0][g + 8];
+            // ---- The unit's end, or that of this CTA's part. ----
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            all_lo = fmaxf(all_lo, sm[w][g]);
-            all_hi = fmaxf(all_hi, sm[w][g + 8]);
-        }
-        llo = lhi = 0.0f;
+            for (int c = 0; c < kChunks; ++c) {
+                float x[16];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            llo += (sm[w][g] == -INFINITY ? 0.0f : exp2_fast(sm[w][g] - all_lo)) * sl[w][g];
-            lhi += (sm[w][g + 8] == -INFINITY ? 0.0f : exp2_fast(sm[w][g + 8] - all_hi)) * sl[w][g + 8];
-        }
-        const float flo = mlo == -INFINITY ? 0.0f : exp2_fast(mlo - all_lo);
-        const float fhi = mhi == -INFINITY ? 0.0f : exp2_fast(mhi - all_hi);
-        float4 *buf = reinterpret_cast<float4 *>(ring_raw + kWarps * R::warp);
-        constexpr int kBuf = R::join / 16;
-        auto give = [&](float4 *to) {
-#pragma unroll
-            for (int p = 0; p < NP; ++p)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    to[(p * 8 + j) * 32 + lane] = make_float4(acc[p][j][0], acc[p][j][1], acc[p][j][2], acc[p][j][3]);
-        };
-        auto take = [&](const float4 *from) {
-#pragma unroll
-            for (int p = 0; p < NP; ++p)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 x = from[(p * 8 + j) * 32 + lane];
-                    acc[p][j][0] += x.x;
-                    acc[p][j][1] += x.y;
-                    acc[p][j][2] += x.z;
-                    acc[p][j][3] += x.w;
-                }
-        };
-#pragma unroll
-        for (int p = 0; p < NP; ++p)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                acc[p][j][0] *= flo;
-                acc[p][j][1] *= flo;
-                acc[p][j][2] *= fhi;
-                acc[p][j][3] *= fhi;
+                for (int r = 0; r < 16; ++r)
+                    x[r] = l[16 * c + r];
+                const float sum = reduce16<false>(x);
+                if (!(lane & 1))
+                    s_red[warp][16 * c + (lane >> 1)] = sum;
             }
-        if (warp & 1)
-            give(buf + (warp >> 1) * kBuf);
-        __syncthreads();
-        if (!(warp & 1))
-            take(buf + (warp >> 1) * kBuf);
-        __syncthreads();
-        if (warp == 2)
-            give(buf);
-        __syncthreads();
-        if (warp == 0) {
-            take(buf);
-            const bool alone = whole && done;
-            const int64_t unit = (int64_t)now.b * a.units + now.unit;
-            if (lane == 0 && whole) {
-                const int64_t last = pos + (now.rounds - 1 - now.round); // (round 0 was at pos - now.round)
-                a.spans[unit] = alone ? make_int2(-1, -1) : make_int2((int)cta, (int)(((last + 1) * ctas - 1) / total));
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = r0 + g + 8 * h;
-                if (row >= a.Nq * a.G)
-                    continue;
-                const float m = h ? all_hi : all_lo, l = h ? lhi : llo;
-                const int iq = row / a.G, head = hk * a.G + row % a.G;
+            softmax_sync();
+            const bool done = now.round + 1 == now.rounds, alone = whole && done;
+            if (tid < N) {
+                // (a row without a token is not masked where all others see the whole round)
+                const float sum = s_lim[tid] == 0 ? 0.0f
+                                                  : (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
+                const float top = s_m[tid];
+                s_inv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum; // (a sum of NaN gives NaN, no key 0)
+                const int row = r0 + tid;
                 if (alone) {
-                    const float inv = 1.0f / l;
-                    __nv_bfloat16 *o = a.o.row(now.b, iq, head);
-#pragma unroll
-                    for (int p = 0; p < NP; ++p)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float x[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                x[j] = l == 0.0f ? 0.0f : acc[p][j][2 * h + e] * inv;
-                            const int d = 64 * p + 16 * c + 8 * e;
-                            if (d < a.D)
-                                Row<__nv_bfloat16, 8, true>::store(o + d, x);
-                        }
-                    if (c == 0 && a.lse)
-                        a.lse[((int64_t)now.b * a.Hq + head) * a.Nq + iq] =
-                            l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-                } else {
-                    const int64_t at = (cta * 2 + whole) * kRows + (row - r0);
-#pragma unroll
-                    for (int p = 0; p < NP; ++p)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float x[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                x[j] = acc[p][j][2 * h + e];
-                            const int d = 64 * p + 16 * c + 8 * e;
-                            if (d < a.D)
-                                Row<float, 8, true>::store(a.part + at * a.D + d, x);
-                        }
-                    if (c == 0)
-                        a.stats[at] = make_float2(m, l);
-                }
+                    if (a.lse && row < a.Nq * a.G)
+                        a.lse[((int64_t)now.b * a.Hq + hk * a.G + row % a.G) * a.Nq + row / a.G] =
+                            sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+                } else
+                    a.stats[(cta * 2 + whole) * N + tid] = make_float2(sum == 0.0f ? -INFINITY : top, sum);
             }
+            if (tid == 0 && whole) {
+                const int64_t last = pos0 + j + (now.rounds - 1 - now.round);
+                a.spans[(int64_t)now.b * a.units + now.unit] =
+                    alone ? make_int2(-1, -1) : make_int2((int)cta, (int)(((last + 1) * ctas - 1) / total));
+            }
+            softmax_sync();
+            ok = wait_or_abort(smem_addr(&ofull), (uint32_t)units_done & 1u, abort) && ok;
+            ++units_done;
+            __syncwarp();
+            tc_fence_after();
+            // (64 channels are 16 lanes of each warp)
+            const int d = DP == 128 ? tid : 16 * warp + lane;
+            const bool live = d < a.D && (DP == 128 || lane < 16);
+            const unsigned long long odds = s_odd;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                float o[16];
+                tmem_ld16(o_col + lanes + 16 * c, o);
+                tmem_wait_ld();
+                if (live) {
+                    for (unsigned long long left = odds; left; left &= left - 1) {
+                        const int at = __ffsll((long long)left) - 1, k = lim_first + at;
+                        const uint32_t pg = a.page.div((uint32_t)k);
+                        const int entry = a.table[now.b * a.table_row + pg];
+                        const float v = (uint32_t)entry < (uint32_t)a.P
+                                            ? __bfloat162float(a.v.row(entry, k - pg * a.page.d, hk)[d])
+                                            : 0.0f;
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            if (k < s_lim[16 * c + r])
+                                o[r] += exp2_fast(side[at * N + 16 * c + r] - s_m[16 * c + r]) * v;
+                    }
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int64_t to = s_out[16 * c + r];
+                        if (to >= 0) {
+                            if (alone) {
+                                const float inv = s_inv[16 * c + r];
+                                a.o.p[to + d] = __float2bfloat16_rn(inv == 0.0f ? 0.0f : o[r] * inv);
+                            } else
+                                a.part[((cta * 2 + whole) * N + 16 * c + r) * a.D + d] = o[r];
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            advance(now);
         }
-        advance(now);
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kColumns);
+    }
+    if (tid == 0 && *abort)
+        atomicAdd(&g_paged_timeouts, 1u);
 }
 
 // One warp per query row and head: the parts of its unit in order.
@@ -477,11 +665,11 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a)
     const int64_t bq = at / a.Hq;
     const int head = (int)(at - bq * a.Hq), b = (int)(bq / a.Nq), iq = (int)(bq - (int64_t)b * a.Nq);
     const int hk = head / a.G, row = iq * a.G + head % a.G;
-    const int2 span = a.spans[(int64_t)b * a.units + hk * a.tiles + row / kRows];
+    const int2 span = a.spans[(int64_t)b * a.units + hk * a.tiles + row / a.rows];
     if (span.x < 0)
         return;
-    const int n = span.y - span.x + 1, r = row % kRows;
-    auto place = [&](int i) { return ((int64_t)(span.x + i) * 2 + (i == 0)) * kRows + r; }; // (the first begins it)
+    const int n = span.y - span.x + 1, r = row % a.rows;
+    auto place = [&](int i) { return ((int64_t)(span.x + i) * 2 + (i == 0)) * a.rows + r; }; // (the first begins it)
     float m = -INFINITY;
     for (int i = lane; i < n; i += 32)
         m = fmaxf(m, a.stats[place(i)].x);
@@ -533,29 +721,76 @@ struct PagedDims {
         return B >= 0 && B <= 65535 && Nq >= 0 && Nq <= kMaxNq && Hkv >= 1 && Hq >= 1 && Hq <= 65535 && Hq % Hkv == 0 &&
                D >= 8 && D <= 128 && D % 8 == 0 && prod_ok({B, Hq, Nq}, &p) && p < ((int64_t)1 << 30);
     }
-    int64_t tiles() const { return (Nq * (Hq / Hkv) + kRows - 1) / kRows; }
+    // Query rows of a unit: 16, 32 or 64.
+    int64_t rows() const
+    {
+        const int64_t r = Nq * (Hq / Hkv);
+        return r <= 16 ? 16 : r <= 32 ? 32 : 64;
+    }
+    int64_t tiles() const { return (Nq * (Hq / Hkv) + rows() - 1) / rows(); }
     int64_t units() const { return Hkv * tiles(); } // of a stream
-    int64_t at_stats() const { return (int64_t)kCtas * 2 * kRows * D * 4; }
-    int64_t at_spans() const { return at_stats() + (int64_t)kCtas * 2 * kRows * 8; }
+    int64_t at_stats() const { return (int64_t)kCtas * 2 * rows() * D * 4; }
+    int64_t at_side() const { return at_stats() + (int64_t)kCtas * 2 * rows() * 8; }
+    int64_t at_spans() const { return at_side() + (int64_t)kCtas * 64 * rows() * 4; }
     int64_t workspace() const { return B == 0 || Nq == 0 ? 0 : at_spans() + B * units() * 8; }
 };
 
-template <int NP> tok_status launch(const PagedArgs &a, cudaStream_t stream)
+template <int DP, int N>
+tok_status launch(const CUtensorMap &k, const CUtensorMap &v, const PagedArgs &a, cudaStream_t stream)
 {
     const cudaError_t e =
-        cudaFuncSetAttribute(paged_kernel<NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<NP>::bytes);
+        cudaFuncSetAttribute(paged_kernel<DP, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<DP, N>::bytes);
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return TOK_ERR_CUDA;
     }
-    paged_kernel<NP><<<kCtas, kWarps * 32, Ring<NP>::bytes, stream>>>(a);
+    paged_kernel<DP, N><<<kCtas, kThreads, Smem<DP, N>::bytes, stream>>>(k, v, a);
     const tok_status st = launch_status();
     return st == TOK_OK ? launch_join(paged_join_kernel, (int64_t)a.B * a.Nq * a.Hq, a, stream) : st;
+}
+
+template <int DP>
+tok_status launch_rows(const CUtensorMap &k, const CUtensorMap &v, const PagedArgs &a, cudaStream_t stream)
+{
+    return a.rows == 16   ? launch<DP, 16>(k, v, a, stream)
+           : a.rows == 32 ? launch<DP, 32>(k, v, a, stream)
+                          : launch<DP, 64>(k, v, a, stream);
+}
+
+// Tensor map of a pool with boxes of 64 channels x `rows` tokens.  Broadcast heads become an extent of 1 (their
+// coordinate factor is 0); without pages every copy lies behind the one page of the map.
+bool pages_map(CUtensorMap *map, const PagesView &x, const void *any, int64_t P, int64_t page_size, int64_t H, int64_t D,
+               int rows)
+{
+    auto str = [](int64_t n, int64_t s) { return (uint64_t)(n > 1 && s != 0 ? s * 2 : 16); };
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)page_size, (uint64_t)(x.h == 0 ? 1 : H), (uint64_t)std::max<int64_t>(P, 1)};
+    const uint64_t strides[3] = {str(page_size, x.t), str(H, x.h), str(P, x.pg)};
+    const uint32_t box[4] = {64, (uint32_t)rows, 1, 1};
+    return encode_tensor_map_sw128(map, 4, P > 0 ? x.p : any, dims, strides, box);
 }
 
 constexpr int64_t kIntMax = ((int64_t)1 << 31) - 1;
 
 } // namespace
+
+tok_status read_and_clear_paged_timeouts(cudaStream_t stream, unsigned int *count)
+{
+    unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(count, g_paged_timeouts, sizeof(unsigned int), 0, cudaMemcpyDeviceToHost,
+                                              stream);
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(stream);
+    if (e == cudaSuccess && *count)
+        e = cudaMemcpyToSymbolAsync(g_paged_timeouts, &zero, sizeof(unsigned int), 0, cudaMemcpyHostToDevice, stream);
+    if (e == cudaSuccess)
+        e = cudaStreamSynchronize(stream);
+    if (e != cudaSuccess) {
+        record_cuda_error(e);
+        return TOK_ERR_CUDA;
+    }
+    return TOK_OK;
+}
+
 } // namespace tok
 
 extern "C" int64_t tok_paged_attention_workspace_size(int64_t B, int64_t Nq, int64_t Hq, int64_t Hkv, int64_t D)
@@ -626,6 +861,7 @@ extern "C" tok_status tok_paged_attention(const tok_heads *q, const tok_pages *k
     char *ws = static_cast<char *>(workspace);
     a.part = reinterpret_cast<float *>(ws);
     a.stats = reinterpret_cast<float2 *>(ws + dim.at_stats());
+    a.side = reinterpret_cast<float *>(ws + dim.at_side());
     a.spans = reinterpret_cast<int2 *>(ws + dim.at_spans());
     a.table_row = table_row;
     a.B = (int)B;
@@ -634,11 +870,19 @@ extern "C" tok_status tok_paged_attention(const tok_heads *q, const tok_pages *k
     a.Hkv = (int)Hkv;
     a.G = (int)(Hq / Hkv);
     a.D = (int)D;
+    a.rows = (int)dim.rows();
     a.tiles = (int)dim.tiles();
     a.units = (int)dim.units();
     a.P = (int)P;
     a.tokens = (int)tokens;
     a.page = FastDiv((uint32_t)page_size);
     a.scale2 = (float)((double)scale * 1.4426950408889634);
-    return D <= 64 ? launch<1>(a, stream) : launch<2>(a, stream);
+    a.box_rows = (int)std::min<int64_t>(page_size & -page_size, kRound);
+    a.kh = Hkv > 1 && a.k.h == 0 ? 0 : 1;
+    a.vh = Hkv > 1 && a.v.h == 0 ? 0 : 1;
+    CUtensorMap km, vm;
+    if (!pages_map(&km, a.k, a.q.p, P, page_size, Hkv, D, a.box_rows) ||
+        !pages_map(&vm, a.v, a.q.p, P, page_size, Hkv, D, a.box_rows))
+        return TOK_ERR_SHAPE;
+    return D <= 64 ? launch_rows<64>(km, vm, a, stream) : launch_rows<128>(km, vm, a, stream);
 }

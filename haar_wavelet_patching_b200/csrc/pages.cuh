@@ -33,7 +33,7 @@ struct PoolView {
         for (const Axis &x : {Axis{P, t->page}, Axis{N, t->token}, Axis{H, t->head}})
             if (x.n > 1 && (x.s < 0 || x.s >= kMax / (x.n - 1)))
                 return false;
-        return true;
+        return (P <= 1 || t->page > 0) && (N <= 1 || t->token > 0);
     }
     bool distinct() const { return nested({{P, t->page}, {N, t->token}, {H, t->head}}, D); }
     bool aligned16() const

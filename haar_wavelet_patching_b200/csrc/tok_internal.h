@@ -55,13 +55,14 @@ tok_status conv_tc_spatial(const void *x, const void *ws, void *y, int64_t B, in
                            int64_t Cin, int64_t Cout, int64_t k, cudaStream_t stream);
 
 // Synchronize `stream`, return in *count the barrier-wait timeouts of this device's
-// Haar (resp. FSQ, FSQ backward, convolution, attention) kernels since the last call, and clear them.
+// Haar (resp. FSQ, FSQ backward, convolution, attention, paged attention) kernels since the last call, and clear them.
 tok_status read_and_clear_haar_timeouts(cudaStream_t stream, unsigned int *count);
 tok_status read_and_clear_fsq_timeouts(cudaStream_t stream, unsigned int *count);
 tok_status read_and_clear_fsq_bwd_timeouts(cudaStream_t stream, unsigned int *count);
 tok_status read_and_clear_conv_timeouts(cudaStream_t stream, unsigned int *count);
 tok_status read_and_clear_attn_timeouts(cudaStream_t stream, unsigned int *count);
 tok_status read_and_clear_attn_bwd_timeouts(cudaStream_t stream, unsigned int *count);
+tok_status read_and_clear_paged_timeouts(cudaStream_t stream, unsigned int *count);
 
 // Remembers a CUDA error for tok_last_cuda_error().
 void record_cuda_error(cudaError_t e);
