@@ -10,12 +10,14 @@
 // cores' tiles for keys and for channels: scores^T = K Q^T (128 keys x N queries), then o^T += V^T P^T
 // (channels x N), and no thread touches a key or a value.  A CTA's warps:
 //   warps 0-3  softmax, a key to a thread (its lane of tensor memory): scores -> weights, rounded to bf16, into shared
-//              memory as the second product's operand.  All keys of a unit share a row's maximum, which is moved only when a
-//              score exceeds it by more than 2^8; sums stay with the threads.  At a unit's end: o / sum -> HBM;
-//   warp 4     tensor copies of keys and values into a ring of 128-byte-swizzled tiles: boxes of as many rows as divide
-//              both a page and a round, a box to a lane, on from one unit into the next;
+//              memory as the second product's operand.  Weights are relative to the score of the unit's first key, and to
+//              the largest one from where one exceeds it by more than 2^16 (every term carries the same factor, so the
+//              quotient is unchanged); a vote of the four warps each round says so.  Sums stay with the threads up to a
+//              unit's end: o / sum -> HBM;
+//   warps 4, 7 tensor copies of keys and of values into rings of 128-byte-swizzled tiles: boxes of as many rows as divide
+//              both a page and a round, a box to a lane, its page looked up one round ahead;
 //   warp 5     one thread issues the MMAs: the next round's scores before this round's second product;
-//   warp 6     copies of the units' queries, one unit ahead.
+//   warp 6     copies of the units' queries and what their rows are, one unit ahead.
 // A round may read rows behind a stream's last token: their scores are masked and their values zeroed in shared memory.
 // All waits are bounded as in the convolutions.
 #include <algorithm>
@@ -32,8 +34,8 @@ constexpr int kRound = 128;    // keys of a round
 constexpr int kMinRounds = 2;  // fewest rounds of a CTA
 constexpr int kCtas = 148;
 constexpr int64_t kMaxNq = 64;
-constexpr int kThreads = 7 * 32;
-constexpr float kGrow = 8.0f;  // log2 of the growth of the maximum that the weights absorb
+constexpr int kThreads = 8 * 32;
+constexpr float kGrow = 16.0f; // log2 of the largest weight
 constexpr float kLowest = -3.402823466e+38f;
 
 struct PagedArgs {
@@ -47,7 +49,7 @@ struct PagedArgs {
     int2 *spans;   // [units]: first and last CTA of a unit, or (-1, .) of one that a CTA has whole
     int64_t table_row;
     int B, Nq, Hq, Hkv, G, D, rows, tiles, units, P, tokens; // rows of a unit; row tiles; units of a stream; tokens of a table row
-    FastDiv page;
+    FastDiv page, group;
     int box_rows;     // rows of a tensor copy
     int kh, vh;       // coordinate factors: 0 for broadcast heads
     float scale2;
@@ -125,13 +127,6 @@ __device__ __forceinline__ int query_count(const PagedArgs &a, int b)
     return a.q_lens ? min(max(a.q_lens[b], 0), a.Nq) : a.Nq;
 }
 
-// Keys that a row of a unit sees.
-__device__ __forceinline__ int limit_of(const PagedArgs &a, int row, int len, int queries)
-{
-    const int i = row / a.G;
-    return row < a.Nq * a.G && i < queries ? min(max(len - queries + i + 1, 0), len) : 0;
-}
-
 // A place in the sequence of rounds.
 struct Place {
     int b, unit, round, rounds, len;
@@ -149,35 +144,52 @@ template <int DP, int N> struct Smem {
     static_assert(bytes <= 227 * 1024 - 4096, "4 KB are for the static part");
 };
 
+// The rounds' shares: the first `more` of `ctas` CTAs have one more than the others.
+struct Shares {
+    uint32_t each, more;
+    __device__ __forceinline__ Shares(uint32_t total, uint32_t ctas) : each(total / ctas), more(total % ctas) {}
+    __device__ __forceinline__ uint32_t begin(uint32_t cta) const { return cta * each + min(cta, more); }
+    __device__ __forceinline__ uint32_t owner(uint32_t round) const
+    {
+        const uint32_t longer = more * (each + 1);
+        return round < longer ? round / (each + 1) : more + (round - longer) / each;
+    }
+};
+
 template <int DP, int N>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PagedArgs a)
 {
     using S = Smem<DP, N>;
-    constexpr int NB = 2 * S::ring, kChunks = N / 16;
+    constexpr int NB = S::ring, kChunks = N / 16; // stages of keys, of values
     constexpr uint32_t kColumns = N == 16 ? 64 : N == 32 ? 128 : 256;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[NB], empty[NB], qfull[2], qempty[2], sfull[2], pfull[2], pfree[2], ofull, drain;
+    __shared__ __align__(8) uint64_t full[2][NB], empty[2][NB], qfull[2], qempty[2], sfull[2], pfull[2], pfree[2], ofull, drain;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
-    __shared__ int64_t s_sum[kThreads / 32];
+    __shared__ uint32_t s_sum[kThreads / 32];
     __shared__ Place s_first;
-    __shared__ float s_m[N], s_inv[N], s_scale[N], s_red[4][N];
-    __shared__ int s_lim[N];
-    __shared__ int64_t s_out[N];
-    __shared__ unsigned long long s_odd; // keys behind lim_first whose values are no numbers
+    // Of a unit (the next one's are made meanwhile): rows' maxima, keys seen, places of the output; keys seen by all rows;
+    // which of the keys behind these have values that are no numbers.
+    __shared__ float s_m[2][N];
+    __shared__ int s_lim[2][N];
+    __shared__ int64_t s_out[2][N];
+    __shared__ int s_all[2];
+    __shared__ unsigned long long s_odd[2];
+    __shared__ float s_inv[N], s_scale[N], s_red[4][N];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     asm volatile("griddepcontrol.launch_dependents;");
 
     if (tid == 0) {
-        for (int i = 0; i < NB; ++i) {
-            mbar_init(smem_addr(&full[i]), 1);
-            mbar_init(smem_addr(&empty[i]), 1);
-        }
+        for (int i = 0; i < NB; ++i)
+            for (int kv = 0; kv < 2; ++kv) {
+                mbar_init(smem_addr(&full[kv][i]), 1);
+                mbar_init(smem_addr(&empty[kv][i]), 1);
+            }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&qfull[i]), 1);
-            mbar_init(smem_addr(&qempty[i]), 1);
+            mbar_init(smem_addr(&qempty[i]), 5);
             mbar_init(smem_addr(&sfull[i]), 1);
             mbar_init(smem_addr(&pfull[i]), 4);
             mbar_init(smem_addr(&pfree[i]), 1);
@@ -188,21 +200,20 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         fence_barrier_init();
     }
 
-    // ---- This CTA's part [pos, end) of the rounds. ----
-    auto block_sum = [&](int64_t v, int64_t &before) { // sum over the block; `before`: of the threads before
-        int64_t x = v;
+    // ---- This CTA's part [pos0, pos0 + count) of the rounds. ----
+    auto block_sum = [&](uint32_t v, uint32_t &before) { // sum over the block; `before`: of the threads before
+        uint32_t x = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(~0u, x, o);
+            const uint32_t y = __shfl_up_sync(~0u, x, o);
             if (lane >= o)
                 x += y;
         }
-        __syncthreads();
         if (lane == 31)
             s_sum[warp] = x;
         __syncthreads();
         before = x - v;
-        int64_t all = 0;
+        uint32_t all = 0;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             before += w < warp ? s_sum[w] : 0;
@@ -210,25 +221,33 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         }
         return all;
     };
-    int64_t total = 0, before;
+    uint32_t total = 0, before = 0, mine = 0;
+    int rounds = 0, len = 0;
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-        int len;
-        total += block_sum(b0 + tid < a.B ? (int64_t)rounds_of(a, b0 + tid, len) * a.units : 0, before);
+        if (b0)
+            __syncthreads();
+        rounds = b0 + tid < a.B ? rounds_of(a, b0 + tid, len) : 0;
+        mine = (uint32_t)(rounds * a.units);
+        total += block_sum(mine, before);
     }
-    const int64_t ctas = min((int64_t)kCtas, max((int64_t)1, total / kMinRounds)), cta = blockIdx.x;
+    const uint32_t ctas = min((uint32_t)kCtas, max(1u, total / kMinRounds)), cta = blockIdx.x;
     if (cta >= ctas)
         return;
-    const int64_t pos0 = total * cta / ctas, end = total * (cta + 1) / ctas;
-    int64_t run = 0;
+    const Shares shares(total, ctas);
+    const uint32_t pos0 = shares.begin(cta);
+    const int count = (int)(shares.begin(cta + 1) - pos0);
+    uint32_t run = 0;
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-        const int b = b0 + tid;
-        int len = 0;
-        const int rounds = b < a.B ? rounds_of(a, b, len) : 0;
-        const int64_t mine = (int64_t)rounds * a.units, all = block_sum(mine, before), at = run + before;
-        if (pos0 >= at && pos0 < at + mine) {
-            const int64_t in = pos0 - at;
-            s_first = Place{b, (int)(in / rounds), (int)(in % rounds), rounds, len};
+        uint32_t all = total;
+        if (a.B > kThreads) { // (else the numbers are at hand)
+            __syncthreads();
+            rounds = b0 + tid < a.B ? rounds_of(a, b0 + tid, len) : 0;
+            mine = (uint32_t)(rounds * a.units);
+            all = block_sum(mine, before);
         }
+        const uint32_t in = pos0 - (run + before);
+        if (pos0 >= run + before && in < mine)
+            s_first = Place{b0 + tid, (int)(in / rounds), (int)(in % rounds), rounds, len};
         run += all;
         if (run > pos0)
             break;
@@ -240,11 +259,9 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_base_s;
-    const uint32_t s_col[2] = {tmem, tmem + N}, o_col = tmem + 2 * N;
+    const uint32_t tmem = tmem_base_s, o_col = tmem + 2 * N; // scores: two times N columns
     volatile int *abort = &abort_s;
     Place now = s_first;
-    const int64_t count = end - pos0; // rounds of this CTA
     auto advance = [&](Place &p) {
         if (++p.round < p.rounds)
             return;
@@ -255,68 +272,103 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         if (++p.b < a.B)
             p.rounds = rounds_of(a, p.b, p.len);
     };
-    auto ends_unit = [&](const Place &p, int64_t j) { return p.round + 1 == p.rounds || j + 1 == count; };
+    auto ends_unit = [&](const Place &p, int j) { return p.round + 1 == p.rounds || j + 1 == count; };
 
-    if (warp == 4) {
-        // ---- Keys and values. ----
-        const int boxes = kRound / a.box_rows; // of a round's keys, per 64 channels
-        constexpr int kSubs = DP / 64;
-        uint32_t n = 0; // tiles
-        bool ok = true;
-        for (int64_t j = 0; j < count && ok; ++j) {
-            const int head = now.unit / a.tiles;
-            for (int kv = 0; kv < 2 && ok; ++kv, ++n) {
-                const uint32_t slot = n % NB, bar = smem_addr(&full[slot]), dst = base + slot * S::tile;
-                if (lane == 0) {
-                    ok = wait_or_abort(smem_addr(&empty[slot]), ((n / NB) & 1u) ^ 1u, abort);
-                    if (ok)
-                        mbar_expect_tx(bar, S::tile);
+    if (warp == 4 || warp == 7) {
+        // ---- Keys (warp 4) and values (warp 7): a box to a lane, its page one round ahead. ----
+        constexpr int kSubs = DP / 64, kMost = kRound / 32;
+        const int kv = warp == 7;
+        const CUtensorMap *map = kv ? &vmap : &kmap;
+        const int factor = kv ? a.vh : a.kh, boxes = kRound / a.box_rows, per = (boxes + 31) / 32; // per: to a lane
+        int page[kMost], in[kMost];
+        auto look_up = [&]() {
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) {
+                const int box = lane + 32 * i, key = now.round * kRound + box * a.box_rows;
+                page[i] = a.P; // (behind the pool: zeros)
+                in[i] = 0;
+                if (box < boxes && key < now.len) {
+                    const uint32_t p = a.page.div((uint32_t)key);
+                    page[i] = a.table[now.b * a.table_row + p];
+                    in[i] = (int)(key - p * a.page.d);
                 }
-                ok = __shfl_sync(~0u, ok, 0);
-                if (!ok)
-                    break;
-                for (int i = lane; i < boxes * kSubs; i += 32) {
-                    const int sub = i / boxes, box = i - sub * boxes, key = now.round * kRound + box * a.box_rows;
-                    int page = a.P, in = 0; // (behind the pool: zeros)
-                    if (key < now.len) {
-                        const uint32_t p = a.page.div((uint32_t)key);
-                        const int entry = a.table[now.b * a.table_row + p];
-                        in = (int)(key - p * a.page.d);
-                        page = (uint32_t)entry < (uint32_t)a.P ? entry : a.P;
-                    }
-                    tma_load_4d(dst + sub * S::sub + box * a.box_rows * 128, kv ? &vmap : &kmap, 64 * sub, in,
-                                head * (kv ? a.vh : a.kh), page, bar);
-                }
-                __syncwarp();
             }
-            advance(now);
+        };
+        look_up();
+        int j = 0;
+        bool ok = true;
+        for (; j < count; ++j) {
+            const int slot = j % NB, head = now.unit / a.tiles * factor;
+            const uint32_t bar = smem_addr(&full[kv][slot]), dst = base + (kv * NB + slot) * S::tile;
+            if (lane == 0) {
+                ok = wait_or_abort(smem_addr(&empty[kv][slot]), ((uint32_t)(j / NB) & 1u) ^ 1u, abort);
+                if (ok)
+                    mbar_expect_tx(bar, S::tile);
+            }
+            ok = __shfl_sync(~0u, ok, 0);
+            if (!ok)
+                break;
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) {
+                const int box = lane + 32 * i;
+                if (i < per && box < boxes) {
+                    const int p = (uint32_t)page[i] < (uint32_t)a.P ? page[i] : a.P;
+#pragma unroll
+                    for (int sub = 0; sub < kSubs; ++sub)
+                        tma_load_4d(dst + sub * S::sub + box * a.box_rows * 128, map, 64 * sub, in[i], head, p, bar);
+                }
+            }
+            __syncwarp();
+            if (j + 1 < count) {
+                advance(now);
+                look_up();
+            }
         }
         if (!ok && lane == 0) // let the copies already issued land before the CTA exits (each wait bounded)
-            for (uint32_t t = n > (uint32_t)NB ? n - NB : 0; t < n; ++t)
-                mbar_wait(smem_addr(&full[t % NB]), (t / NB) & 1u);
+            for (int t = max(0, j - NB); t < j; ++t)
+                mbar_wait(smem_addr(&full[kv][t % NB]), (uint32_t)(t / NB) & 1u);
     } else if (warp == 6) {
-        // ---- Queries. ----
+        // ---- A unit's queries, and what its rows are. ----
         constexpr int kPieces = DP / 8;
-        uint32_t u = 0; // units
-        bool ok = true;
-        for (int64_t j = 0; j < count && ok; ++u) {
-            ok = wait_or_abort(smem_addr(&qempty[u & 1]), ((u >> 1) & 1u) ^ 1u, abort);
+        uint32_t u = 0;
+        for (int j = 0; j < count; ++u) {
+            const int buf = u & 1;
+            bool ok = wait_or_abort(smem_addr(&qempty[buf]), ((u >> 1) & 1u) ^ 1u, abort);
             ok = __all_sync(~0u, ok);
             if (!ok)
                 break;
-            const int hk = now.unit / a.tiles, first = (now.unit - hk * a.tiles) * N;
+            const int hk = now.unit / a.tiles, first = (now.unit - hk * a.tiles) * N, rows = a.Nq * a.G;
 #pragma unroll 4
             for (int i = lane; i < N * kPieces; i += 32) {
-                const int r = i / kPieces, ch = i % kPieces, row = first + r;
-                const bool have = ch * 8 < a.D && row < a.Nq * a.G;
-                copy16(base + S::at_q + (u & 1) * S::q + (ch >> 3) * (N * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                       have ? a.q.row(now.b, row / a.G, hk * a.G + row % a.G) + ch * 8 : a.q.p, have);
+                const int r = i / kPieces, ch = i % kPieces, row = first + r, iq = (int)a.group.div((uint32_t)row);
+                const bool have = ch * 8 < a.D && row < rows;
+                copy16(base + S::at_q + buf * S::q + (ch >> 3) * (N * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                       have ? a.q.row(now.b, iq, hk * a.G + row - iq * a.G) + ch * 8 : a.q.p, have);
+            }
+            const int queries = query_count(a, now.b);
+#pragma unroll
+            for (int r = lane; r < N; r += 32) {
+                const int row = first + r, iq = (int)a.group.div((uint32_t)row);
+                const bool is = row < rows;
+                s_lim[buf][r] = is && iq < queries ? min(max(now.len - queries + iq + 1, 0), now.len) : 0;
+                s_out[buf][r] = is ? now.b * a.o.b + iq * a.o.n + (hk * a.G + row - iq * a.G) * a.o.h : -1;
+            }
+            if (lane == 0) {
+                // The fewest keys that a row with a token sees; without such rows it is of no account.
+                const int iq = (int)a.group.div((uint32_t)first);
+                s_all[buf] = iq < queries ? min(max(now.len - queries + iq + 1, 0), now.len) : now.len;
+                s_odd[buf] = 0;
+                if (now.round == 0) {
+                    const uint32_t last = pos0 + j + now.rounds - 1;
+                    a.spans[(int64_t)now.b * a.units + now.unit] =
+                        j + now.rounds <= count ? make_int2(-1, -1) : make_int2((int)cta, (int)shares.owner(last));
+                }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(smem_addr(&qfull[u & 1]));
+                mbar_arrive(smem_addr(&qfull[buf]));
             j += now.rounds - now.round; // to the next unit
             now.round = now.rounds - 1;
             advance(now);
@@ -325,37 +377,39 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         if (lane == 0) {
             const uint32_t idesc_s = idesc_bf16_f32(kRound, N), idesc_o = idesc_bf16_f32(DP, N) | kATransposed;
             const uint64_t kdesc = sw128_desc(base), qdesc = sw128_desc(base + S::at_q);
-            const uint64_t vdesc = sw128_desc_mn(base, S::sub), pdesc = sw128_desc(base + S::at_p);
+            const uint64_t vdesc = sw128_desc_mn(base + NB * S::tile, S::sub), pdesc = sw128_desc(base + S::at_p);
             bool ok = true;
             Place next = now; // of the round whose scores come next
-            int unit_s = 0;
-            auto scores = [&](int64_t j) { // s_j = k_j q^T
-                const uint32_t n = (uint32_t)(2 * j), slot = n % NB;
-                ok = wait_or_abort(smem_addr(&qfull[unit_s & 1]), (uint32_t)(unit_s >> 1) & 1u, abort) &&
-                     wait_or_abort(smem_addr(&full[slot]), (n / NB) & 1u, abort);
+            uint32_t u = 0;
+            auto scores = [&](int j) { // s_j = k_j q^T
+                const int slot = j % NB;
+                ok = wait_or_abort(smem_addr(&qfull[u & 1]), (u >> 1) & 1u, abort) &&
+                     wait_or_abort(smem_addr(&full[0][slot]), (uint32_t)(j / NB) & 1u, abort);
                 if (!ok)
                     return;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
-                    umma_bf16(s_col[j & 1], kdesc + ((slot * S::tile + (k / 4) * S::sub + (k % 4) * 32) >> 4),
-                              qdesc + (((unit_s & 1) * S::q + (k / 4) * (N * 128) + (k % 4) * 32) >> 4), idesc_s,
-                              k != 0);
+                    umma_bf16(tmem + (j & 1) * N, kdesc + ((slot * S::tile + (k / 4) * S::sub + (k % 4) * 32) >> 4),
+                              qdesc + (((u & 1) * S::q + (k / 4) * (N * 128) + (k % 4) * 32) >> 4), idesc_s, k != 0);
                 umma_commit(smem_addr(&sfull[j & 1]));
-                umma_commit(smem_addr(&empty[slot]));
+                umma_commit(smem_addr(&empty[0][slot]));
                 if (ends_unit(next, j)) {
-                    umma_commit(smem_addr(&qempty[unit_s & 1]));
-                    ++unit_s;
+                    umma_commit(smem_addr(&qempty[u & 1]));
+                    ++u;
                 }
-                advance(next);
+                if (j + 1 < count)
+                    advance(next);
             };
             scores(0);
             bool fresh = true;
-            for (int64_t j = 0; j < count && ok; ++j) {
+            for (int j = 0; j < count && ok; ++j) {
+                const Place p = next; // (of round j + 1; where that begins a unit, round j ended one)
+                const bool last = j + 1 == count || p.round == 0;
                 if (j + 1 < count)
                     scores(j + 1); // (s_(j - 1) has been read: its weights were there)
-                const uint32_t n = (uint32_t)(2 * j + 1), slot = n % NB;
-                ok = ok && wait_or_abort(smem_addr(&full[slot]), (n / NB) & 1u, abort) &&
+                const int slot = j % NB;
+                ok = ok && wait_or_abort(smem_addr(&full[1][slot]), (uint32_t)(j / NB) & 1u, abort) &&
                      wait_or_abort(smem_addr(&pfull[j & 1]), (uint32_t)(j >> 1) & 1u, abort);
                 if (!ok)
                     break;
@@ -365,12 +419,11 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                     umma_bf16(o_col, vdesc + ((slot * S::tile + k * 2048) >> 4),
                               pdesc + (((j & 1) * S::p + (k / 4) * (N * 128) + (k % 4) * 32) >> 4), idesc_o,
                               !fresh || k > 0);
-                umma_commit(smem_addr(&empty[slot]));
+                umma_commit(smem_addr(&empty[1][slot]));
                 umma_commit(smem_addr(&pfree[j & 1]));
-                fresh = ends_unit(now, j);
-                if (fresh)
+                fresh = last;
+                if (last)
                     umma_commit(smem_addr(&ofull));
-                advance(now);
             }
             // Every MMA issued has completed before tensor memory is freed.
             umma_commit(smem_addr(&drain));
@@ -383,10 +436,11 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         float l[N], m[kHold ? N : 1];
         const uint32_t pbase = base + S::at_p + (tid >> 6) * (N * 128) + (tid & 7) * 2;
         const int chunk = (tid >> 3) & 7;
-        float *side = a.side + cta * 64 * N;
+        float *side = a.side + (int64_t)cta * 64 * N;
         bool ok = true, fresh = true, whole = false;
-        int lim_first = 0, units_done = 0;
-        int entry = 0; // of this thread's key, one round ahead; 0 (or what was) where it is none of the stream's
+        int all = 0;    // keys that all rows see
+        uint32_t u = 0; // units
+        int entry = 0;  // of this thread's key, one round ahead; what was where it is none of the stream's
         auto look_up = [&](const Place &p) {
             const int key = p.round * kRound + tid;
             if (key < p.len)
@@ -394,41 +448,29 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         };
         look_up(now);
         // (No thread leaves before the others know: a wait that has run out shows in the next round's vote.)
-        for (int64_t j = 0; j < count; ++j) {
-            const int hk = now.unit / a.tiles, r0 = (now.unit - hk * a.tiles) * N;
+        for (int j = 0; j < count; ++j) {
             const bool first = fresh;
+            const int buf = u & 1;
             if (fresh) {
-                const int queries = query_count(a, now.b);
                 whole = now.round == 0;
-                // (the fewest keys that a row with a token sees; without such rows it is of no account)
-                lim_first = r0 / a.G < queries ? limit_of(a, r0, now.len, queries) : now.len;
-                softmax_sync(); // (the numbers of the unit before are still being read)
-                if (tid < N) {
-                    const int row = r0 + tid;
-                    s_lim[tid] = limit_of(a, row, now.len, queries);
-                    s_out[tid] = row < a.Nq * a.G
-                                     ? now.b * a.o.b + (row / a.G) * a.o.n + (hk * a.G + row % a.G) * a.o.h
-                                     : -1;
-                }
-                if (tid == 0)
-                    s_odd = 0;
-                softmax_sync();
+                ok = wait_or_abort(smem_addr(&qfull[buf]), (u >> 1) & 1u, abort) && ok;
+                all = s_all[buf];
 #pragma unroll
                 for (int r = 0; r < N; ++r)
                     l[r] = 0.0f;
             }
-            ok = wait_or_abort(smem_addr(&sfull[j & 1]), (uint32_t)(j >> 1) & 1u, abort) && ok;
-            __syncwarp();
-            tc_fence_after();
             const int key = now.round * kRound + tid;
             const bool none = key < now.len && (uint32_t)entry >= (uint32_t)a.P; // a key of no page: its score is no number
+            const bool edge = (now.round + 1) * kRound > all; // some row does not see some key
+            Place then = now;
             if (j + 1 < count) {
-                Place then = now;
                 advance(then);
                 look_up(then);
             }
-            const bool edge = (now.round + 1) * kRound > lim_first; // some row does not see some key
-            const uint32_t sc = s_col[j & 1] + lanes;
+            ok = wait_or_abort(smem_addr(&sfull[j & 1]), (uint32_t)(j >> 1) & 1u, abort) && ok;
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t sc = tmem + (j & 1) * N + lanes;
             float s[16];
             auto load = [&](int c) { // 16 rows' scores times log2 e, -inf where the key is not seen
                 tmem_ld16(sc + 16 * c, s);
@@ -439,26 +481,43 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 if (edge) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        s[r] = key < s_lim[16 * c + r] ? s[r] : -INFINITY;
+                        s[r] = key < s_lim[buf][16 * c + r] ? s[r] : -INFINITY;
                 }
             };
-            bool grow = false;
-            if (!first) {
+            if (first) { // weights are relative to the first key's score, unless another one is far above it
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
+                    if (kHold || warp == 0)
+                        load(c);
+                    if (tid == 0) {
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            s_m[buf][16 * c + r] = fmaxf(s[r], kLowest);
+                    }
+                }
+                softmax_sync();
+                if constexpr (kHold)
+#pragma unroll
+                    for (int r = 0; r < N; ++r)
+                        m[r] = s_m[buf][r];
+            }
+            bool grow = !ok;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                if (!kHold || !first)
                     load(c);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        grow |= s[r] > (kHold ? m[kHold ? r : 0] : s_m[16 * c + r]) + kGrow;
-                }
+                for (int r = 0; r < 16; ++r)
+                    grow |= s[r] > (kHold ? m[kHold ? r : 0] : s_m[buf][16 * c + r]) + kGrow;
             }
-            grow = softmax_any(grow || !ok);
-            if (grow && softmax_any(!ok))
-                break;
-            if (first || grow) { // the rows' maxima over the round's keys (and the one before)
+            grow = softmax_any(grow);
+            if (__builtin_expect(grow, 0)) {
+                if (softmax_any(!ok))
+                    break;
+                // The rows' maxima over the round's keys and what weights were relative to.
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
-                    if (!kHold || first)
+                    if (!kHold)
                         load(c);
                     float x[16];
 #pragma unroll
@@ -469,21 +528,14 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                         s_red[warp][16 * c + (lane >> 1)] = top;
                 }
                 softmax_sync();
-                float to = kLowest, from = kLowest; // of row tid
                 if (tid < N) {
-                    to = fmaxf(fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid])), kLowest);
-                    if (!first) {
-                        from = s_m[tid];
-                        to = to > from + kGrow ? to : from;
-                    }
-                }
-                softmax_sync();
-                if (tid < N) {
-                    s_m[tid] = to;
+                    const float top = fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid]));
+                    const float from = s_m[buf][tid], to = top > from + kGrow ? top : from;
+                    s_m[buf][tid] = to;
                     s_scale[tid] = exp2_fast(from - to); // (of the first round: not used)
                 }
                 softmax_sync();
-                if (!first) { // what is there already is relative to the maximum before
+                if (!first) { // what is there already is relative to the value before
                     ok = wait_or_abort(smem_addr(&pfree[(j - 1) & 1]), (uint32_t)((j - 1) >> 1) & 1u, abort) && ok;
                     __syncwarp();
                     tc_fence_after();
@@ -504,7 +556,7 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 if constexpr (kHold)
 #pragma unroll
                     for (int r = 0; r < N; ++r)
-                        m[r] = s_m[r];
+                        m[r] = s_m[buf][r];
             }
             if (j >= 2)
                 ok = wait_or_abort(smem_addr(&pfree[j & 1]), (uint32_t)((j - 2) >> 1) & 1u, abort) && ok;
@@ -512,12 +564,14 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
             // its row is taken out, and what it adds to the rows that see it comes at the unit's end.  What lies
             // behind the stream's last token is nobody's.
             bool odd = false;
-            if (edge && key >= lim_first) {
-                const uint32_t n = (uint32_t)(2 * j + 1), slot = n % NB;
-                if (!wait_or_abort(smem_addr(&full[slot]), (n / NB) & 1u, abort))
+            if (edge && key >= all) {
+                const int slot = j % NB;
+                if (!wait_or_abort(smem_addr(&full[1][slot]), (uint32_t)(j / NB) & 1u, abort))
                     ok = false;
                 else {
-                    unsigned char *row = smem_raw + (base - smem_addr(smem_raw)) + slot * S::tile + tid * 128;
+                    unsigned char *row =
+                        smem_raw + (base - smem_addr(smem_raw)) + (NB + slot) * S::tile + tid * 128;
+#pragma unroll 4
                     for (int i = 0; i < DP / 8; ++i) {
                         const uint4 x = *reinterpret_cast<const uint4 *>(row + (i >> 3) * S::sub + (i & 7) * 16);
                         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -525,11 +579,11 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                         for (int k = 0; k < 4; ++k)
                             odd |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
                     }
-                    if (odd && key < now.len)
-                        atomicOr(&s_odd, 1ull << (key - lim_first));
                     if (odd) {
                         for (int i = 0; i < DP / 8; ++i)
                             *reinterpret_cast<uint4 *>(row + (i >> 3) * S::sub + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        if (key < now.len)
+                            atomicOr(&s_odd[buf], 1ull << (key - all));
                     }
                     odd = odd && key < now.len;
                 }
@@ -542,13 +596,13 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 if (odd) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        side[(key - lim_first) * N + 16 * c + r] = s[r];
+                        side[(key - all) * N + 16 * c + r] = s[r];
                 }
                 __syncwarp();
                 const uint32_t to = pbase + (j & 1) * S::p + 16 * c * 128;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const float e = exp2_fast(s[r] - (kHold ? m[kHold ? r : 0] : s_m[16 * c + r]));
+                    const float e = exp2_fast(s[r] - (kHold ? m[kHold ? r : 0] : s_m[buf][16 * c + r]));
                     l[16 * c + r] += e;
                     // (an operand of the second product: bf16, as the values are)
                     asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + r * 128 + ((chunk ^ (r & 7)) << 4)),
@@ -561,9 +615,10 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_addr(&pfull[j & 1]));
+            __syncwarp(); // the arrival goes out before any lane begins to wait
             fresh = ends_unit(now, j);
             if (!fresh) {
-                ++now.round;
+                now = then;
                 continue;
             }
 
@@ -579,69 +634,71 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                     s_red[warp][16 * c + (lane >> 1)] = sum;
             }
             softmax_sync();
-            const bool done = now.round + 1 == now.rounds, alone = whole && done;
+            const bool alone = whole && now.round + 1 == now.rounds;
             if (tid < N) {
                 // (a row without a token is not masked where all others see the whole round)
-                const float sum = s_lim[tid] == 0 ? 0.0f
-                                                  : (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
-                const float top = s_m[tid];
+                const float sum = s_lim[buf][tid] == 0
+                                      ? 0.0f
+                                      : (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
                 s_inv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum; // (a sum of NaN gives NaN, no key 0)
-                const int row = r0 + tid;
-                if (alone) {
-                    if (a.lse && row < a.Nq * a.G)
-                        a.lse[((int64_t)now.b * a.Hq + hk * a.G + row % a.G) * a.Nq + row / a.G] =
-                            sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-                } else
-                    a.stats[(cta * 2 + whole) * N + tid] = make_float2(sum == 0.0f ? -INFINITY : top, sum);
-            }
-            if (tid == 0 && whole) {
-                const int64_t last = pos0 + j + (now.rounds - 1 - now.round);
-                a.spans[(int64_t)now.b * a.units + now.unit] =
-                    alone ? make_int2(-1, -1) : make_int2((int)cta, (int)(((last + 1) * ctas - 1) / total));
+                if (!alone)
+                    a.stats[(cta * 2 + whole) * N + tid] = make_float2(sum == 0.0f ? -INFINITY : s_m[buf][tid], sum);
+                else if (a.lse && s_out[buf][tid] >= 0) {
+                    const int hk = now.unit / a.tiles, row = (now.unit - hk * a.tiles) * N + tid;
+                    const int iq = (int)a.group.div((uint32_t)row);
+                    a.lse[((int64_t)now.b * a.Hq + hk * a.G + row - iq * a.G) * a.Nq + iq] =
+                        sum == 0.0f ? -INFINITY : (s_m[buf][tid] + log2f(sum)) * 0.6931471805599453f;
+                }
             }
             softmax_sync();
-            ok = wait_or_abort(smem_addr(&ofull), (uint32_t)units_done & 1u, abort) && ok;
-            ++units_done;
+            ok = wait_or_abort(smem_addr(&ofull), u & 1u, abort) && ok;
             __syncwarp();
             tc_fence_after();
             // (64 channels are 16 lanes of each warp)
             const int d = DP == 128 ? tid : 16 * warp + lane;
             const bool live = d < a.D && (DP == 128 || lane < 16);
-            const unsigned long long odds = s_odd;
+            const unsigned long long odds = s_odd[buf];
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
                 float o[16];
                 tmem_ld16(o_col + lanes + 16 * c, o);
                 tmem_wait_ld();
-                if (live) {
+                if (__builtin_expect(live && odds, 0)) {
                     for (unsigned long long left = odds; left; left &= left - 1) {
-                        const int at = __ffsll((long long)left) - 1, k = lim_first + at;
+                        const int at = __ffsll((long long)left) - 1, k = all + at;
                         const uint32_t pg = a.page.div((uint32_t)k);
-                        const int entry = a.table[now.b * a.table_row + pg];
-                        const float v = (uint32_t)entry < (uint32_t)a.P
-                                            ? __bfloat162float(a.v.row(entry, k - pg * a.page.d, hk)[d])
+                        const int e = a.table[now.b * a.table_row + pg];
+                        const float v = (uint32_t)e < (uint32_t)a.P
+                                            ? __bfloat162float(a.v.row(e, k - pg * a.page.d, now.unit / a.tiles)[d])
                                             : 0.0f;
 #pragma unroll
                         for (int r = 0; r < 16; ++r)
-                            if (k < s_lim[16 * c + r])
-                                o[r] += exp2_fast(side[at * N + 16 * c + r] - s_m[16 * c + r]) * v;
+                            if (k < s_lim[buf][16 * c + r])
+                                o[r] += exp2_fast(side[at * N + 16 * c + r] - s_m[buf][16 * c + r]) * v;
                     }
+                }
+                if (live && alone) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
-                        const int64_t to = s_out[16 * c + r];
-                        if (to >= 0) {
-                            if (alone) {
-                                const float inv = s_inv[16 * c + r];
-                                a.o.p[to + d] = __float2bfloat16_rn(inv == 0.0f ? 0.0f : o[r] * inv);
-                            } else
-                                a.part[((cta * 2 + whole) * N + 16 * c + r) * a.D + d] = o[r];
-                        }
+                        const int64_t to = s_out[buf][16 * c + r];
+                        const float inv = s_inv[16 * c + r];
+                        if (to >= 0)
+                            a.o.p[to + d] = __float2bfloat16_rn(inv == 0.0f ? 0.0f : o[r] * inv);
                     }
+                } else if (live) {
+                    float *part = a.part + ((int64_t)(cta * 2 + whole) * N + 16 * c) * a.D + d;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        part[r * a.D] = o[r]; // (of rows that are none, too: nobody reads them)
                 }
                 __syncwarp();
             }
             tc_fence_before();
-            advance(now);
+            if (lane == 0)
+                mbar_arrive(smem_addr(&qempty[buf])); // (this warp is done with the unit's numbers)
+            __syncwarp();
+            ++u;
+            now = then;
         }
     }
     tc_fence_before();
@@ -823,6 +880,9 @@ extern "C" tok_status tok_paged_attention(const tok_heads *q, const tok_pages *k
     const PoolView pk{k_pages, P, page_size, Hkv, D}, pv{v_pages, P, page_size, Hkv, D};
     if (!vq.strides_ok() || !vo.strides_ok() || !pk.strides_ok() || !pv.strides_ok() || !vo.distinct())
         return TOK_ERR_SHAPE;
+    int64_t rounds;
+    if (!prod_ok({B, dim.units(), tokens / kRound + 1}, &rounds) || rounds > kIntMax)
+        return TOK_ERR_SHAPE;
     const int64_t need = dim.workspace();
     if (workspace_bytes < need)
         return TOK_ERR_SHAPE;
@@ -876,6 +936,7 @@ extern "C" tok_status tok_paged_attention(const tok_heads *q, const tok_pages *k
     a.P = (int)P;
     a.tokens = (int)tokens;
     a.page = FastDiv((uint32_t)page_size);
+    a.group = FastDiv((uint32_t)a.G);
     a.scale2 = (float)((double)scale * 1.4426950408889634);
     a.box_rows = (int)std::min<int64_t>(page_size & -page_size, kRound);
     a.kh = Hkv > 1 && a.k.h == 0 ? 0 : 1;
