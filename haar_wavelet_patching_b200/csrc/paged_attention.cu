@@ -173,7 +173,8 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     // which of the keys behind these have values that are no numbers.
     __shared__ float s_m[2][N];
     __shared__ int s_lim[2][N];
-    __shared__ int64_t s_out[2][N];
+    __shared__ __nv_bfloat16 *s_out[2][N];
+    __shared__ int s_rows[2]; // rows that are queries
     __shared__ int s_all[2];
     __shared__ unsigned long long s_odd[2];
     __shared__ float s_inv[N], s_scale[N], s_red[4][N];
@@ -181,6 +182,10 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     asm volatile("griddepcontrol.launch_dependents;");
 
+    if (tid == 32) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+    }
     if (tid == 0) {
         for (int i = 0; i < NB; ++i)
             for (int kv = 0; kv < 2; ++kv) {
@@ -275,28 +280,30 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     auto ends_unit = [&](const Place &p, int j) { return p.round + 1 == p.rounds || j + 1 == count; };
 
     if (warp == 4 || warp == 7) {
-        // ---- Keys (warp 4) and values (warp 7): a box to a lane, its page one round ahead. ----
-        constexpr int kSubs = DP / 64, kMost = kRound / 32;
+        // ---- Keys (warp 4) and values (warp 7): a box to a lane, its page looked up two rounds ahead.  (Boxes
+        // behind the first 32, of pages that four does not divide, are looked up as they come.) ----
+        constexpr int kSubs = DP / 64;
         const int kv = warp == 7;
         const CUtensorMap *map = kv ? &vmap : &kmap;
-        const int factor = kv ? a.vh : a.kh, boxes = kRound / a.box_rows, per = (boxes + 31) / 32; // per: to a lane
-        int page[kMost], in[kMost];
-        auto look_up = [&]() {
-#pragma unroll
-            for (int i = 0; i < kMost; ++i) {
-                const int box = lane + 32 * i, key = now.round * kRound + box * a.box_rows;
-                page[i] = a.P; // (behind the pool: zeros)
-                in[i] = 0;
-                if (box < boxes && key < now.len) {
-                    const uint32_t p = a.page.div((uint32_t)key);
-                    page[i] = a.table[now.b * a.table_row + p];
-                    in[i] = (int)(key - p * a.page.d);
-                }
-            }
+        const int factor = kv ? a.vh : a.kh, boxes = kRound / a.box_rows;
+        auto look_up = [&](const Place &p, int box, int &row) { // page and row; the pool's end (zeros) where there is none
+            const int key = p.round * kRound + box * a.box_rows;
+            row = 0;
+            if (box >= boxes || key >= p.len)
+                return a.P;
+            const uint32_t page = a.page.div((uint32_t)key);
+            row = (int)(key - page * a.page.d);
+            return a.table[p.b * a.table_row + page];
         };
-        look_up();
-        int j = 0;
+        Place ahead = now; // the round looked up next
+        int page0, row0, page1 = 0, row1 = 0;
+        page0 = look_up(ahead, lane, row0);
+        if (count > 1) {
+            advance(ahead);
+            page1 = look_up(ahead, lane, row1);
+        }
         bool ok = true;
+        int j = 0;
         for (; j < count; ++j) {
             const int slot = j % NB, head = now.unit / a.tiles * factor;
             const uint32_t bar = smem_addr(&full[kv][slot]), dst = base + (kv * NB + slot) * S::tile;
@@ -308,20 +315,23 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
             ok = __shfl_sync(~0u, ok, 0);
             if (!ok)
                 break;
+#pragma unroll 1
+            for (int box = lane; box < boxes; box += 32) {
+                if (box >= 32)
+                    page0 = look_up(now, box, row0);
+                const int p = (uint32_t)page0 < (uint32_t)a.P ? page0 : a.P;
 #pragma unroll
-            for (int i = 0; i < kMost; ++i) {
-                const int box = lane + 32 * i;
-                if (i < per && box < boxes) {
-                    const int p = (uint32_t)page[i] < (uint32_t)a.P ? page[i] : a.P;
-#pragma unroll
-                    for (int sub = 0; sub < kSubs; ++sub)
-                        tma_load_4d(dst + sub * S::sub + box * a.box_rows * 128, map, 64 * sub, in[i], head, p, bar);
-                }
+                for (int sub = 0; sub < kSubs; ++sub)
+                    tma_load_4d(dst + sub * S::sub + box * a.box_rows * 128, map, 64 * sub, row0, head, p, bar);
             }
             __syncwarp();
-            if (j + 1 < count) {
+            if (j + 1 < count)
                 advance(now);
-                look_up();
+            page0 = page1;
+            row0 = row1;
+            if (j + 2 < count) {
+                advance(ahead);
+                page1 = look_up(ahead, lane, row1);
             }
         }
         if (!ok && lane == 0) // let the copies already issued land before the CTA exits (each wait bounded)
@@ -351,13 +361,14 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 const int row = first + r, iq = (int)a.group.div((uint32_t)row);
                 const bool is = row < rows;
                 s_lim[buf][r] = is && iq < queries ? min(max(now.len - queries + iq + 1, 0), now.len) : 0;
-                s_out[buf][r] = is ? now.b * a.o.b + iq * a.o.n + (hk * a.G + row - iq * a.G) * a.o.h : -1;
+                s_out[buf][r] = is ? a.o.row(now.b, iq, hk * a.G + row - iq * a.G) : a.o.p;
             }
             if (lane == 0) {
                 // The fewest keys that a row with a token sees; without such rows it is of no account.
                 const int iq = (int)a.group.div((uint32_t)first);
                 s_all[buf] = iq < queries ? min(max(now.len - queries + iq + 1, 0), now.len) : now.len;
                 s_odd[buf] = 0;
+                s_rows[buf] = min(N, rows - first);
                 if (now.round == 0) {
                     const uint32_t last = pos0 + j + now.rounds - 1;
                     a.spans[(int64_t)now.b * a.units + now.unit] =
@@ -564,26 +575,31 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
             // its row is taken out, and what it adds to the rows that see it comes at the unit's end.  What lies
             // behind the stream's last token is nobody's.
             bool odd = false;
-            if (edge && key >= all) {
+            if (__builtin_expect(edge && key >= all, 0)) {
                 const int slot = j % NB;
                 if (!wait_or_abort(smem_addr(&full[1][slot]), (uint32_t)(j / NB) & 1u, abort))
                     ok = false;
                 else {
+                    // (pieces in an order of the row's own, so that 8 rows meet 8 different banks)
                     unsigned char *row =
                         smem_raw + (base - smem_addr(smem_raw)) + (NB + slot) * S::tile + tid * 128;
-#pragma unroll 4
-                    for (int i = 0; i < DP / 8; ++i) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(row + (i >> 3) * S::sub + (i & 7) * 16);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    odd = key >= now.len;
+                    if (!odd) {
+#pragma unroll 2
+                        for (int i = 0; i < DP / 8; ++i) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(row + (i >> 3) * S::sub + ((i ^ tid) & 7) * 16);
+                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            odd |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
+                            for (int k = 0; k < 4; ++k)
+                                odd |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
+                        }
+                        if (odd)
+                            atomicOr(&s_odd[buf], 1ull << (key - all));
                     }
                     if (odd) {
+#pragma unroll 2
                         for (int i = 0; i < DP / 8; ++i)
-                            *reinterpret_cast<uint4 *>(row + (i >> 3) * S::sub + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        if (key < now.len)
-                            atomicOr(&s_odd[buf], 1ull << (key - all));
+                            *reinterpret_cast<uint4 *>(row + (i >> 3) * S::sub + ((i ^ tid) & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     odd = odd && key < now.len;
                 }
@@ -593,7 +609,7 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
             for (int c = 0; c < kChunks; ++c) {
                 if constexpr (!kHold)
                     load(c);
-                if (odd) {
+                if (__builtin_expect(odd, 0)) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
                         side[(key - all) * N + 16 * c + r] = s[r];
@@ -643,7 +659,7 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 s_inv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum; // (a sum of NaN gives NaN, no key 0)
                 if (!alone)
                     a.stats[(cta * 2 + whole) * N + tid] = make_float2(sum == 0.0f ? -INFINITY : s_m[buf][tid], sum);
-                else if (a.lse && s_out[buf][tid] >= 0) {
+                else if (a.lse && tid < s_rows[buf]) {
                     const int hk = now.unit / a.tiles, row = (now.unit - hk * a.tiles) * N + tid;
                     const int iq = (int)a.group.div((uint32_t)row);
                     a.lse[((int64_t)now.b * a.Hq + hk * a.G + row - iq * a.G) * a.Nq + iq] =
@@ -658,6 +674,7 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
             const int d = DP == 128 ? tid : 16 * warp + lane;
             const bool live = d < a.D && (DP == 128 || lane < 16);
             const unsigned long long odds = s_odd[buf];
+            const int live_rows = s_rows[buf];
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
                 float o[16];
@@ -678,13 +695,17 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                     }
                 }
                 if (live && alone) {
+                    __nv_bfloat16 *to[16];
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
-                        const int64_t to = s_out[buf][16 * c + r];
                         const float inv = s_inv[16 * c + r];
-                        if (to >= 0)
-                            a.o.p[to + d] = __float2bfloat16_rn(inv == 0.0f ? 0.0f : o[r] * inv);
+                        to[r] = s_out[buf][16 * c + r] + d;
+                        o[r] = inv == 0.0f ? 0.0f : o[r] * inv;
                     }
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (16 * c + r < live_rows)
+                            *to[r] = __float2bfloat16_rn(o[r]);
                 } else if (live) {
                     float *part = a.part + ((int64_t)(cta * 2 + whole) * N + 16 * c) * a.D + d;
 #pragma unroll
