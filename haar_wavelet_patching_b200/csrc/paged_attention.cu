@@ -31,7 +31,8 @@ static __device__ unsigned int g_paged_timeouts = 0;
 namespace {
 
 constexpr int kRound = 128;    // keys of a round
-constexpr int kMinRounds = 2;  // fewest rounds of a CTA
+// A unit's beginning and end take a CTA about as long as this many rounds; fewest places of a CTA.
+constexpr int kEnd = 2, kMinPlaces = 4;
 constexpr int kCtas = 148;
 constexpr int64_t kMaxNq = 64;
 constexpr int kThreads = 8 * 32;
@@ -137,46 +138,65 @@ template <int DP, int N> struct Smem {
     static constexpr int sub = kRound * 128;     // 64 channels of a round's keys
     static constexpr int tile = DP / 64 * sub;   // keys or values of a round
     static constexpr int q = DP / 64 * N * 128;  // a unit's queries
-    static constexpr int p = 2 * N * 128;        // a round's weights
+    static constexpr int p = kRound * 2 * N;     // a round's weights
+    static constexpr int units = N == 64 ? 2 : 4; // whose queries may be there
     static constexpr int ring = DP == 64 ? (N == 16 ? 6 : N == 32 ? 5 : 4) : N == 16 ? 3 : 2;
-    static constexpr int at_q = 2 * ring * tile, at_p = at_q + 2 * q;
+    static constexpr int at_q = 2 * ring * tile, at_p = at_q + units * q;
     static constexpr int bytes = at_p + 2 * p + 1024;
     static_assert(bytes <= 227 * 1024 - 4096, "4 KB are for the static part");
 };
 
-// The rounds' shares: the first `more` of `ctas` CTAs have one more than the others.
+// The places' shares: the first `more` of `ctas` CTAs have one more than the others.
 struct Shares {
     uint32_t each, more;
     __device__ __forceinline__ Shares(uint32_t total, uint32_t ctas) : each(total / ctas), more(total % ctas) {}
     __device__ __forceinline__ uint32_t begin(uint32_t cta) const { return cta * each + min(cta, more); }
-    __device__ __forceinline__ uint32_t owner(uint32_t round) const
+    __device__ __forceinline__ uint32_t owner(uint32_t pos) const
     {
         const uint32_t longer = more * (each + 1);
-        return round < longer ? round / (each + 1) : more + (round - longer) / each;
+        return pos < longer ? pos / (each + 1) : more + (pos - longer) / each;
     }
 };
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// Shared-memory descriptor of the weights, [key][N rows]: a key's N rows are a line of the 32-, 64- or 128-byte swizzle (16-byte
+// piece i of line k is kept at i ^ (k * 2 N / 128 % (N / 8))), 8 lines an atom.  Fields as in sw128_desc_mn.
+template <int N> __device__ __forceinline__ uint64_t weights_desc(uint32_t saddr)
+{
+    constexpr uint64_t layout = N == 16 ? 6 : N == 32 ? 4 : 2;
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(8 * 2 * N >> 4) << 32) |
+           ((uint64_t)1 << 46) | (layout << 61);
+}
 
 template <int DP, int N>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PagedArgs a)
 {
     using S = Smem<DP, N>;
-    constexpr int NB = S::ring, kChunks = N / 16; // stages of keys, of values
+    constexpr int NB = S::ring, QB = S::units, kChunks = N / 16; // stages of keys, of values
     constexpr uint32_t kColumns = N == 16 ? 64 : N == 32 ? 128 : 256;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[2][NB], empty[2][NB], qfull[2], qempty[2], sfull[2], pfull[2], pfree[2], ofull, drain;
+    __shared__ __align__(8) uint64_t full[2][NB], empty[2][NB], qfull[QB], qempty[QB], sfull[2], pfull[2], pfree[2], ofull, drain;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
     __shared__ uint32_t s_sum[kThreads / 32];
     __shared__ Place s_first;
-    // Of a unit (the next one's are made meanwhile): rows' maxima, keys seen, places of the output; keys seen by all rows;
+    __shared__ uint32_t s_round[2]; // rounds before this CTA's part, and before its end
+    // Of a unit (those of the next ones are made meanwhile): rows' maxima, keys seen, places of the output; keys seen by all rows;
     // which of the keys behind these have values that are no numbers.
-    __shared__ float s_m[2][N];
-    __shared__ int s_lim[2][N];
-    __shared__ __nv_bfloat16 *s_out[2][N];
-    __shared__ int s_rows[2]; // rows that are queries
-    __shared__ int s_all[2];
-    __shared__ unsigned long long s_odd[2];
+    __shared__ __align__(16) float s_m[QB][N];
+    __shared__ int s_lim[QB][N];
+    __shared__ __nv_bfloat16 *s_out[QB][N];
+    __shared__ int s_rows[QB]; // rows that are queries
+    __shared__ int s_all[QB];
+    __shared__ unsigned long long s_odd[QB];
     __shared__ float s_inv[N], s_scale[N], s_red[4][N];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -192,9 +212,11 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 mbar_init(smem_addr(&full[kv][i]), 1);
                 mbar_init(smem_addr(&empty[kv][i]), 1);
             }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < QB; ++i) {
             mbar_init(smem_addr(&qfull[i]), 1);
             mbar_init(smem_addr(&qempty[i]), 5);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sfull[i]), 1);
             mbar_init(smem_addr(&pfull[i]), 4);
             mbar_init(smem_addr(&pfree[i]), 1);
@@ -205,7 +227,7 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         fence_barrier_init();
     }
 
-    // ---- This CTA's part [pos0, pos0 + count) of the rounds. ----
+    // ---- This CTA's part [pos0, pos1) of the sequence; a unit has its rounds' places and kEnd more. ----
     auto block_sum = [&](uint32_t v, uint32_t &before) { // sum over the block; `before`: of the threads before
         uint32_t x = v;
 #pragma unroll
@@ -228,33 +250,42 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     };
     uint32_t total = 0, before = 0, mine = 0;
     int rounds = 0, len = 0;
+    auto places_of = [&](int b) {
+        rounds = b < a.B ? rounds_of(a, b, len) : 0;
+        mine = b < a.B ? (uint32_t)((rounds + kEnd) * a.units) : 0;
+    };
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         if (b0)
             __syncthreads();
-        rounds = b0 + tid < a.B ? rounds_of(a, b0 + tid, len) : 0;
-        mine = (uint32_t)(rounds * a.units);
+        places_of(b0 + tid);
         total += block_sum(mine, before);
     }
-    const uint32_t ctas = min((uint32_t)kCtas, max(1u, total / kMinRounds)), cta = blockIdx.x;
+    const uint32_t ctas = min((uint32_t)kCtas, max(1u, total / kMinPlaces)), cta = blockIdx.x;
     if (cta >= ctas)
         return;
     const Shares shares(total, ctas);
-    const uint32_t pos0 = shares.begin(cta);
-    const int count = (int)(shares.begin(cta + 1) - pos0);
+    const uint32_t pos0 = shares.begin(cta), pos1 = shares.begin(cta + 1);
     uint32_t run = 0;
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         uint32_t all = total;
         if (a.B > kThreads) { // (else the numbers are at hand)
             __syncthreads();
-            rounds = b0 + tid < a.B ? rounds_of(a, b0 + tid, len) : 0;
-            mine = (uint32_t)(rounds * a.units);
+            places_of(b0 + tid);
             all = block_sum(mine, before);
         }
-        const uint32_t in = pos0 - (run + before);
-        if (pos0 >= run + before && in < mine)
-            s_first = Place{b0 + tid, (int)(in / rounds), (int)(in % rounds), rounds, len};
+        const uint32_t at = run + before, b = (uint32_t)(b0 + tid);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) { // this stream has the part's first place; the one behind its last
+            const uint32_t pos = e ? pos1 : pos0;
+            if (mine > 0 && pos >= at && (pos - at < mine || (e && pos == total && pos - at == mine))) {
+                const uint32_t in = pos - at, unit = in / (rounds + kEnd), round = in - unit * (rounds + kEnd);
+                s_round[e] = at - kEnd * b * a.units + unit * rounds + min(round, (uint32_t)rounds);
+                if (!e)
+                    s_first = Place{(int)b, (int)unit, (int)round, rounds, len};
+            }
+        }
         run += all;
-        if (run > pos0)
+        if (run > pos1)
             break;
     }
     if (warp == 5) {
@@ -267,6 +298,8 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     const uint32_t tmem = tmem_base_s, o_col = tmem + 2 * N; // scores: two times N columns
     volatile int *abort = &abort_s;
     Place now = s_first;
+    const int count = (int)(s_round[1] - s_round[0]);
+    uint32_t unit_pos = pos0 - now.round; // the unit's first place
     auto advance = [&](Place &p) {
         if (++p.round < p.rounds)
             return;
@@ -277,6 +310,11 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         if (++p.b < a.B)
             p.rounds = rounds_of(a, p.b, p.len);
     };
+    if (now.round >= now.rounds && count > 0) { // behind a unit's rounds: the next one
+        unit_pos += now.rounds + kEnd;
+        now.round = now.rounds - 1;
+        advance(now);
+    }
     auto ends_unit = [&](const Place &p, int j) { return p.round + 1 == p.rounds || j + 1 == count; };
 
     if (warp == 4 || warp == 7) {
@@ -342,8 +380,8 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         constexpr int kPieces = DP / 8;
         uint32_t u = 0;
         for (int j = 0; j < count; ++u) {
-            const int buf = u & 1;
-            bool ok = wait_or_abort(smem_addr(&qempty[buf]), ((u >> 1) & 1u) ^ 1u, abort);
+            const int buf = u % QB;
+            bool ok = wait_or_abort(smem_addr(&qempty[buf]), ((u / QB) & 1u) ^ 1u, abort);
             ok = __all_sync(~0u, ok);
             if (!ok)
                 break;
@@ -370,7 +408,7 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 s_odd[buf] = 0;
                 s_rows[buf] = min(N, rows - first);
                 if (now.round == 0) {
-                    const uint32_t last = pos0 + j + now.rounds - 1;
+                    const uint32_t last = unit_pos + now.rounds - 1;
                     a.spans[(int64_t)now.b * a.units + now.unit] =
                         j + now.rounds <= count ? make_int2(-1, -1) : make_int2((int)cta, (int)shares.owner(last));
                 }
@@ -380,21 +418,22 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_addr(&qfull[buf]));
+            unit_pos += now.rounds + kEnd;
             j += now.rounds - now.round; // to the next unit
             now.round = now.rounds - 1;
             advance(now);
         }
     } else if (warp == 5) {
         if (lane == 0) {
-            const uint32_t idesc_s = idesc_bf16_f32(kRound, N), idesc_o = idesc_bf16_f32(DP, N) | kATransposed;
+            const uint32_t idesc_s = idesc_bf16_f32(kRound, N), idesc_o = idesc_bf16_f32(DP, N) | kATransposed | kBTransposed;
             const uint64_t kdesc = sw128_desc(base), qdesc = sw128_desc(base + S::at_q);
-            const uint64_t vdesc = sw128_desc_mn(base + NB * S::tile, S::sub), pdesc = sw128_desc(base + S::at_p);
+            const uint64_t vdesc = sw128_desc_mn(base + NB * S::tile, S::sub), pdesc = weights_desc<N>(base + S::at_p);
             bool ok = true;
             Place next = now; // of the round whose scores come next
             uint32_t u = 0;
             auto scores = [&](int j) { // s_j = k_j q^T
                 const int slot = j % NB;
-                ok = wait_or_abort(smem_addr(&qfull[u & 1]), (u >> 1) & 1u, abort) &&
+                ok = wait_or_abort(smem_addr(&qfull[u % QB]), (u / QB) & 1u, abort) &&
                      wait_or_abort(smem_addr(&full[0][slot]), (uint32_t)(j / NB) & 1u, abort);
                 if (!ok)
                     return;
@@ -402,17 +441,18 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
                     umma_bf16(tmem + (j & 1) * N, kdesc + ((slot * S::tile + (k / 4) * S::sub + (k % 4) * 32) >> 4),
-                              qdesc + (((u & 1) * S::q + (k / 4) * (N * 128) + (k % 4) * 32) >> 4), idesc_s, k != 0);
+                              qdesc + (((u % QB) * S::q + (k / 4) * (N * 128) + (k % 4) * 32) >> 4), idesc_s, k != 0);
                 umma_commit(smem_addr(&sfull[j & 1]));
                 umma_commit(smem_addr(&empty[0][slot]));
                 if (ends_unit(next, j)) {
-                    umma_commit(smem_addr(&qempty[u & 1]));
+                    umma_commit(smem_addr(&qempty[u % QB]));
                     ++u;
                 }
                 if (j + 1 < count)
                     advance(next);
             };
-            scores(0);
+            if (count > 0)
+                scores(0);
             bool fresh = true;
             for (int j = 0; j < count && ok; ++j) {
                 const Place p = next; // (of round j + 1; where that begins a unit, round j ended one)
@@ -428,7 +468,7 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
 #pragma unroll
                 for (int k = 0; k < kRound / 16; ++k)
                     umma_bf16(o_col, vdesc + ((slot * S::tile + k * 2048) >> 4),
-                              pdesc + (((j & 1) * S::p + (k / 4) * (N * 128) + (k % 4) * 32) >> 4), idesc_o,
+                              pdesc + (((j & 1) * S::p + k * (16 * 2 * N)) >> 4), idesc_o,
                               !fresh || k > 0);
                 umma_commit(smem_addr(&empty[1][slot]));
                 umma_commit(smem_addr(&pfree[j & 1]));
@@ -443,10 +483,10 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     } else {
         // ---- Softmax: thread = key. ----
         const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-        constexpr bool kHold = N == 16; // a row's scores and maxima stay in registers
-        float l[N], m[kHold ? N : 1];
-        const uint32_t pbase = base + S::at_p + (tid >> 6) * (N * 128) + (tid & 7) * 2;
-        const int chunk = (tid >> 3) & 7;
+        constexpr bool kHold = N == 16; // a key's scores and what they are relative to stay in registers
+        float l[N] = {}, m[kHold ? N : 1];
+        const uint32_t pbase = base + S::at_p + tid * (2 * N);
+        const int mix = tid * 2 * N / 128 % (N / 8);
         float *side = a.side + (int64_t)cta * 64 * N;
         bool ok = true, fresh = true, whole = false;
         int all = 0;    // keys that all rows see
@@ -458,13 +498,22 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 entry = a.table[p.b * a.table_row + a.page.div((uint32_t)key)];
         };
         look_up(now);
-        // (No thread leaves before the others know: a wait that has run out shows in the next round's vote.)
-        for (int j = 0; j < count; ++j) {
-            const bool first = fresh;
-            const int buf = u & 1;
+        // No thread leaves before the others know: a wait that has run out shows in the next round's vote.
+        // Round -1 is a unit's end without waits, arrivals and results: its code is fetched while the first keys are on
+        // their way (it takes 10,000 cycles where it comes from HBM, 2,700 else).
+        for (int j = -1; j < count; ++j) {
+            const bool dry = j < 0, first = fresh;
+            const int buf = u % QB;
+            auto wait = [&](uint64_t &bar, uint32_t parity) {
+                if (!dry)
+                    ok = wait_or_abort(smem_addr(&bar), parity & 1u, abort) && ok;
+                __syncwarp();
+            };
+            Place then = now;
+            if (!dry) {
             if (fresh) {
                 whole = now.round == 0;
-                ok = wait_or_abort(smem_addr(&qfull[buf]), (u >> 1) & 1u, abort) && ok;
+                wait(qfull[buf], u / QB);
                 all = s_all[buf];
 #pragma unroll
                 for (int r = 0; r < N; ++r)
@@ -473,82 +522,94 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
             const int key = now.round * kRound + tid;
             const bool none = key < now.len && (uint32_t)entry >= (uint32_t)a.P; // a key of no page: its score is no number
             const bool edge = (now.round + 1) * kRound > all; // some row does not see some key
-            Place then = now;
             if (j + 1 < count) {
                 advance(then);
                 look_up(then);
             }
-            ok = wait_or_abort(smem_addr(&sfull[j & 1]), (uint32_t)(j >> 1) & 1u, abort) && ok;
-            __syncwarp();
+            wait(sfull[j & 1], (uint32_t)(j >> 1));
             tc_fence_after();
             const uint32_t sc = tmem + (j & 1) * N + lanes;
             float s[16];
-            auto load = [&](int c) { // 16 rows' scores times log2 e, -inf where the key is not seen
+            // 16 rows' scores times log2 e less what they are relative to; -inf where the key is not seen.
+            auto load = [&](int c, bool absolute) {
                 tmem_ld16(sc + 16 * c, s);
                 tmem_wait_ld();
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    s[r] = none ? __int_as_float(0x7FC00000) : s[r] * a.scale2;
-                if (edge) {
+                for (int r = 0; r < 16; r += 4) {
+                    const float4 from = absolute ? make_float4(0, 0, 0, 0)
+                                        : kHold  ? make_float4(m[kHold ? r : 0], m[kHold ? r + 1 : 0],
+                                                               m[kHold ? r + 2 : 0], m[kHold ? r + 3 : 0])
+                                                 : *reinterpret_cast<const float4 *>(&s_m[buf][16 * c + r]);
+                    s[r] = fmaf(s[r], a.scale2, -from.x);
+                    s[r + 1] = fmaf(s[r + 1], a.scale2, -from.y);
+                    s[r + 2] = fmaf(s[r + 2], a.scale2, -from.z);
+                    s[r + 3] = fmaf(s[r + 3], a.scale2, -from.w);
+                }
+                if (__builtin_expect(edge || none, 0)) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
+                    for (int r = 0; r < 16; ++r) {
+                        s[r] = none ? __int_as_float(0x7FC00000) : s[r];
                         s[r] = key < s_lim[buf][16 * c + r] ? s[r] : -INFINITY;
+                    }
+                }
+            };
+            auto hold = [&]() {
+                if constexpr (kHold) {
+#pragma unroll
+                    for (int r = 0; r < N; r += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(&s_m[buf][r]);
+                        m[r] = x.x;
+                        m[r + 1] = x.y;
+                        m[r + 2] = x.z;
+                        m[r + 3] = x.w;
+                    }
                 }
             };
             if (first) { // weights are relative to the first key's score, unless another one is far above it
+                if (warp == 0) {
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    if (kHold || warp == 0)
-                        load(c);
-                    if (tid == 0) {
+                    for (int c = 0; c < kChunks; ++c) {
+                        load(c, true);
+                        if (lane == 0) {
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            s_m[buf][16 * c + r] = fmaxf(s[r], kLowest);
+                            for (int r = 0; r < 16; ++r)
+                                s_m[buf][16 * c + r] = fmaxf(s[r], kLowest);
+                        }
+                        __syncwarp();
                     }
                 }
                 softmax_sync();
-                if constexpr (kHold)
-#pragma unroll
-                    for (int r = 0; r < N; ++r)
-                        m[r] = s_m[buf][r];
+                hold();
             }
-            bool grow = !ok;
+            float top = -INFINITY;
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
-                if (!kHold || !first)
-                    load(c);
+                load(c, false);
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    grow |= s[r] > (kHold ? m[kHold ? r : 0] : s_m[buf][16 * c + r]) + kGrow;
+                    top = fmaxf(top, s[r]);
             }
-            grow = softmax_any(grow);
-            if (__builtin_expect(grow, 0)) {
+            if (__builtin_expect(softmax_any(top > kGrow || !ok), 0)) {
                 if (softmax_any(!ok))
                     break;
                 // The rows' maxima over the round's keys and what weights were relative to.
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
-                    if (!kHold)
-                        load(c);
-                    float x[16];
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        x[r] = s[r];
-                    const float top = reduce16<true>(x);
+                    load(c, true);
+                    const float most = reduce16<true>(s);
                     if (!(lane & 1))
-                        s_red[warp][16 * c + (lane >> 1)] = top;
+                        s_red[warp][16 * c + (lane >> 1)] = most;
                 }
                 softmax_sync();
                 if (tid < N) {
-                    const float top = fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid]));
-                    const float from = s_m[buf][tid], to = top > from + kGrow ? top : from;
+                    const float most = fmaxf(fmaxf(s_red[0][tid], s_red[1][tid]), fmaxf(s_red[2][tid], s_red[3][tid]));
+                    const float from = s_m[buf][tid], to = most > from + kGrow ? most : from;
                     s_m[buf][tid] = to;
                     s_scale[tid] = exp2_fast(from - to); // (of the first round: not used)
                 }
                 softmax_sync();
                 if (!first) { // what is there already is relative to the value before
-                    ok = wait_or_abort(smem_addr(&pfree[(j - 1) & 1]), (uint32_t)((j - 1) >> 1) & 1u, abort) && ok;
-                    __syncwarp();
+                    wait(pfree[(j - 1) & 1], (uint32_t)((j - 1) >> 1));
                     tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c) {
@@ -564,13 +625,12 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                     }
                     tmem_wait_st();
                 }
+                hold();
                 if constexpr (kHold)
-#pragma unroll
-                    for (int r = 0; r < N; ++r)
-                        m[r] = s_m[buf][r];
+                    load(0, false);
             }
             if (j >= 2)
-                ok = wait_or_abort(smem_addr(&pfree[j & 1]), (uint32_t)((j - 2) >> 1) & 1u, abort) && ok;
+                wait(pfree[j & 1], (uint32_t)((j - 2) >> 1));
             // A value that some rows see and others do not meets weights of 0: where it is no finite number,
             // its row is taken out, and what it adds to the rows that see it comes at the unit's end.  What lies
             // behind the stream's last token is nobody's.
@@ -608,23 +668,27 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
                 if constexpr (!kHold)
-                    load(c);
+                    load(c, false);
                 if (__builtin_expect(odd, 0)) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        side[(key - all) * N + 16 * c + r] = s[r];
+                        side[(key - all) * N + 16 * c + r] = s[r] + s_m[buf][16 * c + r];
                 }
                 __syncwarp();
-                const uint32_t to = pbase + (j & 1) * S::p + 16 * c * 128;
+                // (an operand of the second product: bf16, as the values are)
+                uint32_t w[8];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float e = exp2_fast(s[r] - (kHold ? m[kHold ? r : 0] : s_m[buf][16 * c + r]));
-                    l[16 * c + r] += e;
-                    // (an operand of the second product: bf16, as the values are)
-                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + r * 128 + ((chunk ^ (r & 7)) << 4)),
-                                 "h"(__bfloat16_as_ushort(__float2bfloat16_rn(e)))
-                                 : "memory");
+                for (int r = 0; r < 16; r += 2) {
+                    const float e0 = exp2_fast(s[r]), e1 = exp2_fast(s[r + 1]);
+                    l[16 * c + r] += e0;
+                    l[16 * c + r + 1] += e1;
+                    w[r / 2] = pack_bf16x2(e0, e1);
                 }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(pbase + (j & 1) * S::p + (((2 * c + i) ^ mix) << 4)),
+                                 "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                                 : "memory");
             }
             tc_fence_before();
             fence_proxy_async_smem();
@@ -633,6 +697,7 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 mbar_arrive(smem_addr(&pfull[j & 1]));
             __syncwarp(); // the arrival goes out before any lane begins to wait
             fresh = ends_unit(now, j);
+            }
             if (!fresh) {
                 now = then;
                 continue;
@@ -657,7 +722,9 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                                       ? 0.0f
                                       : (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
                 s_inv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum; // (a sum of NaN gives NaN, no key 0)
-                if (!alone)
+                if (dry)
+                    ;
+                else if (!alone)
                     a.stats[(cta * 2 + whole) * N + tid] = make_float2(sum == 0.0f ? -INFINITY : s_m[buf][tid], sum);
                 else if (a.lse && tid < s_rows[buf]) {
                     const int hk = now.unit / a.tiles, row = (now.unit - hk * a.tiles) * N + tid;
@@ -667,20 +734,21 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 }
             }
             softmax_sync();
-            ok = wait_or_abort(smem_addr(&ofull), u & 1u, abort) && ok;
-            __syncwarp();
+            wait(ofull, u);
             tc_fence_after();
             // (64 channels are 16 lanes of each warp)
             const int d = DP == 128 ? tid : 16 * warp + lane;
-            const bool live = d < a.D && (DP == 128 || lane < 16);
+            const bool live = d < a.D && (DP == 128 || lane < 16) && !dry;
             const unsigned long long odds = s_odd[buf];
-            const int live_rows = s_rows[buf];
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                float o[16];
-                tmem_ld16(o_col + lanes + 16 * c, o);
+            const int live_rows = dry ? 8 : s_rows[buf];
+            float *part = a.part + (int64_t)(cta * 2 + whole) * N * a.D + d;
+            // (a loop: code that runs once per unit costs more in its fetches than in its steps)
+#pragma unroll 1
+            for (int r0 = 0; r0 < live_rows; r0 += 8) {
+                float o[8];
+                tmem_ld8(o_col + lanes + r0, o);
                 tmem_wait_ld();
-                if (__builtin_expect(live && odds, 0)) {
+                if (live) {
                     for (unsigned long long left = odds; left; left &= left - 1) {
                         const int at = __ffsll((long long)left) - 1, k = all + at;
                         const uint32_t pg = a.page.div((uint32_t)k);
@@ -689,36 +757,27 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                                             ? __bfloat162float(a.v.row(e, k - pg * a.page.d, now.unit / a.tiles)[d])
                                             : 0.0f;
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            if (k < s_lim[buf][16 * c + r])
-                                o[r] += exp2_fast(side[at * N + 16 * c + r] - s_m[buf][16 * c + r]) * v;
-                    }
-                }
-                if (live && alone) {
-                    __nv_bfloat16 *to[16];
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float inv = s_inv[16 * c + r];
-                        to[r] = s_out[buf][16 * c + r] + d;
-                        o[r] = inv == 0.0f ? 0.0f : o[r] * inv;
+                        for (int r = 0; r < 8; ++r)
+                            if (k < s_lim[buf][r0 + r])
+                                o[r] += exp2_fast(side[at * N + r0 + r] - s_m[buf][r0 + r]) * v;
                     }
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (16 * c + r < live_rows)
-                            *to[r] = __float2bfloat16_rn(o[r]);
-                } else if (live) {
-                    float *part = a.part + ((int64_t)(cta * 2 + whole) * N + 16 * c) * a.D + d;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        part[r * a.D] = o[r]; // (of rows that are none, too: nobody reads them)
+                    for (int r = 0; r < 8; ++r) {
+                        if (alone && r0 + r < live_rows) {
+                            const float inv = s_inv[r0 + r];
+                            s_out[buf][r0 + r][d] = __float2bfloat16_rn(inv == 0.0f ? 0.0f : o[r] * inv);
+                        }
+                        if (!alone)
+                            part[(r0 + r) * a.D] = o[r]; // (of rows that are none, too: nobody reads them)
+                    }
                 }
                 __syncwarp();
             }
             tc_fence_before();
-            if (lane == 0)
+            if (lane == 0 && !dry)
                 mbar_arrive(smem_addr(&qempty[buf])); // (this warp is done with the unit's numbers)
             __syncwarp();
-            ++u;
+            u += !dry;
             now = then;
         }
     }
@@ -902,7 +961,7 @@ extern "C" tok_status tok_paged_attention(const tok_heads *q, const tok_pages *k
     if (!vq.strides_ok() || !vo.strides_ok() || !pk.strides_ok() || !pv.strides_ok() || !vo.distinct())
         return TOK_ERR_SHAPE;
     int64_t rounds;
-    if (!prod_ok({B, dim.units(), tokens / kRound + 1}, &rounds) || rounds > kIntMax)
+    if (!prod_ok({B, dim.units(), tokens / kRound + 1 + kEnd}, &rounds) || rounds > kIntMax)
         return TOK_ERR_SHAPE;
     const int64_t need = dim.workspace();
     if (workspace_bytes < need)

@@ -682,7 +682,7 @@ TOK_API tok_status tok_paged_write(const tok_heads *k, const tok_heads *v, const
  * tok_paged_attention_workspace_size() bytes, overwritten; calls that may overlap need one each.
  * Results do not depend on the device's timing (every sum has a fixed order).
  * Shape rule: D a multiple of 8, 8 <= D <= 128; Hq a multiple of Hkv; 0 <= Nq <= 64; B, Hq <= 65535; B * Hq * Nq <
- * 2^30; P * page_size, M * page_size < 2^31; B * Hkv * (1 + Nq * Hq / Hkv / 64) * (1 + M * page_size / 128) < 2^31; page and
+ * 2^30; P * page_size, M * page_size < 2^31; B * Hkv * (1 + Nq * Hq / Hkv / 64) * (3 + M * page_size / 128) < 2^31; page and
  * token strides of the pools positive (a head stride may be 0); the size is -1 for an invalid shape.
  */
 TOK_API int64_t tok_paged_attention_workspace_size(int64_t B, int64_t Nq, int64_t Hq, int64_t Hkv, int64_t D);
