@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kRound = 128;    // keys of a round
 // A unit's beginning and end take a CTA about as long as this many rounds; fewest places of a CTA.
-constexpr int kEnd = 2, kMinPlaces = 4;
+constexpr int kEnd = 1, kMinPlaces = 3;
 constexpr int kCtas = 148;
 constexpr int64_t kMaxNq = 64;
 constexpr int kThreads = 8 * 32;
@@ -115,6 +115,22 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&r)[16])
                  : "memory");
 }
 
+// Tensor copy of data that is read once: first to leave L2, so that code, tables and partial results stay there.
+__device__ __forceinline__ void tma_load_4d_once(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
+                                                 uint32_t bar, uint64_t policy)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
+                 "%4, %5}], [%6], %7;" ::"r"(dst),
+                 "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ uint64_t evict_first()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 constexpr uint32_t kATransposed = 1u << 15; // instruction descriptor: A is MN-major
 
 __device__ __forceinline__ int rounds_of(const PagedArgs &a, int b, int &len)
@@ -158,14 +174,6 @@ struct Shares {
     }
 };
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
-                 : "r"(taddr)
-                 : "memory");
-}
-
 // Shared-memory descriptor of the weights, [key][N rows]: a key's N rows are a line of the 32-, 64- or 128-byte swizzle (16-byte
 // piece i of line k is kept at i ^ (k * 2 N / 128 % (N / 8))), 8 lines an atom.  Fields as in sw128_desc_mn.
 template <int N> __device__ __forceinline__ uint64_t weights_desc(uint32_t saddr)
@@ -197,7 +205,7 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     __shared__ int s_rows[QB]; // rows that are queries
     __shared__ int s_all[QB];
     __shared__ unsigned long long s_odd[QB];
-    __shared__ float s_inv[N], s_scale[N], s_red[4][N];
+    __shared__ __align__(16) float s_inv[N], s_scale[N], s_red[4][N];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     asm volatile("griddepcontrol.launch_dependents;");
@@ -323,6 +331,7 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         constexpr int kSubs = DP / 64;
         const int kv = warp == 7;
         const CUtensorMap *map = kv ? &vmap : &kmap;
+        const uint64_t policy = evict_first();
         const int factor = kv ? a.vh : a.kh, boxes = kRound / a.box_rows;
         auto look_up = [&](const Place &p, int box, int &row) { // page and row; the pool's end (zeros) where there is none
             const int key = p.round * kRound + box * a.box_rows;
@@ -360,7 +369,7 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 const int p = (uint32_t)page0 < (uint32_t)a.P ? page0 : a.P;
 #pragma unroll
                 for (int sub = 0; sub < kSubs; ++sub)
-                    tma_load_4d(dst + sub * S::sub + box * a.box_rows * 128, map, 64 * sub, row0, head, p, bar);
+                    tma_load_4d_once(dst + sub * S::sub + box * a.box_rows * 128, map, 64 * sub, row0, head, p, bar, policy);
             }
             __syncwarp();
             if (j + 1 < count)
@@ -466,10 +475,9 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                     break;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < kRound / 16; ++k)
+                for (int k = 0; k < kRound / 16; ++k) // (leaving out steps of 16 keys behind the last one cost 10% of a long call)
                     umma_bf16(o_col, vdesc + ((slot * S::tile + k * 2048) >> 4),
-                              pdesc + (((j & 1) * S::p + k * (16 * 2 * N)) >> 4), idesc_o,
-                              !fresh || k > 0);
+                              pdesc + (((j & 1) * S::p + k * (16 * 2 * N)) >> 4), idesc_o, !fresh || k > 0);
                 umma_commit(smem_addr(&empty[1][slot]));
                 umma_commit(smem_addr(&pfree[j & 1]));
                 fresh = last;
@@ -499,18 +507,14 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         };
         look_up(now);
         // No thread leaves before the others know: a wait that has run out shows in the next round's vote.
-        // Round -1 is a unit's end without waits, arrivals and results: its code is fetched while the first keys are on
-        // their way (it takes 10,000 cycles where it comes from HBM, 2,700 else).
-        for (int j = -1; j < count; ++j) {
-            const bool dry = j < 0, first = fresh;
+        for (int j = 0; j < count; ++j) {
+            const bool first = fresh;
             const int buf = u % QB;
             auto wait = [&](uint64_t &bar, uint32_t parity) {
-                if (!dry)
-                    ok = wait_or_abort(smem_addr(&bar), parity & 1u, abort) && ok;
+                ok = wait_or_abort(smem_addr(&bar), parity & 1u, abort) && ok;
                 __syncwarp();
             };
             Place then = now;
-            if (!dry) {
             if (fresh) {
                 whole = now.round == 0;
                 wait(qfull[buf], u / QB);
@@ -631,37 +635,43 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
             }
             if (j >= 2)
                 wait(pfree[j & 1], (uint32_t)((j - 2) >> 1));
-            // A value that some rows see and others do not meets weights of 0: where it is no finite number,
-            // its row is taken out, and what it adds to the rows that see it comes at the unit's end.  What lies
-            // behind the stream's last token is nobody's.
+            // Values behind the stream's last token are nobody's and meet weights of 0: zeros in their place.  A value that some rows see and others do not also meets such weights: where it is
+            // no finite number, its row is taken out, and what it adds to the rows that see it comes at the unit's end.
             bool odd = false;
-            if (__builtin_expect(edge && key >= all, 0)) {
-                const int slot = j % NB;
-                if (!wait_or_abort(smem_addr(&full[1][slot]), (uint32_t)(j / NB) & 1u, abort))
-                    ok = false;
-                else {
-                    // (pieces in an order of the row's own, so that 8 rows meet 8 different banks)
-                    unsigned char *row =
-                        smem_raw + (base - smem_addr(smem_raw)) + (NB + slot) * S::tile + tid * 128;
-                    odd = key >= now.len;
-                    if (!odd) {
-#pragma unroll 2
-                        for (int i = 0; i < DP / 8; ++i) {
-                            const uint4 x = *reinterpret_cast<const uint4 *>(row + (i >> 3) * S::sub + ((i ^ tid) & 7) * 16);
-                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            if (edge) {
+                constexpr int kPieces = DP / 8; // of a row; piece i of row k is kept at i ^ k within its 8
+                const int slot = j % NB, begin = now.round * kRound, keys = min(now.len - begin, kRound);
+                unsigned char *tile = smem_raw + (base - smem_addr(smem_raw)) + (NB + slot) * S::tile;
+                auto piece = [&](int row, int i) {
+                    return reinterpret_cast<uint4 *>(tile + (i >> 3) * S::sub + row * 128 + ((i ^ row) & 7) * 16);
+                };
+                wait(full[1][slot], (uint32_t)(j / NB));
+#pragma unroll 4
+                for (int i = keys * kPieces + tid; i < kRound * kPieces; i += 128)
+                    *piece(i / kPieces, i % kPieces) = make_uint4(0, 0, 0, 0);
+                const int some0 = max(all - begin, 0), some = (keys - some0) * kPieces;
+                if (some > 0) {
+                    bool bad = false;
+                    for (int i = tid; i < some; i += 128) {
+                        const uint4 x = *piece(some0 + i / kPieces, i % kPieces);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            bad |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
+                    }
+                    if (__builtin_expect(softmax_any(bad), 0) && tid >= some0 && tid < keys) {
+                        for (int i = 0; i < kPieces; ++i) {
+                            const uint4 x = *piece(tid, i);
+                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                             for (int k = 0; k < 4; ++k)
                                 odd |= (w[k] & 0x7F80u) == 0x7F80u || (w[k] & 0x7F800000u) == 0x7F800000u;
                         }
-                        if (odd)
+                        if (odd) {
+                            for (int i = 0; i < kPieces; ++i)
+                                *piece(tid, i) = make_uint4(0, 0, 0, 0);
                             atomicOr(&s_odd[buf], 1ull << (key - all));
+                        }
                     }
-                    if (odd) {
-#pragma unroll 2
-                        for (int i = 0; i < DP / 8; ++i)
-                            *reinterpret_cast<uint4 *>(row + (i >> 3) * S::sub + ((i ^ tid) & 7) * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    odd = odd && key < now.len;
                 }
             }
             __syncwarp();
@@ -697,7 +707,6 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 mbar_arrive(smem_addr(&pfull[j & 1]));
             __syncwarp(); // the arrival goes out before any lane begins to wait
             fresh = ends_unit(now, j);
-            }
             if (!fresh) {
                 now = then;
                 continue;
@@ -721,10 +730,8 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 const float sum = s_lim[buf][tid] == 0
                                       ? 0.0f
                                       : (s_red[0][tid] + s_red[1][tid]) + (s_red[2][tid] + s_red[3][tid]);
-                s_inv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum; // (a sum of NaN gives NaN, no key 0)
-                if (dry)
-                    ;
-                else if (!alone)
+                s_inv[tid] = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum); // (a sum of NaN gives NaN, no key 0)
+                if (!alone)
                     a.stats[(cta * 2 + whole) * N + tid] = make_float2(sum == 0.0f ? -INFINITY : s_m[buf][tid], sum);
                 else if (a.lse && tid < s_rows[buf]) {
                     const int hk = now.unit / a.tiles, row = (now.unit - hk * a.tiles) * N + tid;
@@ -738,17 +745,16 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
             tc_fence_after();
             // (64 channels are 16 lanes of each warp)
             const int d = DP == 128 ? tid : 16 * warp + lane;
-            const bool live = d < a.D && (DP == 128 || lane < 16) && !dry;
+            const bool live = d < a.D && (DP == 128 || lane < 16);
             const unsigned long long odds = s_odd[buf];
-            const int live_rows = dry ? 8 : s_rows[buf];
+            const int live_rows = s_rows[buf];
             float *part = a.part + (int64_t)(cta * 2 + whole) * N * a.D + d;
-            // (a loop: code that runs once per unit costs more in its fetches than in its steps)
 #pragma unroll 1
-            for (int r0 = 0; r0 < live_rows; r0 += 8) {
-                float o[8];
-                tmem_ld8(o_col + lanes + r0, o);
+            for (int c = 0; 16 * c < live_rows; ++c) {
+                float o[16];
+                tmem_ld16(o_col + lanes + 16 * c, o);
                 tmem_wait_ld();
-                if (live) {
+                if (__builtin_expect(odds && live, 0)) {
                     for (unsigned long long left = odds; left; left &= left - 1) {
                         const int at = __ffsll((long long)left) - 1, k = all + at;
                         const uint32_t pg = a.page.div((uint32_t)k);
@@ -757,27 +763,36 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                                             ? __bfloat162float(a.v.row(e, k - pg * a.page.d, now.unit / a.tiles)[d])
                                             : 0.0f;
 #pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            if (k < s_lim[buf][r0 + r])
-                                o[r] += exp2_fast(side[at * N + r0 + r] - s_m[buf][r0 + r]) * v;
+                        for (int r = 0; r < 16; ++r)
+                            if (k < s_lim[buf][16 * c + r])
+                                o[r] += exp2_fast(side[at * N + 16 * c + r] - s_m[buf][16 * c + r]) * v;
                     }
+                }
+                if (alone && live) {
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        if (alone && r0 + r < live_rows) {
-                            const float inv = s_inv[r0 + r];
-                            s_out[buf][r0 + r][d] = __float2bfloat16_rn(inv == 0.0f ? 0.0f : o[r] * inv);
+                    for (int g = 0; g < 16; g += 4) {
+                        if (16 * c + g >= live_rows)
+                            break;
+                        const float4 inv = *reinterpret_cast<const float4 *>(&s_inv[16 * c + g]);
+                        const float f[4] = {inv.x, inv.y, inv.z, inv.w};
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            if (16 * c + g + r < live_rows)
+                                s_out[buf][16 * c + g + r][d] = __float2bfloat16_rn(f[r] == 0.0f ? 0.0f : o[g + r] * f[r]);
                         }
-                        if (!alone)
-                            part[(r0 + r) * a.D] = o[r]; // (of rows that are none, too: nobody reads them)
                     }
+                } else if (live) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        part[(16 * c + r) * a.D] = o[r]; // (of rows that are none, too: nobody reads them)
                 }
                 __syncwarp();
             }
             tc_fence_before();
-            if (lane == 0 && !dry)
+            if (lane == 0)
                 mbar_arrive(smem_addr(&qempty[buf])); // (this warp is done with the unit's numbers)
             __syncwarp();
-            u += !dry;
+            ++u;
             now = then;
         }
     }
