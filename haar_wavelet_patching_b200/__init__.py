@@ -858,47 +858,91 @@ def tok_cross_attention_backward(q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v
 
 
 # ---------------------------------------------------------------------------
-# Embedding of codes.
+# A step over the codes, token by token.  These calls are short, so their checks are one expression each where all is
+# well; what is wrong is found out afterwards.
 # ---------------------------------------------------------------------------
-def _check_on(dev, dtype, shape, **tensors):
-    """Contiguous tensors of one dtype and shape on `dev`; None is left out."""
-    for name, t in tensors.items():
-        if t is not None and (t.device != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {dev}")
+_i32, _f32, _bf16 = torch.int32, torch.float32, torch.bfloat16
+_raw_stream, _device_now = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _counter(t, dev, name="bad_count"):
-    if t is not None and (t.device != dev or t.dtype != torch.int32 or t.numel() < 1):
-        raise ValueError(f"{name} must be an int32 CUDA tensor")
-    return None if t is None else t.data_ptr()
+def _enqueue(name, dev, stream, *args):
+    """_call for a device index."""
+    s = _raw_stream(dev) if stream is None else stream.cuda_stream
+    f = getattr(_lib or lib(), name)
+    if _device_now() == dev:
+        status = f(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, s)
+    if status != TOK_OK:
+        raise TokError(status, name)
+
+
+def _device_of(t, name):
+    """The index of a CUDA tensor's device."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    return t.get_device()
+
+
+def _is(t, dtype, dev, shape):
+    return t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()
+
+
+def _need(t, name, dtype, dev, shape):
+    """A contiguous tensor of this dtype and shape on this device, or None."""
+    if t is not None and not _is(t, dtype, dev, shape):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on cuda:{dev}")
+
+
+def _counter(t, dev):
+    if t is None:
+        return None
+    if t.get_device() != dev or t.dtype is not _i32 or t.numel() < 1:
+        raise ValueError("bad_count must be an int32 CUDA tensor on the device of the inputs")
+    return t.data_ptr()
 
 
 def _row_stride(t, name):
     """The stride of the rows of [..., D], dense in D, its leading dimensions taken as one index."""
+    if t.is_contiguous():
+        return t.shape[-1]
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"the last dimension of {name} must be dense")
-    return t.shape[-1] if t.is_contiguous() else _token_stride(t.unsqueeze(-2), name)
+    return _token_stride(t.unsqueeze(-2), name)
 
 
-def _codes(codes, rows, name):
-    if codes.device.type != "cuda":
-        raise ValueError("codes must be a CUDA tensor (there is no CPU path)")
-    if codes.dtype != torch.int32 or not codes.is_contiguous():
+def _workspace_of(need, workspace, like, stream, what):
+    if need < 0:
+        raise ValueError(what)
+    if workspace is None:
+        return _new(like, need, torch.uint8, stream) if need else None
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the device of the inputs")
+    return workspace
+
+
+# ---------------------------------------------------------------------------
+# Embedding of codes.
+# ---------------------------------------------------------------------------
+def _codes_check(codes, dev, rows, name):
+    if codes.dtype is not _i32 or not codes.is_contiguous():
         raise ValueError("codes must be a contiguous int32 CUDA tensor")
-    if rows.device != codes.device or rows.shape[:-1] != codes.shape or rows.dim() < 1:
+    if rows.get_device() != dev or rows.dim() < 1 or rows.shape[:-1] != codes.shape:
         raise ValueError(f"{name} must be [..., D] on the device of codes [...]")
 
 
 def tok_embed_codes(codes, table, y, scale=1.0, bad_count=None, stream=None):
     """y[..., :] = scale * table[codes]: codes [...] int32, table [V, D], y [..., D] (float32 or bfloat16, rows
     strided).  A code outside the table gives a row of NaN and adds 1 to bad_count (int32 CUDA tensor)."""
-    _codes(codes, y, "y")
-    if table.dim() != 2 or table.device != codes.device or table.dtype != y.dtype or table.shape[1] != y.shape[-1]:
+    dev = _device_of(codes, "codes")
+    _codes_check(codes, dev, y, "y")
+    if table.dim() != 2 or table.get_device() != dev or table.dtype is not y.dtype or table.shape[1] != y.shape[-1]:
         raise ValueError("table must be [V, D] with the dtype, device and D of y")
     V, D = table.shape
-    _call("tok_embed_codes", codes.device, stream, codes.data_ptr(), table.data_ptr(), y.data_ptr(),
-          _counter(bad_count, codes.device), _dtype_code(y), codes.numel(), V, D, _row_stride(table, "table"),
-          _row_stride(y, "y"), scale)
+    _enqueue("tok_embed_codes", dev, stream, codes.data_ptr(), table.data_ptr(), y.data_ptr(),
+             _counter(bad_count, dev), _dtype_code(y), codes.numel(), V, D, _row_stride(table, "table"),
+             _row_stride(y, "y"), scale)
     return y
 
 
@@ -909,45 +953,40 @@ def embed_codes_backward_workspace_size(N, V, D) -> int:
 def tok_embed_codes_backward(grad_y, codes, grad_table, scale=1.0, workspace=None, stream=None):
     """Gradient of tok_embed_codes into grad_table [V, D] (overwritten): grad_y [..., D], codes [...]; the two
     gradients' dtypes are their own.  workspace: embed_codes_backward_workspace_size bytes, allocated if None."""
-    _codes(codes, grad_y, "grad_y")
-    dev = codes.device
-    if grad_table.dim() != 2 or grad_table.device != dev or grad_table.shape[1] != grad_y.shape[-1]:
+    dev = _device_of(codes, "codes")
+    _codes_check(codes, dev, grad_y, "grad_y")
+    if grad_table.dim() != 2 or grad_table.get_device() != dev or grad_table.shape[1] != grad_y.shape[-1]:
         raise ValueError("grad_table must be [V, D] with the device and D of grad_y")
     N, (V, D) = codes.numel(), grad_table.shape
     ws = _workspace_of(embed_codes_backward_workspace_size(N, V, D), workspace, codes, stream,
                        f"no embedding for (N, V, D) = {(N, V, D)}: V at most 2^18, D at most 65536")
-    _call("tok_embed_codes_backward", dev, stream, codes.data_ptr(), grad_y.data_ptr(), grad_table.data_ptr(),
-          _dtype_code(grad_y), _dtype_code(grad_table), N, V, D, _row_stride(grad_y, "grad_y"),
-          _row_stride(grad_table, "grad_table"), scale, *_bytes(ws))
+    _enqueue("tok_embed_codes_backward", dev, stream, codes.data_ptr(), grad_y.data_ptr(), grad_table.data_ptr(),
+             _dtype_code(grad_y), _dtype_code(grad_table), N, V, D, _row_stride(grad_y, "grad_y"),
+             _row_stride(grad_table, "grad_table"), scale, *_bytes(ws))
     return grad_table
-
-
-def _workspace_of(need, workspace, like, stream, what):
-    if need < 0:
-        raise ValueError(what)
-    if workspace is None:
-        return _new(like, need, torch.uint8, stream) if need else None
-    if workspace.device != like.device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor on the device of the inputs")
-    return workspace
 
 
 # ---------------------------------------------------------------------------
 # Pages of a cache of keys and values.
 # ---------------------------------------------------------------------------
-def _tables_check(lens, held, free, pages, table, held_out, free_out):
-    dev = lens.device
-    if dev.type != "cuda":
-        raise ValueError("lens must be a CUDA tensor (there is no CPU path)")
-    if lens.dim() != 1 or table.dim() != 2 or pages.dim() != 1:
-        raise ValueError("lens must be [B], table [B, M], pages [F]")
-    _check_on(dev, torch.int32, lens.shape, lens=lens, held=held, held_out=held_out)
-    _check_on(dev, torch.int32, torch.Size((1,)), free=free, free_out=free_out)
-    _check_on(dev, torch.int32, pages.shape, pages=pages)
-    if table.device != dev or table.dtype != torch.int32 or table.shape[0] != lens.shape[0] \
+_ONE = torch.Size((1,))
+
+
+def _table_check(table, dev, B):
+    """The table's row stride."""
+    if table.dtype is not _i32 or table.get_device() != dev or table.dim() != 2 or table.shape[0] != B \
             or (table.shape[1] > 1 and table.stride(1) != 1):
         raise ValueError("table must be an int32 CUDA tensor [B, M] with dense rows")
-    return lens.shape[0], table.shape[1], pages.shape[0]
+    return table.stride(0) if B > 1 else table.shape[1]
+
+
+def _counts_check(dev, lens, held, free, pages, held_out, free_out):
+    shape = lens.shape
+    if not (len(shape) == 1 and pages.dim() == 1 and _is(lens, _i32, dev, shape) and _is(held, _i32, dev, shape)
+            and _is(held_out, _i32, dev, shape) and _is(free, _i32, dev, _ONE) and _is(free_out, _i32, dev, _ONE)
+            and _is(pages, _i32, dev, pages.shape)):
+        raise ValueError("lens, held and held_out must be [B], free and free_out [1], pages [F], all contiguous int32 "
+                         "tensors on one CUDA device")
 
 
 def tok_page_tables(lens, fresh, held, free, pages, table, slots, held_out, free_out, page_size, bad_count=None,
@@ -956,63 +995,64 @@ def tok_page_tables(lens, fresh, held, free, pages, table, slots, held_out, free
     come off the end of pages[:free] in the order of streams and go into table [B, M]; slots [B, N] gets
     page * page_size + row of each new token (-1 behind them), held_out and free_out the new counts (they may be
     held and free).  A stream without room gets slots of -1 and adds 1 to bad_count.  All int32."""
-    B, M, F = _tables_check(lens, held, free, pages, table, held_out, free_out)
-    if slots.dim() != 2 or slots.shape[0] != B:
-        raise ValueError("slots must be [B, N]")
-    _check_on(lens.device, torch.int32, slots.shape, slots=slots)
-    _check_on(lens.device, torch.int32, lens.shape, fresh=fresh)
-    _call("tok_page_tables", lens.device, stream, lens.data_ptr(), None if fresh is None else fresh.data_ptr(),
-          held.data_ptr(), free.data_ptr(), pages.data_ptr(), table.data_ptr(), slots.data_ptr(), held_out.data_ptr(),
-          free_out.data_ptr(), _counter(bad_count, lens.device), B, slots.shape[1], M, F, page_size,
-          table.stride(0) if B > 1 else M)
+    dev = _device_of(lens, "lens")
+    _counts_check(dev, lens, held, free, pages, held_out, free_out)
+    B = lens.shape[0]
+    row = _table_check(table, dev, B)
+    if slots.dim() != 2 or slots.shape[0] != B or not _is(slots, _i32, dev, slots.shape):
+        raise ValueError("slots must be a contiguous int32 CUDA tensor [B, N]")
+    _need(fresh, "fresh", _i32, dev, lens.shape)
+    _enqueue("tok_page_tables", dev, stream, lens.data_ptr(), None if fresh is None else fresh.data_ptr(),
+             held.data_ptr(), free.data_ptr(), pages.data_ptr(), table.data_ptr(), slots.data_ptr(),
+             held_out.data_ptr(), free_out.data_ptr(), _counter(bad_count, dev), B, slots.shape[1], table.shape[1],
+             pages.shape[0], page_size, row)
     return slots
 
 
 def tok_page_release(lens, held, free, pages, table, held_out, free_out, page_size, bad_count=None, stream=None):
     """Give back the pages that lens[b] tokens do not need: onto pages[free:], their table entries become -1; held_out and
     free_out get the new counts (they may be held and free)."""
-    B, M, F = _tables_check(lens, held, free, pages, table, held_out, free_out)
-    _call("tok_page_release", lens.device, stream, lens.data_ptr(), held.data_ptr(), free.data_ptr(), pages.data_ptr(),
-          table.data_ptr(), held_out.data_ptr(), free_out.data_ptr(), _counter(bad_count, lens.device), B, M, F,
-          page_size, table.stride(0) if B > 1 else M)
+    dev = _device_of(lens, "lens")
+    _counts_check(dev, lens, held, free, pages, held_out, free_out)
+    B = lens.shape[0]
+    row = _table_check(table, dev, B)
+    _enqueue("tok_page_release", dev, stream, lens.data_ptr(), held.data_ptr(), free.data_ptr(), pages.data_ptr(),
+             table.data_ptr(), held_out.data_ptr(), free_out.data_ptr(), _counter(bad_count, dev), B, table.shape[1],
+             pages.shape[0], page_size, row)
 
 
-def _pool(t: torch.Tensor) -> _Pages:
-    p, n, h, _ = t.stride()
-    return _Pages(t.data_ptr(), p, n, h)
+def _view4(t, name, dev):
+    """Strides of a bfloat16 tensor of four dimensions with dense channels."""
+    if t.dtype is not _bf16 or t.get_device() != dev or t.dim() != 4:
+        raise ValueError(f"{name} must be a bfloat16 tensor of four dimensions on cuda:{dev}")
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError(f"the channels of {name} must be dense")
+    return s
 
 
-def _pools_check(k_pages, v_pages, heads, channels, dev):
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
-        raise ValueError("k_pages and v_pages must be [P, page_size, H, D], alike")
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if t.dtype != torch.bfloat16 or t.device != dev:
-            raise ValueError(f"{name} must be a bfloat16 CUDA tensor on the device of the tokens")
-        if t.stride(3) != 1:
-            raise ValueError(f"the channels of {name} must be dense")
-    if k_pages.shape[3] != channels or (heads is not None and k_pages.shape[2] != heads):
-        raise ValueError(f"the pages have (H, D) = {tuple(k_pages.shape[2:])}, the tokens {(heads, channels)}")
+def _heads_of(t, name, dev):
+    s = _view4(t, name, dev)
+    return _Heads(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _pool_of(t, name, dev):
+    s = _view4(t, name, dev)
+    return _Pages(t.data_ptr(), s[0], s[1], s[2])
 
 
 def paged_write(k, v, k_pages, v_pages, slots, bad_count=None, stream=None):
     """Keys and values k, v [B, N, H, D] (dense channels, other strides free) into the pages [P, page_size, H, D] at
     slots [B, N] int32 (page * page_size + row; below 0: left out), all bfloat16.  A slot behind the pool is left
     out and adds 1 to bad_count.  Slots must differ."""
-    dev = k.device
-    if dev.type != "cuda":
-        raise ValueError("k must be a CUDA tensor (there is no CPU path)")
-    if k.dim() != 4 or k.shape != v.shape:
-        raise ValueError("k and v must be [B, N, H, D], alike")
-    for t, name in ((k, "k"), (v, "v")):
-        if t.dtype != torch.bfloat16 or t.device != dev:
-            raise ValueError(f"{name} must be a bfloat16 CUDA tensor on the device of k")
-        if t.stride(3) != 1:
-            raise ValueError(f"the channels of {name} must be dense")
-    B, N, H, D = k.shape
-    _pools_check(k_pages, v_pages, H, D, dev)
-    _check_on(dev, torch.int32, torch.Size((B, N)), slots=slots)
-    _call("tok_paged_write", dev, stream, _heads(k), _heads(v), slots.data_ptr(), _pool(k_pages), _pool(v_pages),
-          _counter(bad_count, dev), B, N, H, D, k_pages.shape[0], k_pages.shape[1])
+    dev = _device_of(k, "k")
+    shape, pool = k.shape, k_pages.shape
+    args = (_heads_of(k, "k", dev), _heads_of(v, "v", dev), slots.data_ptr(), _pool_of(k_pages, "k_pages", dev),
+            _pool_of(v_pages, "v_pages", dev))
+    if v.shape != shape or v_pages.shape != pool or pool[2:] != shape[2:]:
+        raise ValueError("k and v must be [B, N, H, D], alike, k_pages and v_pages [P, page_size, H, D], alike")
+    _need(slots, "slots", _i32, dev, shape[:2])
+    _enqueue("tok_paged_write", dev, stream, *args, _counter(bad_count, dev), *shape, pool[0], pool[1])
 
 
 tok_paged_write = paged_write
@@ -1029,34 +1069,25 @@ def tok_paged_attention(q, k_pages, v_pages, table, k_lens, o, lse=None, q_lens=
     k_lens[b] - q_lens[b] + i of its stream and sees the tokens up to itself; the others get o = 0, lse = -inf.
     lse [B, Hq, Nq] fp32 or None; scale: 1/sqrt(D) by default; workspace: paged_attention_workspace_size bytes,
     allocated if None."""
-    dev = q.device
-    if dev.type != "cuda":
-        raise ValueError("q must be a CUDA tensor (there is no CPU path)")
-    if q.dim() != 4 or o.shape != q.shape:
-        raise ValueError("q and o must be [B, Nq, Hq, D], alike")
-    for t, name in ((q, "q"), (o, "o")):
-        if t.dtype != torch.bfloat16 or t.device != dev:
-            raise ValueError(f"{name} must be a bfloat16 CUDA tensor on the device of q")
-        if t.stride(3) != 1:
-            raise ValueError(f"the channels of {name} must be dense")
+    dev = _device_of(q, "q")
+    args = (_heads_of(q, "q", dev), _pool_of(k_pages, "k_pages", dev), _pool_of(v_pages, "v_pages", dev))
+    out = _heads_of(o, "o", dev)
     B, Nq, Hq, D = q.shape
-    _pools_check(k_pages, v_pages, None, D, dev)
-    P, page_size, Hkv, _ = k_pages.shape
-    if table.device != dev or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B \
-            or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError("table must be an int32 CUDA tensor [B, M] with dense rows")
+    P, page_size, Hkv, _ = pool = k_pages.shape
+    if o.shape != q.shape or v_pages.shape != pool or pool[3] != D:
+        raise ValueError("q and o must be [B, Nq, Hq, D], alike, k_pages and v_pages [P, page_size, Hkv, D], alike")
+    row = _table_check(table, dev, B)
     if k_lens is None:
         raise ValueError("k_lens must be a contiguous int32 CUDA tensor [B]")
-    _check_on(dev, torch.int32, torch.Size((B,)), k_lens=k_lens, q_lens=q_lens)
-    _stats(lse, "lse", (B, Nq, 0, Hq, Hkv, D), dev)
-    ws = _workspace_of(paged_attention_workspace_size(B, Nq, Hq, Hkv, D), workspace, q, stream,
+    _need(k_lens, "k_lens", _i32, dev, q.shape[:1])
+    _need(q_lens, "q_lens", _i32, dev, q.shape[:1])
+    _need(lse, "lse", _f32, dev, (B, Hq, Nq))
+    ws = _workspace_of((_lib or lib()).tok_paged_attention_workspace_size(B, Nq, Hq, Hkv, D), workspace, q, stream,
                        f"no paged attention for (B, Nq, Hq, Hkv, D) = {(B, Nq, Hq, Hkv, D)}: D a multiple of 8, at "
                        "most 128; Hq a multiple of Hkv; Nq at most 64")
-    M = table.shape[1]
-    _call("tok_paged_attention", dev, stream, _heads(q), _pool(k_pages), _pool(v_pages), table.data_ptr(),
-          k_lens.data_ptr(), None if q_lens is None else q_lens.data_ptr(), _heads(o),
-          None if lse is None else lse.data_ptr(), B, Nq, Hq, Hkv, D, P, page_size, M, table.stride(0) if B > 1 else M,
-          D ** -0.5 if scale is None else scale, *_bytes(ws))
+    _enqueue("tok_paged_attention", dev, stream, *args, table.data_ptr(), k_lens.data_ptr(),
+             None if q_lens is None else q_lens.data_ptr(), out, None if lse is None else lse.data_ptr(), B, Nq, Hq, Hkv, D,
+             P, page_size, table.shape[1], row, D ** -0.5 if scale is None else scale, *_bytes(ws))
     return o
 
 
@@ -1069,26 +1100,28 @@ def tok_verify_codes(logits, codes, u, out, accepted, draft_logits=None, n_draft
     None (K), temperature a number or fp32 [B] -> out [B, K + 1] int32 (the codes that stand, the drawn one, then -1),
     accepted [B] int32.  Draft i stands if u q(x) < p(x); the code behind is drawn with u[:, K] from max(p - q, 0), or
     from p behind all drafts."""
-    dev = logits.device
-    if dev.type != "cuda":
-        raise ValueError("logits must be a CUDA tensor (there is no CPU path)")
+    dev = _device_of(logits, "logits")
     if logits.dim() != 3 or logits.shape[1] < 1 or logits.shape[2] < 1:
         raise ValueError("logits must be [B, K + 1, V] with V >= 1")
-    B, K, V = logits.shape[0], logits.shape[1] - 1, logits.shape[2]
-    for t, name, rows in ((logits, "logits", K + 1), (draft_logits, "draft_logits", K)):
-        if t is not None and (t.device != dev or t.dtype != logits.dtype or t.shape != (B, rows, V)
-                              or (V > 1 and t.stride(2) != 1)):
-            raise ValueError(f"{name} must be [B, {rows}, V] with the dtype and device of logits, dense in V")
-    _check_on(dev, torch.int32, torch.Size((B, K)), codes=codes)
-    _check_on(dev, torch.float32, torch.Size((B, K + 1)), u=u)
-    _check_on(dev, torch.int32, torch.Size((B, K + 1)), out=out)
-    _check_on(dev, torch.int32, torch.Size((B,)), n_draft=n_draft, accepted=accepted)
-    tp, ta = _setting(temperature, "temperature", torch.float32, B, dev)
+    B, rows, V = logits.shape
+    K, one, strides = rows - 1, (B,), logits.stride()
     drafted = draft_logits is not None and K > 0
-    _call("tok_verify_codes", dev, stream, logits.data_ptr(), draft_logits.data_ptr() if drafted else None,
-          _dtype_code(logits), codes.data_ptr(), u.data_ptr(), None if n_draft is None else n_draft.data_ptr(), tp, ta,
-          out.data_ptr(), accepted.data_ptr(), B, K, V, logits.stride(0), logits.stride(1),
-          draft_logits.stride(0) if drafted else 0, draft_logits.stride(1) if drafted else 0)
+    d = draft_logits.stride() if drafted else (0, 0, 1)
+    if V > 1 and (strides[2] != 1 or d[2] != 1):
+        raise ValueError("the last dimension of logits and draft_logits must be dense")
+    if draft_logits is not None and (draft_logits.get_device() != dev or draft_logits.dtype is not logits.dtype
+                                     or draft_logits.shape != (B, K, V)):
+        raise ValueError(f"draft_logits must be {(B, K, V)} with the dtype and device of logits")
+    if not (_is(codes, _i32, dev, (B, K)) and _is(u, _f32, dev, (B, rows)) and _is(out, _i32, dev, (B, rows))
+            and _is(accepted, _i32, dev, one)):
+        raise ValueError("codes must be [B, K] int32, u [B, K + 1] float32, out [B, K + 1] and accepted [B] int32, all "
+                         "contiguous on the device of logits")
+    _need(n_draft, "n_draft", _i32, dev, one)
+    tp, ta = (None, temperature) if not isinstance(temperature, torch.Tensor) else \
+        _setting(temperature, "temperature", _f32, B, logits.device)
+    _enqueue("tok_verify_codes", dev, stream, logits.data_ptr(), draft_logits.data_ptr() if drafted else None,
+             _dtype_code(logits), codes.data_ptr(), u.data_ptr(), None if n_draft is None else n_draft.data_ptr(), tp, ta,
+             out.data_ptr(), accepted.data_ptr(), B, K, V, strides[0], strides[1], d[0], d[1])
     return out, accepted
 
 

@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kRound = 128;    // keys of a round
 // A unit's beginning and end take a CTA about as long as this many rounds; fewest places of a CTA.
-constexpr int kEnd = 1, kMinPlaces = 3;
+constexpr int kEnd = 1, kMinPlaces = 4;
 constexpr int kCtas = 148;
 constexpr int64_t kMaxNq = 64;
 constexpr int kThreads = 8 * 32;

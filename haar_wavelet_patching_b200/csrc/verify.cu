@@ -95,41 +95,55 @@ __device__ __forceinline__ uint32_t order_key(float x)
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// exp((x - top) / T) in 64 bits: with y = 64 log2(e) (x - top) / T = k + f, 2^(k / 64) from a table and the
-// exponent, 2^(f / 64) by its Taylor polynomial of degree 4 (|f ln 2 / 64| <= 0.0055: what is left out is below
-// 2^-44.5 relative).  Of +inf as top: 1 for +inf, 0 for all else.
+// exp((x - top') / T) in 64 bits, top' so close to the row's largest logit that n0 below is whole (it falls out of every
+// quotient): with y = 256 log2(e) x / T = n0 + k + f, k whole, 2^(k / 256) comes from a table and the exponent,
+// 2^(f / 256) = 1 + f (c1 + f (c2 + f c3)): what is left out is below 2^-42 relative.  Weights below 2^-1000 of the largest,
+// -inf and NaN are 0.  Of +inf as top, and where T is so small that y is no place in a table: 1 for top, 0 for all else.
+constexpr int kTable = 256;
 struct Weights {
-    const double *table; // 2^(j / 64)
-    double per_t, top;
-    bool infinite;
+    const double *table; // 2^(j / 256)
+    double per_t, magic; // 256 log2(e) / T; 1.5 2^52 - n0
+    float top, least;    // logits up to `least` have no weight, but for top
+    bool only_top;
+    __device__ __forceinline__ Weights(const double *table, float top, double T) : table(table), top(top)
+    {
+        per_t = kTable / 0.6931471805599453 / T;
+        const double y = (double)top * per_t;
+        only_top = !(fabs(y) < 1125899906842624.0); // 2^50
+        magic = 6755399441055744.0 - rint(y);       // (a sum's low bits are its whole part)
+        least = fmaxf((float)((double)top - 1000.0 * kTable / per_t), kLowest);
+    }
     __device__ __forceinline__ double operator()(float x) const
     {
-        constexpr double kMagic = 6755399441055744.0; // 1.5 2^52: a sum's low bits are its integer part
-        constexpr double c1 = 0.6931471805599453 / 64, c2 = c1 * c1 / 2, c3 = c2 * c1 / 3, c4 = c3 * c1 / 4;
-        if (infinite)
-            return x == INFINITY ? 1.0 : 0.0;
-        const double y = ((double)x - top) * per_t;
-        if (!(x >= kLowest) || y < -64.0 * 1000.0) // (-inf and NaN do not count; 2^-1000 is as good as 0)
-            return 0.0;
-        const double kd = y + kMagic, f = y - (kd - kMagic);
+        constexpr double c1 = 0.6931471805599453 / kTable, c2 = c1 * c1 / 2, c3 = c2 * c1 / 3;
+        if (__builtin_expect(only_top, 0))
+            return x == top ? 1.0 : 0.0;
+        const double d = (double)fmaxf(x, least), kd = fma(d, per_t, magic), f = fma(d, per_t, magic - kd);
         const int k = __double2loint(kd);
-        const double q = fma(fma(fma(c4, f, c3), f, c2), f, c1) * f, t = table[k & 63];
-        const double w = fma(t, q, t);
-        return __hiloint2double(__double2hiint(w) + ((k >> 6) << 20), __double2loint(w));
+        const double t = table[k & (kTable - 1)], w = fma(t * f, fma(fma(c3, f, c2), f, c1), t);
+        return x > least || x == top ? __hiloint2double(__double2hiint(w) + ((k >> 8) << 20), __double2loint(w)) : 0.0;
     }
 };
 
 struct Shared {
-    double table[64];
-    double sums[2][kWarps];                    // of the warps' ranges
-    float2 job[kWarps];                        // maximum and sum of a job
-    float2 row[kRowsAtOnce + 1];               // of this CTA's slice of each row
-    float2 all[kRowsAtOnce + 1];               // of the rows
-    unsigned long long best[kRowsAtOnce + 1];  // greedy: the largest, of this CTA's slice
+    double table[kTable];
+    double sums[2][kWarps];         // of the warps' ranges
+    uint64_t part[kRowsAtOnce][kWarps]; // of a row's parts: maximum and sum; greedy: the largest one's place
+    uint64_t row[kRowsAtOnce];      // of this CTA's slice of each row
+    float2 all[kRowsAtOnce];        // of the rows
     double range[kMaxCluster * kWarps];
     double warp[kWarps];
     int first, last;
 };
+
+__device__ __forceinline__ uint64_t as_bits(float2 x)
+{
+    return (uint64_t)__float_as_uint(x.y) << 32 | __float_as_uint(x.x);
+}
+__device__ __forceinline__ float2 as_pair(uint64_t x)
+{
+    return make_float2(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32)));
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs g, int C)
@@ -149,8 +163,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs g,
     const bool greedy = !(temperature > 0.0f);
     temperature = greedy ? 1.0f : fminf(temperature, 3.4e38f); // (an infinite one would turn infinite differences into NaN)
     const float per_t = fminf(fmaxf(1.4426950408889634f / temperature, 1e-37f), 3.4e38f); // a normal number
-    if (tid < 64)
-        sh.table[tid] = exp2((double)tid / 64.0);
+    if (tid < kTable)
+        sh.table[tid] = exp2((double)tid / kTable);
     auto barrier = [&]() TOK_INLINE {
         if (C > 1)
             cluster_sync();
@@ -176,77 +190,94 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs g,
         return r < places ? logits + (int64_t)(i0 + r) * g.logits_row : draft + (int64_t)(i0 + r - places) * g.draft_row;
     };
 
-    // Maxima and sums of `rows` rows; greedy: the first of the largest instead.
+    // Maxima and sums of `rows` rows; greedy: the first of the largest instead.  A warp has its part of each row in
+    // turn, the next kBatch x 32 vectors on their way while it works on the last.
     auto scan = [&](int rows, int i0) TOK_INLINE {
-        int parts = 1; // of a row's slice: a job each
-        while (rows * parts * 2 <= kWarps)
-            parts *= 2;
-        for (int j0 = 0; j0 < rows * parts; j0 += kWarps) {
-            const int job = j0 + warp, r = job / parts, part = job - r * parts;
-            float m = kLowest, z = 0.0f;
-            unsigned long long best = 0;
-            if (r < rows) {
-                const Slice s = slice(row_of(r, i0));
-                const uint4 *vec = reinterpret_cast<const uint4 *>(s.p + s.head);
-                const int per = (s.nv + parts - 1) / parts, v0 = min(s.nv, part * per), v1 = min(s.nv, v0 + per);
-                constexpr int kBatch = 4;
-                auto take = [&](const float *x, int count, int idx) TOK_INLINE {
-                    float top = x[0];
+        constexpr int kBatch = 4;
+        float m = kLowest, z = 0.0f;
+        uint64_t best = 0;
+        auto take = [&](const float *x, int count, int idx) TOK_INLINE {
+            float top = x[0];
 #pragma unroll
-                    for (int k = 1; k < N; ++k)
-                        if (k < count)
-                            top = fmaxf(top, x[k]);
-                    if (greedy) {
-                        if (top >= m) { // (NaN: not)
-#pragma unroll
-                            for (int k = 0; k < N; ++k)
-                                if (k < count && x[k] >= kLowest) {
-                                    const unsigned long long place =
-                                        (unsigned long long)order_key(x[k]) << 32 | (uint32_t)~(idx + k);
-                                    best = place > best ? place : best;
-                                }
-                            m = top;
-                        }
-                        return;
-                    }
-                    if (top > m) {
-                        z *= exp2_approx((m - top) * per_t);
-                        m = top;
-                    }
+            for (int k = 1; k < N; ++k)
+                if (k < count)
+                    top = fmaxf(top, x[k]);
+            if (greedy) {
+                if (top >= m) { // (NaN: not)
 #pragma unroll
                     for (int k = 0; k < N; ++k)
-                        if (k < count)
-                            z += exp2_approx((fmaxf(x[k], -INFINITY) - m) * per_t);
-                };
-                for (int c0 = v0; c0 < v1; c0 += 32 * kBatch) {
-                    uint4 v[kBatch];
-#pragma unroll
-                    for (int e = 0; e < kBatch; ++e)
-                        if (c0 + 32 * e + lane < v1)
-                            v[e] = __ldg(vec + c0 + 32 * e + lane);
-#pragma unroll
-                    for (int e = 0; e < kBatch; ++e)
-                        if (c0 + 32 * e + lane < v1) {
-                            float x[N];
-                            Vec<T>::split(v[e], x);
-                            take(x, N, begin + s.head + (c0 + 32 * e + lane) * N);
+                        if (k < count && x[k] >= kLowest) {
+                            const uint64_t place = (uint64_t)order_key(x[k]) << 32 | (uint32_t)~(idx + k);
+                            best = place > best ? place : best;
                         }
+                    m = top;
                 }
-                const int odd0 = part == 0 ? 0 : n, odd1 = part == 0 ? s.head : n;
-                const int rest0 = part == parts - 1 ? s.head + s.nv * N : n;
-                for (int i = odd0 + lane; i < odd1; i += 32) {
-                    const float x = Vec<T>::one(s.p + i);
-                    take(&x, 1, begin + i);
+                return;
+            }
+            if (top > m) {
+                z *= exp2_approx((m - top) * per_t);
+                m = top;
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (k < count)
+                    z += exp2_approx((fmaxf(x[k], -INFINITY) - m) * per_t);
+        };
+        Slice s{};
+        const uint4 *vec = nullptr;
+        int v0 = 0, v1 = 0;
+        auto part_of = [&](int r) TOK_INLINE { // this warp's vectors of row r
+            s = slice(row_of(r, i0));
+            const int per = (s.nv + kWarps - 1) / kWarps;
+            v0 = min(s.nv, warp * per);
+            v1 = min(s.nv, v0 + per);
+            vec = reinterpret_cast<const uint4 *>(s.p + s.head);
+        };
+        uint4 next[kBatch];
+        auto fetch = [&]() TOK_INLINE {
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e)
+                if (v0 + 32 * e + lane < v1)
+                    next[e] = __ldg(vec + v0 + 32 * e + lane);
+        };
+        part_of(0);
+        fetch();
+        for (int r = 0; r < rows;) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e)
+                v[e] = next[e];
+            const Slice now = s;
+            const int c0 = v0, c1 = v1;
+            const bool last = c0 + 32 * kBatch >= c1; // of the row's part
+            if (!last)
+                v0 += 32 * kBatch;
+            else if (r + 1 < rows)
+                part_of(r + 1);
+            if (!last || r + 1 < rows)
+                fetch();
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e)
+                if (c0 + 32 * e + lane < c1) {
+                    float x[N];
+                    Vec<T>::split(v[e], x);
+                    take(x, N, begin + now.head + (c0 + 32 * e + lane) * N);
                 }
-                for (int i = rest0 + lane; i < n; i += 32) {
-                    const float x = Vec<T>::one(s.p + i);
-                    take(&x, 1, begin + i);
-                }
+            if (!last)
+                continue;
+            // The codes before the first vector (the first warp's) and behind the last one (the last warp's).
+            const int odd0 = warp == 0 ? 0 : now.head + now.nv * N;
+            const int odd1 = warp == 0 ? now.head : warp == kWarps - 1 ? n : odd0;
+            for (int i = odd0 + lane; i < odd1; i += 32) {
+                const float x = Vec<T>::one(now.p + i);
+                take(&x, 1, begin + i);
             }
             if (greedy) {
 #pragma unroll
-                for (int o = 16; o; o >>= 1)
-                    best = max(best, __shfl_xor_sync(~0u, best, o));
+                for (int o = 16; o; o >>= 1) {
+                    const uint64_t y = __shfl_xor_sync(~0u, best, o);
+                    best = y > best ? y : best;
+                }
             } else {
                 float top = m;
 #pragma unroll
@@ -258,67 +289,52 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs g,
                     z += __shfl_xor_sync(~0u, z, o);
                 m = top;
             }
-            // The parts of a row are neighbouring warps of the same round (or one warp is the row's).
-            if (lane == 0) {
-                if (greedy)
-                    sh.sums[0][warp] = __longlong_as_double((long long)best);
-                else
-                    sh.job[warp] = make_float2(m, z);
-            }
-            __syncthreads();
-            if (tid < kWarps && (j0 + tid) % parts == 0 && (j0 + tid) / parts < rows) {
-                const int r2 = (j0 + tid) / parts;
-                if (greedy) {
-                    unsigned long long x = 0;
-                    for (int k = 0; k < parts; ++k)
-                        x = max(x, (unsigned long long)__double_as_longlong(sh.sums[0][tid + k]));
-                    sh.best[r2] = x;
-                } else {
-                    float top = kLowest, sum = 0.0f;
-                    for (int k = 0; k < parts; ++k)
-                        top = fmaxf(top, sh.job[tid + k].x);
-                    for (int k = 0; k < parts; ++k)
-                        sum += sh.job[tid + k].y * exp2_approx((sh.job[tid + k].x - top) * per_t);
-                    sh.row[r2] = make_float2(top, sum);
-                }
-            }
-            __syncthreads();
+            if (lane == 0)
+                sh.part[r][warp] = greedy ? best : as_bits(make_float2(m, z));
+            m = kLowest;
+            z = 0.0f;
+            best = 0;
+            ++r;
         }
-        if (C > 1)
-            cluster_sync();
-        for (int r = tid; r < rows; r += kThreads) {
+        // One warp adds a row's parts up, then the CTAs' (in order).
+        auto joined = [&](uint64_t mine) TOK_INLINE -> uint64_t { // lanes' parts, over kWarps lanes
             if (greedy) {
-                unsigned long long x = sh.best[r];
-                for (int c = 0; c < C && C > 1; ++c)
-                    x = max(x, (unsigned long long)ld_cluster64(&sh.best[r], c));
-                sh.all[r] = make_float2(__uint_as_float((uint32_t)x), x ? 1.0f : 0.0f); // the index's bits, inverted
-            } else {
-                float2 x = sh.row[r];
-                if (C > 1) {
-                    float top = kLowest, sum = 0.0f;
-                    float2 y[kMaxCluster];
 #pragma unroll
-                    for (int c = 0; c < kMaxCluster; ++c)
-                        if (c < C) {
-                            const uint64_t w = ld_cluster64(&sh.row[r], c);
-                            y[c] = make_float2(__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32)));
-                            top = fmaxf(top, y[c].x);
-                        }
-#pragma unroll
-                    for (int c = 0; c < kMaxCluster; ++c)
-                        if (c < C)
-                            sum += y[c].y * exp2_approx((y[c].x - top) * per_t);
-                    x = make_float2(top, sum);
+                for (int o = kWarps / 2; o; o >>= 1) {
+                    const uint64_t y = __shfl_xor_sync(~0u, mine, o);
+                    mine = y > mine ? y : mine;
                 }
-                sh.all[r] = x;
+                return mine;
             }
+            const float2 x = as_pair(mine);
+            float top = x.x, sum;
+#pragma unroll
+            for (int o = kWarps / 2; o; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+            sum = x.y * exp2_approx((x.x - top) * per_t);
+#pragma unroll
+            for (int o = kWarps / 2; o; o >>= 1)
+                sum += __shfl_xor_sync(~0u, sum, o);
+            return as_bits(make_float2(top, sum));
+        };
+        const uint64_t none = greedy ? 0 : as_bits(make_float2(kLowest, 0.0f));
+        __syncthreads();
+        for (int r = warp; r < rows; r += kWarps) {
+            const uint64_t x = joined(sh.part[r][lane % kWarps]);
+            if (lane == 0)
+                sh.row[r] = x;
+        }
+        barrier();
+        for (int r = warp; r < rows; r += kWarps) {
+            uint64_t x = sh.row[r];
+            if (C > 1)
+                x = joined(lane % kWarps < C ? ld_cluster64(&sh.row[r], lane % kWarps) : none);
+            if (lane == 0) // greedy: the index's bits, inverted, and whether there is one
+                sh.all[r] = greedy ? make_float2(__uint_as_float((uint32_t)x), x ? 1.0f : 0.0f) : as_pair(x);
         }
         barrier(); // (also: no CTA's rows are overwritten while another reads them)
     };
-    auto weights_of = [&](float top) TOK_INLINE {
-        return Weights{sh.table, 64.0 / 0.6931471805599453 / (double)temperature, top == INFINITY ? 0.0 : (double)top,
-                       top == INFINITY};
-    };
+    auto weights_of = [&](float top) TOK_INLINE { return Weights(sh.table, top, (double)temperature); };
     // This warp's range [lo, hi) of the slice, in whole vectors of the row's.
     auto range_of = [&](int w, int &lo, int &hi) TOK_INLINE {
         const int per = ((n + kWarps - 1) / kWarps + N - 1) / N * N;
@@ -416,10 +432,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs g,
                 stands = false;
             else {
                 const T *p = logits + (int64_t)place * g.logits_row, *q = draft ? draft + (int64_t)place * g.draft_row : nullptr;
-                const double ep = weights_of(p_row.x)(Vec<T>::one(p + x));
-                const double eq = q ? weights_of(q_row.x)(Vec<T>::one(q + x)) : 1.0;
-                // v eq / zq < ep / zp.  (eq is 0 where the draft's row has no code.)
-                double left = v * eq * (double)p_row.y, right = ep * (q ? (double)q_row.y : 1.0);
+                const Weights wp = weights_of(p_row.x), wq = weights_of(q_row.x);
+                const double ep = wp(Vec<T>::one(p + x)), eq = q ? wq(Vec<T>::one(q + x)) : 1.0;
+                // v eq / zq < ep / zp.  (eq is 0 where the draft's row has no code; the sums in 32 bits are of weights
+                // relative to the largest logit.)
+                double left = v * eq * ((double)p_row.y * wp(p_row.x));
+                double right = ep * (q ? (double)q_row.y * wq(q_row.x) : 1.0);
                 if (v * eq == 0.0 || ep == 0.0)
                     stands = ep > 0.0;
                 else if (fabs(left - right) > kDoubt * right)
@@ -575,10 +593,9 @@ template <typename T> tok_status launch(VerifyArgs g, int64_t B, cudaStream_t st
 {
     constexpr int N = Vec<T>::N;
     auto slice_of = [&](int c) { return ((g.V + c - 1) / c + N - 1) / N * N; };
-    // CTAs per stream: several while there are SMs without a stream.
-    int C = 1;
-    while (C < kMaxCluster && B * C * 2 <= 148 && slice_of(C) > 2 * kThreads)
-        C *= 2;
+    // CTAs per stream: as many as are resident at a time, two to an SM.
+    const int64_t fit = std::max<int64_t>(1, 2 * 148 / B), need = std::max<int64_t>(1, g.V / (2 * kThreads));
+    const int C = (int)std::min(std::min<int64_t>(kMaxCluster, fit), need);
     g.slice = slice_of(C);
     g.at_once = B * C <= 2 * 148 ? g.K + 1 : 1;
     cudaLaunchConfig_t cfg{};
