@@ -7,7 +7,7 @@
 // every row of g read once, so it is bound by HBM as well, if no row is added to twice: the tokens are sorted by
 // code, stable, so the order of a sum is that of the tokens and no atomics are needed.
 //
-//   sort_kernel: one cluster sorts (code, token) pairs by digits of up to 10 bits, a slice of the
+//   sort_kernel: one cluster sorts (code, token) pairs by digits of 8 or 10 bits, a slice of the
 //   pairs to a CTA and a contiguous part of it to a warp.  Each pass counts digits per warp, adds the counts up over warps, CTAs and
 //   digits, and moves each pair to its place.  (2 passes up to 2^20 codes.)
 //
@@ -115,7 +115,7 @@ template <typename T> void launch_embed(int v, const EmbedArgs &g, cudaStream_t 
 // Gradient: sorting.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kMaxSortCtas = 8;
+constexpr int kMaxSortCtas = 16; // (beyond 8 a cluster is not portable, but this GPU holds it)
 constexpr int kAbsorb = 8;
 
 struct SortArgs {
@@ -124,7 +124,7 @@ struct SortArgs {
     uint2 *bounds;      // [chunks + 1]: first token (in sorted order) and row of each chunk
     uint32_t *joins;    // number of rows to join (cleared here)
     uint32_t N, V;
-    int passes, bits;
+    int passes;
     uint32_t chunks, len;
 };
 
@@ -161,13 +161,14 @@ __device__ __forceinline__ uint32_t load_cluster(const uint32_t *p, uint32_t ran
     return v;
 }
 
+template <int kBits> // of a digit
 __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs g, int C)
 {
+    constexpr int digits = 1 << kBits;
     extern __shared__ uint32_t hist[]; // [warps][digits]
-    __shared__ uint32_t totals[1024], base[1024], sums[32];
+    __shared__ uint32_t totals[digits], base[digits], sums[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = C > 1 ? cluster_rank() : 0;
-    const int digits = 1 << g.bits;
     // This warp's pairs: contiguous parts of contiguous slices, whole 32s.
     const uint32_t per = (((g.N + C * kSortWarps - 1) / (C * kSortWarps)) + 31) & ~31u;
     const uint64_t first = (uint64_t)(rank * kSortWarps + warp) * per;
@@ -179,24 +180,48 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs g,
     for (int pass = 0; pass < g.passes; ++pass) {
         const uint64_t *src = g.pairs[(pass + 1) & 1];
         uint64_t *dst = g.pairs[pass & 1];
-        const int shift = pass * g.bits;
+        const int shift = pass * kBits;
         auto pair = [&](uint32_t i) -> uint64_t {
             if (pass > 0)
                 return src[i];
             const uint32_t c = (uint32_t)g.codes[i];
             return (uint64_t)(c < g.V ? c : g.V) << 32 | i; // (codes outside the table behind all others)
         };
+        // f(pair, whether there is one) for this warp's pairs, 32 at a time in order, kAtOnce x 32 loads on their way.
+        auto batches = [&](auto &&f) {
+            constexpr int kAtOnce = 8;
+            for (uint32_t i = i0; i < i1; i += 32 * kAtOnce) {
+                uint64_t p[kAtOnce];
+#pragma unroll
+                for (int e = 0; e < kAtOnce; ++e)
+                    p[e] = i + 32 * e + lane < i1 ? pair(i + 32 * e + lane) : 0;
+#pragma unroll
+                for (int e = 0; e < kAtOnce; ++e)
+                    if (i + 32 * e < i1)
+                        f(p[e], i + 32 * e + lane < i1);
+            }
+        };
+        // The lanes with the same digit, by a vote per bit (the instruction that matches whole values takes 10 times as
+        // long with 32 warps at it).
+        auto alike = [&](uint32_t d, bool on) {
+            uint32_t same = __ballot_sync(~0u, on);
+#pragma unroll
+            for (int b = 0; b < kBits; ++b) {
+                const bool bit = d >> b & 1;
+                const uint32_t set = __ballot_sync(~0u, bit);
+                same &= bit ? set : ~set;
+            }
+            return same;
+        };
         for (int d = lane; d < digits; d += 32)
             mine[d] = 0;
         __syncwarp();
-        for (uint32_t i = i0; i < i1; i += 32) {
-            const bool on = i + lane < i1;
-            const uint32_t d = on ? (uint32_t)(pair(i + lane) >> 32) >> shift & (digits - 1) : ~0u;
-            const uint32_t same = __match_any_sync(~0u, d);
+        batches([&](uint64_t p, bool on) {
+            const uint32_t d = (uint32_t)(p >> 32) >> shift & (digits - 1), same = alike(d, on);
             if (on && (same & ((1u << lane) - 1)) == 0)
                 mine[d] += __popc(same);
             __syncwarp();
-        }
+        });
         __syncthreads();
         for (int d = tid; d < digits; d += kSortThreads) { // counts of the warps before
             uint32_t run = 0;
@@ -213,28 +238,31 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs g,
         else
             __syncthreads();
         uint32_t before = 0, all = 0;
-        if (tid < digits)
-            for (int c = 0; c < C; ++c) {
-                const uint32_t x = C > 1 ? load_cluster(&totals[tid], c) : totals[tid];
-                before += c < (int)rank ? x : 0;
-                all += x;
+        if (tid < digits) {
+            uint32_t x[kMaxSortCtas];
+#pragma unroll
+            for (int c = 0; c < kMaxSortCtas; ++c)
+                x[c] = c >= C ? 0 : C > 1 ? load_cluster(&totals[tid], c) : totals[tid];
+#pragma unroll
+            for (int c = 0; c < kMaxSortCtas; ++c) {
+                before += c < (int)rank ? x[c] : 0;
+                all += x[c];
             }
+        }
         const uint32_t at = block_scan(all, sums);
         if (tid < digits)
             base[tid] = at + before;
         __syncthreads();
-        for (uint32_t i = i0; i < i1; i += 32) {
-            const bool on = i + lane < i1;
-            const uint64_t p = on ? pair(i + lane) : 0;
-            const uint32_t d = on ? (uint32_t)(p >> 32) >> shift & (digits - 1) : ~0u;
-            const uint32_t same = __match_any_sync(~0u, d), below = __popc(same & ((1u << lane) - 1));
+        batches([&](uint64_t p, bool on) {
+            const uint32_t d = (uint32_t)(p >> 32) >> shift & (digits - 1), same = alike(d, on);
+            const uint32_t below = __popc(same & ((1u << lane) - 1));
             if (on)
                 dst[base[d] + mine[d] + below] = p;
             __syncwarp();
             if (on && below == 0)
                 mine[d] += __popc(same);
             __syncwarp();
-        }
+        });
         if (C > 1)
             cluster_sync(); // (also: nobody reads totals any more)
         else
@@ -244,22 +272,35 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs g,
     // thread i finds the borders between its element and that of the token before.
     const uint64_t *sorted = g.pairs[(g.passes - 1) & 1];
     auto key = [&](uint32_t i) -> uint32_t { return i < g.N ? (uint32_t)(sorted[i] >> 32) : g.V; };
-    for (uint32_t i = rank * kSortThreads + tid; i <= g.N; i += C * kSortThreads) {
-        const uint32_t k = key(i), kp = i ? key(i - 1) : 0;
-        if (i && kp == g.V)
-            continue; // (a code outside the table before: no elements from there on)
-        const uint32_t lo = i ? (i - 1 + kp) / g.len + 1 : 0;
-        const uint32_t hi = k == g.V ? g.chunks : (i + k) / g.len;
-        if (lo > hi)
-            continue;
-        uint32_t rem = 0; // tokens of the code before from here on (up to kAbsorb)
-        while (i && rem < kAbsorb && key(i + rem) == kp)
-            ++rem;
-        for (uint32_t c = lo; c <= hi; ++c) {
-            uint2 b = make_uint2(i, min(c * g.len - i, g.V)); // the row of element c * len
-            if (i && b.y == kp && rem < kAbsorb) // the border cuts a row: its rest goes to the chunk before
-                b = make_uint2(i + rem, kp + 1);
-            g.bounds[c] = b;
+    const uint32_t step = C * kSortThreads;
+    constexpr int kAtOnce = 4;
+    for (uint64_t j = rank * kSortThreads + tid; j <= g.N; j += (uint64_t)step * kAtOnce) {
+        uint32_t ks[kAtOnce], kps[kAtOnce];
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) {
+            const uint32_t i = (uint32_t)min(j + (uint64_t)step * e, (uint64_t)g.N);
+            ks[e] = key(i);
+            kps[e] = i ? key(i - 1) : 0;
+        }
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) {
+            const uint64_t at = j + (uint64_t)step * e;
+            const uint32_t i = (uint32_t)at, k = ks[e], kp = kps[e];
+            if (at > g.N || (i && kp == g.V))
+                continue; // (a code outside the table before: no elements from there on)
+            const uint32_t lo = i ? (i - 1 + kp) / g.len + 1 : 0;
+            const uint32_t hi = k == g.V ? g.chunks : (i + k) / g.len;
+            if (lo > hi)
+                continue;
+            uint32_t rem = 0; // tokens of the code before from here on (up to kAbsorb)
+            while (i && rem < kAbsorb && key(i + rem) == kp)
+                ++rem;
+            for (uint32_t c = lo; c <= hi; ++c) {
+                uint2 b = make_uint2(i, min(c * g.len - i, g.V)); // the row of element c * len
+                if (i && b.y == kp && rem < kAbsorb) // the border cuts a row: its rest goes to the chunk before
+                    b = make_uint2(i + rem, kp + 1);
+                g.bounds[c] = b;
+            }
         }
     }
 }
@@ -284,8 +325,33 @@ struct SumArgs {
     float scale;
 };
 
+// V elements as they lie in memory.
+template <int kBytes> struct RawOf;
+template <> struct RawOf<16> {
+    using type = uint4;
+};
+template <> struct RawOf<8> {
+    using type = uint2;
+};
+template <> struct RawOf<4> {
+    using type = uint32_t;
+};
+template <> struct RawOf<2> {
+    using type = unsigned short;
+};
+template <typename T, int V> struct Raw {
+    using type = typename RawOf<V * (int)sizeof(T)>::type;
+    static __device__ __forceinline__ void add(const type &x, float *acc)
+    {
+        const T *v = reinterpret_cast<const T *>(&x);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            acc[e] += (float)v[e];
+    }
+};
+
 template <typename TG, typename TT, int V>
-__global__ void __launch_bounds__(kSumThreads, 4) sum_kernel(const SumArgs g)
+__global__ void __launch_bounds__(kSumThreads, 3) sum_kernel(const SumArgs g)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
@@ -320,29 +386,39 @@ __global__ void __launch_bounds__(kSumThreads, 4) sum_kernel(const SumArgs g)
             acc[e] = 0.0f;
         ++v;
     };
-    uint64_t p[kBatch];
-    float x[kBatch][V];
-    auto fetch = [&](uint32_t t) {
+    // Tokens' rows one batch ahead of the sums, the tokens two.
+    using R = Raw<TG, V>;
+    uint64_t p[kBatch], q[kBatch];
+    typename R::type x[kBatch], y[kBatch];
+    auto tokens = [&](uint32_t t, uint64_t (&to)[kBatch]) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-            if (t + k < b1.x)
-                p[k] = g.sorted[t + k];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            if (t + k < b1.x)
-                Row<TG, V, (V > 1)>::load(src + (int64_t)(uint32_t)p[k] * g.grad_row, x[k]);
+            to[k] = t + k < b1.x ? g.sorted[t + k] : 0;
     };
+    auto rows = [&](uint32_t t, const uint64_t (&of)[kBatch], typename R::type (&to)[kBatch]) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (t + k < b1.x)
+                to[k] = *reinterpret_cast<const typename R::type *>(src + (int64_t)(uint32_t)of[k] * g.grad_row);
+    };
+    tokens(b0.x, p);
+    rows(b0.x, p, x);
+    tokens(b0.x + kBatch, q);
     for (uint32_t t = b0.x; t < b1.x; t += kBatch) {
-        fetch(t);
+        rows(t + kBatch, q, y);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
             if (t + k < b1.x) {
                 while (v < (uint32_t)(p[k] >> 32))
                     emit();
-#pragma unroll
-                for (int e = 0; e < V; ++e)
-                    acc[e] += x[k][e];
+                R::add(x[k], acc);
             }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            x[k] = y[k];
+            p[k] = q[k];
+        }
+        tokens(t + 2 * kBatch, q);
     }
     while (v < b1.y)
         emit();
@@ -399,15 +475,15 @@ struct Plan {
     int64_t at_order, at_bounds, at_joins, at_part, bytes;
     Plan(int64_t N, int64_t V, int64_t D)
     {
-        // Chunks of a group of 256 threads that hold up to 2048 channels: two rounds of 4 CTAs per SM.
-        const int64_t groups = 148 * 8 * std::max<int64_t>(1, 2048 / std::max<int64_t>(D, 64));
+        // Chunks of a group of 256 threads that hold up to 2048 channels: four rounds of 3 CTAs per SM.
+        const int64_t groups = 148 * 12 * std::max<int64_t>(1, 2048 / std::max<int64_t>(D, 64));
         len = std::max<int64_t>(4 * kAbsorb, (N + V + groups - 1) / groups);
         chunks = (N + V + len - 1) / len;
         int width = 1; // bits of the largest key, V
         while (V >> width)
             ++width;
-        passes = width > 10 ? 2 : 1;
-        bits = (width + passes - 1) / passes;
+        passes = width <= 8 ? 1 : 2;
+        bits = width <= 16 ? 8 : 10;
         C = 1;
         while (C < kMaxSortCtas && N > (int64_t)C * kSortThreads)
             C *= 2;
@@ -559,11 +635,13 @@ extern "C" tok_status tok_embed_codes_backward(const int32_t *codes, const void 
     s.N = (uint32_t)N;
     s.V = (uint32_t)V;
     s.passes = plan.passes;
-    s.bits = plan.bits;
     s.chunks = (uint32_t)plan.chunks;
     s.len = (uint32_t)plan.len;
     const int smem = (kSortWarps << plan.bits) * 4;
-    cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    void (*sort)(SortArgs, int) = plan.bits == 8 ? sort_kernel<8> : sort_kernel<10>;
+    cudaError_t e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(sort, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) {
         record_cuda_error(e);
         return TOK_ERR_CUDA;
@@ -579,7 +657,7 @@ extern "C" tok_status tok_embed_codes_backward(const int32_t *codes, const void 
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, sort_kernel, s, plan.C);
+    e = cudaLaunchKernelEx(&cfg, sort, s, plan.C);
     if (e != cudaSuccess) {
         record_cuda_error(e);
         cudaGetLastError();
