@@ -187,18 +187,21 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs g,
             const uint32_t c = (uint32_t)g.codes[i];
             return (uint64_t)(c < g.V ? c : g.V) << 32 | i; // (codes outside the table behind all others)
         };
-        // f(pair, whether there is one) for this warp's pairs, 32 at a time in order, kAtOnce x 32 loads on their way.
-        auto batches = [&](auto &&f) {
-            constexpr int kAtOnce = 8;
+        // f(pair, whether there is one) for this warp's pairs, 32 at a time in order, kAtOnce x 32 loads on their way;
+        // what fits into one batch is loaded once per pass.
+        constexpr int kAtOnce = 8;
+        uint64_t held[kAtOnce];
+        auto batches = [&](bool load, auto &&f) {
             for (uint32_t i = i0; i < i1; i += 32 * kAtOnce) {
-                uint64_t p[kAtOnce];
+                if (load || i1 - i0 > 32 * kAtOnce) {
 #pragma unroll
-                for (int e = 0; e < kAtOnce; ++e)
-                    p[e] = i + 32 * e + lane < i1 ? pair(i + 32 * e + lane) : 0;
+                    for (int e = 0; e < kAtOnce; ++e)
+                        held[e] = i + 32 * e + lane < i1 ? pair(i + 32 * e + lane) : 0;
+                }
 #pragma unroll
                 for (int e = 0; e < kAtOnce; ++e)
                     if (i + 32 * e < i1)
-                        f(p[e], i + 32 * e + lane < i1);
+                        f(held[e], i + 32 * e + lane < i1);
             }
         };
         // The lanes with the same digit, by a vote per bit (the instruction that matches whole values takes 10 times as
@@ -216,11 +219,9 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs g,
         for (int d = lane; d < digits; d += 32)
             mine[d] = 0;
         __syncwarp();
-        batches([&](uint64_t p, bool on) {
-            const uint32_t d = (uint32_t)(p >> 32) >> shift & (digits - 1), same = alike(d, on);
-            if (on && (same & ((1u << lane) - 1)) == 0)
-                mine[d] += __popc(same);
-            __syncwarp();
+        batches(true, [&](uint64_t p, bool on) {
+            if (on)
+                atomicAdd(&mine[(uint32_t)(p >> 32) >> shift & (digits - 1)], 1u);
         });
         __syncthreads();
         for (int d = tid; d < digits; d += kSortThreads) { // counts of the warps before
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs g,
         if (tid < digits)
             base[tid] = at + before;
         __syncthreads();
-        batches([&](uint64_t p, bool on) {
+        batches(false, [&](uint64_t p, bool on) {
             const uint32_t d = (uint32_t)(p >> 32) >> shift & (digits - 1), same = alike(d, on);
             const uint32_t below = __popc(same & ((1u << lane) - 1));
             if (on)
@@ -293,8 +294,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs g,
             if (lo > hi)
                 continue;
             uint32_t rem = 0; // tokens of the code before from here on (up to kAbsorb)
-            while (i && rem < kAbsorb && key(i + rem) == kp)
-                ++rem;
+            if (i && k == kp) {
+                uint32_t more = 0;
+#pragma unroll
+                for (int r = 0; r < kAbsorb; ++r)
+                    more |= (uint32_t)(key(i + r) == kp) << r;
+                rem = __ffs(~more) - 1; // (bit kAbsorb is not set)
+            }
             for (uint32_t c = lo; c <= hi; ++c) {
                 uint2 b = make_uint2(i, min(c * g.len - i, g.V)); // the row of element c * len
                 if (i && b.y == kp && rem < kAbsorb) // the border cuts a row: its rest goes to the chunk before
