@@ -36,7 +36,7 @@ ABI_SYMBOLS = ("tok_abi_version", "tok_status_str", "tok_last_cuda_error", "tok_
                "tok_cross_attention", "tok_cross_attention_backward_workspace_size", "tok_cross_attention_backward",
                "tok_embed_codes", "tok_embed_codes_backward_workspace_size", "tok_embed_codes_backward",
                "tok_page_tables", "tok_page_release", "tok_paged_write", "tok_paged_attention_workspace_size",
-               "tok_paged_attention", "tok_verify_codes")
+               "tok_paged_attention", "tok_verify_codes_workspace_size", "tok_verify_codes")
 
 _lib = None
 
@@ -155,7 +155,9 @@ def lib():
         L.tok_paged_attention.restype = i32
         L.tok_paged_attention.argtypes = [hp, pp, pp, vp, vp, vp, hp, vp] + [i64] * 9 + [f32, vp, i64, vp]
         L.tok_verify_codes.restype = i32
-        L.tok_verify_codes.argtypes = [vp, vp, i32, vp, vp, vp, vp, f32, vp, vp] + [i64] * 7 + [vp]
+        L.tok_verify_codes.argtypes = [vp, vp, i32, vp, vp, vp, vp, f32, vp, vp] + [i64] * 7 + [vp, i64, vp]
+        L.tok_verify_codes_workspace_size.restype = i64
+        L.tok_verify_codes_workspace_size.argtypes = [i64] * 3
         _lib = L
     return _lib
 
@@ -1094,12 +1096,17 @@ def tok_paged_attention(q, k_pages, v_pages, table, k_lens, o, lse=None, q_lens=
 # ---------------------------------------------------------------------------
 # Verifying drafted codes.
 # ---------------------------------------------------------------------------
-def tok_verify_codes(logits, codes, u, out, accepted, draft_logits=None, n_draft=None, temperature=1.0, stream=None):
+def verify_codes_workspace_size(B, K, V) -> int:
+    return int(lib().tok_verify_codes_workspace_size(B, K, V))
+
+
+def tok_verify_codes(logits, codes, u, out, accepted, draft_logits=None, n_draft=None, temperature=1.0, workspace=None,
+                     stream=None):
     """Which drafted codes stand, and the code behind them: logits [B, K + 1, V] (float32 or bfloat16), draft_logits
     [B, K, V] or None (each draft was certain), codes [B, K] int32, u [B, K + 1] fp32 in [0, 1), n_draft [B] int32 or
     None (K), temperature a number or fp32 [B] -> out [B, K + 1] int32 (the codes that stand, the drawn one, then -1),
     accepted [B] int32.  Draft i stands if u q(x) < p(x); the code behind is drawn with u[:, K] from max(p - q, 0), or
-    from p behind all drafts."""
+    from p behind all drafts.  workspace: verify_codes_workspace_size bytes, allocated if None."""
     dev = _device_of(logits, "logits")
     if logits.dim() != 3 or logits.shape[1] < 1 or logits.shape[2] < 1:
         raise ValueError("logits must be [B, K + 1, V] with V >= 1")
@@ -1117,11 +1124,13 @@ def tok_verify_codes(logits, codes, u, out, accepted, draft_logits=None, n_draft
         raise ValueError("codes must be [B, K] int32, u [B, K + 1] float32, out [B, K + 1] and accepted [B] int32, all "
                          "contiguous on the device of logits")
     _need(n_draft, "n_draft", _i32, dev, one)
+    ws = _workspace_of((_lib or lib()).tok_verify_codes_workspace_size(B, K, V), workspace, logits, stream,
+                       f"no verification for (B, K, V) = {(B, K, V)}: K at most 63, V at most 2^18")
     tp, ta = (None, temperature) if not isinstance(temperature, torch.Tensor) else \
         _setting(temperature, "temperature", _f32, B, logits.device)
     _enqueue("tok_verify_codes", dev, stream, logits.data_ptr(), draft_logits.data_ptr() if drafted else None,
              _dtype_code(logits), codes.data_ptr(), u.data_ptr(), None if n_draft is None else n_draft.data_ptr(), tp, ta,
-             out.data_ptr(), accepted.data_ptr(), B, K, V, strides[0], strides[1], d[0], d[1])
+             out.data_ptr(), accepted.data_ptr(), B, K, V, strides[0], strides[1], d[0], d[1], *_bytes(ws))
     return out, accepted
 
 
@@ -1306,4 +1315,4 @@ def verify_codes(logits, codes, u, draft_logits=None, n_draft=None, temperature=
     """(out, accepted): see tok_verify_codes.  out feeds embed_codes where V is the table's."""
     out = _new(logits, logits.shape[:2], torch.int32, stream)
     accepted = _new(logits, logits.shape[:1], torch.int32, stream)
-    return tok_verify_codes(logits, codes, u, out, accepted, draft_logits, n_draft, temperature, stream)
+    return tok_verify_codes(logits, codes, u, out, accepted, draft_logits, n_draft, temperature, None, stream)

@@ -709,16 +709,19 @@ TOK_API tok_status tok_paged_attention(const tok_heads *q, const tok_pages *k_pa
  * clamped to [0, 1) (NaN: 0).  So the codes are distributed as draws from p.  temperature <= 0 (or NaN): p and q are 1 at the
  * first of the largest logits.  Logits of NaN count as -inf; where a logit is +inf only these count, alike.  A row of
  * logits all -inf refuses the draft and draws -1.  A drafted code outside [0, V) does not stand.
- * Probabilities are taken and added up in 64 bits, in a fixed order; a draft's test is decided in 32 bits where these
- * leave no doubt.
+ * Probabilities are within 2^-33 and added up in 64 bits, in a fixed order; a draft's test takes its two in 64 bits.
+ * Temperatures above 2^100 count as that.  workspace: 16-byte-aligned device memory of tok_verify_codes_workspace_size()
+ * bytes, overwritten; calls that may overlap need one each.  The size is -1 for an invalid shape.
  * Shape rule: 0 <= B <= 2^20, 0 <= K <= 63, 1 <= V <= 2^18; rows logits_row apart, streams logits_batch apart
  * (draft_row, draft_batch), 0 <= strides < 2^40.
  */
+TOK_API int64_t tok_verify_codes_workspace_size(int64_t B, int64_t K, int64_t V);
 TOK_API tok_status tok_verify_codes(const void *logits, const void *draft_logits, tok_dtype dtype,
                                     const int32_t *codes, const float *u, const int32_t *n_draft,
                                     const float *temperature, float temperature_all, int32_t *out, int32_t *accepted,
                                     int64_t B, int64_t K, int64_t V, int64_t logits_batch, int64_t logits_row,
-                                    int64_t draft_batch, int64_t draft_row, cudaStream_t stream);
+                                    int64_t draft_batch, int64_t draft_row, void *workspace, int64_t workspace_bytes,
+                                    cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -166,23 +166,25 @@ def test_paged_attention_rules(lib):
 
 
 def verify(lib, x=at(1), d=at(2), dtype=1, codes=at(3), u=at(4), n=NULL, t=NULL, out=at(5), acc=at(6), B=4, K=3, V=100,
-           lb=400, lr=100, db=300, dr=100):
-    return lib.tok_verify_codes(x, d, dtype, codes, u, n, t, 1.0, out, acc, B, K, V, lb, lr, db, dr, NULL)
+           lb=400, lr=100, db=300, dr=100, ws=at(7), wb=1 << 27):
+    return lib.tok_verify_codes(x, d, dtype, codes, u, n, t, 1.0, out, acc, B, K, V, lb, lr, db, dr, ws, wb, NULL)
 
 
 def test_verify_rules(lib):
     for kw in (dict(B=-1), dict(B=(1 << 20) + 1), dict(K=-1), dict(K=64), dict(V=0), dict(V=(1 << 18) + 1), dict(lb=-1),
-               dict(lr=-1), dict(db=1 << 40), dict(dr=-100)):
+               dict(lr=-1), dict(db=1 << 40), dict(dr=-100), dict(wb=lib.tok_verify_codes_workspace_size(4, 3, 100) - 1)):
         assert verify(lib, **kw) == hwp.TOK_ERR_SHAPE, kw
     assert verify(lib, dtype=2) == hwp.TOK_ERR_DTYPE
-    for kw in (dict(x=NULL), dict(codes=NULL), dict(u=NULL), dict(out=NULL), dict(acc=NULL)):
+    for kw in (dict(x=NULL), dict(codes=NULL), dict(u=NULL), dict(out=NULL), dict(acc=NULL), dict(ws=NULL)):
         assert verify(lib, **kw) == hwp.TOK_ERR_NULL
-    for i, name in enumerate(("x", "d", "codes", "u", "n", "t", "out", "acc")):
+    for i, name in enumerate(("x", "d", "codes", "u", "n", "t", "out", "acc", "ws")):
         assert verify(lib, **{name: F((i + 9) * 0x10000000 + 1)}) == hwp.TOK_ERR_ALIGN, name
     for kw in (dict(out=at(1)), dict(out=at(2)), dict(out=at(3)), dict(acc=at(4)), dict(acc=at(5)), dict(n=at(6)),
-               dict(t=at(5))):
+               dict(t=at(5)), dict(ws=at(1)), dict(ws=at(3)), dict(ws=at(5)), dict(ws=at(6))):
         assert verify(lib, **kw) == hwp.TOK_ERR_ALIAS, kw
-    assert verify(lib, B=0, x=NULL, d=NULL, codes=NULL, u=NULL, out=NULL, acc=NULL) == hwp.TOK_OK
+    assert verify(lib, B=0, x=NULL, d=NULL, codes=NULL, u=NULL, out=NULL, acc=NULL, ws=NULL, wb=0) == hwp.TOK_OK
+    size = lib.tok_verify_codes_workspace_size
+    assert size(1, 64, 5) == -1 and size(-1, 1, 5) == -1 and size(1, 1, 0) == -1 and size(0, 3, 5) == 0 and size(2, 3, 5) > 0
 
 
 def test_bindings_refuse():
