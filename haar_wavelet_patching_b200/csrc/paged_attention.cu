@@ -8,9 +8,10 @@
 //
 // There are few query rows and many keys, so the products are taken transposed, with the 128 rows of the tensor
 // cores' tiles for keys and for channels: scores^T = K Q^T (128 keys x N queries), then o^T += V^T P^T
-// (channels x N), and no thread touches a key or a value.  A CTA's warps:
-//   warps 0-3  softmax, a key to a thread (its lane of tensor memory): scores -> weights, rounded to bf16, into shared
-//              memory as the second product's operand.  Weights are relative to the score of the unit's first key, and to
+// (channels x 2 N, the weights and what their rounding has left; one column more or less is no time), and no thread touches a
+// key or a value.  A CTA's warps:
+//   warps 0-3  softmax, a key to a thread (its lane of tensor memory): scores -> weights, a bf16 number and another for
+//              the rest of each, into shared memory as the second product's operand.  Weights are relative to the score of the unit's first key, and to
 //              the largest one from where one exceeds it by more than 2^16 (every term carries the same factor, so the
 //              quotient is unchanged); a vote of the four warps each round says so.  Sums stay with the threads up to a
 //              unit's end: o / sum -> HBM;
@@ -154,8 +155,11 @@ template <int DP, int N> struct Smem {
     static constexpr int sub = kRound * 128;     // 64 channels of a round's keys
     static constexpr int tile = DP / 64 * sub;   // keys or values of a round
     static constexpr int q = DP / 64 * N * 128;  // a unit's queries
-    static constexpr int p = kRound * 2 * N;     // a round's weights
-    static constexpr int units = N == 64 ? 2 : 4; // whose queries may be there
+    // Columns of the second product: the weights rounded to bf16, as the values are, and behind them what that has left, so that
+    // the output's rounding alone counts.  With 64 rows there is no room: a weight is off by up to 2^-9.
+    static constexpr int wide = N == 64 ? N : 2 * N;
+    static constexpr int p = kRound * 2 * wide;  // a round's weights
+    static constexpr int units = N == 64 ? 2 : N == 16 && DP == 128 ? 3 : 4; // whose queries may be there
     static constexpr int ring = DP == 64 ? (N == 16 ? 6 : N == 32 ? 5 : 4) : N == 16 ? 3 : 2;
     static constexpr int at_q = 2 * ring * tile, at_p = at_q + units * q;
     static constexpr int bytes = at_p + 2 * p + 1024;
@@ -174,7 +178,7 @@ struct Shares {
     }
 };
 
-// Shared-memory descriptor of the weights, [key][N rows]: a key's N rows are a line of the 32-, 64- or 128-byte swizzle (16-byte
+// Shared-memory descriptor of the weights, [key][N columns]: a key's are a line of the 32-, 64- or 128-byte swizzle (16-byte
 // piece i of line k is kept at i ^ (k * 2 N / 128 % (N / 8))), 8 lines an atom.  Fields as in sw128_desc_mn.
 template <int N> __device__ __forceinline__ uint64_t weights_desc(uint32_t saddr)
 {
@@ -434,9 +438,9 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         }
     } else if (warp == 5) {
         if (lane == 0) {
-            const uint32_t idesc_s = idesc_bf16_f32(kRound, N), idesc_o = idesc_bf16_f32(DP, N) | kATransposed | kBTransposed;
+            const uint32_t idesc_s = idesc_bf16_f32(kRound, N), idesc_o = idesc_bf16_f32(DP, S::wide) | kATransposed | kBTransposed;
             const uint64_t kdesc = sw128_desc(base), qdesc = sw128_desc(base + S::at_q);
-            const uint64_t vdesc = sw128_desc_mn(base + NB * S::tile, S::sub), pdesc = weights_desc<N>(base + S::at_p);
+            const uint64_t vdesc = sw128_desc_mn(base + NB * S::tile, S::sub), pdesc = weights_desc<S::wide>(base + S::at_p);
             bool ok = true;
             Place next = now; // of the round whose scores come next
             uint32_t u = 0;
@@ -477,7 +481,7 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
 #pragma unroll
                 for (int k = 0; k < kRound / 16; ++k) // (leaving out steps of 16 keys behind the last one cost 10% of a long call)
                     umma_bf16(o_col, vdesc + ((slot * S::tile + k * 2048) >> 4),
-                              pdesc + (((j & 1) * S::p + k * (16 * 2 * N)) >> 4), idesc_o, !fresh || k > 0);
+                              pdesc + (((j & 1) * S::p + k * (16 * 2 * S::wide)) >> 4), idesc_o, !fresh || k > 0);
                 umma_commit(smem_addr(&empty[1][slot]));
                 umma_commit(smem_addr(&pfree[j & 1]));
                 fresh = last;
@@ -493,8 +497,8 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         const uint32_t lanes = (uint32_t)(32 * warp) << 16;
         constexpr bool kHold = N == 16; // a key's scores and what they are relative to stay in registers
         float l[N] = {}, m[kHold ? N : 1];
-        const uint32_t pbase = base + S::at_p + tid * (2 * N);
-        const int mix = tid * 2 * N / 128 % (N / 8);
+        const uint32_t pbase = base + S::at_p + tid * (2 * S::wide);
+        const int mix = tid * 2 * S::wide / 128 % (S::wide / 8);
         float *side = a.side + (int64_t)cta * 64 * N;
         bool ok = true, fresh = true, whole = false;
         int all = 0;    // keys that all rows see
@@ -616,14 +620,15 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                     wait(pfree[(j - 1) & 1], (uint32_t)((j - 1) >> 1));
                     tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
+                    for (int c = 0; c < S::wide / 16; ++c) {
                         float o[16];
                         tmem_ld16(o_col + lanes + 16 * c, o);
                         tmem_wait_ld();
 #pragma unroll
                         for (int r = 0; r < 16; ++r) {
-                            o[r] *= s_scale[16 * c + r];
-                            l[16 * c + r] *= s_scale[16 * c + r];
+                            o[r] *= s_scale[c % kChunks * 16 + r];
+                            if (c < kChunks)
+                                l[c % kChunks * 16 + r] *= s_scale[c % kChunks * 16 + r];
                         }
                         tmem_st16(o_col + lanes + 16 * c, o);
                     }
@@ -685,18 +690,21 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                         side[(key - all) * N + 16 * c + r] = s[r] + s_m[buf][16 * c + r];
                 }
                 __syncwarp();
-                // (an operand of the second product: bf16, as the values are)
-                uint32_t w[8];
+                constexpr int kParts = S::wide / N;
+                uint32_t w[kParts * 8];
 #pragma unroll
                 for (int r = 0; r < 16; r += 2) {
                     const float e0 = exp2_fast(s[r]), e1 = exp2_fast(s[r + 1]);
                     l[16 * c + r] += e0;
                     l[16 * c + r + 1] += e1;
                     w[r / 2] = pack_bf16x2(e0, e1);
+                    if constexpr (kParts == 2)
+                        w[8 + r / 2] = pack_bf16x2(e0 - bf16_lo(w[r / 2]), e1 - bf16_hi(w[r / 2]));
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(pbase + (j & 1) * S::p + (((2 * c + i) ^ mix) << 4)),
+                for (int i = 0; i < 2 * kParts; ++i)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     pbase + (j & 1) * S::p + (((i / 2 * (N / 8) + 2 * c + i % 2) ^ mix) << 4)),
                                  "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
                                  : "memory");
             }
@@ -753,6 +761,14 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
             for (int c = 0; 16 * c < live_rows; ++c) {
                 float o[16];
                 tmem_ld16(o_col + lanes + 16 * c, o);
+                if constexpr (S::wide > N) {
+                    float rest[16];
+                    tmem_ld16(o_col + lanes + N + 16 * c, rest);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        o[r] += rest[r];
+                }
                 tmem_wait_ld();
                 if (__builtin_expect(odds && live, 0)) {
                     for (unsigned long long left = odds; left; left &= left - 1) {
