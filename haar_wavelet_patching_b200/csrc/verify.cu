@@ -34,7 +34,8 @@ constexpr int kMaxRows = 2 * (int)kMaxK + 1;
 constexpr int kCodes = 2;     // of a lane at a time in a pass (4 spill: 24.5 us for 22.5 with 4 streams)
 constexpr int kMaxParts = 16; // of a row in the scan
 constexpr float kLowest = -3.402823466e+38f;
-// Relative: a lane adds up to 2^13 terms in fp32, each sum is within 2^13 2^-24 + 2^-20 (exponentials) < 2^-10.
+// Relative: a thread adds up to 2^7 terms in fp32 and exponentials are within 2^-15 (the rounding of arguments up to 126), so
+// a sum is within 2^-14 and a test within four times that.
 constexpr double kDoubt = 1.0 / 512;
 
 struct VerifyArgs {

@@ -146,6 +146,23 @@ def test_places_that_are_not_seen_hold_anything(bad, D, Nq, page):
     assert not bool(o[:, Nq - 1].isfinite().all())
 
 
+@pytest.mark.parametrize("Nq,Hq", [(1, 2), (5, 8), (20, 8)])
+@pytest.mark.parametrize("n", [40, 3000, 20000])
+def test_infinite_values_that_all_see(Nq, Hq, n):
+    """One gives its channel that infinity, two of different signs give NaN; other channels have what they have."""
+    D, page = 64, 16
+    kp, vp, table = cache([n], page, 2, D)
+    q = randn(1, Nq, Hq, D, seed=2)
+    want = reference(q, kp, vp, table, [n])
+    for t, d, x in ((0, 3, INF), (7, 5, -INF), (1, 9, INF), (n - Nq, 9, -INF), (n // 2, 11, INF), (n // 2 - 1, 11, INF)):
+        vp[int(table[0, t // page]), t % page, :, d] = x
+    o = hwp.paged_attention(q, kp, vp, table, dev([n]))
+    assert bool((o[..., 3] == INF).all()) and bool((o[..., 5] == -INF).all()) and bool((o[..., 11] == INF).all())
+    assert bool(o[..., 9].isnan().all())
+    rest = [d for d in range(D) if d not in (3, 5, 9, 11)]
+    check(o[..., rest], want[0][..., rest], want[1][..., rest], "o")
+
+
 def test_one_value_that_is_no_number_for_each_query():
     """Token t's value is NaN in channel t alone: query i has NaN in the channels of the tokens that it sees."""
     Nq, n, D = 16, 50, 64
