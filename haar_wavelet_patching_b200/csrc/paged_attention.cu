@@ -16,7 +16,7 @@
 //              quotient is unchanged); a vote of the four warps each round says so.  Sums stay with the threads up to a
 //              unit's end: o / sum -> HBM;
 //   warps 4, 7 tensor copies of keys and of values into rings of 128-byte-swizzled tiles: boxes of as many rows as divide
-//              both a page and a round, a box to a lane, its page looked up one round ahead;
+//              both a page and a round, or four rows of any places;
 //   warp 5     one thread issues the MMAs: the next round's scores before this round's second product;
 //   warp 6     copies of the units' queries and what their rows are, one unit ahead.
 // A round may read rows behind a stream's last token: their scores are masked and their values zeroed in shared memory.
@@ -26,6 +26,7 @@
 // 16, 31 us (floor 18.8), of which about 6 are the launch, the shares and the first copies, and 5 the join; drafts of 5 to a stream
 // on pages of 24: 22.5 us, the same chain.
 #include <algorithm>
+#include <numeric>
 
 #include "pages.cuh"
 
@@ -58,6 +59,10 @@ struct PagedArgs {
     FastDiv page, group;
     int box_rows;     // rows of a tensor copy
     int kh, vh;       // coordinate factors: 0 for broadcast heads
+    // Small boxes: rows of any places, four to a copy, of a map in which page, token and head are one coordinate.
+    struct Gather {
+        int page, token, head, rows; // what one of each adds; the map's rows (0: not so)
+    } gk, gv;
     float scale2;
 };
 
@@ -127,6 +132,14 @@ __device__ __forceinline__ void tma_load_4d_once(uint32_t dst, const CUtensorMap
     asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
                  "%4, %5}], [%6], %7;" ::"r"(dst),
                  "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_gather4_once(uint32_t dst, const CUtensorMap *map, int x, const int (&y)[4], uint32_t bar,
+                                                 uint64_t policy)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+                 "{%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+                 "l"((uint64_t)map), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar), "l"(policy)
                  : "memory");
 }
 __device__ __forceinline__ uint64_t evict_first()
@@ -334,8 +347,9 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     auto ends_unit = [&](const Place &p, int j) { return p.round + 1 == p.rounds || j + 1 == count; };
 
     if (warp == 4 || warp == 7) {
-        // ---- Keys (warp 4) and values (warp 7): a box to a lane, its page looked up two rounds ahead.  (Boxes
-        // behind the first 32, of pages that four does not divide, are looked up as they come.) ----
+        // ---- Keys (warp 4) and values (warp 7): a box to a lane, its page looked up two rounds ahead, or four rows to a lane, looked
+        // up one round ahead.  (Boxes behind the first 32 are looked up as they come: small ones, of pools whose strides have too little
+        // in common for the other form.) ----
         constexpr int kSubs = DP / 64;
         const int kv = warp == 7;
         const CUtensorMap *map = kv ? &vmap : &kmap;
@@ -350,43 +364,84 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
             row = (int)(key - page * a.page.d);
             return a.table[p.b * a.table_row + page];
         };
-        Place ahead = now; // the round looked up next
-        int page0, row0, page1 = 0, row1 = 0;
-        page0 = look_up(ahead, lane, row0);
-        if (count > 1) {
-            advance(ahead);
-            page1 = look_up(ahead, lane, row1);
-        }
         bool ok = true;
         int j = 0;
-        for (; j < count; ++j) {
-            const int slot = j % NB, head = now.unit / a.tiles * factor;
-            const uint32_t bar = smem_addr(&full[kv][slot]), dst = base + (kv * NB + slot) * S::tile;
+        auto room = [&]() { // a stage for round j
             if (lane == 0) {
+                const int slot = j % NB;
                 ok = wait_or_abort(smem_addr(&empty[kv][slot]), ((uint32_t)(j / NB) & 1u) ^ 1u, abort);
                 if (ok)
-                    mbar_expect_tx(bar, S::tile);
+                    mbar_expect_tx(smem_addr(&full[kv][slot]), S::tile);
             }
             ok = __shfl_sync(~0u, ok, 0);
-            if (!ok)
-                break;
-#pragma unroll 1
-            for (int box = lane; box < boxes; box += 32) {
-                if (box >= 32)
-                    page0 = look_up(now, box, row0);
-                const int p = (uint32_t)page0 < (uint32_t)a.P ? page0 : a.P;
+            return ok;
+        };
+        Place ahead = now; // the round looked up next
+        const PagedArgs::Gather &gather = kv ? a.gv : a.gk;
+        if (gather.rows) {
+            // Lane l has the rows 4 l .. 4 l + 3.
+            auto look_up4 = [&](const Place &p, int (&y)[4]) {
+                const int head = p.unit / a.tiles * gather.head;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = p.round * kRound + 4 * lane + i;
+                    y[i] = 0; // (any row where there is none: it is masked as what lies behind the last token)
+                    if (key < p.len) {
+                        const uint32_t page = a.page.div((uint32_t)key), e = (uint32_t)a.table[p.b * a.table_row + page];
+                        if (e < (uint32_t)a.P)
+                            y[i] = (int)e * gather.page + (int)(key - page * a.page.d) * gather.token + head;
+                    }
+                }
+            };
+            int y0[4], y1[4];
+            look_up4(ahead, y0);
+            for (; j < count; ++j) {
+                if (j + 1 < count) {
+                    advance(ahead);
+                    look_up4(ahead, y1);
+                }
+                if (!room())
+                    break;
+                const int slot = j % NB;
 #pragma unroll
                 for (int sub = 0; sub < kSubs; ++sub)
-                    tma_load_4d_once(dst + sub * S::sub + box * a.box_rows * 128, map, 64 * sub, row0, head, p, bar, policy);
+                    tma_gather4_once(base + (kv * NB + slot) * S::tile + sub * S::sub + lane * 512, map, 64 * sub, y0,
+                                     smem_addr(&full[kv][slot]), policy);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    y0[i] = y1[i];
             }
-            __syncwarp();
-            if (j + 1 < count)
-                advance(now);
-            page0 = page1;
-            row0 = row1;
-            if (j + 2 < count) {
+        } else {
+            int page0, row0, page1 = 0, row1 = 0;
+            page0 = look_up(ahead, lane, row0);
+            if (count > 1) {
                 advance(ahead);
                 page1 = look_up(ahead, lane, row1);
+            }
+            for (; j < count; ++j) {
+                if (!room())
+                    break;
+                const int slot = j % NB, head = now.unit / a.tiles * factor;
+                const uint32_t bar = smem_addr(&full[kv][slot]), dst = base + (kv * NB + slot) * S::tile;
+#pragma unroll 1
+                for (int box = lane; box < boxes; box += 32) {
+                    if (box >= 32)
+                        page0 = look_up(now, box, row0);
+                    const int p = (uint32_t)page0 < (uint32_t)a.P ? page0 : a.P;
+#pragma unroll
+                    for (int sub = 0; sub < kSubs; ++sub)
+                        tma_load_4d_once(dst + sub * S::sub + box * a.box_rows * 128, map, 64 * sub, row0, head, p, bar, policy);
+                }
+                __syncwarp();
+                if (j + 1 < count)
+                    advance(now);
+                page0 = page1;
+                row0 = row1;
+                if (j + 2 < count) {
+                    advance(ahead);
+                    page1 = look_up(ahead, lane, row1);
+                }
             }
         }
         if (!ok && lane == 0) // let the copies already issued land before the CTA exits (each wait bounded)
@@ -943,6 +998,27 @@ bool pages_map(CUtensorMap *map, const PagesView &x, const void *any, int64_t P,
 
 constexpr int64_t kIntMax = ((int64_t)1 << 31) - 1;
 
+// Tensor map of a pool for copies of four rows: page, token and head as one coordinate, in units of what their strides have in
+// common; false (and no rows) where that is less than a row.
+bool gather_map(CUtensorMap *map, PagedArgs::Gather *g, const PagesView &x, int64_t P, int64_t page_size, int64_t H, int64_t D)
+{
+    const int64_t pg = P > 1 ? x.pg : 0, t = page_size > 1 ? x.t : 0, h = H > 1 ? x.h : 0;
+    int64_t unit = std::gcd(std::gcd(pg, t), h);
+    unit = unit ? unit : (D + 7) / 8 * 8;
+    if (unit < D || P < 1 || pg / unit >= kIntMax || t / unit >= kIntMax || h / unit >= kIntMax)
+        return false;
+    int64_t a, b;
+    if (!prod_ok({P - 1, pg / unit}, &a) || !prod_ok({page_size - 1, t / unit}, &b) || a > kIntMax || b > kIntMax)
+        return false;
+    const int64_t rows = a + b + (H - 1) * (h / unit) + 1;
+    if (rows >= kIntMax)
+        return false;
+    const uint64_t dims[2] = {(uint64_t)D, (uint64_t)rows}, strides[1] = {(uint64_t)unit * 2};
+    const uint32_t box[2] = {64, 1};
+    *g = {(int)(pg / unit), (int)(t / unit), (int)(h / unit), (int)rows};
+    return encode_tensor_map_sw128(map, 2, x.p, dims, strides, box);
+}
+
 } // namespace
 
 tok_status read_and_clear_paged_timeouts(cudaStream_t stream, unsigned int *count)
@@ -1057,8 +1133,17 @@ extern "C" tok_status tok_paged_attention(const tok_heads *q, const tok_pages *k
     a.kh = Hkv > 1 && a.k.h == 0 ? 0 : 1;
     a.vh = Hkv > 1 && a.v.h == 0 ? 0 : 1;
     CUtensorMap km, vm;
-    if (!pages_map(&km, a.k, a.q.p, P, page_size, Hkv, D, a.box_rows) ||
-        !pages_map(&vm, a.v, a.q.p, P, page_size, Hkv, D, a.box_rows))
+    // Boxes of 1 or 2 rows are bound by the copies' issue: four rows of any pages to a copy instead (4 streams of 9952 keys, 12 key
+    // heads x 96, pages of 1: 258 -> 92 us).  From 4 rows on boxes are no more copies and cost less: 83 us on pages of 4, 56 of 8, 48 of 16.
+    if (a.box_rows <= 2) {
+        PagedArgs::Gather gk{}, gv{};
+        if (gather_map(&km, &gk, a.k, P, page_size, Hkv, D) && gather_map(&vm, &gv, a.v, P, page_size, Hkv, D)) {
+            a.gk = gk;
+            a.gv = gv;
+        }
+    }
+    if (a.gk.rows == 0 && (!pages_map(&km, a.k, a.q.p, P, page_size, Hkv, D, a.box_rows) ||
+        !pages_map(&vm, a.v, a.q.p, P, page_size, Hkv, D, a.box_rows)))
         return TOK_ERR_SHAPE;
     return D <= 64 ? launch_rows<64>(km, vm, a, stream) : launch_rows<128>(km, vm, a, stream);
 }

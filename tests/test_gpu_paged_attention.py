@@ -146,6 +146,36 @@ def test_places_that_are_not_seen_hold_anything(bad, D, Nq, page):
     assert not bool(o[:, Nq - 1].isfinite().all())
 
 
+@pytest.mark.parametrize("page", [1, 3, 6, 4])
+@pytest.mark.parametrize("D", [64, 72])
+def test_small_pages_in_any_layout(page, D):
+    """Pools whose strides have rows in common, or only 8 elements, heads between tokens and broadcast heads: equal bits."""
+    lens, H = [300, 129, 5], 3
+    kp, vp, table = cache(lens, page, H, D)
+    q = randn(3, 4, 6, D, seed=2)
+    o, _ = both(q, kp, vp, table, dev(lens))
+    P = kp.shape[0]
+    for extra, order in ((8, (0, 1, 2, 3)), (0, (0, 2, 1, 3)), (D, (1, 0, 2, 3)), (24, (2, 0, 1, 3))):
+        pools = []
+        for x in (kp, vp):
+            shape = [x.shape[i] for i in order]
+            wide = torch.full((*shape[:2], shape[2] * D + extra), NAN, dtype=torch.bfloat16, device="cuda")
+            y = wide[..., : shape[2] * D].unflatten(-1, (shape[2], D)).permute(*(order.index(i) for i in range(4)))
+            assert y.shape == x.shape
+            y.copy_(x)
+            pools.append(y)
+        assert torch.equal(hwp.paged_attention(q, *pools, table, dev(lens)), o)
+    one = [x[:, :, :1].expand(P, page, H, D) for x in (kp, vp)]
+    same = [x.contiguous() for x in one]
+    assert torch.equal(hwp.paged_attention(q, *one, table, dev(lens)), hwp.paged_attention(q, *same, table, dev(lens)))
+    # The last page and row of the pool, and pages that are not there.
+    last = torch.full_like(table, P - 1)
+    both(q, kp, vp, last, dev([page, 1, 0]))
+    last[0, 0] = P
+    o = hwp.paged_attention(q, kp, vp, last, dev([page, 1, 0]))
+    assert bool(o[0, 3].isnan().all()) and bool(o[1, 3].isfinite().all())
+
+
 @pytest.mark.parametrize("Nq,Hq", [(1, 2), (5, 8), (20, 8)])
 @pytest.mark.parametrize("n", [40, 3000, 20000])
 def test_infinite_values_that_all_see(Nq, Hq, n):
