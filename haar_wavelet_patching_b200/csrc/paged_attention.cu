@@ -22,7 +22,7 @@
 // A round may read rows behind a stream's last token: their scores are masked and their values zeroed in shared memory.
 // All waits are bounded as in the convolutions.
 //
-// Measured, bf16: 4 streams x 56,320 keys, 8 key heads x 128: 150 us (923 MB, 6.2 TB/s); 16 streams of up to 3520 keys, in pages of
+// Measured, bf16: 4 streams x 56,320 keys, 8 key heads x 128: 146 us (923 MB, 6.3 TB/s); 16 streams of up to 3520 keys, in pages of
 // 16, 31 us (floor 18.8), of which about 6 are the launch, the shares and the first copies, and 5 the join; drafts of 5 to a stream
 // on pages of 24: 22.5 us, the same chain.
 #include <algorithm>

@@ -13,7 +13,7 @@
 //   for max(p - q, 0) once more, now that both sums are known; the range, then the thread's share, then the code at which
 //   the running sum exceeds the target.
 // Measured, 64,000 codes: 96 streams of up to 6 drafts, fp32, 90 us: the scan 32 (172 MB, 5.4 TB/s), then two passes of
-// 12 million weights, bound by their 30 instructions a weight; 4 streams of 4 drafts, bf16, 22 us, a chain of short steps.
+// 12 million weights, bound by the latency of a weight's chain at 24 warps an SM; 4 streams of 4 drafts, bf16, 22 us, a chain of short steps.
 #include <algorithm>
 
 #include "tma.cuh"
@@ -102,7 +102,7 @@ __device__ __forceinline__ uint32_t order_key(float x)
 }
 
 // exp((x - top) / T), top the row's largest logit, but for a factor of the row (`unit`), within 2^-33 and as a 64-bit number,
-// with most of its steps in 32 bits, as instructions bound the passes.  With x - base exact, its product with
+// with most of its steps in 32 bits.  With x - base exact, its product with
 // 1024 log2(e) / T (two 32-bit numbers, lo the rest of hi) is k + f, k whole; 2^(k / 1024) comes from a table and the
 // exponent, 2^(f / 1024) - 1 = f (c1 + f c2) (|f c1| < 2^-11: the cubic term is below 2^-36, the rounding of f and of the
 // polynomial below 2^-34).  base is 0 up to |top| / T of 2000: logits that count are then below 2700 T and k below 2^22.  Above
