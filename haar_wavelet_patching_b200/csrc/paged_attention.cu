@@ -11,10 +11,10 @@
 // (channels x 2 N, the weights and what their rounding has left; one column more or less is no time), and no thread touches a
 // key or a value.  A CTA's warps:
 //   warps 0-3  softmax, a key to a thread (its lane of tensor memory): scores -> weights, a bf16 number and another for
-//              the rest of each, into shared memory as the second product's operand.  Weights are relative to the score of the unit's first key, and to
-//              the largest one from where one exceeds it by more than 2^16 (every term carries the same factor, so the
-//              quotient is unchanged); a vote of the four warps each round says so.  Sums stay with the threads up to a
-//              unit's end: o / sum -> HBM;
+//              the rest of each, into shared memory as the second product's operand.  Weights are relative to the score of
+//              the unit's first key, and to the largest one from where one exceeds it by more than 2^16 (every term carries
+//              the same factor, so the quotient is unchanged); a vote of the four warps each round says so.  Sums stay with
+//              the threads up to a unit's end: o / sum -> HBM;
 //   warps 4, 7 tensor copies of keys and of values into rings of 128-byte-swizzled tiles: boxes of as many rows as divide
 //              both a page and a round, or four rows of any places;
 //   warp 5     one thread issues the MMAs: the next round's scores before this round's second product;
@@ -699,8 +699,9 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
             }
             if (j >= 2)
                 wait(pfree[j & 1], (uint32_t)((j - 2) >> 1));
-            // Values behind the stream's last token are nobody's and meet weights of 0: zeros in their place.  A value that some rows see and others do not also meets such weights: where it is
-            // no finite number, its row is taken out, and what it adds to the rows that see it comes at the unit's end.
+            // Values behind the stream's last token are nobody's and meet weights of 0: zeros in their place.  A value that some
+            // rows see and others do not also meets such weights: where it is no finite number, its row is taken out, and what
+            // it adds to the rows that see it comes at the unit's end.
             bool odd = false;
             if (edge) {
                 constexpr int kPieces = DP / 8; // of a row; piece i of row k is kept at i ^ k within its 8
@@ -1134,7 +1135,8 @@ extern "C" tok_status tok_paged_attention(const tok_heads *q, const tok_pages *k
     a.vh = Hkv > 1 && a.v.h == 0 ? 0 : 1;
     CUtensorMap km, vm;
     // Boxes of 1 or 2 rows are bound by the copies' issue: four rows of any pages to a copy instead (4 streams of 9952 keys, 12 key
-    // heads x 96, pages of 1: 258 -> 92 us).  From 4 rows on boxes are no more copies and cost less: 83 us on pages of 4, 56 of 8, 48 of 16.
+    // heads x 96, pages of 1: 258 -> 92 us).  From 4 rows on boxes are no more copies and cost less: 83 us on pages of 4,
+    // 56 of 8, 48 of 16.
     if (a.box_rows <= 2) {
         PagedArgs::Gather gk{}, gv{};
         if (gather_map(&km, &gk, a.k, P, page_size, Hkv, D) && gather_map(&vm, &gv, a.v, P, page_size, Hkv, D)) {

@@ -13,7 +13,8 @@
 //   for max(p - q, 0) once more, now that both sums are known; the range, then the thread's share, then the code at which
 //   the running sum exceeds the target.
 // Measured, 64,000 codes: 96 streams of up to 6 drafts, fp32, 90 us: the scan 32 (172 MB, 5.4 TB/s), then two passes of
-// 12 million weights, bound by the latency of a weight's chain at 24 warps an SM; 4 streams of 4 drafts, bf16, 22 us, a chain of short steps.
+// 12 million weights, bound by the latency of a weight's chain at 24 warps an SM; 4 streams of 4 drafts, bf16, 22 us,
+// a chain of short steps.
 #include <algorithm>
 
 #include "tma.cuh"

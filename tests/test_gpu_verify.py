@@ -102,6 +102,17 @@ def test_spreads_and_temperatures(spread, noise, temperature, B):
         check(logits, codes, u, None, None, temperature)
 
 
+@pytest.mark.parametrize("offset", [0.0, 700.0, -1900.0, 2100.0, -1e5, 1e12])
+@pytest.mark.parametrize("temperature", [0.01, 0.9, 40.0])
+def test_rows_far_from_zero(offset, temperature):
+    """The weights are the differences' alone, on both sides of where these are taken before the product with 1 / T."""
+    logits, draft, codes, u = data(6, 3, 4001, F32, 5.0 * temperature, 1.0)
+    logits[1::2] += offset
+    draft[::2] -= offset
+    check(logits, codes, u, draft, None, temperature)
+    check(logits, codes, u, None, None, temperature)
+
+
 def test_counts_and_temperatures_per_stream():
     B, K, V = 12, 5, 2000
     logits, draft, codes, u = data(B, K, V)
