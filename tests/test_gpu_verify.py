@@ -237,6 +237,24 @@ def test_graph_streams_repeat_and_empty():
     del graph
 
 
+@pytest.mark.parametrize("B,K,V", [(1, 1, 9), (5, 63, 40), (7, 3, 40000)])
+def test_workspace_and_surroundings(B, K, V):
+    """A workspace of just the size that is asked for, whatever lies in it; nothing beside it and the outputs is written."""
+    logits, draft, codes, u = data(B, K, V)
+    want = hwp.verify_codes(logits, codes, u, draft)
+    need = hwp.verify_codes_workspace_size(B, K, V)
+    for fill in (0, 255):
+        ws = torch.full((need + 32,), fill, dtype=torch.uint8, device="cuda")
+        out = torch.full((B + 2, K + 1), -7, dtype=torch.int32, device="cuda")
+        accepted = torch.full((B + 2,), -7, dtype=torch.int32, device="cuda")
+        hwp.tok_verify_codes(logits, codes, u, out[1:-1], accepted[1:-1], draft, workspace=ws[16: 16 + need])
+        assert torch.equal(out[1:-1], want[0]) and torch.equal(accepted[1:-1], want[1])
+        assert bool((ws[:16] == fill).all()) and bool((ws[16 + need:] == fill).all())
+        assert all(bool((x[i] == -7).all()) for x in (out, accepted) for i in (0, -1))
+    with pytest.raises(hwp.TokError):
+        hwp.tok_verify_codes(logits, codes, u, *want, draft, workspace=ws[16: 16 + need - 1])
+
+
 def test_follows_sample_codes_without_drafts():
     """K = 0 is a plain draw: sample_codes' without filters."""
     logits, _, codes, u = data(20, 0, 64000)
