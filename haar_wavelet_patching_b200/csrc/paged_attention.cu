@@ -57,6 +57,7 @@ struct PagedArgs {
     int64_t table_row;
     int B, Nq, Hq, Hkv, G, D, rows, tiles, units, P, tokens; // rows of a unit; row tiles; units of a stream; tokens of a table row
     FastDiv page, group;
+    int none;         // the page of copies that bring zeros (PoolMap)
     int box_rows;     // rows of a tensor copy
     int kh, vh;       // coordinate factors: 0 for broadcast heads
     // Small boxes: rows of any places, four to a copy, of a map in which page, token and head are one coordinate.
@@ -355,11 +356,11 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         const CUtensorMap *map = kv ? &vmap : &kmap;
         const uint64_t policy = evict_first();
         const int factor = kv ? a.vh : a.kh, boxes = kRound / a.box_rows;
-        auto look_up = [&](const Place &p, int box, int &row) { // page and row; the pool's end (zeros) where there is none
+        auto look_up = [&](const Place &p, int box, int &row) { // page and row; a.none (zeros) where there is none
             const int key = p.round * kRound + box * a.box_rows;
             row = 0;
             if (box >= boxes || key >= p.len)
-                return a.P;
+                return a.none;
             const uint32_t page = a.page.div((uint32_t)key);
             row = (int)(key - page * a.page.d);
             return a.table[p.b * a.table_row + page];
@@ -428,7 +429,7 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 for (int box = lane; box < boxes; box += 32) {
                     if (box >= 32)
                         page0 = look_up(now, box, row0);
-                    const int p = (uint32_t)page0 < (uint32_t)a.P ? page0 : a.P;
+                    const int p = (uint32_t)page0 < (uint32_t)a.P ? page0 : a.none;
 #pragma unroll
                     for (int sub = 0; sub < kSubs; ++sub)
                         tma_load_4d_once(dst + sub * S::sub + box * a.box_rows * 128, map, 64 * sub, row0, head, p, bar, policy);
@@ -985,16 +986,13 @@ tok_status launch_rows(const CUtensorMap &k, const CUtensorMap &v, const PagedAr
                           : launch<DP, 64>(k, v, a, stream);
 }
 
-// Tensor map of a pool with boxes of 64 channels x `rows` tokens.  Broadcast heads become an extent of 1 (their
-// coordinate factor is 0); without pages every copy lies behind the one page of the map.
+// Tensor map of a pool with boxes of 64 channels x `rows` tokens; `any`: an address with a row of channels, for a pool without pages.
 bool pages_map(CUtensorMap *map, const PagesView &x, const void *any, int64_t P, int64_t page_size, int64_t H, int64_t D,
                int rows)
 {
-    auto str = [](int64_t n, int64_t s) { return (uint64_t)(n > 1 && s != 0 ? s * 2 : 16); };
-    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)page_size, (uint64_t)(x.h == 0 ? 1 : H), (uint64_t)std::max<int64_t>(P, 1)};
-    const uint64_t strides[3] = {str(page_size, x.t), str(H, x.h), str(P, x.pg)};
+    const PoolMap m = pool_map(x, P, page_size, H, D);
     const uint32_t box[4] = {64, (uint32_t)rows, 1, 1};
-    return encode_tensor_map_sw128(map, 4, P > 0 ? x.p : any, dims, strides, box);
+    return encode_tensor_map_sw128(map, 4, P > 0 ? x.p : any, m.dims, m.strides, box);
 }
 
 constexpr int64_t kIntMax = ((int64_t)1 << 31) - 1;
@@ -1126,6 +1124,7 @@ extern "C" tok_status tok_paged_attention(const tok_heads *q, const tok_pages *k
     a.tiles = (int)dim.tiles();
     a.units = (int)dim.units();
     a.P = (int)P;
+    a.none = pool_map(a.k, P, page_size, Hkv, D).none; // (the same for both pools)
     a.tokens = (int)tokens;
     a.page = FastDiv((uint32_t)page_size);
     a.group = FastDiv((uint32_t)a.G);

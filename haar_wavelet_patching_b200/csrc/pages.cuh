@@ -19,6 +19,25 @@ inline PagesView view(const tok_pages *t)
     return PagesView{static_cast<__nv_bfloat16 *>(t->ptr), t->page, t->token, t->head};
 }
 
+// A pool as the map of the tensor copies has it, innermost first: extents of channels, tokens, heads and pages, byte strides
+// of the last three.  Broadcast heads become an extent of 1 (their coordinate factor is 0).  Page `none` lies behind the map's
+// last one, so that a copy of it brings zeros and reads nothing.  A pool without pages has no element to point at: its map is
+// one row of channels (of the queries), and every copy is one of `none`.
+struct PoolMap {
+    uint64_t dims[4], strides[3];
+    int none;
+};
+
+inline PoolMap pool_map(const PagesView &x, int64_t P, int64_t page_size, int64_t H, int64_t D)
+{
+    if (P <= 0)
+        return PoolMap{{(uint64_t)D, 1, 1, 1}, {16, 16, 16}, 1};
+    auto str = [](int64_t n, int64_t s) { return (uint64_t)(n > 1 && s != 0 ? s * 2 : 16); };
+    return PoolMap{{(uint64_t)D, (uint64_t)page_size, (uint64_t)(x.h == 0 ? 1 : H), (uint64_t)P},
+                   {str(page_size, x.t), str(H, x.h), str(P, x.pg)},
+                   (int)P};
+}
+
 // Host: argument rules.
 struct PoolView {
     const tok_pages *t;
