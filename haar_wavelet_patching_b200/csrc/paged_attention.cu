@@ -895,7 +895,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedArgs a)
     const int head = (int)(at - bq * a.Hq), b = (int)(bq / a.Nq), iq = (int)(bq - (int64_t)b * a.Nq);
     const int hk = head / a.G, row = iq * a.G + head % a.G;
     const int2 span = a.spans[(int64_t)b * a.units + hk * a.tiles + row / a.rows];
-    if (span.x < 0)
+    if (!span_joins(span.x, span.y, kCtas))
         return;
     const int n = span.y - span.x + 1, r = row % a.rows;
     auto place = [&](int i) { return ((int64_t)(span.x + i) * 2 + (i == 0)) * a.rows + r; }; // (the first begins it)

@@ -38,6 +38,14 @@ inline PoolMap pool_map(const PagesView &x, int64_t P, int64_t page_size, int64_
                    (int)P};
 }
 
+// Whether the CTAs first .. last have written partial results of a unit that are to be joined.  (A CTA that has a unit whole leaves
+// a negative number.  Where a wait has run out, units that were not reached have whatever the workspace held, which
+// must not be followed: the call has failed, and the join's loads and loops stay within the CTAs' places.)
+__host__ __device__ constexpr bool span_joins(int first, int last, int ctas)
+{
+    return first >= 0 && first <= last && last < ctas;
+}
+
 // Host: argument rules.
 struct PoolView {
     const tok_pages *t;

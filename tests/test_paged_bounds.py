@@ -28,6 +28,17 @@ int main(int argc, char **argv)
 }
 """
 
+SPANS = r"""
+#include <stdio.h>
+#include <stdlib.h>
+#include "pages.cuh"
+int main(int argc, char **argv)
+{
+    for (int i = 2; i + 1 < argc; i += 2)
+        printf("%d ", (int)tok::span_joins(atoi(argv[i]), atoi(argv[i + 1]), atoi(argv[1])));
+}
+"""
+
 
 def program(folder, text):
     """The compiled program as a function of its arguments: the numbers that it prints."""
@@ -59,3 +70,11 @@ def test_copies_of_no_page_lie_behind_the_map(pool_map, P, page, H, D, order):
     has = 2 * ((P - 1) * stride + (page - 1) * token + (H - 1) * head + D) if P else 2 * D
     assert dims[0] == D and all(d >= 1 for d in dims) and reach == has
     assert all(s % 16 == 0 and s >= 16 for s in strides)
+
+
+def test_spans_that_no_cta_has_written_are_not_followed(tmp_path):
+    """After a wait that ran out a unit's span is what the workspace held: never a place behind the CTAs', never a long loop."""
+    ctas, low, high = 148, -2 ** 31, 2 ** 31 - 1
+    spans = [(a, b) for a in (low, -1, 0, 5, 147, 148, high) for b in (low, -1, 0, 5, 147, 148, high)]
+    got = program(tmp_path, SPANS)(ctas, *(v for s in spans for v in s))
+    assert [bool(g) for g in got] == [0 <= a <= b < ctas for a, b in spans]
