@@ -267,6 +267,8 @@ bool tables_ok(int64_t B, int64_t N, int64_t M, int64_t F, int64_t page_size, in
            (B <= 1 || (table_row >= M && table_row < ((int64_t)1 << 38) / B));
 }
 
+int64_t table_bytes(int64_t B, int64_t M, int64_t table_row) { return B > 0 ? 4 * ((B - 1) * table_row + M) : 0; }
+
 // Whether any of the arrays that are written meets another one (an in-place pair is passed once).
 struct Range {
     const void *p;
@@ -294,10 +296,10 @@ extern "C" tok_status tok_page_tables(const int32_t *lens, const int32_t *fresh,
     using namespace tok;
     if (!tables_ok(B, N, M, F, page_size, table_row))
         return TOK_ERR_SHAPE;
-    if (B == 0)
+    if (B == 0 && (!free_count || !free_out))
         return TOK_OK;
-    if (!lens || !held || !free_count || !held_out || !free_out || (F > 0 && !pages) || (M > 0 && !table) ||
-        (N > 0 && !slots))
+    if (!free_count || !free_out ||
+        (B > 0 && (!lens || !held || !held_out || (F > 0 && !pages) || (M > 0 && !table) || (N > 0 && !slots))))
         return TOK_ERR_NULL;
     for (const void *p : {(const void *)lens, (const void *)fresh, (const void *)held, (const void *)free_count,
                           (const void *)pages, (const void *)table, (const void *)slots, (const void *)held_out,
@@ -306,7 +308,7 @@ extern "C" tok_status tok_page_tables(const int32_t *lens, const int32_t *fresh,
             return TOK_ERR_ALIGN;
     if (any_meet({{lens, 4 * B, false}, {fresh, 4 * B, false}, {held == held_out ? nullptr : held, 4 * B, false},
                   {free_count == free_out ? nullptr : free_count, 4, false}, {pages, 4 * F, false},
-                  {table, 4 * ((B - 1) * table_row + M), true}, {slots, 4 * B * N, true}, {held_out, 4 * B, true},
+                  {table, table_bytes(B, M, table_row), true}, {slots, 4 * B * N, true}, {held_out, 4 * B, true},
                   {free_out, 4, true}, {bad_count, 4, true}}))
         return TOK_ERR_ALIAS;
     TablesArgs g{};
@@ -357,9 +359,10 @@ extern "C" tok_status tok_page_release(const int32_t *lens, const int32_t *held,
     using namespace tok;
     if (!tables_ok(B, 0, M, F, page_size, table_row))
         return TOK_ERR_SHAPE;
-    if (B == 0)
+    if (B == 0 && (!free_count || !free_out))
         return TOK_OK;
-    if (!lens || !held || !free_count || !held_out || !free_out || (F > 0 && !pages) || (M > 0 && !table))
+    if (!free_count || !free_out ||
+        (B > 0 && (!lens || !held || !held_out || (F > 0 && !pages) || (M > 0 && !table))))
         return TOK_ERR_NULL;
     for (const void *p : {(const void *)lens, (const void *)held, (const void *)free_count, (const void *)pages,
                           (const void *)table, (const void *)held_out, (const void *)free_out,
@@ -368,7 +371,7 @@ extern "C" tok_status tok_page_release(const int32_t *lens, const int32_t *held,
             return TOK_ERR_ALIGN;
     if (any_meet({{lens, 4 * B, false}, {held == held_out ? nullptr : held, 4 * B, false},
                   {free_count == free_out ? nullptr : free_count, 4, false}, {pages, 4 * F, true},
-                  {table, 4 * ((B - 1) * table_row + M), true}, {held_out, 4 * B, true}, {free_out, 4, true},
+                  {table, table_bytes(B, M, table_row), true}, {held_out, 4 * B, true}, {free_out, 4, true},
                   {bad_count, 4, true}}))
         return TOK_ERR_ALIAS;
     TablesArgs g{};

@@ -633,7 +633,7 @@ TOK_API tok_status tok_embed_codes_backward(const int32_t *codes, const void *gr
  * tok_page_release -- the pages that lens[b] tokens (negative: 0) do not need go back to the list, so that taking
  *   them anew gives each stream the same ones; their table entries become -1.  A list without room for all of them
  *   (F) stays as it is, as does everything else, and bad_count gets 1.
- * free_count is clamped to [0, F], held to [0, M].
+ * free_count is clamped to [0, F], held to [0, M]; so are free_out (written for B = 0, too, where both counts are given) and held_out.
  * Shape rule: 0 <= B <= 65535, 0 <= N, M, F < 2^31, page_size >= 1, M * page_size < 2^31, B * N, B * M < 2^31; table
  * rows table_row >= M elements apart, below 2^38 / B.
  */

@@ -227,3 +227,21 @@ def test_write_far_behind_2_31_elements():
     o = hwp.paged_attention(q, pool, v_pool, table, dev([page]))
     near = hwp.paged_attention(q, pool[P - 1:].clone(), v_pool[P - 1:].clone(), dev([[0]]), dev([page]))
     assert torch.equal(o, near)
+
+
+@pytest.mark.parametrize("free,F", [(7, 9), (12, 9), (-3, 9), (0, 0)])
+def test_without_streams_the_count_is_still_written(free, F):
+    """B = 0: nothing is taken or given back, and free_out gets the count, in place or into another tensor."""
+    none, table, pages = dev([]), torch.empty(0, 5, dtype=I32, device="cuda"), dev(range(F))
+    want = min(max(free, 0), F)
+    for in_place in (False, True):
+        f = dev([free])
+        fo = f if in_place else dev([99])
+        slots = torch.empty(0, 3, dtype=I32, device="cuda")
+        hwp.tok_page_tables(none, None, none, f, pages, table, slots, none, fo, 4)
+        assert fo.item() == want
+        f = dev([free])
+        fo = f if in_place else dev([99])
+        hwp.tok_page_release(none, none, f, pages, table, none, fo, 4)
+        assert fo.item() == want and (in_place or f.item() == free)
+        assert pages.tolist() == list(range(F))
