@@ -25,6 +25,8 @@
 // Measured, bf16: 4 streams x 56,320 keys, 8 key heads x 128: 146 us (923 MB, 6.3 TB/s); 16 streams of up to 3520 keys, in pages of
 // 16, 31 us (floor 18.8), of which about 6 are the launch, the shares and the first copies, and 5 the join; drafts of 5 to a stream
 // on pages of 24: 22.5 us, the same chain.
+// With more than 32 rows of a key head the softmax warps' instructions bound it (64 rows of a key to a thread): 4 x 56,320 keys,
+// 36 rows, 128 channels 326 us (298 with weights rounded once, which are off by up to 2^-9), 64 channels 302 (268).
 #include <algorithm>
 #include <numeric>
 
@@ -174,13 +176,20 @@ template <int DP, int N> struct Smem {
     static constexpr int tile = DP / 64 * sub;   // keys or values of a round
     static constexpr int q = DP / 64 * N * 128;  // a unit's queries
     // Columns of the second product: the weights rounded to bf16, as the values are, and behind them what that has left, so that
-    // the output's rounding alone counts.  With 64 rows there is no room: a weight is off by up to 2^-9.
-    static constexpr int wide = N == 64 ? N : 2 * N;
-    static constexpr int p = kRound * 2 * wide;  // a round's weights
+    // the output's rounding alone counts.  A key's are a line of shared memory; with 64 rows they are two, as a line of the swizzle
+    // has 128 bytes, in tiles of their own: first the weights' two (of rounds in turn), then the rests', of which there is one where
+    // the room is short: it is written once the product before has read it.
+    static constexpr int wide = 2 * N;
+    static constexpr bool split = N == 64;
+    static constexpr int line = split ? 2 * N : 2 * wide, p = kRound * line; // a round's weights
+    static constexpr int rests = !split ? 0 : DP == 64 ? 2 : 1;
     static constexpr int units = N == 64 ? 2 : N == 16 && DP == 128 ? 3 : 4; // whose queries may be there
     static constexpr int ring = DP == 64 ? (N == 16 ? 6 : N == 32 ? 5 : 4) : N == 16 ? 3 : 2;
     static constexpr int at_q = 2 * ring * tile, at_p = at_q + units * q;
-    static constexpr int bytes = at_p + 2 * p + 1024;
+    static constexpr int bytes = at_p + (2 + rests) * p + 1024;
+    // From at_p on, of round j: its weights, its rests.
+    static __device__ __forceinline__ int weights(int j) { return (j & 1) * p; }
+    static __device__ __forceinline__ int rest(int j) { return (rests == 2 ? 2 + (j & 1) : 2) * p; }
     static_assert(bytes <= 227 * 1024 - 4096, "4 KB are for the static part");
 };
 
@@ -196,7 +205,7 @@ struct Shares {
     }
 };
 
-// Shared-memory descriptor of the weights, [key][N columns]: a key's are a line of the 32-, 64- or 128-byte swizzle (16-byte
+// Shared-memory descriptor of weights and rests side by side, [key][N columns]: a key's are a line of the 32-, 64- or 128-byte swizzle (16-byte
 // piece i of line k is kept at i ^ (k * 2 N / 128 % (N / 8))), 8 lines an atom.  Fields as in sw128_desc_mn.
 template <int N> __device__ __forceinline__ uint64_t weights_desc(uint32_t saddr)
 {
@@ -500,7 +509,7 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         if (lane == 0) {
             const uint32_t idesc_s = idesc_bf16_f32(kRound, N), idesc_o = idesc_bf16_f32(DP, S::wide) | kATransposed | kBTransposed;
             const uint64_t kdesc = sw128_desc(base), qdesc = sw128_desc(base + S::at_q);
-            const uint64_t vdesc = sw128_desc_mn(base + NB * S::tile, S::sub), pdesc = weights_desc<S::wide>(base + S::at_p);
+            const uint64_t vdesc = sw128_desc_mn(base + NB * S::tile, S::sub);
             bool ok = true;
             Place next = now; // of the round whose scores come next
             uint32_t u = 0;
@@ -538,10 +547,16 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 if (!ok)
                     break;
                 tc_fence_after();
+                const uint32_t weights = base + S::at_p + S::weights(j);
+                uint64_t pdesc;
+                if constexpr (S::split)
+                    pdesc = sw128_desc_mn(weights, S::rest(j) - S::weights(j));
+                else
+                    pdesc = weights_desc<S::wide>(weights);
 #pragma unroll
                 for (int k = 0; k < kRound / 16; ++k) // (leaving out steps of 16 keys behind the last one cost 10% of a long call)
                     umma_bf16(o_col, vdesc + ((slot * S::tile + k * 2048) >> 4),
-                              pdesc + (((j & 1) * S::p + k * (16 * 2 * S::wide)) >> 4), idesc_o, !fresh || k > 0);
+                              pdesc + (k * (16 * S::line) >> 4), idesc_o, !fresh || k > 0);
                 umma_commit(smem_addr(&empty[1][slot]));
                 umma_commit(smem_addr(&pfree[j & 1]));
                 fresh = last;
@@ -557,8 +572,8 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         const uint32_t lanes = (uint32_t)(32 * warp) << 16;
         constexpr bool kHold = N == 16; // a key's scores and what they are relative to stay in registers
         float l[N] = {}, m[kHold ? N : 1];
-        const uint32_t pbase = base + S::at_p + tid * (2 * S::wide);
-        const int mix = tid * 2 * S::wide / 128 % (S::wide / 8);
+        const uint32_t pbase = base + S::at_p + tid * S::line;
+        const int mix = tid * S::line / 128 % (S::line / 16);
         float *side = a.side + (int64_t)cta * 64 * N;
         bool ok = true, fresh = true, whole = false;
         int all = 0;    // keys that all rows see
@@ -698,7 +713,10 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                 if constexpr (kHold)
                     load(0, false);
             }
-            if (j >= 2)
+            if constexpr (S::rests == 1) { // (the products end in order)
+                if (j >= 1)
+                    wait(pfree[(j - 1) & 1], (uint32_t)((j - 1) >> 1));
+            } else if (j >= 2)
                 wait(pfree[j & 1], (uint32_t)((j - 2) >> 1));
             // Values behind the stream's last token are nobody's and meet weights of 0: zeros in their place.  A value that some
             // rows see and others do not also meets such weights: where it is no finite number, its row is taken out, and what
@@ -751,23 +769,23 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                         side[(key - all) * N + 16 * c + r] = s[r] + s_m[buf][16 * c + r];
                 }
                 __syncwarp();
-                constexpr int kParts = S::wide / N;
-                uint32_t w[kParts * 8];
+                uint32_t w[16]; // weights, then rests
 #pragma unroll
                 for (int r = 0; r < 16; r += 2) {
                     const float e0 = exp2_fast(s[r]), e1 = exp2_fast(s[r + 1]);
                     l[16 * c + r] += e0;
                     l[16 * c + r + 1] += e1;
                     w[r / 2] = pack_bf16x2(e0, e1);
-                    if constexpr (kParts == 2)
-                        w[8 + r / 2] = pack_bf16x2(e0 - bf16_lo(w[r / 2]), e1 - bf16_hi(w[r / 2]));
+                    w[8 + r / 2] = pack_bf16x2(e0 - bf16_lo(w[r / 2]), e1 - bf16_hi(w[r / 2]));
                 }
 #pragma unroll
-                for (int i = 0; i < 2 * kParts; ++i)
+                for (int i = 0; i < 4; ++i) {
+                    const int piece = (S::split ? 0 : i / 2 * (N / 8)) + 2 * c + i % 2; // of the key's line
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     pbase + (j & 1) * S::p + (((i / 2 * (N / 8) + 2 * c + i % 2) ^ mix) << 4)),
+                                     pbase + (S::split && i >= 2 ? S::rest(j) : S::weights(j)) + ((piece ^ mix) << 4)),
                                  "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
                                  : "memory");
+                }
             }
             tc_fence_before();
             fence_proxy_async_smem();
@@ -821,16 +839,13 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
 #pragma unroll 1
             for (int c = 0; 16 * c < live_rows; ++c) {
                 float o[16];
+                float rest[16];
                 tmem_ld16(o_col + lanes + 16 * c, o);
-                if constexpr (S::wide > N) {
-                    float rest[16];
-                    tmem_ld16(o_col + lanes + N + 16 * c, rest);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        o[r] += fabsf(o[r]) < INFINITY ? rest[r] : 0.0f; // (of an infinite value the rest is no number)
-                }
+                tmem_ld16(o_col + lanes + N + 16 * c, rest);
                 tmem_wait_ld();
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    o[r] += fabsf(o[r]) < INFINITY ? rest[r] : 0.0f; // (of an infinite value the rest is no number)
                 if (__builtin_expect(odds && live, 0)) {
                     for (unsigned long long left = odds; left; left &= left - 1) {
                         const int at = __ffsll((long long)left) - 1, k = all + at;

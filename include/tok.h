@@ -676,9 +676,8 @@ TOK_API tok_status tok_paged_write(const tok_heads *k, const tok_heads *v, const
  * (NULL: Nq; clamped to [0, Nq]), is token k_lens[b] - q_lens[b] + i and sees the tokens up to itself. The keys and values
  * that it does not see show nowhere in its result, NaN included.  A query without a token (i >= q_lens[b], or
  * a token before the first) has o = 0 and lse = -inf.  Formulas, head groups and the values that are not numbers are
- * tok_cross_attention's; so are the rules for q and o.  Weights enter their product within 2^-17 of their fp32 values (with more
- * than 32 query rows of a key head, Nq * Hq / Hkv, rounded to bf16), sums and scores are fp32.  A query that sees a token whose entry of the table is outside
- * [0, P) has NaN in both.
+ * tok_cross_attention's; so are the rules for q and o.  Weights enter their product within 2^-17 of their fp32 values, sums and
+ * scores are fp32.  A query that sees a token whose entry of the table is outside [0, P) has NaN in both.
  * lse [B, Hq, Nq] fp32 or NULL.  workspace: 16-byte-aligned device memory of
  * tok_paged_attention_workspace_size() bytes, overwritten; calls that may overlap need one each.
  * Results do not depend on the device's timing (every sum has a fixed order).
