@@ -365,3 +365,34 @@ def test_equals_cross_attention_without_pages():
     for o in (hwp.cross_attention(q, k, v, lens),
               hwp.paged_attention(q, k.view(-1, page, Hkv, D), v.view(-1, page, Hkv, D), table, lens)):
         check(o, want[0], want[1], "o")
+
+
+@pytest.mark.parametrize("n", [100, 20000])
+@pytest.mark.parametrize("entry", [-1, 10 ** 6, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("Nq,Hq,page", [(3, 4, 16), (1, 2, 1), (20, 8, 24)])
+def test_an_entry_outside_the_pool_reaches_no_other_stream(n, entry, Nq, Hq, page):
+    """The other streams' outputs and lse are finite and have the bits that they have without it."""
+    lens = [300, n, 40]
+    kp, vp, table = cache(lens, page, 2, 64)
+    q = randn(3, Nq, Hq, 64, seed=2)
+    fine, fine_lse = hwp.paged_attention(q, kp, vp, table, dev(lens), with_lse=True)
+    assert bool(fine.isfinite().all()) and bool(fine_lse.isfinite().all())
+    table[1, n // 2 // page] = entry
+    o, lse = hwp.paged_attention(q, kp, vp, table, dev(lens), with_lse=True)
+    assert bool(o[1].isnan().all()) and bool(lse[1].isnan().all())
+    for b in (0, 2):
+        assert torch.equal(o[b], fine[b]) and torch.equal(lse[b], fine_lse[b])
+
+
+@pytest.mark.parametrize("Nq,Hq", [(1, 2), (64, 4)])
+@pytest.mark.parametrize("page,D", [(1, 64), (16, 64), (24, 128), (64, 128)])
+def test_an_empty_pool(page, Nq, Hq, D):
+    """No page: a query that would see a token is NaN, the others are 0, whatever the pool's strides and its null address."""
+    kp = torch.empty(0, page, 2, D, dtype=torch.bfloat16, device="cuda")
+    q = randn(3, Nq, Hq, D)
+    lens = [0, 2 * page, 3]
+    o, lse = hwp.paged_attention(q, kp, kp, dev([[0, -1, 5]] * 3), dev(lens), with_lse=True)
+    for b, n in enumerate(lens):
+        see = torch.arange(Nq, device="cuda") + n - Nq >= 0
+        assert bool(o[b, see].isnan().all()) and bool(lse[b, :, see].isnan().all())
+        assert bool((o[b, ~see] == 0).all()) and bool((lse[b, :, ~see] == -INF).all())
