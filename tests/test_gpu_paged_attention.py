@@ -396,3 +396,24 @@ def test_an_empty_pool(page, Nq, Hq, D):
         see = torch.arange(Nq, device="cuda") + n - Nq >= 0
         assert bool(o[b, see].isnan().all()) and bool(lse[b, :, see].isnan().all())
         assert bool((o[b, ~see] == 0).all()) and bool((lse[b, :, ~see] == -INF).all())
+
+
+@pytest.mark.parametrize("Nq,Hq", [(1, 2), (5, 8), (20, 8)])
+@pytest.mark.parametrize("D", [64, 96])
+@pytest.mark.parametrize("n,at", [(40, 0), (40, 19), (3000, 2000), (20000, 0), (20000, 15000)])
+def test_infinite_scores(Nq, Hq, D, n, at):
+    """A key of infinity: queries with a positive channel there have NaN in both, those with a negative one do not count it."""
+    page = 16
+    kp, vp, table = cache([n], page, 1, D)
+    q = randn(1, Nq, Hq, D, seed=2)
+    q[..., 0] = q[..., 0].abs() + 1
+    q[:, :, 1::2, 0] *= -1
+    kp[int(table[0, at // page]), at % page, 0, 0] = INF
+    o, lse = hwp.paged_attention(q, kp, vp, table, dev([n]), with_lse=True)
+    assert bool(o[:, :, ::2].isnan().all()) and bool(lse[:, ::2].isnan().all())
+    # The tokens but that one, as a cache of their own: the last queries' positions are the same.
+    rest = torch.tensor([t for t in range(n) if t != at], device="cuda")
+    where = table[0, rest // page].long(), rest % page
+    want = reference(q, kp[where][None], vp[where][None], dev([[0]]), [n - 1])
+    check(o[:, :, 1::2], want[0][:, :, 1::2], want[1][:, :, 1::2], "o")
+    check(lse[:, 1::2], want[2][:, 1::2], want[3][:, 1::2], "lse")
