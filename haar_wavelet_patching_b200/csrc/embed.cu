@@ -7,8 +7,8 @@
 // every row of g read once, so it is bound by HBM as well, if no row is added to twice: the tokens are sorted by
 // code, stable, so the order of a sum is that of the tokens and no atomics are needed.
 //
-//   sort_kernel: one cluster sorts (code, token) pairs by digits of 8 or 10 bits, a slice of the
-//   pairs to a CTA and a contiguous part of it to a warp.  Each pass counts digits per warp, adds the counts up over warps, CTAs and
+//   sort_kernel: one cluster sorts (code, token) pairs by digits of 8 or 10 bits, a slice of the pairs to a CTA and a
+//   contiguous part of it to a warp.  Each pass counts digits per warp, adds the counts up over warps, CTAs and
 //   digits, and moves each pair to its place.  (2 passes up to 2^20 codes.)
 //
 //   sum_kernel: the table's row ends and the tokens, merged in the order of codes, are one sequence of V + N
@@ -16,9 +16,9 @@
 //   codes' frequencies.  Where a border cuts a row with fewer than kAbsorb tokens behind it, the
 //   group before takes these too; else both store partial sums (fp32), and join_kernel adds them up.
 //
-// Measured, 56,320 tokens, a table of 64,000 x 2048 bf16: forward 60 us (461 MB of rows in and out), gradient 113 us: sorting
-// 20, sums 77 (493 MB, 6.4 TB/s), joining and the launches' gaps 16.  10,395 tokens, 64,000 x 1004 fp32, both: 83 us, of
-// which the sort's chain of barriers counts for more.  80 tokens, forward: 1.7 us, the launch.
+// Measured, 56,320 tokens, a table of 64,000 x 2048 bf16: forward 60 us (461 MB of rows in and out), gradient 113 us:
+// sorting 20, sums 77 (493 MB, 6.4 TB/s), joining and the launches' gaps 16.  10,395 tokens, 64,000 x 1004 fp32,
+// both: 83 us, of which the sort's chain of barriers counts for more.  80 tokens, forward: 1.7 us, the launch.
 #include <algorithm>
 #include <utility>
 
@@ -313,12 +313,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs g,
             for (int n = 0; n < kAlone && lo < end; ++n)
                 border(lo++, i, kp, rem);
             __syncwarp();
-            // More between two tokens (of few ones in a large table): all lanes (1 token, 64,000 x 512: 37 -> 22 us; with 4 borders
-            // to a lane 110 tokens took 34 us for 33).
+            // More between two tokens (of few ones in a large table): all lanes (1 token, 64,000 x 512: 37 -> 22 us;
+            // with 4 borders to a lane 110 tokens took 34 us for 33).
             for (uint32_t many = __ballot_sync(~0u, lo < end); many; many &= many - 1) {
                 const int from = __ffs(many) - 1;
                 const uint32_t c0 = __shfl_sync(~0u, lo, from), c1 = __shfl_sync(~0u, end, from);
-                const uint32_t fi = __shfl_sync(~0u, i, from), fk = __shfl_sync(~0u, kp, from), fr = __shfl_sync(~0u, rem, from);
+                const uint32_t fi = __shfl_sync(~0u, i, from), fk = __shfl_sync(~0u, kp, from);
+                const uint32_t fr = __shfl_sync(~0u, rem, from);
                 for (uint32_t c = c0 + lane; c < c1; c += 32)
                     border(c, fi, fk, fr);
             }

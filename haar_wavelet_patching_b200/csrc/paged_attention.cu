@@ -1,32 +1,33 @@
 // Attention of a few new tokens of each stream over its keys and values in pages.
 //
-// The call is bound by reading the keys and values once.  Up to 64 query rows (queries x the heads of a group) of one key
-// head are a unit; its keys come in rounds of 128.  Streams differ in length, so the rounds of all units of all
-// streams, in order, are one sequence, which the SMs' CTAs share out in equal contiguous parts.  A CTA that
-// has a unit whole writes its result; of a unit that several CTAs have parts of, partial results (fp32) go to the
+// The call is bound by reading the keys and values once.  Up to 64 query rows (queries x the heads of a group) of one
+// key head are a unit; its keys come in rounds of 128.  Streams differ in length, so the rounds of all units of all
+// streams, in order, are one sequence, which the SMs' CTAs share out in equal contiguous parts.  A CTA that has a
+// unit whole writes its result; of a unit that several CTAs have parts of, partial results (fp32) go to the
 // workspace, at most two per CTA, and paged_join_kernel, launched early, adds them up in order.
 //
 // There are few query rows and many keys, so the products are taken transposed, with the 128 rows of the tensor
 // cores' tiles for keys and for channels: scores^T = K Q^T (128 keys x N queries), then o^T += V^T P^T
-// (channels x 2 N, the weights and what their rounding has left; one column more or less is no time), and no thread touches a
-// key or a value.  A CTA's warps:
-//   warps 0-3  softmax, a key to a thread (its lane of tensor memory): scores -> weights, a bf16 number and another for
-//              the rest of each, into shared memory as the second product's operand.  Weights are relative to the score of
-//              the unit's first key, and to the largest one from where one exceeds it by more than 2^16 (every term carries
-//              the same factor, so the quotient is unchanged); a vote of the four warps each round says so.  Sums stay with
-//              the threads up to a unit's end: o / sum -> HBM;
-//   warps 4, 7 tensor copies of keys and of values into rings of 128-byte-swizzled tiles: boxes of as many rows as divide
-//              both a page and a round, or four rows of any places;
+// (channels x 2 N, the weights and what their rounding has left; one column more or less is no time), and no thread
+// touches a key or a value.  A CTA's warps:
+//   warps 0-3  softmax, a key to a thread (its lane of tensor memory): scores -> weights, a bf16 number and another
+//              for the rest of each, into shared memory as the second product's operand.  Weights are relative to the
+//              score of the unit's first key, and to the largest one from where one exceeds it by more than 2^16
+//              (every term carries the same factor, so the quotient is unchanged); a vote of the four warps each
+//              round says so.  Sums stay with the threads up to a unit's end: o / sum -> HBM;
+//   warps 4, 7 tensor copies of keys and of values into rings of 128-byte-swizzled tiles: boxes of as many rows as
+//              divide both a page and a round, or four rows of any places;
 //   warp 5     one thread issues the MMAs: the next round's scores before this round's second product;
 //   warp 6     copies of the units' queries and what their rows are, one unit ahead.
 // A round may read rows behind a stream's last token: their scores are masked and their values zeroed in shared memory.
 // All waits are bounded as in the convolutions.
 //
-// Measured, bf16: 4 streams x 56,320 keys, 8 key heads x 128: 146 us (923 MB, 6.3 TB/s); 16 streams of up to 3520 keys, in pages of
-// 16, 31 us (floor 18.8), of which about 6 are the launch, the shares and the first copies, and 5 the join; drafts of 5 to a stream
-// on pages of 24: 22.5 us, the same chain.
-// With more than 32 rows of a key head the softmax warps' instructions bound it (64 rows of a key to a thread): 4 x 56,320 keys,
-// 36 rows, 128 channels 326 us (298 with weights rounded once, which are off by up to 2^-9), 64 channels 302 (268).
+// Measured, bf16: 4 streams x 56,320 keys, 8 key heads x 128: 146 us (923 MB, 6.3 TB/s); 16 streams of up to 3520
+// keys, in pages of 16, 31 us (floor 18.8), of which about 6 are the launch, the shares and the first copies, and 5
+// the join; drafts of 5 to a stream on pages of 24: 22.5 us, the same chain.
+// With more than 32 rows of a key head the softmax warps' instructions bound it (64 rows of a key to a thread):
+// 4 x 56,320 keys, 36 rows, 128 channels 326 us (298 with weights rounded once, which are off by up to 2^-9),
+// 64 channels 302 (268).
 #include <algorithm>
 #include <numeric>
 
@@ -57,7 +58,8 @@ struct PagedArgs {
     float *side;   // [kCtas][64][rows]: scores of keys whose values are no numbers
     int2 *spans;   // [units]: first and last CTA of a unit, or (-1, .) of one that a CTA has whole
     int64_t table_row;
-    int B, Nq, Hq, Hkv, G, D, rows, tiles, units, P, tokens; // rows of a unit; row tiles; units of a stream; tokens of a table row
+    int B, Nq, Hq, Hkv, G, D;
+    int rows, tiles, units, P, tokens; // rows of a unit; row tiles; units of a stream; pages; tokens of a table row
     FastDiv page, group;
     int none;         // the page of copies that bring zeros (PoolMap)
     int box_rows;     // rows of a tensor copy
@@ -132,16 +134,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&r)[16])
 __device__ __forceinline__ void tma_load_4d_once(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
                                                  uint32_t bar, uint64_t policy)
 {
-    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
-                 "%4, %5}], [%6], %7;" ::"r"(dst),
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+                 "[%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
                  "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
                  : "memory");
 }
 __device__ __forceinline__ void tma_gather4_once(uint32_t dst, const CUtensorMap *map, int x, const int (&y)[4], uint32_t bar,
                                                  uint64_t policy)
 {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
-                 "{%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+    asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+                 "[%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
                  "l"((uint64_t)map), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar), "l"(policy)
                  : "memory");
 }
@@ -175,10 +177,11 @@ template <int DP, int N> struct Smem {
     static constexpr int sub = kRound * 128;     // 64 channels of a round's keys
     static constexpr int tile = DP / 64 * sub;   // keys or values of a round
     static constexpr int q = DP / 64 * N * 128;  // a unit's queries
-    // Columns of the second product: the weights rounded to bf16, as the values are, and behind them what that has left, so that
-    // the output's rounding alone counts.  A key's are a line of shared memory; with 64 rows they are two, as a line of the swizzle
-    // has 128 bytes, in tiles of their own: first the weights' two (of rounds in turn), then the rests', of which there is one where
-    // the room is short: it is written once the product before has read it.
+    // Columns of the second product: the weights rounded to bf16, as the values are, and behind them what that has
+    // left, so that the output's rounding alone counts.  A key's are a line of shared memory; with 64 rows they are
+    // two, as a line of the swizzle has 128 bytes, in tiles of their own: first the weights' two (of rounds in turn),
+    // then the rests', of which there is one where the room is short: it is written once the product before has read
+    // it.
     static constexpr int wide = 2 * N;
     static constexpr bool split = N == 64;
     static constexpr int line = split ? 2 * N : 2 * wide, p = kRound * line; // a round's weights
@@ -205,8 +208,9 @@ struct Shares {
     }
 };
 
-// Shared-memory descriptor of weights and rests side by side, [key][N columns]: a key's are a line of the 32-, 64- or 128-byte swizzle (16-byte
-// piece i of line k is kept at i ^ (k * 2 N / 128 % (N / 8))), 8 lines an atom.  Fields as in sw128_desc_mn.
+// Shared-memory descriptor of weights and rests side by side, [key][N columns]: a key's are a line of the 32-, 64- or
+// 128-byte swizzle (16-byte piece i of line k is kept at i ^ (k * 2 N / 128 % (N / 8))), 8 lines an atom.  Fields as
+// in sw128_desc_mn.
 template <int N> __device__ __forceinline__ uint64_t weights_desc(uint32_t saddr)
 {
     constexpr uint64_t layout = N == 16 ? 6 : N == 32 ? 4 : 2;
@@ -222,14 +226,15 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     constexpr int NB = S::ring, QB = S::units, kChunks = N / 16; // stages of keys, of values
     constexpr uint32_t kColumns = N == 16 ? 64 : N == 32 ? 128 : 256;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t full[2][NB], empty[2][NB], qfull[QB], qempty[QB], sfull[2], pfull[2], pfree[2], ofull, drain;
+    __shared__ __align__(8) uint64_t full[2][NB], empty[2][NB], qfull[QB], qempty[QB], sfull[2], pfull[2], pfree[2];
+    __shared__ __align__(8) uint64_t ofull, drain;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
     __shared__ uint32_t s_sum[kThreads / 32];
     __shared__ Place s_first;
     __shared__ uint32_t s_round[2]; // rounds before this CTA's part, and before its end
-    // Of a unit (those of the next ones are made meanwhile): rows' maxima, keys seen, places of the output; keys seen by all rows;
-    // which of the keys behind these have values that are no numbers.
+    // Of a unit (those of the next ones are made meanwhile): rows' maxima, keys seen, places of the output; keys seen
+    // by all rows; which of the keys behind these have values that are no numbers.
     __shared__ __align__(16) float s_m[QB][N];
     __shared__ int s_lim[QB][N];
     __shared__ __nv_bfloat16 *s_out[QB][N];
@@ -357,9 +362,9 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
     auto ends_unit = [&](const Place &p, int j) { return p.round + 1 == p.rounds || j + 1 == count; };
 
     if (warp == 4 || warp == 7) {
-        // ---- Keys (warp 4) and values (warp 7): a box to a lane, its page looked up two rounds ahead, or four rows to a lane, looked
-        // up one round ahead.  (Boxes behind the first 32 are looked up as they come: small ones, of pools whose strides have too little
-        // in common for the other form.) ----
+        // ---- Keys (warp 4) and values (warp 7): a box to a lane, its page looked up two rounds ahead, or four rows
+        // to a lane, looked up one round ahead.  (Boxes behind the first 32 are looked up as they come: small ones,
+        // of pools whose strides have too little in common for the other form.) ----
         constexpr int kSubs = DP / 64;
         const int kv = warp == 7;
         const CUtensorMap *map = kv ? &vmap : &kmap;
@@ -441,7 +446,8 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                     const int p = (uint32_t)page0 < (uint32_t)a.P ? page0 : a.none;
 #pragma unroll
                     for (int sub = 0; sub < kSubs; ++sub)
-                        tma_load_4d_once(dst + sub * S::sub + box * a.box_rows * 128, map, 64 * sub, row0, head, p, bar, policy);
+                        tma_load_4d_once(dst + sub * S::sub + box * a.box_rows * 128, map, 64 * sub, row0, head, p, bar,
+                                         policy);
                 }
                 __syncwarp();
                 if (j + 1 < count)
@@ -507,7 +513,8 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
         }
     } else if (warp == 5) {
         if (lane == 0) {
-            const uint32_t idesc_s = idesc_bf16_f32(kRound, N), idesc_o = idesc_bf16_f32(DP, S::wide) | kATransposed | kBTransposed;
+            const uint32_t idesc_s = idesc_bf16_f32(kRound, N);
+            const uint32_t idesc_o = idesc_bf16_f32(DP, S::wide) | kATransposed | kBTransposed;
             const uint64_t kdesc = sw128_desc(base), qdesc = sw128_desc(base + S::at_q);
             const uint64_t vdesc = sw128_desc_mn(base + NB * S::tile, S::sub);
             bool ok = true;
@@ -553,8 +560,9 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                     pdesc = sw128_desc_mn(weights, S::rest(j) - S::weights(j));
                 else
                     pdesc = weights_desc<S::wide>(weights);
+                // (Leaving out steps of 16 keys behind the last one cost 10% of a long call.)
 #pragma unroll
-                for (int k = 0; k < kRound / 16; ++k) // (leaving out steps of 16 keys behind the last one cost 10% of a long call)
+                for (int k = 0; k < kRound / 16; ++k)
                     umma_bf16(o_col, vdesc + ((slot * S::tile + k * 2048) >> 4),
                               pdesc + (k * (16 * S::line) >> 4), idesc_o, !fresh || k > 0);
                 umma_commit(smem_addr(&empty[1][slot]));
@@ -718,9 +726,9 @@ paged_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ C
                     wait(pfree[(j - 1) & 1], (uint32_t)((j - 1) >> 1));
             } else if (j >= 2)
                 wait(pfree[j & 1], (uint32_t)((j - 2) >> 1));
-            // Values behind the stream's last token are nobody's and meet weights of 0: zeros in their place.  A value that some
-            // rows see and others do not also meets such weights: where it is no finite number, its row is taken out, and what
-            // it adds to the rows that see it comes at the unit's end.
+            // Values behind the stream's last token are nobody's and meet weights of 0: zeros in their place.  A
+            // value that some rows see and others do not also meets such weights: where it is no finite number, its
+            // row is taken out, and what it adds to the rows that see it comes at the unit's end.
             bool odd = false;
             if (edge) {
                 constexpr int kPieces = DP / 8; // of a row; piece i of row k is kept at i ^ k within its 8
@@ -1001,7 +1009,8 @@ tok_status launch_rows(const CUtensorMap &k, const CUtensorMap &v, const PagedAr
                           : launch<DP, 64>(k, v, a, stream);
 }
 
-// Tensor map of a pool with boxes of 64 channels x `rows` tokens; `any`: an address with a row of channels, for a pool without pages.
+// Tensor map of a pool with boxes of 64 channels x `rows` tokens; `any`: an address with a row of channels, for a
+// pool without pages.
 bool pages_map(CUtensorMap *map, const PagesView &x, const void *any, int64_t P, int64_t page_size, int64_t H, int64_t D,
                int rows)
 {
@@ -1012,8 +1021,8 @@ bool pages_map(CUtensorMap *map, const PagesView &x, const void *any, int64_t P,
 
 constexpr int64_t kIntMax = ((int64_t)1 << 31) - 1;
 
-// Tensor map of a pool for copies of four rows: page, token and head as one coordinate, in units of what their strides have in
-// common; false (and no rows) where that is less than a row.
+// Tensor map of a pool for copies of four rows: page, token and head as one coordinate, in units of what their
+// strides have in common; false (and no rows) where that is less than a row.
 bool gather_map(CUtensorMap *map, PagedArgs::Gather *g, const PagesView &x, int64_t P, int64_t page_size, int64_t H, int64_t D)
 {
     const int64_t pg = P > 1 ? x.pg : 0, t = page_size > 1 ? x.t : 0, h = H > 1 ? x.h : 0;
@@ -1148,9 +1157,9 @@ extern "C" tok_status tok_paged_attention(const tok_heads *q, const tok_pages *k
     a.kh = Hkv > 1 && a.k.h == 0 ? 0 : 1;
     a.vh = Hkv > 1 && a.v.h == 0 ? 0 : 1;
     CUtensorMap km, vm;
-    // Boxes of 1 or 2 rows are bound by the copies' issue: four rows of any pages to a copy instead (4 streams of 9952 keys, 12 key
-    // heads x 96, pages of 1: 258 -> 92 us).  From 4 rows on boxes are no more copies and cost less: 83 us on pages of 4,
-    // 56 of 8, 48 of 16.
+    // Boxes of 1 or 2 rows are bound by the copies' issue: four rows of any pages to a copy instead (4 streams of
+    // 9952 keys, 12 key heads x 96, pages of 1: 258 -> 92 us).  From 4 rows on boxes are no more copies and cost
+    // less: 83 us on pages of 4, 56 of 8, 48 of 16.
     if (a.box_rows <= 2) {
         PagedArgs::Gather gk{}, gv{};
         if (gather_map(&km, &gk, a.k, P, page_size, Hkv, D) && gather_map(&vm, &gv, a.v, P, page_size, Hkv, D)) {

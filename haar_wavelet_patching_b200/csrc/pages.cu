@@ -1,13 +1,13 @@
 // Pages of a cache of keys and values: the streams' page tables and the new tokens' slots, pages given back,
 // and keys and values written into the pages.
 //
-// tables_kernel is one cluster: each CTA adds up what all streams need (one pass of scans over B numbers, so no CTA waits
-// for another), then the CTAs share the tokens' slots and the new pages.  Counts are
-// written behind a cluster barrier, as they may replace the ones that were read.  It is bound by latency: the launch, the
-// loads of the counts, a scan, the loads of table entries, the stores.  Measured: 16 streams of 5 tokens 4.8 us, 256 of 880 15.4 (eight
+// tables_kernel is one cluster: each CTA adds up what all streams need (one pass of scans over B numbers, so no CTA
+// waits for another), then the CTAs share the tokens' slots and the new pages.  Counts are written behind a cluster
+// barrier, as they may replace the ones that were read.  It is bound by latency: the launch, the loads of the counts,
+// a scan, the loads of table entries, the stores.  Measured: 16 streams of 5 tokens 4.8 us, 256 of 880 15.4 (eight
 // slots of a thread at a time, their loads together: 16.8).
-// write_kernel moves up to four pieces of 16 bytes per thread, bound by HBM: 28,160 tokens of 8 heads x 128, a quarter of them
-// with slots of -1, 28.7 us (173 MB, 6.0 TB/s); 16 streams of 5 tokens 2.2 us, the launch.
+// write_kernel moves up to four pieces of 16 bytes per thread, bound by HBM: 28,160 tokens of 8 heads x 128, a quarter
+// of them with slots of -1, 28.7 us (173 MB, 6.0 TB/s); 16 streams of 5 tokens 2.2 us, the launch.
 #include <algorithm>
 
 #include "pages.cuh"
@@ -262,8 +262,8 @@ bool tables_ok(int64_t B, int64_t N, int64_t M, int64_t F, int64_t page_size, in
 {
     int64_t p;
     return B >= 0 && B <= 65535 && N >= 0 && M >= 0 && F >= 0 && F <= kIntMax && page_size >= 1 &&
-           prod_ok({M, page_size}, &p) && p <= kIntMax && page_size <= kIntMax && prod_ok({B, N}, &p) && p <= kIntMax && N <= kIntMax &&
-           M <= kIntMax && prod_ok({B, M}, &p) && p <= kIntMax &&
+           page_size <= kIntMax && N <= kIntMax && M <= kIntMax && prod_ok({M, page_size}, &p) && p <= kIntMax &&
+           prod_ok({B, N}, &p) && p <= kIntMax && prod_ok({B, M}, &p) && p <= kIntMax &&
            (B <= 1 || (table_row >= M && table_row < ((int64_t)1 << 38) / B));
 }
 

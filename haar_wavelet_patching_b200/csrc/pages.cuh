@@ -19,10 +19,10 @@ inline PagesView view(const tok_pages *t)
     return PagesView{static_cast<__nv_bfloat16 *>(t->ptr), t->page, t->token, t->head};
 }
 
-// A pool as the map of the tensor copies has it, innermost first: extents of channels, tokens, heads and pages, byte strides
-// of the last three.  Broadcast heads become an extent of 1 (their coordinate factor is 0).  Page `none` lies behind the map's
-// last one, so that a copy of it brings zeros and reads nothing.  A pool without pages has no element to point at: its map is
-// one row of channels (of the queries), and every copy is one of `none`.
+// A pool as the map of the tensor copies has it, innermost first: extents of channels, tokens, heads and pages, byte
+// strides of the last three.  Broadcast heads become an extent of 1 (their coordinate factor is 0).  Page `none` lies
+// behind the map's last one, so that a copy of it brings zeros and reads nothing.  A pool without pages has no
+// element to point at: its map is one row of channels (of the queries), and every copy is one of `none`.
 struct PoolMap {
     uint64_t dims[4], strides[3];
     int none;
@@ -38,9 +38,10 @@ inline PoolMap pool_map(const PagesView &x, int64_t P, int64_t page_size, int64_
                    (int)P};
 }
 
-// Whether the CTAs first .. last have written partial results of a unit that are to be joined.  (A CTA that has a unit whole leaves
-// a negative number.  Where a wait has run out, units that were not reached have whatever the workspace held, which
-// must not be followed: the call has failed, and the join's loads and loops stay within the CTAs' places.)
+// Whether the CTAs first .. last have written partial results of a unit that are to be joined.  (A CTA that has a
+// unit whole leaves a negative number.  Where a wait has run out, units that were not reached have whatever the
+// workspace held, which must not be followed: the call has failed, and the join's loads and loops stay within the
+// CTAs' places.)
 __host__ __device__ constexpr bool span_joins(int first, int last, int ctas)
 {
     return first >= 0 && first <= last && last < ctas;

@@ -3,15 +3,15 @@
 // With p_i and q_i the model's and the draft's distributions at place i, draft x_i stands if u_i q_i(x_i) < p_i(x_i);
 // behind the last that stands a code is drawn from max(p_i - q_i, 0) or, behind all drafts, from p_i.
 //
-// As many borders as codes lie in [0, 1), so the draw's weights and sums take more than 32 bits (Weights); a test has one
-// border, so that 32 bits settle all but about one in 1,000 (kDoubt), and those are taken again.
+// As many borders as codes lie in [0, 1), so the draw's weights and sums take more than 32 bits (Weights); a test has
+// one border, so that 32 bits settle all but about one in 1,000 (kDoubt), and those are taken again.
 //
-// scan_kernel: the maxima and sums of exponentials of all rows that a draft or the code behind the drafts may need, in 32
-//   bits (each thread's running maximum and sum), a part of a row to a CTA: one pass.
-// verify_kernel, launched early: a cluster of up to 8 CTAs has a stream, a contiguous slice of the codes each.  All tests
-//   at once; then the row that the draw is from, and the draft's, by Weights: the sums of the weights of each warp's range,
-//   for max(p - q, 0) once more, now that both sums are known; the range, then the thread's share, then the code at which
-//   the running sum exceeds the target.
+// scan_kernel: the maxima and sums of exponentials of all rows that a draft or the code behind the drafts may need,
+//   in 32 bits (each thread's running maximum and sum), a part of a row to a CTA: one pass.
+// verify_kernel, launched early: a cluster of up to 8 CTAs has a stream, a contiguous slice of the codes each.  All
+//   tests at once; then the row that the draw is from, and the draft's, by Weights: the sums of the weights of each
+//   warp's range, for max(p - q, 0) once more, now that both sums are known; the range, then the thread's share, then
+//   the code at which the running sum exceeds the target.
 // Measured, 64,000 codes: 96 streams of up to 6 drafts, fp32, 90 us: the scan 32 (172 MB, 5.4 TB/s), then two passes of
 // 12 million weights, bound by the latency of a weight's chain at 24 warps an SM; 4 streams of 4 drafts, bf16, 22 us,
 // a chain of short steps.
@@ -35,8 +35,8 @@ constexpr int kMaxRows = 2 * (int)kMaxK + 1;
 constexpr int kCodes = 2;     // of a lane at a time in a pass (4 spill: 24.5 us for 22.5 with 4 streams)
 constexpr int kMaxParts = 16; // of a row in the scan
 constexpr float kLowest = -3.402823466e+38f;
-// Relative: a thread adds up to 2^7 terms in fp32 and exponentials are within 2^-15 (the rounding of arguments up to 126), so
-// a sum is within 2^-14 and a test within four times that.
+// Relative: a thread adds up to 2^7 terms in fp32 and exponentials are within 2^-15 (the rounding of arguments up to
+// 126), so a sum is within 2^-14 and a test within four times that.
 constexpr double kDoubt = 1.0 / 512;
 
 struct VerifyArgs {
@@ -48,7 +48,7 @@ struct VerifyArgs {
     int64_t logits_batch, logits_row, draft_batch, draft_row;
     int K, V, slice; // codes per CTA
     int parts, part; // of a row in the scan; codes of a part
-    uint64_t *stats; // [B][2 K + 1][parts]: of the model's rows, then the draft's; maximum and sum, greedy: the largest one's place
+    uint64_t *stats; // [B][2 K + 1][parts], the model's rows, then the draft's: maximum and sum; greedy: the largest's place
 };
 
 // 16 bytes are N codes.
@@ -102,14 +102,14 @@ __device__ __forceinline__ uint32_t order_key(float x)
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// exp((x - top) / T), top the row's largest logit, but for a factor of the row (`unit`), within 2^-33 and as a 64-bit number,
-// with most of its steps in 32 bits.  With x - base exact, its product with
-// 1024 log2(e) / T (two 32-bit numbers, lo the rest of hi) is k + f, k whole; 2^(k / 1024) comes from a table and the
-// exponent, 2^(f / 1024) - 1 = f (c1 + f c2) (|f c1| < 2^-11: the cubic term is below 2^-36, the rounding of f and of the
-// polynomial below 2^-34).  base is 0 up to |top| / T of 2000: logits that count are then below 2700 T and k below 2^22.  Above
-// that it is top: logits that count differ from top by less than half of it, so that the difference is exact.  Such
-// errors of 64,000 weights do not add up to what would move a draw; one weight by itself is taken with exact_weight.
-// Weights below 2^-1000 of the largest, -inf and NaN are 0.  Of +inf as top, or with a temperature next to 0, only top counts.
+// exp((x - top) / T), top the row's largest logit, but for a factor of the row (`unit`), within 2^-33 and as a 64-bit
+// number, with most of its steps in 32 bits.  With x - base exact, its product with 1024 log2(e) / T (two 32-bit
+// numbers, lo the rest of hi) is k + f, k whole; 2^(k / 1024) comes from a table and the exponent, 2^(f / 1024) - 1 =
+// f (c1 + f c2) (|f c1| < 2^-11: the cubic term is below 2^-36, the rounding of f and of the polynomial below 2^-34).
+// base is 0 up to |top| / T of 2000: logits that count are then below 2700 T and k below 2^22.  Above that it is top:
+// logits that count differ from top by less than half of it, so that the difference is exact.  Such errors of 64,000
+// weights do not add up to what would move a draw; one weight by itself is taken with exact_weight.  Weights below
+// 2^-1000 of the largest, -inf and NaN are 0.  Of +inf as top, or with a temperature next to 0, only top counts.
 constexpr int kTable = 1024;
 struct Weights {
     const double *table; // 2^(j / 1024)
@@ -153,7 +153,8 @@ struct Weights {
     __device__ __forceinline__ double operator()(const Row &r, float x) const
     {
         constexpr float c1 = (float)(0.6931471805599453 / kTable), c2 = c1 * c1 / 2;
-        const float d = fminf(x, r.cap) - r.base, m = fmaf(d, r.hi, 12582912.0f); // (1.5 2^23: a sum's low bits are its whole part)
+        const float d = fminf(x, r.cap) - r.base;
+        const float m = fmaf(d, r.hi, 12582912.0f); // (1.5 2^23: a sum's low bits are its whole part)
         const float f = fmaf(d, r.lo, fmaf(d, r.hi, 12582912.0f - m));
         const int k = __float_as_int(m) - r.k;
         const double t = table[k & (kTable - 1)], w = fma(t, (double)(f * fmaf(f, c2, c1)), t);
@@ -358,8 +359,9 @@ __global__ void __launch_bounds__(kMaxThreads) verify_kernel(const VerifyArgs g,
     for (int i = warp; i < drafts + 1 + (draft ? drafts : 0); i += warps) {
         const int r = i <= drafts ? i : g.K + 1 + (i - drafts - 1);
         const uint64_t none = greedy ? 0 : as_bits(make_float2(kLowest, 0.0f));
-        const uint64_t x = joined<kMaxParts>(
-            lane % kMaxParts < g.parts ? g.stats[(b * (2 * g.K + 1) + r) * g.parts + lane % kMaxParts] : none, greedy, st.per_t());
+        const int at = lane % kMaxParts;
+        const uint64_t x = joined<kMaxParts>(at < g.parts ? g.stats[(b * (2 * g.K + 1) + r) * g.parts + at] : none, greedy,
+                                             st.per_t());
         if (lane == 0) // greedy: the index's bits, inverted, and whether there is one
             sh.all[r] = greedy ? make_float2(__uint_as_float((uint32_t)x), x ? 1.0f : 0.0f) : as_pair(x);
     }
@@ -369,8 +371,9 @@ __global__ void __launch_bounds__(kMaxThreads) verify_kernel(const VerifyArgs g,
         if (draft && at < drafts)
             q_row = sh.all[g.K + 1 + at];
     };
-    // All passes over the codes in one loop, as it is the length of the code that counts with few streams: the sums of p's and
-    // q's weights, for a test in doubt or for the draw; of max(p - q, 0); of p's alone, where nothing is left of that.
+    // All passes over the codes in one loop, as it is the length of the code that counts with few streams: the sums
+    // of p's and q's weights, for a test in doubt or for the draw; of max(p - q, 0); of p's alone, where nothing is
+    // left of that.
     enum { kTests, kSums, kRest, kAlone } step = kTests;
     const T *p = nullptr, *q = nullptr;
     int place = 0, but = -1; // the place that the code is drawn at; the code that is left out
@@ -379,8 +382,8 @@ __global__ void __launch_bounds__(kMaxThreads) verify_kernel(const VerifyArgs g,
     auto emit = [&](int code) TOK_INLINE { g.out[b * (g.K + 1) + place] = code; };
     for (int passes = 0;; ++passes) {
         if (step == kTests) {
-            // v eq / zq < ep / zp: with the scan's sums at once, with exact ones one at a time.  (eq is 0 where the draft's
-            // row has no code.)
+            // v eq / zq < ep / zp: with the scan's sums at once, with exact ones one at a time.  (eq is 0 where the
+            // draft's row has no code.)
             if (again ? tid == place : tid < drafts) {
                 rows_of(tid);
                 int stands = 0;
@@ -622,8 +625,8 @@ template <typename T> tok_status launch(VerifyArgs g, int64_t B, cudaStream_t st
     const tok_status st = launch_status();
     if (st != TOK_OK)
         return st;
-    // With few streams an SM each for up to 8 CTAs of all threads that it takes (4 streams: 22 us, with 256 threads 39), else
-    // as many small CTAs as are resident at a time.
+    // With few streams an SM each for up to 8 CTAs of all threads that it takes (4 streams: 22 us, with 256 threads
+    // 39), else as many small CTAs as are resident at a time.
     const int64_t most = std::min<int64_t>(kMaxCluster, std::max<int64_t>(1, g.V / 2048));
     const bool few = B * most <= 148;
     const int C = (int)(few ? most : std::min(most, std::max<int64_t>(1, kCtas * 148 / B)));
@@ -692,7 +695,8 @@ extern "C" tok_status tok_verify_codes(const void *logits, const void *draft_log
     if (!logits || !u || !out || !accepted || !workspace || (K > 0 && !codes))
         return TOK_ERR_NULL;
     if (!aligned(logits, size) || !aligned(draft_logits, size) || !aligned(codes, 4) || !aligned(u, 4) ||
-        !aligned(n_draft, 4) || !aligned(temperature, 4) || !aligned(out, 4) || !aligned(accepted, 4) || !aligned(workspace, 16))
+        !aligned(n_draft, 4) || !aligned(temperature, 4) || !aligned(out, 4) || !aligned(accepted, 4) ||
+        !aligned(workspace, 16))
         return TOK_ERR_ALIGN;
     struct Range {
         const void *p;

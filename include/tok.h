@@ -600,9 +600,10 @@ TOK_API tok_status tok_cross_attention_backward(const tok_heads *q, const tok_he
  *   table, y : [V, D] and [N, D] of `dtype`, rows table_row and y_row elements apart, channels dense;
  *              computed in fp32, rounded once.
  * tok_embed_codes_backward -- grad_table[v] = scale * the sum of grad_y[n] over the tokens n
- *   with code v (overwritten; zero for a code without a token).  grad_y and grad_table have dtypes
- *   of their own.  Sums are fp32 and added in an order that depends on N, V, D, the dtypes, the
- *   alignment of the two tensors and the codes alone: tokens are sorted by code first, in rising order within a code.
+ *   with code v (overwritten; zero for a code without a token, if the scale is finite).  grad_y and grad_table have
+ *   dtypes of their own.  Sums are fp32: of m tokens they are off by up to m 2^-24 times the sum of |grad_y| (most are
+ *   added up in parts and are nearer).  Their order depends on N, V, D, the dtypes, the alignment of the two tensors
+ *   and the codes alone: tokens are sorted by code first, in rising order within a code.
  *   workspace: 16-byte-aligned device memory of tok_embed_codes_backward_workspace_size()
  *   bytes, overwritten; calls that may overlap need one each.  The size is -1 for an invalid shape.
  * Shape rule: 0 <= N < 2^30, 1 <= V <= 2^18, 1 <= D <= 65536; row strides at least D and below 2^38 / rows.
@@ -633,7 +634,8 @@ TOK_API tok_status tok_embed_codes_backward(const int32_t *codes, const void *gr
  * tok_page_release -- the pages that lens[b] tokens (negative: 0) do not need go back to the list, so that taking
  *   them anew gives each stream the same ones; their table entries become -1.  A list without room for all of them
  *   (F) stays as it is, as does everything else, and bad_count gets 1.
- * free_count is clamped to [0, F], held to [0, M]; so are free_out (written for B = 0, too, where both counts are given) and held_out.
+ * free_count is clamped to [0, F], held to [0, M]; so are free_out (written for B = 0, too, where both counts are
+ * given) and held_out.
  * Shape rule: 0 <= B <= 65535, 0 <= N, M, F < 2^31, page_size >= 1, M * page_size < 2^31, B * N, B * M < 2^31; table
  * rows table_row >= M elements apart, below 2^38 / B.
  */
@@ -658,8 +660,8 @@ typedef struct {
 /*
  * tok_paged_write -- k and v [B, N, H, D] bf16 into the pages: token n of stream b goes to slot slots[b][n]
  *   (page slot / page_size, row slot % page_size).  Slots below 0 are left out; one behind the pool
- *   is left out and adds 1 to bad_count (device int32 or NULL; the caller zeroes it).  Of several tokens with the same slot
- *   the last one, in the order of (b, n), need not win: the row is a mix of theirs.
+ *   is left out and adds 1 to bad_count (device int32 or NULL; the caller zeroes it).  Of several tokens with the
+ *   same slot the last one, in the order of (b, n), need not win: the row is a mix of theirs.
  * Shape rule: D a multiple of 8, 8 <= D <= 128; B, H <= 65535; B * N, P * page_size < 2^31; as tok_cross_attention
  * for strides and alignment (pointers and strides multiples of 16 bytes).
  */
@@ -673,17 +675,17 @@ TOK_API tok_status tok_paged_write(const tok_heads *k, const tok_heads *v, const
  *   q, o [B, Nq, Hq, D] bf16; k_pages, v_pages [P, page_size, Hkv, D] bf16; table [B, M] int32, rows
  *   table_row elements apart: token t of stream b is row t % page_size of page table[b][t / page_size].
  * Stream b has k_lens[b] tokens (clamped to [0, M * page_size]), the new ones among them: query i, for i < q_lens[b]
- * (NULL: Nq; clamped to [0, Nq]), is token k_lens[b] - q_lens[b] + i and sees the tokens up to itself. The keys and values
- * that it does not see show nowhere in its result, NaN included.  A query without a token (i >= q_lens[b], or
+ * (NULL: Nq; clamped to [0, Nq]), is token k_lens[b] - q_lens[b] + i and sees the tokens up to itself.  The keys and
+ * values that it does not see show nowhere in its result, NaN included.  A query without a token (i >= q_lens[b], or
  * a token before the first) has o = 0 and lse = -inf.  Formulas, head groups and the values that are not numbers are
- * tok_cross_attention's; so are the rules for q and o.  Weights enter their product within 2^-17 of their fp32 values, sums and
- * scores are fp32.  A query that sees a token whose entry of the table is outside [0, P) has NaN in both.
+ * tok_cross_attention's; so are the rules for q and o.  Weights enter their product within 2^-17 of their fp32 values,
+ * sums and scores are fp32.  A query that sees a token whose entry of the table is outside [0, P) has NaN in both.
  * lse [B, Hq, Nq] fp32 or NULL.  workspace: 16-byte-aligned device memory of
  * tok_paged_attention_workspace_size() bytes, overwritten; calls that may overlap need one each.
  * Results do not depend on the device's timing (every sum has a fixed order).
  * Shape rule: D a multiple of 8, 8 <= D <= 128; Hq a multiple of Hkv; 0 <= Nq <= 64; B, Hq <= 65535; B * Hq * Nq <
- * 2^30; P * page_size, M * page_size < 2^31; B * Hkv * (1 + Nq * Hq / Hkv / 64) * (3 + M * page_size / 128) < 2^31; page and
- * token strides of the pools positive (a head stride may be 0); the size is -1 for an invalid shape.
+ * 2^30; P * page_size < 2^31, M * page_size < 2^31 - 128; B * Hkv * (1 + Nq * Hq / Hkv / 64) * (3 + M * page_size / 128)
+ * < 2^31; page and token strides of the pools positive (a head stride may be 0); the size is -1 for an invalid shape.
  */
 TOK_API int64_t tok_paged_attention_workspace_size(int64_t B, int64_t Nq, int64_t Hq, int64_t Hkv, int64_t D);
 TOK_API tok_status tok_paged_attention(const tok_heads *q, const tok_pages *k_pages, const tok_pages *v_pages,
@@ -694,7 +696,7 @@ TOK_API tok_status tok_paged_attention(const tok_heads *q, const tok_pages *k_pa
 
 /*
  * tok_verify_codes -- which of the drafted codes stand, and the code that follows them, from given numbers in [0, 1).
- *   logits       : [B, K + 1, V] of `dtype` (input), the model's logits for each drafted code and for the one behind them
+ *   logits       : [B, K + 1, V] of `dtype` (input), the model's, for each drafted code and for the one behind them
  *   draft_logits : [B, K, V] of `dtype`, the logits that the drafts were drawn from, or NULL: each draft was certain
  *   codes        : [B, K] int32, the drafted codes (input; may be NULL for K = 0)
  *   u            : [B, K + 1] fp32 in [0, 1) (input)
@@ -706,9 +708,9 @@ TOK_API tok_status tok_paged_attention(const tok_heads *q, const tok_pages *k_pa
  * stands if all before it do and u[b][i] q_i(x_i) < p_i(x_i); behind the last that stands, a code is drawn with
  * u[b][K]: from max(p_i - q_i, 0) where draft i does not stand (from p_i where that is 0 throughout), from p_i behind
  * all drafts.  Drawn is the first code, in index order, at which the running sum exceeds u times the total; u is
- * clamped to [0, 1) (NaN: 0).  So the codes are distributed as draws from p.  temperature <= 0 (or NaN): p and q are 1 at the
- * first of the largest logits.  Logits of NaN count as -inf; where a logit is +inf only these count, alike.  A row of
- * logits all -inf refuses the draft and draws -1.  A drafted code outside [0, V) does not stand.
+ * clamped to [0, 1) (NaN: 0).  So the codes are distributed as draws from p.  temperature <= 0 (or NaN): p and q are 1
+ * at the first of the largest logits.  Logits of NaN count as -inf; where a logit is +inf only these count, alike.  A
+ * row of logits all -inf refuses the draft and draws -1.  A drafted code outside [0, V) does not stand.
  * Probabilities are within 2^-33 and added up in 64 bits, in a fixed order; a draft's test takes its two in 64 bits.
  * Temperatures above 2^100 count as that.  workspace: 16-byte-aligned device memory of tok_verify_codes_workspace_size()
  * bytes, overwritten; calls that may overlap need one each.  The size is -1 for an invalid shape.
